@@ -427,6 +427,166 @@ pafp8_status pafp8_append_kv(int32_t src_dtype, const void *k_new, const void *v
                              void *k_cache, void *v_cache, int32_t num_pages, int32_t page_size,
                              float k_scale, float v_scale, uint32_t *status, void *stream);
 
+/* Block tables and slot maps of one step, built on the device from request
+ * lengths: what pafp8_norm_rope_append, pafp8_append_kv and the run calls take
+ * as batch_indices, positions, slots, kv_indices and tree_mask.  With c_b
+ * tokens held by request b, n_b new ones and P = page_size, request b has
+ * ceil((c_b + n_b) / P) pages, of which those from ceil(c_b / P) on are taken
+ * from the free list, request after request.  All arrays are device memory.
+ *
+ *   cached_lens, new_lens  int32 [batch]: c_b and n_b, >= 0
+ *   block_table    int32 [batch, block_stride], the first block_width entries
+ *                  of a row used: in, the pages of the tokens held; the new
+ *                  pages are written behind them (the same call again writes
+ *                  the same entries)
+ *   free_pages     int32 [num_free]; free_used int32 [1]: entries taken before
+ *                  this step; free_used_out int32 [1]: entries taken after it
+ *                  (not free_used itself: the step could not be repeated)
+ *   kv_indptr, qo_indptr  int32 [batch + 1], last_page_len int32 [batch]:
+ *                  the arrays pafp8_plan_create takes, on the device
+ *                  (last_page_len 0 for a request with no tokens)
+ *   kv_indices     int32 [max_pages]: the page ids; entries behind
+ *                  kv_indptr[batch] are left as they were
+ *   batch_indices, positions  int32 [max_tokens], slots int64 [max_tokens]:
+ *                  per new token its request, its position c_b + u and its
+ *                  cache slot page * P + position % P.  Tokens behind
+ *                  qo_indptr[batch] get -1, 0 and -1, so a batch padded to
+ *                  max_tokens (a captured graph) writes nothing for them.
+ *   parents        int32 [max_tokens] or NULL: token u's parent among its
+ *                  request's new tokens, smaller than u, or -1 (a root, which
+ *                  follows the cached tokens).  NULL: a chain, u after u - 1.
+ *   rope_positions int32 [max_tokens] or NULL: c_b + depth(u), depth the
+ *                  number of u's ancestors among the new tokens
+ *   tree_mask      uint32 [max_tokens, mask_words] or NULL: bit w % 32 of word
+ *                  w / 32 is set when new token w is u or an ancestor of u;
+ *                  mask_words >= ceil(max n_b / 32).  Both are 0 behind the
+ *                  last token.
+ *   status         uint32 [1] or NULL: the kernel ORs in 1 when a length is
+ *                  negative, the free list or an array is too short, a page id
+ *                  in use is outside [0, num_pages), a parent is not smaller
+ *                  than its token, or a token has no bit in mask_words.  What
+ *                  has no room is not written; a token without a page gets
+ *                  slot -1, an entry without a page id -1; a parent that is
+ *                  not allowed counts as -1.
+ * Sums of pages and of tokens must stay below 2^31.  The new pages' order and
+ * every output depend on the inputs alone.  Nothing is allocated or
+ * synchronized.  Outputs must not overlap each other or the inputs, but for
+ * block_table. */
+typedef struct pafp8_tables_desc {
+    const int32_t *cached_lens;
+    const int32_t *new_lens;
+    int32_t *block_table;
+    const int32_t *free_pages;
+    const int32_t *free_used;
+    int32_t *free_used_out;
+    int32_t *kv_indptr;
+    int32_t *last_page_len;
+    int32_t *kv_indices;
+    int32_t *qo_indptr;
+    int32_t *batch_indices;
+    int32_t *positions;
+    int64_t *slots;
+    const int32_t *parents;
+    int32_t *rope_positions;
+    uint32_t *tree_mask;
+    uint32_t *status;
+    int64_t block_stride;
+    int64_t max_pages;
+    int64_t max_tokens;
+    int32_t batch;
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t num_free;
+    int32_t block_width;
+    int32_t mask_words;
+} pafp8_tables_desc;
+
+pafp8_status pafp8_build_tables(const pafp8_tables_desc *desc, void *stream);
+
+/* RMS norm of every query and key head, rotary rotation, and the append of
+ * keys and values to the paged cache, in one pass over a projection's output:
+ *   x' = x * rsqrt(mean over head_dim of x^2 + eps) * weight   (NULL: x' = x)
+ *   (y_a, y_b) = (x'_a c - x'_b s, x'_b c + x'_a s)   for each rotated pair
+ * in fp32, then q_out = y (fp8: as pafp8_append_kv quantizes, with q_scale),
+ * and at the token's slot k_cache = y and v_cache = v (fp8: quantized with
+ * k_scale / v_scale; a 2-byte cache: rounded once).
+ *
+ *   src_dtype      F16 or BF16: q, k, v and the weights
+ *   q, k, v        device [nnz, num_qo_heads | num_kv_heads, head_dim], heads
+ *                  of a token contiguous, tokens q_stride | k_stride |
+ *                  v_stride elements apart (one packed projection or three
+ *                  tensors); 16-byte aligned, strides multiples of 8
+ *   q_weight, k_weight  device [head_dim] of src_dtype, 16-byte aligned, or
+ *                  NULL (each alone: that norm is left out)
+ *   eps            finite, >= 0
+ *   cos_sin        device float [max_position, rot_dim], 16-byte aligned: row
+ *                  t holds the rot_dim / 2 cosines, then the sines, of the
+ *                  angles at position t
+ *   rot_dim        dims rotated, the head's first: a multiple of 16 up to
+ *                  head_dim
+ *   interleaved    0: dims (i, i + rot_dim / 2) make pair i; 1: dims (2i,
+ *                  2i + 1)
+ *   positions      device int32, num_axes (1 to 3) rows of nnz, pos_stride
+ *                  apart: the token's position on each axis (time, height,
+ *                  width)
+ *   pair_axis      device uint8 [rot_dim / 2]: the axis pair i turns by, in
+ *                  [0, num_axes); NULL: axis 0 for all
+ *   slots          device int64 [nnz]: cache slot (page * page_size + token in
+ *                  the page) of each token, no slot twice; -1: a padding
+ *                  token, for which nothing is written
+ *   q_out          device [nnz, num_qo_heads, head_dim], contiguous, of
+ *                  q_out_dtype: src_dtype (q_scale must be 1), E4M3FN or
+ *                  E5M2; may be q itself if q is contiguous and keeps its type
+ *   k_cache,
+ *   v_cache        device caches of kv_dtype (E4M3FN, E5M2 or src_dtype) in
+ *                  kv_layout, 16-byte aligned; only the tokens' rows are
+ *                  written.  A 2-byte cache takes scales of 1.
+ *   status         device uint32 or NULL: the kernel ORs in 1 for a token whose
+ *                  slot lies outside the pool (its keys and values are not
+ *                  written) or whose position lies outside [0, max_position)
+ *                  (nothing of it is written)
+ * Shapes served: head_dim 128 or 64, page_size a multiple of 16.  Nothing is
+ * allocated or synchronized. */
+typedef struct pafp8_rope_desc {
+    const void *q;
+    const void *k;
+    const void *v;
+    const void *q_weight;
+    const void *k_weight;
+    const float *cos_sin;
+    const int32_t *positions;
+    const uint8_t *pair_axis;
+    const int64_t *slots;
+    void *q_out;
+    void *k_cache;
+    void *v_cache;
+    uint32_t *status;
+    int64_t nnz;
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t pos_stride;
+    int32_t src_dtype;
+    int32_t q_out_dtype;
+    int32_t kv_dtype;
+    int32_t kv_layout;
+    int32_t num_qo_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t rot_dim;
+    int32_t interleaved;
+    int32_t num_axes;
+    int32_t max_position;
+    int32_t num_pages;
+    int32_t page_size;
+    float eps;
+    float q_scale;
+    float k_scale;
+    float v_scale;
+} pafp8_rope_desc;
+
+pafp8_status pafp8_norm_rope_append(const pafp8_rope_desc *desc, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -42,7 +43,8 @@ _NAME_CODES = {"default": DTYPE_DEFAULT, "f16": F16, "float16": F16, "bf16": BF1
 EXPORTS = ("pafp8_abi_version", "pafp8_last_error", "pafp8_plan_create", "pafp8_plan_destroy",
            "pafp8_workspace_bytes", "pafp8_plan_metadata", "pafp8_plan_upload", "pafp8_run",
            "pafp8_run_stage", "pafp8_device_status", "pafp8_run_decode_noalloc", "pafp8_append_kv",
-           "pafp8_run_head_scales", "pafp8_run_pod", "pafp8_host_workspace_bytes", "pafp8_run_host")
+           "pafp8_run_head_scales", "pafp8_run_pod", "pafp8_host_workspace_bytes", "pafp8_run_host",
+           "pafp8_build_tables", "pafp8_norm_rope_append")
 
 
 class Pafp8Error(RuntimeError):
@@ -70,6 +72,31 @@ class pod_phase(ctypes.Structure):
                 ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t)]
 
+
+class tables_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "cached_lens", "new_lens", "block_table", "free_pages", "free_used", "free_used_out", "kv_indptr",
+        "last_page_len", "kv_indices", "qo_indptr", "batch_indices", "positions", "slots", "parents", "rope_positions",
+        "tree_mask", "status")] + \
+        [(n, ctypes.c_int64) for n in ("block_stride", "max_pages", "max_tokens")] + \
+        [(n, ctypes.c_int32) for n in ("batch", "page_size", "num_pages", "num_free", "block_width", "mask_words")]
+
+
+class rope_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "q", "k", "v", "q_weight", "k_weight", "cos_sin", "positions", "pair_axis", "slots", "q_out", "k_cache",
+        "v_cache", "status")] + \
+        [(n, ctypes.c_int64) for n in ("nnz", "q_stride", "k_stride", "v_stride", "pos_stride")] + \
+        [(n, ctypes.c_int32) for n in (
+            "src_dtype", "q_out_dtype", "kv_dtype", "kv_layout", "num_qo_heads", "num_kv_heads", "head_dim", "rot_dim",
+            "interleaved", "num_axes", "max_position", "num_pages", "page_size")] + \
+        [(n, ctypes.c_float) for n in ("eps", "q_scale", "k_scale", "v_scale")]
+
+
+# The same two structures as struct formats: packing one costs a third of a
+# microsecond, filling a ctypes structure field by field five.
+_TABLES = struct.Struct("@17P3q6i")
+_ROPE = struct.Struct("@13P5q13i4f0q")
 
 _lib = None
 
@@ -114,8 +141,22 @@ def lib() -> ctypes.CDLL:
     L.pafp8_run_pod.argtypes = [ctypes.POINTER(pod_phase), ctypes.POINTER(pod_phase), i32, i32, vp, i32, vp,
                                 f32, f32, f32, i32, vp]
     L.pafp8_run_pod.restype = i32
+    # Their descriptions come packed (_TABLES, _ROPE) or as the structures above.
+    L.pafp8_build_tables.argtypes, L.pafp8_build_tables.restype = [vp, vp], i32
+    L.pafp8_norm_rope_append.argtypes, L.pafp8_norm_rope_append.restype = [vp, vp], i32
     _lib = L
     return L
+
+
+_I64 = _F32 = _U8 = None  # torch's dtype objects, once torch is in use
+
+
+def _I32():
+    """torch.int32 (imports torch on the first call: the module itself does not)."""
+    global _I64, _F32, _U8
+    import torch
+    _I64, _F32, _U8 = torch.int64, torch.float32, torch.uint8
+    return torch.int32
 
 
 _OBJ_CODES = {}  # dtype objects seen before -> code (the run calls pass torch dtypes)
@@ -319,6 +360,147 @@ def pafp8_append_kv(k_new, v_new, batch_indices, positions, kv_indptr, kv_indice
         _ptr(kv_indices), dtype_code(kv_dtype if kv_dtype is not None else k_cache.dtype), layout,
         _ptr(k_cache), _ptr(v_cache), int(num_pages if num_pages is not None else k_cache.shape[0]),
         page_size, float(k_scale), float(v_scale), _ptr(status), _stream(stream)))
+
+
+def _refuse(t, name, dtype, dev) -> None:
+    """The sentence for an array that _bad found wanting."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
+    raise ValueError(f"{name} (shape {tuple(t.shape)}, strides {t.stride()}) is not contiguous or too small")
+
+
+def _addr(t, name, n, dtype, dev) -> int:
+    """The address of a contiguous tensor of `dtype` on device `dev` with n
+    elements at least (None: 0); ValueError otherwise."""
+    if t is None:
+        return 0
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
+        _refuse(t, name, dtype, dev)
+    return t.data_ptr()
+
+
+def _device_of(t, name) -> int:
+    """The current CUDA device, which `t` must be on."""
+    import torch
+    dev = torch.cuda.current_device() if t.is_cuda else -2
+    if t.get_device() != dev:
+        _refuse(t, name, t.dtype, dev)
+    return dev
+
+
+def pafp8_build_tables(cached_lens, new_lens, block_table, free_pages, free_used, free_used_out, kv_indptr,
+                       last_page_len, kv_indices, qo_indptr, batch_indices, positions, slots, *, page_size, num_pages,
+                       parents=None, rope_positions=None, tree_mask=None, status=None, stream=None) -> None:
+    """Block tables and slot maps of one step from request lengths, on the
+    device (see include/pafp8.h; StepTables owns the outputs).  Arrays are
+    contiguous device int32 tensors, slots int64; block_table is
+    [batch, width] with contiguous rows; tree_mask is [tokens, words]."""
+    i32 = _I32()
+    dev = _device_of(cached_lens, "cached_lens")
+    batch, tokens = cached_lens.numel(), slots.numel()
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2:
+            raise ValueError(f"tree_mask has shape {tuple(tree_mask.shape)}, not [tokens, words]")
+        words = tree_mask.shape[1]
+    rows, width = block_table.shape
+    if rows < batch or block_table.dtype is not i32 or block_table.get_device() != dev or \
+            (width > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table {tuple(block_table.shape)} of {block_table.dtype} on {block_table.device} is not "
+                         f"an int32 [batch {batch}, width] device tensor with contiguous rows")
+    _check(lib().pafp8_build_tables(_TABLES.pack(
+        _addr(cached_lens, "cached_lens", batch, i32, dev), _addr(new_lens, "new_lens", batch, i32, dev),
+        block_table.data_ptr(), _addr(free_pages, "free_pages", 0, i32, dev), _addr(free_used, "free_used", 1, i32, dev),
+        _addr(free_used_out, "free_used_out", 1, i32, dev), _addr(kv_indptr, "kv_indptr", batch + 1, i32, dev),
+        _addr(last_page_len, "last_page_len", batch, i32, dev), _addr(kv_indices, "kv_indices", 0, i32, dev),
+        _addr(qo_indptr, "qo_indptr", batch + 1, i32, dev), _addr(batch_indices, "batch_indices", tokens, i32, dev),
+        _addr(positions, "positions", tokens, i32, dev), _addr(slots, "slots", tokens, _I64, dev),
+        _addr(parents, "parents", tokens, i32, dev), _addr(rope_positions, "rope_positions", tokens, i32, dev),
+        _addr(tree_mask, "tree_mask", tokens * words, i32, dev), _addr(status, "status", 1, i32, dev),
+        block_table.stride(0) if rows > 1 else width, kv_indices.numel(), tokens, batch, page_size, num_pages,
+        free_pages.numel(), width, words), _stream(stream)))
+
+
+def pafp8_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, q_out, k_cache, v_cache, *,
+                           eps=1e-6, pair_axis=None, interleaved=False, q_scale=1.0, k_scale=1.0, v_scale=1.0,
+                           kv_layout="NHD", status=None, stream=None) -> None:
+    """Per-head RMS norm of q [n, Hq, D] and k [n, Hkv, D], rotary rotation,
+    and the append of k and v to the paged cache at `slots`, in one pass (see
+    include/pafp8.h).  q, k and v may be slices of one packed projection (any
+    token stride); positions is int32 [n] or [axes, n], slots int64 [n],
+    cos_sin float32 [max_position, rot_dim].  Types come from the tensors."""
+    i32 = _I32()
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    dt = q.dtype
+    layout = _LAYOUTS[kv_layout] if isinstance(kv_layout, str) else int(kv_layout)
+    if k.shape != (n, hkv, d) or v.shape != k.shape or q_out.shape != q.shape:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} and q_out {tuple(q_out.shape)} are "
+                         "not [n, Hq, D], [n, Hkv, D], [n, Hkv, D] and [n, Hq, D]")
+    if k.dtype is not dt or v.dtype is not dt:
+        raise ValueError(f"q, k and v have different dtypes ({dt}, {k.dtype}, {v.dtype})")
+    dev = _device_of(q, "q")
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    if k.get_device() != dev or v.get_device() != dev or qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or \
+            (hq > 1 and qs[1] != d) or (hkv > 1 and (ks[1] != d or vs[1] != d)):
+        raise ValueError(f"q, k and v (on {q.device}, {k.device}, {v.device}; strides {qs}, {ks}, {vs}) must lie on the "
+                         "current CUDA device with the heads of a token contiguous")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if positions.dtype is not i32 or positions.get_device() != dev or positions.dim() > 2 or \
+            positions.shape[-1] != n or (n > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions {tuple(positions.shape)} of {positions.dtype} on {positions.device} is not an int32 "
+                         f"[{n}] or [axes, {n}] device tensor with contiguous rows")
+    limit, rot = cos_sin.shape
+    pages, a, b, _ = k_cache.shape
+    ps, heads = (b, a) if layout == LAYOUT_HND else (a, b)
+    if heads != hkv or k_cache.shape[3] != d or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} do not hold {hkv} heads of "
+                         f"{d} in layout {kv_layout}")
+    kt = k_cache.dtype
+    _check(lib().pafp8_norm_rope_append(_ROPE.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_weight, "q_weight", d, dt, dev),
+        _addr(k_weight, "k_weight", d, dt, dev), _addr(cos_sin, "cos_sin", 0, _F32, dev), positions.data_ptr(),
+        _addr(pair_axis, "pair_axis", rot // 2, _U8, dev), _addr(slots, "slots", n, _I64, dev),
+        _addr(q_out, "q_out", 0, q_out.dtype, dev), _addr(k_cache, "k_cache", 0, kt, dev),
+        _addr(v_cache, "v_cache", 0, kt, dev), _addr(status, "status", 1, i32, dev), n, qs[0], ks[0], vs[0],
+        positions.stride(0) if axes > 1 else n, dtype_code(dt), dtype_code(q_out.dtype), dtype_code(kt), layout, hq, hkv,
+        d, rot, 1 if interleaved else 0, axes, limit, pages, ps, eps, q_scale, k_scale, v_scale), _stream(stream)))
+
+
+class StepTables:
+    """Owns the device arrays that pafp8_build_tables fills for a step of up
+    to `batch` requests, `max_pages` pages and `max_tokens` new tokens:
+    kv_indptr, last_page_len, kv_indices, qo_indptr, batch_indices, positions,
+    slots, free_used, and, with mask_words > 0, rope_positions and tree_mask
+    (int32 words).  The arrays keep their addresses, so a step that uses them
+    can be captured into a graph."""
+
+    def __init__(self, *, batch: int, max_pages: int, max_tokens: int, page_size: int, num_pages: int,
+                 mask_words: int = 0, device="cuda"):
+        import torch
+        self.page_size, self.num_pages = int(page_size), int(num_pages)
+
+        def ints(*shape, dtype=torch.int32):
+            return torch.zeros(shape, dtype=dtype, device=device)
+
+        self.kv_indptr, self.qo_indptr, self.last_page_len = ints(batch + 1), ints(batch + 1), ints(batch)
+        self.kv_indices, self.free_used = ints(max_pages), ints(1)
+        self.batch_indices, self.positions = ints(max_tokens), ints(max_tokens)
+        self.slots = ints(max_tokens, dtype=torch.int64)
+        self.rope_positions = ints(max_tokens) if mask_words > 0 else None
+        self.tree_mask = ints(max_tokens, mask_words) if mask_words > 0 else None
+        self.status = ints(1)
+
+    def build(self, cached_lens, new_lens, block_table, free_pages, free_used, *, parents=None, stream=None) -> None:
+        """Fill the arrays (and block_table's new entries) for these lengths;
+        self.free_used holds the free list's entries taken after the step."""
+        pafp8_build_tables(cached_lens, new_lens, block_table, free_pages, free_used, self.free_used, self.kv_indptr,
+                           self.last_page_len, self.kv_indices, self.qo_indptr, self.batch_indices, self.positions,
+                           self.slots, page_size=self.page_size, num_pages=self.num_pages, parents=parents,
+                           rope_positions=self.rope_positions, tree_mask=self.tree_mask, status=self.status,
+                           stream=stream)
 
 
 # ---- convenience owner of a plan ---------------------------------------

@@ -1490,4 +1490,156 @@ pafp8_status pafp8_append_kv(int32_t src_dtype, const void* k_new, const void* v
     return PAFP8_OK;
 }
 
+pafp8_status pafp8_build_tables(const pafp8_tables_desc* desc, void* stream) {
+    if (desc == nullptr) return fail(PAFP8_ERR_ARG, "the description is NULL");
+    const pafp8_tables_desc& d = *desc;
+    if (d.batch < 0 || d.num_pages < 0 || d.num_free < 0 || d.max_pages < 0 || d.max_tokens < 0 || d.block_width < 0)
+        return fail(PAFP8_ERR_SHAPE,
+                    "batch %d, num_pages %d, num_free %d, max_pages %lld, max_tokens %lld and block_width %d must "
+                    "not be negative",
+                    (int)d.batch, (int)d.num_pages, (int)d.num_free, (long long)d.max_pages, (long long)d.max_tokens,
+                    (int)d.block_width);
+    if (d.page_size <= 0 || d.page_size % kPageSize != 0)
+        return fail(PAFP8_ERR_UNSUPPORTED, "page_size %d is not served by this library (a multiple of %d)",
+                    (int)d.page_size, kPageSize);
+    if (d.block_stride < d.block_width)
+        return fail(PAFP8_ERR_SHAPE, "block_stride %lld is smaller than block_width %d", (long long)d.block_stride,
+                    (int)d.block_width);
+    if (d.max_pages > INT32_MAX || d.max_tokens > INT32_MAX)
+        return fail(PAFP8_ERR_SHAPE, "max_pages %lld and max_tokens %lld must stay below 2^31", (long long)d.max_pages,
+                    (long long)d.max_tokens);
+    if (d.tree_mask != nullptr && d.mask_words <= 0)
+        return fail(PAFP8_ERR_SHAPE, "mask_words %d must be positive with a tree_mask", (int)d.mask_words);
+    if (d.free_used == nullptr || d.free_used_out == nullptr || d.kv_indptr == nullptr || d.qo_indptr == nullptr)
+        return fail(PAFP8_ERR_ARG, "free_used, free_used_out, kv_indptr and qo_indptr must be non-NULL");
+    if (d.free_used == d.free_used_out)
+        return fail(PAFP8_ERR_ARG, "free_used_out must not be free_used: the launch reads one while it writes the other");
+    if (d.batch > 0 && (d.cached_lens == nullptr || d.new_lens == nullptr || d.last_page_len == nullptr))
+        return fail(PAFP8_ERR_ARG, "cached_lens, new_lens and last_page_len must be non-NULL");
+    if ((d.batch > 0 && d.block_width > 0 && d.block_table == nullptr) || (d.num_free > 0 && d.free_pages == nullptr) ||
+        (d.max_pages > 0 && d.kv_indices == nullptr))
+        return fail(PAFP8_ERR_ARG, "block_table, free_pages and kv_indices must be non-NULL");
+    if (d.max_tokens > 0 && (d.batch_indices == nullptr || d.positions == nullptr || d.slots == nullptr))
+        return fail(PAFP8_ERR_ARG, "batch_indices, positions and slots must be non-NULL");
+    if (((uintptr_t)d.cached_lens | (uintptr_t)d.new_lens | (uintptr_t)d.block_table | (uintptr_t)d.free_pages |
+         (uintptr_t)d.free_used | (uintptr_t)d.free_used_out | (uintptr_t)d.kv_indptr | (uintptr_t)d.last_page_len |
+         (uintptr_t)d.kv_indices | (uintptr_t)d.qo_indptr | (uintptr_t)d.batch_indices | (uintptr_t)d.positions |
+         (uintptr_t)d.parents | (uintptr_t)d.rope_positions | (uintptr_t)d.tree_mask | (uintptr_t)d.status) % 4 != 0 ||
+        (uintptr_t)d.slots % 8 != 0)
+        return fail(PAFP8_ERR_ARG, "the arrays must be aligned to their elements (slots to 8 bytes, the others to 4)");
+    const cudaError_t e = launch_tables(d, (cudaStream_t)stream);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PAFP8_ERR_CUDA, "tables kernel launch failed: %s", cudaGetErrorString(e));
+    }
+    return PAFP8_OK;
+}
+
+pafp8_status pafp8_norm_rope_append(const pafp8_rope_desc* desc, void* stream) {
+    if (desc == nullptr) return fail(PAFP8_ERR_ARG, "the description is NULL");
+    const pafp8_rope_desc& d = *desc;
+    if (!is_2byte(d.src_dtype))
+        return fail(PAFP8_ERR_DTYPE, "q, k and v of dtype %s: norm_rope_append takes f16 or bf16 rows",
+                    dtype_name(d.src_dtype));
+    if (d.q_out_dtype != d.src_dtype && !is_fp8(d.q_out_dtype))
+        return fail(PAFP8_ERR_DTYPE, "q_out of dtype %s: it must be %s (the type of q), e4m3fn or e5m2",
+                    dtype_name(d.q_out_dtype), dtype_name(d.src_dtype));
+    if (d.kv_dtype != d.src_dtype && !is_fp8(d.kv_dtype))
+        return fail(PAFP8_ERR_DTYPE, "a cache of dtype %s: it must be %s (the type of k and v), e4m3fn or e5m2",
+                    dtype_name(d.kv_dtype), dtype_name(d.src_dtype));
+    if (d.kv_layout != PAFP8_LAYOUT_NHD && d.kv_layout != PAFP8_LAYOUT_HND)
+        return fail(PAFP8_ERR_ARG, "kv_layout %d is neither NHD (0) nor HND (1)", (int)d.kv_layout);
+    if (d.nnz < 0 || d.num_pages < 0)
+        return fail(PAFP8_ERR_SHAPE, "nnz %lld and num_pages %d must not be negative", (long long)d.nnz, (int)d.num_pages);
+    if (d.num_qo_heads <= 0 || d.num_kv_heads <= 0 || d.num_qo_heads > 65536 || d.num_kv_heads > 65536)
+        return fail(PAFP8_ERR_SHAPE, "head counts must be in [1, 65536] (num_qo_heads %d, num_kv_heads %d)",
+                    (int)d.num_qo_heads, (int)d.num_kv_heads);
+    if (d.head_dim != kHeadDim && d.head_dim != 64)
+        return fail(PAFP8_ERR_UNSUPPORTED, "head_dim %d is not served by this library (%d or 64)", (int)d.head_dim,
+                    kHeadDim);
+    if (d.rot_dim <= 0 || d.rot_dim % 16 != 0 || d.rot_dim > d.head_dim)
+        return fail(PAFP8_ERR_UNSUPPORTED, "rot_dim %d is not served (a multiple of 16 up to head_dim %d)", (int)d.rot_dim,
+                    (int)d.head_dim);
+    if (d.page_size <= 0 || d.page_size % kPageSize != 0)
+        return fail(PAFP8_ERR_UNSUPPORTED, "page_size %d is not served by this library (a multiple of %d)",
+                    (int)d.page_size, kPageSize);
+    if (d.num_axes < 1 || d.num_axes > 3) return fail(PAFP8_ERR_SHAPE, "num_axes %d is not 1, 2 or 3", (int)d.num_axes);
+    if (d.max_position <= 0) return fail(PAFP8_ERR_SHAPE, "max_position %d must be positive", (int)d.max_position);
+    if (!std::isfinite(d.eps) || d.eps < 0.0f) return fail(PAFP8_ERR_ARG, "eps %g must be finite and >= 0", (double)d.eps);
+    if (!scale_ok(d.q_scale) || !scale_ok(d.k_scale) || !scale_ok(d.v_scale))
+        return fail(PAFP8_ERR_ARG, "scales must be finite and > 0 (q %g, k %g, v %g)", (double)d.q_scale, (double)d.k_scale,
+                    (double)d.v_scale);
+    if (!is_fp8(d.q_out_dtype) && d.q_scale != 1.0f)
+        return fail(PAFP8_ERR_ARG, "q_scale %g given with a %s q_out: only an fp8 query is quantized by q_scale",
+                    (double)d.q_scale, dtype_name(d.q_out_dtype));
+    if (!is_fp8(d.kv_dtype) && (d.k_scale != 1.0f || d.v_scale != 1.0f))
+        return fail(PAFP8_ERR_ARG, "k_scale %g and v_scale %g given with a %s cache: it holds the values as they are",
+                    (double)d.k_scale, (double)d.v_scale, dtype_name(d.kv_dtype));
+    if (d.nnz == 0) return PAFP8_OK;
+    if (d.q == nullptr || d.k == nullptr || d.v == nullptr || d.cos_sin == nullptr || d.positions == nullptr || d.slots == nullptr ||
+        d.q_out == nullptr || d.k_cache == nullptr || d.v_cache == nullptr)
+        return fail(PAFP8_ERR_ARG,
+                    "q, k, v, cos_sin, positions, slots, q_out, k_cache and v_cache must be non-NULL");
+    const int64_t q_row = (int64_t)d.num_qo_heads * d.head_dim, kv_row = (int64_t)d.num_kv_heads * d.head_dim;
+    if (d.nnz > 1 && (d.q_stride < q_row || d.k_stride < kv_row || d.v_stride < kv_row || d.pos_stride < 0))
+        return fail(PAFP8_ERR_SHAPE,
+                    "token strides must cover a token's heads (q %lld of %lld, k %lld and v %lld of %lld elements)",
+                    (long long)d.q_stride, (long long)q_row, (long long)d.k_stride, (long long)d.v_stride, (long long)kv_row);
+    if (d.num_axes > 1 && d.pos_stride < d.nnz)
+        return fail(PAFP8_ERR_SHAPE, "pos_stride %lld is smaller than nnz %lld", (long long)d.pos_stride, (long long)d.nnz);
+    if (((uintptr_t)d.q | (uintptr_t)d.k | (uintptr_t)d.v | (uintptr_t)d.q_weight | (uintptr_t)d.k_weight | (uintptr_t)d.cos_sin |
+         (uintptr_t)d.q_out | (uintptr_t)d.k_cache | (uintptr_t)d.v_cache) % 16 != 0)
+        return fail(PAFP8_ERR_ARG,
+                    "q, k, v, the weights, cos_sin, q_out, k_cache and v_cache must be 16-byte aligned");
+    if (d.nnz > 1 && (d.q_stride % 8 != 0 || d.k_stride % 8 != 0 || d.v_stride % 8 != 0))
+        return fail(PAFP8_ERR_ARG, "token strides must be multiples of 8 elements (q %lld, k %lld, v %lld)",
+                    (long long)d.q_stride, (long long)d.k_stride, (long long)d.v_stride);
+    if (((uintptr_t)d.positions | (uintptr_t)d.status) % 4 != 0 || (uintptr_t)d.slots % 8 != 0)
+        return fail(PAFP8_ERR_ARG, "positions and status must be 4-byte aligned, slots 8-byte aligned");
+    if (d.q_out == d.q && (d.q_out_dtype != d.src_dtype || (d.nnz > 1 && d.q_stride != q_row)))
+        return fail(PAFP8_ERR_ARG, "q_out may be q only if q is contiguous and q_out keeps its type");
+    RopeParams p{};
+    p.q = d.q;
+    p.k = d.k;
+    p.v = d.v;
+    p.q_stride = d.q_stride;
+    p.k_stride = d.k_stride;
+    p.v_stride = d.v_stride;
+    p.q_weight = d.q_weight;
+    p.k_weight = d.k_weight;
+    p.cos_sin = d.cos_sin;
+    p.positions = d.positions;
+    p.pair_axis = d.pair_axis;
+    p.slots = (const long long*)d.slots;
+    p.q_out = d.q_out;
+    p.k_cache = d.k_cache;
+    p.v_cache = d.v_cache;
+    p.status = d.status;
+    p.nnz = d.nnz;
+    p.pos_stride = d.pos_stride;
+    p.num_slots = (long long)d.num_pages * d.page_size;
+    p.num_qo_heads = d.num_qo_heads;
+    p.num_kv_heads = d.num_kv_heads;
+    p.head_dim = d.head_dim;
+    p.rot_dim = d.rot_dim;
+    p.max_position = d.max_position;
+    p.num_axes = d.num_axes;
+    p.src_dtype = d.src_dtype;
+    p.kv_dtype = d.kv_dtype;
+    p.q_out_dtype = d.q_out_dtype;
+    p.interleaved = d.interleaved != 0;
+    p.hnd = d.kv_layout == PAFP8_LAYOUT_HND;
+    p.page_size = d.page_size;
+    p.eps = d.eps;
+    p.q_inv = 1.0f / d.q_scale;  // IEEE fp32 division: fp32(1/scale)
+    p.k_inv = 1.0f / d.k_scale;
+    p.v_inv = 1.0f / d.v_scale;
+    const cudaError_t e = launch_rope(p, (cudaStream_t)stream);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PAFP8_ERR_CUDA, "norm_rope_append kernel launch failed: %s", cudaGetErrorString(e));
+    }
+    return PAFP8_OK;
+}
+
 }  // extern "C"

@@ -140,6 +140,31 @@ struct AppendParams {
     float k_inv, v_inv;      // fp32(1 / scale)
 };
 
+using TablesParams = pafp8_tables_desc;  // the kernel takes the call's description as it is
+
+struct RopeParams {
+    const void* q;               // [nnz, Hq, D], tokens q_stride elements apart
+    const void* k;               // [nnz, Hkv, D]
+    const void* v;
+    long long q_stride, k_stride, v_stride;
+    const void* q_weight;        // [D] of src_dtype, or nullptr: no norm
+    const void* k_weight;
+    const float* cos_sin;        // [max_position, rot_dim]: cosines, then sines
+    const int32_t* positions;    // [num_axes] rows pos_stride apart, of nnz
+    const uint8_t* pair_axis;    // [rot_dim / 2] or nullptr (axis 0)
+    const long long* slots;      // [nnz]
+    void* q_out;                 // [nnz, Hq, D] of q_out_dtype
+    void* k_cache;
+    void* v_cache;
+    uint32_t* status;            // or nullptr
+    long long nnz, pos_stride, num_slots;
+    int num_qo_heads, num_kv_heads, head_dim, rot_dim, max_position, num_axes;
+    int src_dtype, kv_dtype, q_out_dtype;
+    int interleaved;             // pairs: 0 dims (i, i + rot_dim / 2), 1 dims (2i, 2i + 1)
+    int hnd, page_size;
+    float eps, q_inv, k_inv, v_inv;  // inv: fp32(1 / scale)
+};
+
 struct PrefillParams {
     const void* q;           // [nnz_qo, Hq, D]
     int head_dim;            // D: 128 or 64
@@ -172,6 +197,8 @@ cudaError_t launch_decode(const DecodeParams& p, const CUtensorMap& tmap_k,
                           const CUtensorMap& tmap_v, int num_ctas, int heads_per_cta,
                           int group, int heads_per_box, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream);
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 // Size of the built-in scratch of the no-allocation decode entry point, and
 // the device ordinals it serves.
 constexpr size_t kNoAllocScratchBytes = PAFP8_NOALLOC_SCRATCH_BYTES;
