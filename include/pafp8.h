@@ -81,7 +81,7 @@ typedef enum pafp8_status {
     PAFP8_ERR_UNSUPPORTED = 8  /* valid request this library does not serve  */
 } pafp8_status;
 
-enum { PAFP8_MODE_DECODE = 0, PAFP8_MODE_PREFILL = 1 };
+enum { PAFP8_MODE_DECODE = 0, PAFP8_MODE_PREFILL = 1, PAFP8_MODE_TREE = 2 };
 
 /* Layout of k_cache / v_cache (head_dim is always innermost):
  *   NHD  [num_pages, page_size, num_kv_heads, head_dim]  (token-major page)
@@ -96,7 +96,7 @@ enum { PAFP8_LAYOUT_NHD = 0, PAFP8_LAYOUT_HND = 1 };
  * head_dim 128 or 64; page_size a multiple of 16 in either layout, a page of 16 m tokens
  * being read as m 16-token sub-pages (token slots 16 j .. 16 j + 15 of every head, so
  * num_pages * page_size / 16 must stay below 2^31); num_qo_heads a multiple of num_kv_heads with
- * group size num_qo_heads/num_kv_heads <= 8 (decode) or <= 16 (prefill).
+ * group size num_qo_heads/num_kv_heads <= 8 (decode), <= 16 (prefill) or <= 128 (tree).
  *
  * Dtype rules (checked by pafp8_plan_create, re-checked by pafp8_run):
  *   kv_dtype   E4M3FN or E5M2.  Decode also takes an F16 or BF16 cache
@@ -125,7 +125,7 @@ enum { PAFP8_LAYOUT_NHD = 0, PAFP8_LAYOUT_HND = 1 };
  * kv_layout    NHD (0, also what a zeroed description gives) or HND; the
  *              caches given to pafp8_run are read in that layout. */
 typedef struct pafp8_plan_desc {
-    int32_t mode;  /* PAFP8_MODE_DECODE or PAFP8_MODE_PREFILL */
+    int32_t mode;  /* PAFP8_MODE_DECODE, PAFP8_MODE_PREFILL or PAFP8_MODE_TREE */
     int32_t batch;
     int32_t num_qo_heads;
     int32_t num_kv_heads;
@@ -159,7 +159,7 @@ const char *pafp8_last_error(void);
  *                   pages (its kv_len = (npages-1)*page_size + last_page_len);
  *                   ignored for a request with no pages (kv_len 0: output 0,
  *                   lse -inf).
- *   qo_indptr_h     host int32 [batch+1] for prefill (request b owns query
+ *   qo_indptr_h     host int32 [batch+1] for prefill and tree (request b owns query
  *                   rows qo_indptr_h[b] .. qo_indptr_h[b+1]-1, with
  *                   qo_len <= kv_len); NULL for decode (row b is request b).
  * The arrays are copied; the caller may free them after the call.  On
@@ -290,6 +290,36 @@ pafp8_status pafp8_run_head_scales(const pafp8_plan *plan, int32_t q_dtype, cons
                                    const float *q_scales, const float *k_scales,
                                    const float *v_scales, int32_t o_dtype, void *o, float *lse,
                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Attention of a tree of drafted tokens over the cache, for a plan of
+ * PAFP8_MODE_TREE (made like a prefill plan: qo_indptr_h gives request b's
+ * T_b = qo_len drafted tokens, the last T_b of its kv_len cached ones, their
+ * keys and values already in the cache).  Drafted token u sees every key
+ * j < kv_len - T_b, and key kv_len - T_b + w where bit w % 32 of word w / 32
+ * of its mask row is set -- itself and its ancestors, in the masks that
+ * pafp8_build_tables writes, but any mask is taken: bits from T_b on are
+ * ignored, and a token that sees nothing gives o = 0, lse = -inf.
+ *   tree_mask   device uint32 [nnz_qo, mask_words], mask_words >=
+ *               ceil(T_b / 32) for every request
+ *   q_scales,
+ *   k_scales,
+ *   v_scales    NULL, or per-head scales as pafp8_run_head_scales takes them
+ *               (the per-tensor ones must then be 1)
+ * Every other argument and check is pafp8_run's.  Served: the dtypes of a
+ * prefill plan (fp8 cache with any query, 2-byte cache of the query's own
+ * dtype), head_dim 128 or 64, both layouts, up to 128 query heads per KV
+ * head.  A 2-byte query over an fp8 cache is multiplied exactly to 2^-18 of
+ * its row's largest magnitude; probabilities are rounded to 8 significant
+ * bits for a bf16 output over an fp8 cache, 12 for an f16 one, and to the
+ * cache's type over a 2-byte cache.  A NaN or infinity in the value row of a
+ * cached token reaches every drafted token of its request, whether its mask
+ * shows that token or not. */
+pafp8_status pafp8_run_tree(const pafp8_plan *plan, int32_t q_dtype, const void *q, int32_t k_dtype,
+                            const void *k_cache, int32_t v_dtype, const void *v_cache,
+                            const int32_t *kv_indices, const uint32_t *tree_mask, int32_t mask_words,
+                            float q_scale, float k_scale, float v_scale, const float *q_scales,
+                            const float *k_scales, const float *v_scales, int32_t o_dtype, void *o, float *lse,
+                            void *workspace, size_t workspace_bytes, void *stream);
 
 /* Synchronize `stream`, read and clear the workspace status word that the
  * kernels set.  Returns PAFP8_OK, PAFP8_ERR_BOUNDS (a page index was out of

@@ -30,7 +30,8 @@ LIB_PATH = os.path.join(_HERE, "libpafp8.so")
 
 # dtype codes of include/pafp8.h
 DTYPE_DEFAULT, F16, BF16, E4M3FN, E5M2, F32, INT8, UINT8 = range(8)
-MODE_DECODE, MODE_PREFILL = 0, 1
+MODE_DECODE, MODE_PREFILL, MODE_TREE = 0, 1, 2
+_MODES = {"decode": MODE_DECODE, "prefill": MODE_PREFILL, "tree": MODE_TREE}
 LAYOUT_NHD, LAYOUT_HND = 0, 1
 _LAYOUTS = {"NHD": LAYOUT_NHD, "HND": LAYOUT_HND}
 STATUS = {0: "OK", 1: "ERR_DTYPE", 2: "ERR_SHAPE", 3: "ERR_ARG", 4: "ERR_WORKSPACE", 5: "ERR_CUDA",
@@ -44,7 +45,7 @@ EXPORTS = ("pafp8_abi_version", "pafp8_last_error", "pafp8_plan_create", "pafp8_
            "pafp8_workspace_bytes", "pafp8_plan_metadata", "pafp8_plan_upload", "pafp8_run",
            "pafp8_run_stage", "pafp8_device_status", "pafp8_run_decode_noalloc", "pafp8_append_kv",
            "pafp8_run_head_scales", "pafp8_run_pod", "pafp8_host_workspace_bytes", "pafp8_run_host",
-           "pafp8_build_tables", "pafp8_norm_rope_append")
+           "pafp8_build_tables", "pafp8_norm_rope_append", "pafp8_run_tree")
 
 
 class Pafp8Error(RuntimeError):
@@ -141,6 +142,9 @@ def lib() -> ctypes.CDLL:
     L.pafp8_run_pod.argtypes = [ctypes.POINTER(pod_phase), ctypes.POINTER(pod_phase), i32, i32, vp, i32, vp,
                                 f32, f32, f32, i32, vp]
     L.pafp8_run_pod.restype = i32
+    L.pafp8_run_tree.argtypes = [vp, i32, vp, i32, vp, i32, vp, vp, vp, i32, f32, f32, f32, vp, vp, vp, i32, vp, vp, vp,
+                                 sz, vp]
+    L.pafp8_run_tree.restype = i32
     # Their descriptions come packed (_TABLES, _ROPE) or as the structures above.
     L.pafp8_build_tables.argtypes, L.pafp8_build_tables.restype = [vp, vp], i32
     L.pafp8_norm_rope_append.argtypes, L.pafp8_norm_rope_append.restype = [vp, vp], i32
@@ -303,6 +307,25 @@ def pafp8_run_head_scales(handle: int, q, k_cache, v_cache, kv_indices, o, lse, 
         dtype_code(v_dtype if v_dtype is not None else v_cache.dtype), _ptr(v_cache),
         _ptr(kv_indices), _ptr(q_scales), _ptr(k_scales), _ptr(v_scales),
         dtype_code(o_dtype if o_dtype is not None else o.dtype), _ptr(o), _ptr(lse),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def pafp8_run_tree(handle: int, q, k_cache, v_cache, kv_indices, tree_mask, o, lse, workspace, *, q_scale=1.0,
+                   k_scale=1.0, v_scale=1.0, q_scales=None, k_scales=None, v_scales=None, q_dtype=None, k_dtype=None,
+                   v_dtype=None, o_dtype=None, stream=None) -> None:
+    """Attention of a tree of drafted tokens (a plan of mode "tree"): tree_mask
+    [nnz_qo, words] of int32 (bits), as StepTables holds it; per-head scale
+    tensors instead of the per-tensor ones when k_scales is given."""
+    if tree_mask.dim() != 2 or tree_mask.element_size() != 4 or not tree_mask.is_contiguous() or \
+            tree_mask.shape[0] < q.shape[0] or tree_mask.get_device() != q.get_device():
+        raise ValueError(f"tree_mask {tuple(tree_mask.shape)} of {tree_mask.dtype} on {tree_mask.device} is not a "
+                         f"contiguous int32 [{q.shape[0]}, words] tensor on the query's device")
+    _check(lib().pafp8_run_tree(
+        handle, dtype_code(q_dtype if q_dtype is not None else q.dtype), _ptr(q),
+        dtype_code(k_dtype if k_dtype is not None else k_cache.dtype), _ptr(k_cache),
+        dtype_code(v_dtype if v_dtype is not None else v_cache.dtype), _ptr(v_cache),
+        _ptr(kv_indices), _ptr(tree_mask), tree_mask.shape[1], q_scale, k_scale, v_scale, _ptr(q_scales), _ptr(k_scales),
+        _ptr(v_scales), dtype_code(o_dtype if o_dtype is not None else o.dtype), _ptr(o), _ptr(lse),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -516,7 +539,7 @@ class Plan:
                  kv_layout: str = "NHD"):
         kv_indptr_h = _i32_host(kv_indptr)
         self.desc = plan_desc(
-            mode=MODE_DECODE if mode == "decode" else MODE_PREFILL, batch=len(kv_indptr_h) - 1,
+            mode=_MODES.get(mode, MODE_PREFILL), batch=len(kv_indptr_h) - 1,
             num_qo_heads=num_qo_heads, num_kv_heads=num_kv_heads, head_dim=head_dim,
             page_size=page_size, num_pages=num_pages, q_dtype=dtype_code(q_dtype),
             kv_dtype=dtype_code(kv_dtype),
@@ -553,6 +576,9 @@ class Plan:
 
     def run_head_scales(self, q, k_cache, v_cache, kv_indices, o, lse, workspace, **kw) -> None:
         pafp8_run_head_scales(self.handle, q, k_cache, v_cache, kv_indices, o, lse, workspace, **kw)
+
+    def run_tree(self, q, k_cache, v_cache, kv_indices, tree_mask, o, lse, workspace, **kw) -> None:
+        pafp8_run_tree(self.handle, q, k_cache, v_cache, kv_indices, tree_mask, o, lse, workspace, **kw)
 
     def run_stage(self, stage, q, k_cache, v_cache, kv_indices, o, lse, workspace, **kw) -> None:
         pafp8_run_stage(self.handle, stage, q, k_cache, v_cache, kv_indices, o, lse, workspace, **kw)

@@ -70,11 +70,11 @@ pafp8_status check_kv_dtype(int32_t kv, const char* what, int32_t mode, int32_t 
                         "%s has dtype %s but q is %s: an fp8 query needs an fp8 cache (the QK "
                         "product runs on the tensor cores in one operand type)",
                         what, dtype_name(kv), dtype_name(q));
-        if (mode == PAFP8_MODE_PREFILL && kv != q)
+        if (mode != PAFP8_MODE_DECODE && kv != q)
             return fail(PAFP8_ERR_DTYPE,
-                        "%s has dtype %s but q is %s: prefill takes a 2-byte cache only of the "
+                        "%s has dtype %s but q is %s: %s takes a 2-byte cache only of the "
                         "query's own dtype (decode accepts either mix)",
-                        what, dtype_name(kv), dtype_name(q));
+                        what, dtype_name(kv), dtype_name(q), mode == PAFP8_MODE_TREE ? "tree attention" : "prefill");
         return PAFP8_OK;
     }
     if (kv == PAFP8_INT8 || kv == PAFP8_UINT8)
@@ -134,6 +134,8 @@ struct pafp8_plan {
     int page_mult = 1;
     std::vector<int32_t> vptr;
     int num_ctas = 0, num_partials = 0, num_merge = 0;
+    int rows_pad = 0;    // tree: rows of the largest row tile
+    int mask_words = 0;  // tree: words the longest draft needs
     size_t meta_bytes = 0, part_o_off = 0, part_lse_off = 0, status_off = 0, ws_bytes = 0;
     void* uploaded_ws = nullptr;
     // Side stream and fork/join events of pafp8_run_pod for a decode plan,
@@ -470,8 +472,160 @@ void build_prefill_meta(pafp8_plan* pl) {
     pl->num_merge = 0;
 }
 
+// Tree partition.  A line is a (request, row tile of 128 / group tokens) pair,
+// its cost its 128-key tiles plus kTreeSegCost for starting it.  Heads are
+// dealt to CTAs in blocks of hb (a divisor of the KV heads): the lines, laid
+// end to end once per head block, are cut into num_ctas / hb ranges of equal
+// cost, and CTA i * hb + h takes range i for head h of the block, so the CTAs
+// reading the heads of one token-major page run at the same time.  hb is the
+// largest divisor whose busiest CTA is within 3 % of the best one's.  A
+// segment that is not its whole line has a slot for its partial state; a
+// split line's slots are consecutive.
+constexpr int kTreeSegCost = 1;
+void build_tree_meta(pafp8_plan* pl) {
+    const int B = pl->desc.batch, hkv = pl->desc.num_kv_heads, g = pl->group;
+    const int TQ = kTileRows / g;
+    struct Line { int32_t b, t0, nt; };
+    std::vector<Line> lines;
+    int64_t cost = 0;
+    pl->rows_pad = 0;
+    for (int b = 0; b < B; ++b) {
+        const int qo = pl->qo_indptr[b + 1] - pl->qo_indptr[b];
+        const int32_t n = pl->kv_indptr[b + 1] - pl->kv_indptr[b];
+        const int64_t kv = n > 0 ? (int64_t)(n - 1) * pl->desc.page_size + pl->last_page_len[b] : 0;
+        pl->mask_words = std::max(pl->mask_words, (qo + 31) / 32);
+        for (int t0 = 0; t0 < qo; t0 += TQ) {
+            lines.push_back({b, t0, (int32_t)((kv + kTileKeys - 1) / kTileKeys)});
+            cost += lines.back().nt + kTreeSegCost;
+            pl->rows_pad = std::max(pl->rows_pad, std::min(TQ, qo - t0) * g);
+        }
+    }
+    int hb = 1;
+    int64_t groups = 1;
+    {
+        int64_t best = INT64_MAX;
+        for (int pass = 0; pass < 2; ++pass)
+            for (int d = 1; d <= hkv && d <= pl->desc.num_ctas; ++d) {
+                if (hkv % d != 0) continue;
+                const int64_t total = cost * (hkv / d), n = pl->desc.num_ctas / d, busiest = (total + n - 1) / n;
+                if (pass == 0)
+                    best = std::min(best, busiest);
+                else if (100 * busiest <= 103 * best)
+                    hb = d;
+            }
+        groups = std::max<int64_t>(1, std::min<int64_t>(pl->desc.num_ctas / hb, (int64_t)(hkv / hb) * (cost - (int64_t)lines.size() * kTreeSegCost)));
+    }
+    const int nhb = hkv / hb;
+    const int64_t total = cost * nhb;
+    // Ranges of the line axis, the same for every head of a block: (line of
+    // the block, tiles), cut at multiples of total / groups.
+    struct Part { int32_t block, line, a, e; };
+    std::vector<Part> parts;
+    std::vector<int64_t> range_ptr(1, 0);
+    {
+        int64_t at = 0, i = 0;  // cost before this line; the range being filled
+        auto end_of = [&](int64_t k) { return (k + 1) * total / groups; };
+        for (int blk = 0; blk < nhb; ++blk)
+            for (size_t l = 0; l < lines.size(); ++l) {
+                const int64_t c = lines[l].nt + kTreeSegCost;
+                int64_t a = 0;  // tiles of this line placed
+                while (a < lines[l].nt) {
+                    // Tiles of this line that end inside range i.
+                    int64_t e = i + 1 >= groups ? lines[l].nt : std::min<int64_t>(lines[l].nt, end_of(i) - at - kTreeSegCost);
+                    if (e > a) {
+                        parts.push_back({blk, (int32_t)l, (int32_t)a, (int32_t)e});
+                        a = e;
+                    }
+                    if (a < lines[l].nt) {
+                        range_ptr.push_back((int64_t)parts.size());
+                        ++i;
+                    }
+                }
+                at += c;
+                while (i + 1 < groups && at >= end_of(i)) {
+                    range_ptr.push_back((int64_t)parts.size());
+                    ++i;
+                }
+            }
+        while ((int64_t)range_ptr.size() < groups + 1) range_ptr.push_back((int64_t)parts.size());
+    }
+    // Slots, numbered line by line: parts of a line are consecutive in `parts`
+    // and the heads of a block follow one another.
+    std::vector<int32_t> slot0(parts.size(), -1);
+    std::vector<int32_t> merges;
+    int32_t nslot = 0, nmerge = 0;
+    for (size_t k = 0; k < parts.size();) {
+        size_t e = k + 1;
+        while (e < parts.size() && parts[e].line == parts[k].line && parts[e].block == parts[k].block) ++e;
+        const int32_t n = (int32_t)(e - k);
+        if (n > 1) {
+            const Line& ln = lines[parts[k].line];
+            const int qo = pl->qo_indptr[ln.b + 1] - pl->qo_indptr[ln.b];
+            for (int32_t i = 0; i < n; ++i) slot0[k + i] = nslot + i;  // head h of the block: + h n
+            for (int h = 0; h < hb; ++h) {
+                const int32_t rec[8] = {nslot + h * n, nslot + (h + 1) * n, pl->qo_indptr[ln.b] + ln.t0,
+                                        parts[k].block * hb + h, std::min(TQ, qo - ln.t0) * g, n, 0, 0};
+                merges.insert(merges.end(), rec, rec + 8);
+                ++nmerge;
+            }
+            nslot += n * hb;
+        }
+        k = e;
+    }
+
+    std::vector<int32_t>& m = pl->meta;
+    m.assign(kMetaHeaderWords, 0);
+    m[kMetaMagic] = kMetaMagicValue;
+    m[kMetaMode] = PAFP8_MODE_TREE;
+    m[kMetaBatch] = B;
+    m[kMetaHeadBlocks] = nhb;
+    m[kMetaHeadsPerCta] = hb;
+    m[kMetaGroup] = g;
+    m[kMetaTileRows] = TQ;
+    const int G = parts.empty() ? 0 : (int)(groups * hb);
+    m[kMetaNumCtas] = G;
+    m[kMetaNumPartials] = nslot;
+    m[kMetaNumMerge] = nmerge;
+    m[kMetaOffTile] = (int32_t)m.size();
+    m.insert(m.end(), merges.begin(), merges.end());
+    m[kMetaOffSeg] = (int32_t)m.size();  // 16-byte aligned: everything before is in multiples of four words
+    std::vector<int32_t> cta_ptr(1, 0);
+    int32_t nseg = 0;
+    for (int64_t i = 0; i < (G > 0 ? groups : 0); ++i)
+        for (int h = 0; h < hb; ++h) {
+            for (int64_t k = range_ptr[i]; k < range_ptr[i + 1]; ++k) {
+                const Part& pt = parts[k];
+                const Line& ln = lines[pt.line];
+                // A split line's parts: this head's slots lie h * n after head 0's.
+                int32_t slot = -1;
+                if (slot0[k] >= 0) {
+                    int64_t a = k, e = k;
+                    while (a > 0 && parts[a - 1].line == pt.line && parts[a - 1].block == pt.block) --a;
+                    while (e + 1 < (int64_t)parts.size() && parts[e + 1].line == pt.line && parts[e + 1].block == pt.block) ++e;
+                    slot = slot0[k] + h * (int32_t)(e - a + 1);
+                }
+                const int32_t n = pl->kv_indptr[ln.b + 1] - pl->kv_indptr[ln.b];
+                const int32_t rec[kTreeSegWords] = {pt.block * hb + h, ln.t0, pt.a, pt.e, slot, pl->qo_indptr[ln.b],
+                                                    pl->qo_indptr[ln.b + 1] - pl->qo_indptr[ln.b],
+                                                    (n - 1) * pl->desc.page_size + pl->last_page_len[ln.b],
+                                                    pl->kv_indptr[ln.b], 0, 0, 0};
+                m.insert(m.end(), rec, rec + kTreeSegWords);
+                ++nseg;
+            }
+            cta_ptr.push_back(nseg);
+        }
+    m[kMetaNumSegs] = nseg;
+    m[kMetaOffCtaSeg] = (int32_t)m.size();
+    m.insert(m.end(), cta_ptr.begin(), cta_ptr.end());
+    pl->num_ctas = G;
+    pl->num_partials = nslot;
+    pl->num_merge = nmerge;
+}
+
 void layout_workspace(pafp8_plan* pl) {
-    const size_t heads = (size_t)pl->heads_per_cta * pl->group;
+    // Rows of a partial state: a decode CTA's query heads, a tree plan's
+    // largest row tile.
+    const size_t heads = pl->desc.mode == PAFP8_MODE_TREE ? (size_t)pl->rows_pad : (size_t)pl->heads_per_cta * pl->group;
     pl->meta_bytes = align_up(pl->meta.size() * sizeof(int32_t), 256);
     pl->part_o_off = pl->meta_bytes;
     pl->part_lse_off = align_up(pl->part_o_off + (size_t)pl->num_partials * heads * pl->desc.head_dim * 4, 256);
@@ -756,8 +910,9 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
     if (desc_in == nullptr) return fail(PAFP8_ERR_ARG, "plan description is NULL");
     pafp8_plan_desc d = *desc_in;
 
-    if (d.mode != PAFP8_MODE_DECODE && d.mode != PAFP8_MODE_PREFILL)
-        return fail(PAFP8_ERR_ARG, "mode %d is neither decode (0) nor prefill (1)", (int)d.mode);
+    if (d.mode != PAFP8_MODE_DECODE && d.mode != PAFP8_MODE_PREFILL && d.mode != PAFP8_MODE_TREE)
+        return fail(PAFP8_ERR_ARG, "mode %d is neither decode (0) nor prefill (1) nor tree (2)", (int)d.mode);
+    const char* mode_name = d.mode == PAFP8_MODE_DECODE ? "decode" : d.mode == PAFP8_MODE_PREFILL ? "prefill" : "tree attention";
 
     pafp8_status st;
     if ((st = check_q_dtype(d.q_dtype)) != PAFP8_OK) return st;
@@ -773,11 +928,12 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
         return fail(PAFP8_ERR_SHAPE, "num_qo_heads %d is not a multiple of num_kv_heads %d",
                     (int)d.num_qo_heads, (int)d.num_kv_heads);
     const int group = d.num_qo_heads / d.num_kv_heads;
-    const int max_group = d.mode == PAFP8_MODE_DECODE ? kMaxGroupDecode : kMaxGroupPrefill;
+    const int max_group = d.mode == PAFP8_MODE_DECODE ? kMaxGroupDecode
+                          : d.mode == PAFP8_MODE_PREFILL ? kMaxGroupPrefill : kMaxGroupTree;
     if (group > max_group)
         return fail(PAFP8_ERR_UNSUPPORTED,
                     "%s serves up to %d query heads per KV head; got %d (%d / %d)",
-                    d.mode == PAFP8_MODE_DECODE ? "decode" : "prefill", max_group, group,
+                    mode_name, max_group, group,
                     (int)d.num_qo_heads, (int)d.num_kv_heads);
     if (d.head_dim != kHeadDim && d.head_dim != 64)
         return fail(PAFP8_ERR_UNSUPPORTED, "head_dim %d is not served by this library (%d or 64)",
@@ -801,8 +957,8 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
         return fail(PAFP8_ERR_ARG, "kv_indptr and last_page_len host arrays are required");
     if (d.mode == PAFP8_MODE_DECODE && qo_indptr_h != nullptr)
         return fail(PAFP8_ERR_ARG, "decode takes no qo_indptr (one query row per request)");
-    if (d.mode == PAFP8_MODE_PREFILL && d.batch > 0 && qo_indptr_h == nullptr)
-        return fail(PAFP8_ERR_ARG, "prefill needs the qo_indptr host array");
+    if (d.mode != PAFP8_MODE_DECODE && d.batch > 0 && qo_indptr_h == nullptr)
+        return fail(PAFP8_ERR_ARG, "%s needs the qo_indptr host array", mode_name);
 
     if (d.batch > 0 && kv_indptr_h[0] != 0)
         return fail(PAFP8_ERR_SHAPE, "kv_indptr[0] is %d, not 0", (int)kv_indptr_h[0]);
@@ -816,7 +972,7 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
                         (int)last_page_len_h[b], (int)d.page_size);
         if (n > 0 && d.num_pages == 0)
             return fail(PAFP8_ERR_SHAPE, "request %d has pages but num_pages is 0", b);
-        if (d.mode == PAFP8_MODE_PREFILL) {
+        if (d.mode != PAFP8_MODE_DECODE) {
             if (b == 0 && qo_indptr_h[0] != 0)
                 return fail(PAFP8_ERR_SHAPE, "qo_indptr[0] is %d, not 0", (int)qo_indptr_h[0]);
             const int64_t qo = (int64_t)qo_indptr_h[b + 1] - qo_indptr_h[b];
@@ -863,13 +1019,16 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
         const int64_t kv = n > 0 ? (n - 1) * d.page_size + pl->last_page_len[b] : 0;
         pl->vptr[b + 1] = pl->vptr[b] + (int32_t)((kv + kPageSize - 1) / kPageSize);
     }
-    if (d.mode == PAFP8_MODE_PREFILL) {
+    if (d.mode != PAFP8_MODE_DECODE) {
         if (d.batch > 0)
             pl->qo_indptr.assign(qo_indptr_h, qo_indptr_h + d.batch + 1);
         else
             pl->qo_indptr.assign(1, 0);
         pl->nnz_qo = pl->qo_indptr.back();
-        build_prefill_meta(pl);
+        if (d.mode == PAFP8_MODE_TREE)
+            build_tree_meta(pl);
+        else
+            build_prefill_meta(pl);
     } else {
         pl->nnz_qo = d.batch;
         build_decode_meta(pl);
@@ -925,6 +1084,12 @@ pafp8_status pafp8_plan_upload(pafp8_plan* plan, void* workspace, size_t workspa
 
 namespace {
 
+// The ancestor masks of pafp8_run_tree.
+struct TreeMask {
+    const uint32_t* bits;
+    int32_t words;
+};
+
 // Checks and launches of the run entry points.  Per-head scale tensors
 // (device arrays) replace the per-tensor scales when k_scales is not NULL.
 // With launch false only the checks run.
@@ -933,10 +1098,14 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
                       const int32_t* kv_indices, float q_scale, float k_scale, float v_scale,
                       const float* q_scales, const float* k_scales, const float* v_scales,
                       int32_t o_dtype, void* o, float* lse, void* workspace, size_t workspace_bytes,
-                      void* stream, bool launch) {
+                      void* stream, bool launch, const TreeMask* tree) {
     if (plan == nullptr) return fail(PAFP8_ERR_ARG, "plan is NULL");
     if (stage < 0 || stage > 2) return fail(PAFP8_ERR_ARG, "stage %d is not 0, 1 or 2", (int)stage);
     const pafp8_plan_desc& d = plan->desc;
+    if ((d.mode == PAFP8_MODE_TREE) != (tree != nullptr))
+        return fail(PAFP8_ERR_ARG, d.mode == PAFP8_MODE_TREE
+                                       ? "a tree plan runs through pafp8_run_tree, which takes its mask"
+                                       : "pafp8_run_tree serves tree plans only");
     pafp8_status st;
     if (k_dtype != v_dtype)
         return fail(PAFP8_ERR_DTYPE, "k_cache has dtype %s but v_cache has %s",
@@ -987,6 +1156,13 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
         return fail(PAFP8_ERR_ARG, "q, o, k_cache and v_cache must be 16-byte aligned");
     if ((uintptr_t)lse % 4 != 0 || (uintptr_t)kv_indices % 4 != 0)
         return fail(PAFP8_ERR_ARG, "lse and kv_indices must be 4-byte aligned");
+    if (tree != nullptr) {
+        if (plan->nnz_qo > 0 && (tree->bits == nullptr || (uintptr_t)tree->bits % 4 != 0))
+            return fail(PAFP8_ERR_ARG, "tree_mask must be non-NULL and 4-byte aligned");
+        if (plan->nnz_qo > 0 && tree->words < plan->mask_words)
+            return fail(PAFP8_ERR_SHAPE, "mask_words %d cannot hold the plan's longest draft (%d words of 32 tokens)",
+                        (int)tree->words, plan->mask_words);
+    }
     if (!launch) return PAFP8_OK;
 
     cudaStream_t s = (cudaStream_t)stream;
@@ -1045,6 +1221,49 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
                                false, d.head_dim)) != PAFP8_OK)
             return st;
         cudaError_t e = launch_prefill(pp, tq, tk, tv, to, plan->num_ctas, s);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return fail(PAFP8_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
+        }
+        return PAFP8_OK;
+    }
+    if (d.mode == PAFP8_MODE_TREE) {
+        if (plan->num_ctas == 0) return PAFP8_OK;  // no drafted token
+        TreeParams tp{};
+        tp.q = q;
+        tp.kv_indices = kv_indices;
+        tp.o = o;
+        tp.lse = lse;
+        tp.meta = (const int32_t*)ws;
+        tp.part_o = (float*)(ws + plan->part_o_off);
+        tp.part_lse = (float*)(ws + plan->part_lse_off);
+        tp.status = (uint32_t*)(ws + plan->status_off);
+        tp.tree_mask = tree->bits;
+        tp.mask_words = tree->words;
+        tp.rows_pad = plan->rows_pad;
+        tp.q_dtype = q_dtype;
+        tp.kv_dtype = k_dtype;
+        tp.o_dtype = o_dtype;
+        tp.q_pieces = is_fp8(q_dtype) || is_2byte(k_dtype) ? 1 : q_dtype == PAFP8_BF16 ? 2 : 3;
+        tp.num_qo_heads = d.num_qo_heads;
+        tp.num_pages = d.num_pages;
+        tp.page_mult = plan->page_mult;
+        tp.group = plan->group;
+        tp.sm_scale_log2 = sm_log2;
+        tp.v_scale = v_scale;
+        tp.q_scales = k_scales != nullptr ? q_scales : nullptr;
+        tp.k_scales = k_scales;
+        tp.v_scales = k_scales != nullptr ? v_scales : nullptr;
+        tp.sm_scale = d.sm_scale;
+        tp.wait_cycles = wait_cycles();
+        auto encode = is_2byte(k_dtype) ? encode_cache_map_2byte : encode_cache_map;
+        CUtensorMap tk, tv;
+        if ((st = encode(&tk, k_cache, d.num_pages, d.num_kv_heads, d.kv_layout, d.head_dim, d.page_size)) != PAFP8_OK)
+            return st;
+        if ((st = encode(&tv, v_cache, d.num_pages, d.num_kv_heads, d.kv_layout, d.head_dim, d.page_size)) != PAFP8_OK)
+            return st;
+        const cudaError_t e = d.head_dim == 64 ? launch_tree_d64(tp, tk, tv, plan->num_ctas, plan->num_merge, s)
+                                               : launch_tree_d128(tp, tk, tv, plan->num_ctas, plan->num_merge, s);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return fail(PAFP8_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
@@ -1113,10 +1332,10 @@ pafp8_status run_impl(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
                       const int32_t* kv_indices, float q_scale, float k_scale, float v_scale,
                       const float* q_scales, const float* k_scales, const float* v_scales,
                       int32_t o_dtype, void* o, float* lse, void* workspace, size_t workspace_bytes,
-                      void* stream, bool launch = true) {
+                      void* stream, bool launch = true, const TreeMask* tree = nullptr) {
     const pafp8_status st = run_body(plan, stage, q_dtype, q, k_dtype, k_cache, v_dtype, v_cache, kv_indices,
                                      q_scale, k_scale, v_scale, q_scales, k_scales, v_scales, o_dtype, o, lse,
-                                     workspace, workspace_bytes, stream, launch);
+                                     workspace, workspace_bytes, stream, launch, tree);
     if (st != PAFP8_OK || !launch || !debug_sync()) return st;
     return pafp8_device_status(plan, workspace, stream);
 }
@@ -1204,6 +1423,21 @@ pafp8_status pafp8_run_head_scales(const pafp8_plan* plan, int32_t q_dtype, cons
         return fail(PAFP8_ERR_ARG, "k_scales and v_scales (device arrays of num_kv_heads floats) are required");
     return run_impl(plan, 0, q_dtype, q, k_dtype, k_cache, v_dtype, v_cache, kv_indices, 1.0f, 1.0f, 1.0f,
                     q_scales, k_scales, v_scales, o_dtype, o, lse, workspace, workspace_bytes, stream);
+}
+
+pafp8_status pafp8_run_tree(const pafp8_plan* plan, int32_t q_dtype, const void* q, int32_t k_dtype,
+                            const void* k_cache, int32_t v_dtype, const void* v_cache, const int32_t* kv_indices,
+                            const uint32_t* tree_mask, int32_t mask_words, float q_scale, float k_scale, float v_scale,
+                            const float* q_scales, const float* k_scales, const float* v_scales, int32_t o_dtype,
+                            void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (k_scales == nullptr && (q_scales != nullptr || v_scales != nullptr))
+        return fail(PAFP8_ERR_ARG, "per-head scales need both k_scales and v_scales");
+    if (k_scales != nullptr && (q_scale != 1.0f || k_scale != 1.0f || v_scale != 1.0f))
+        return fail(PAFP8_ERR_ARG, "per-head scales replace the per-tensor ones, which must then be 1 (q %g, k %g, v %g)",
+                    (double)q_scale, (double)k_scale, (double)v_scale);
+    const TreeMask mask{tree_mask, mask_words};
+    return run_impl(plan, 0, q_dtype, q, k_dtype, k_cache, v_dtype, v_cache, kv_indices, q_scale, k_scale, v_scale,
+                    q_scales, k_scales, v_scales, o_dtype, o, lse, workspace, workspace_bytes, stream, true, &mask);
 }
 
 pafp8_status pafp8_device_status(const pafp8_plan* plan, void* workspace, void* stream) {

@@ -14,6 +14,7 @@ constexpr int kHeadDim = 128;   // head_dim served by this library
 constexpr int kPageSize = 16;   // page_size served by this library
 constexpr int kMaxGroupDecode = 8;
 constexpr int kMaxGroupPrefill = 16;
+constexpr int kMaxGroupTree = 128;  // a row tile holds at least one token
 constexpr int kTileRows = 128;   // prefill query rows (token x head) per tile
 constexpr int kTileKeys = 128;   // prefill keys per KV tile (8 pages)
 // Default bound of a kernel's pipeline waits, in SM clock cycles (~1 s).
@@ -36,19 +37,23 @@ enum MetaHeader : int {
     kMetaOffReqPage,     // int32[batch]   first entry of the request in kv_indices
     kMetaOffReqKvLen,    // int32[batch]   kv_len of the request
     kMetaOffCtaSeg,      // int32[num_ctas+1] CSR of segments per CTA
-    kMetaOffSeg,         // int32[4*num_segs] (row, page_begin, page_end, out_slot)
+    kMetaOffSeg,         // int32[4*num_segs] (row, page_begin, page_end, out_slot); tree: [kTreeSegWords*num_segs]
+                         // hk, t0, tile_begin, tile_end, slot, qo_begin, qo_len, kv_len, page_begin, 0, 0, 0
     kMetaOffMergePtr,    // int32[num_merge+1]
     kMetaOffMergeRow,    // int32[num_merge]
     kMetaOffMergeSlot,   // int32[num_partials]
     kMetaOffReqQo,       // int32[batch+1] qo_indptr (prefill)
     kMetaNumTiles,       // prefill tiles
-    kMetaOffTile,        // int32[8*num_tiles] prefill items: b, hk, t0, nkv, qo_begin, qo_len, kv_len, page_begin
+    kMetaOffTile,        // int32[8*num_tiles] prefill items: b, hk, t0, nkv, qo_begin, qo_len, kv_len, page_begin;
+                         // tree: int32[8*num_merge] split lines: slot0, slot1, first query row, hk, rows, 0, 0, 0
     kMetaTileRows,       // packed query rows per prefill tile
     kMetaOffRowMerge,    // int32[rows] merge entry of each decode row, or -1
     kMetaNumChunks,      // decode pages handed out at run time, in chunks
     kMetaOffChunk,       // int32[4*num_chunks] (row, page_begin, page_end, out_slot)
     kMetaHeaderWords = 32
 };
+
+constexpr int kTreeSegWords = 12;
 
 // Decode work handed out at run time: the last 1/kDynDiv of every row's
 // pages, cut into chunks of about 1/kDynChunksPerCta of a CTA's share of
@@ -190,6 +195,31 @@ struct PrefillParams {
     long long wait_cycles;   // bound of a pipeline wait (SM clock cycles)
 };
 
+struct TreeParams {
+    const void* q;           // [nnz_qo, Hq, D]
+    const int32_t* kv_indices;
+    void* o;                 // [nnz_qo, Hq, D]
+    float* lse;              // [nnz_qo, Hq] or nullptr
+    const int32_t* meta;     // device copy of the metadata words
+    float* part_o;           // [num_partials, rows_pad, D]
+    float* part_lse;         // [num_partials, rows_pad] (log2 domain)
+    uint32_t* status;
+    const uint32_t* tree_mask;  // [nnz_qo, mask_words]
+    int mask_words;
+    int rows_pad;            // rows of the largest row tile
+    int q_dtype, kv_dtype, o_dtype;
+    int q_pieces;            // e4m3 pieces of a query row (1 for an fp8 query or a 2-byte cache)
+    int q_buffers, stages;   // set by the launcher from the shared memory there is
+    int num_qo_heads, num_pages, page_mult, group;
+    float sm_scale_log2;     // sm_scale * q_scale * k_scale * log2(e)
+    float v_scale;
+    const float* q_scales;   // per-head scales, as in DecodeParams
+    const float* k_scales;
+    const float* v_scales;
+    float sm_scale;
+    long long wait_cycles;   // bound of a pipeline wait (SM clock cycles)
+};
+
 // Launchers (decode.cu, prefill_d128.cu / prefill_d64.cu).  Return the launch's cudaError_t.
 // heads_per_box: KV heads covered by one TMA box of the cache maps (the
 // whole head block when the page-wide map could be encoded, else 1).
@@ -224,5 +254,12 @@ inline cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tma
     return p.head_dim == 64 ? launch_prefill_d64(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream)
                             : launch_prefill_d128(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
 }
+
+// The tree kernel over its plan's segments and, with split lines, the merge of
+// their partial states (tree_d128.cu, tree_d64.cu).
+cudaError_t launch_tree_d128(const TreeParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int num_ctas,
+                             int num_merge, cudaStream_t stream);
+cudaError_t launch_tree_d64(const TreeParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int num_ctas,
+                            int num_merge, cudaStream_t stream);
 
 }  // namespace pafp8

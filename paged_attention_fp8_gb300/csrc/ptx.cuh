@@ -356,6 +356,11 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
     return d;
 }
 
+// The same for 64-byte rows under the 64-byte swizzle (an fp8 V tile of 64
+// dims): 64 one-byte elements along M or N per row, 8-row atoms 512 bytes
+// apart along K; one column block, so the leading byte offset is unused.
+__device__ __forceinline__ uint64_t sw64_mnmajor_desc(uint32_t saddr) { return sw64_kmajor_desc(saddr); }
+
 // Instruction descriptor: f32 accumulator, K-major A and B, M x N.
 // a_fmt/b_fmt: kind::f16 -> 0 f16, 1 bf16; kind::f8f6f4 -> 0 e4m3, 1 e5m2.
 __host__ __device__ constexpr uint32_t make_idesc(int a_fmt, int b_fmt, int m, int n) {
@@ -449,6 +454,21 @@ __device__ __forceinline__ void tc_mma_f8_ss_k2(uint32_t d_tmem, uint64_t a, uin
         " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
         " add.s64 da, %1, 2;\n add.s64 db, %2, 2;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, t;\n}\n"
         ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+// kind::f8f6f4 with A in TMEM (8 columns per K step of 32 one-byte elements)
+// and an MN-major B of DH-byte rows, K = 4 x 32: a K step is 32 rows of DH
+// bytes on.
+template <int DH>
+__device__ __forceinline__ void tc_mma_f8_ts_mn_k4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                                   uint32_t accum) {
+    asm volatile(
+        "{\n .reg .pred p, t;\n .reg .b64 db;\n .reg .b32 ta;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, %4, %4;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
+        " add.u32 ta, %1, 8;\n add.s64 db, %2, %5;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [ta], db, %3, t;\n"
+        " add.u32 ta, %1, 16;\n add.s64 db, %2, %6;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [ta], db, %3, t;\n"
+        " add.u32 ta, %1, 24;\n add.s64 db, %2, %7;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [ta], db, %3, t;\n}\n"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accum), "n"(2 * DH), "n"(4 * DH), "n"(6 * DH)
         : "memory");
 }
 #undef PAFP8_K8_SS_BODY
@@ -591,6 +611,30 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
+}
+
+// 32 lanes x 16 columns.
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11,"
+        " %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
