@@ -51,7 +51,7 @@
 //               on the maximum through shared memory;
 //   warps 8-11  helpers: build the next segment's Q pieces, then the finished
 //               segment's epilogue;
-//   warp 12     TMA producer, warp 13 MMA issuer and TMEM owner.
+//   warps 12, 14, 15  TMA producers;  warp 13  MMA issuer and TMEM owner.
 // TMEM columns: S / P buffers 0-127 and 128-255 (tile parity), O_hi from 256,
 // O_lo from 256 + D.  MMA order: QK(j + 1) before PV(j), across segments, so
 // the softmax of a tile overlaps the tensor work of its neighbours.
@@ -410,9 +410,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_init(bar(tStage), 4);
         mbar_init(bar(tDrain), 1);
         for (int i = 0; i < NS; ++i) {
-            mbar_init(bar(tKFull + i), 1);
+            mbar_init(bar(tKFull + i), 3);  // producer warps
             mbar_init(bar(tKEmpty + i), 1);
-            mbar_init(bar(tVFull + i), 1);
+            mbar_init(bar(tVFull + i), 3);
             mbar_init(bar(tVEmpty + i), 1);
         }
         asm volatile("st.shared.u32 [%0], 0;" ::"r"(flag) : "memory");
@@ -426,12 +426,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(base + L.tmem_slot) : "memory");
 
-    if (warp == 12) {
-        // ------------------------------------------------------------ producer
+    if (warp == 12 || warp >= 14) {
+        // ----------------------------------------------------------- producers
+        // A box holds the 16 tokens of one (sub-)page, and a warp's box takes it
+        // about 130 cycles to issue, 16 boxes a tile 2100: more than the tile's
+        // time at full bandwidth (1400).  So three warps share the boxes, every
+        // third one each, and each warp expects its own bytes.
+        const int pw = warp == 12 ? 0 : warp - 13;
         if (lane == 0) {
             prefetch_tmap(&tmk);
             prefetch_tmap(&tmv);
         }
+        constexpr int kBoxes = 8 * (k2 ? NH : 1);      // boxes of a K or V tile: (half, sub-page)
+        const int box = 3 * lane + pw, i8 = box & 7;   // this lane's box
+        constexpr uint32_t kBoxBytes = k2 ? 2048u : (uint32_t)(kPageSize * DH);
         long long n = 0;  // tiles issued
         int stage = 0;
         uint32_t phase = 0;
@@ -441,25 +449,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const int m = p.page_mult;
             const int nsub = (sg.kv_len + kPageSize - 1) / kPageSize;  // 16-token sub-pages of the request
             const int* idx = p.kv_indices + sg.page0;
-            auto fetch = [&](int tile) -> int {  // the page entry of sub-page `lane` (0-7) of a tile
-                const int v = tile * (kTileKeys / kPageSize) + (lane & 7);
+            auto fetch = [&](int tile) -> int {  // the page entry of this lane's sub-page
+                const int v = tile * (kTileKeys / kPageSize) + i8;
                 return v < nsub ? __ldg(idx + (m == 1 ? v : v / m)) : 0;
             };
             int next = fetch(sg.tile0);
             for (int t = sg.tile0; t < sg.tile1 && ok; ++t) {
                 int page = next;
                 if (t + 1 < sg.tile1) next = fetch(t + 1);
-                const int sub = t * (kTileKeys / kPageSize) + (lane & 7);
-                const int np = min(kTileKeys / kPageSize, nsub - t * (kTileKeys / kPageSize));
-                const bool bad = (lane & 7) < np && (page < 0 || page >= p.num_pages);
-                if (bad) page = 0;
-                if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.status, kStatusBounds);
+                const int sub = t * (kTileKeys / kPageSize) + i8;
+                const bool mine = box < kBoxes && sub < nsub;
+                const bool bad = mine && (page < 0 || page >= p.num_pages);
+                if (bad) {
+                    page = 0;
+                    atomicOr(p.status, kStatusBounds);
+                }
                 const int slot = m == 1 ? 0 : (sub % m) * kPageSize;
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, mine)) * kBoxBytes;
                 for (int kv = 0; kv < 2; ++kv) {
                     const int full = (kv ? tVFull : tKFull) + stage, empty = (kv ? tVEmpty : tKEmpty) + stage;
                     if (lane == 0) {
                         ok = wait(empty, phase ^ 1u);
-                        if (ok) mbar_arrive_expect_tx(bar(full), (uint32_t)(np * kPageSize * DH * ES));
+                        if (ok) mbar_arrive_expect_tx(bar(full), bytes);
                     }
                     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
                     if (!ok) {
@@ -467,13 +478,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         break;
                     }
                     const CUtensorMap* map = kv ? &tmv : &tmk;
-                    const uint32_t dst = base + (kv ? L.v : L.k) + (uint32_t)stage * kTile;
-                    if constexpr (k2) {  // lane 8 h + i: dim half h of sub-page i
-                        const int i = lane & 7, h = lane >> 3;
-                        if (h < NH && i < np)
-                            tma_load_5d(dst + h * kHalf + i * 2048u, map, bar(full), 0, h, slot, sg.hk, page);
-                    } else {
-                        if (lane < np) tma_load_4d(dst + lane * (uint32_t)(kPageSize * DH), map, bar(full), 0, sg.hk, slot, page);
+                    const uint32_t dst = base + (kv ? L.v : L.k) + (uint32_t)stage * kTile + (uint32_t)box * kBoxBytes;
+                    if (mine) {
+                        if constexpr (k2)
+                            tma_load_5d(dst, map, bar(full), 0, box >> 3, slot, sg.hk, page);
+                        else
+                            tma_load_4d(dst, map, bar(full), 0, sg.hk, slot, page);
                     }
                     __syncwarp();
                 }
@@ -493,6 +503,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (s < n) mbar_wait(bar(tVFull + s), (uint32_t)(((n - 1 - s) / NS) & 1));
             }
         }
+        __syncwarp();
     } else if (warp == 13) {
         // ----------------------------------------------------------------- MMA
         if (lane == 0 && s_begin < s_end) {
@@ -676,88 +687,112 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t tO = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
         uint32_t stage_phase = 0;
         bool ok = true;
-        // Segment si's Q rows (copies and all) into its buffer.
+        // Segment si's Q rows into its buffer: DH / 8 lanes a row, eight elements
+        // a lane, each row stored to all its copies.  A compact loop: unrolled
+        // over whole rows the code ran once a segment and spent 10 us on
+        // instruction fetches.
         auto build_q = [&](int si) -> bool {
             const Seg sg = load_seg(segs, si);
             const int nth = si - s_begin, buf = NQB == 2 ? nth & 1 : 0;
             const int use = NQB == 2 ? nth >> 1 : nth;  // earlier uses of this buffer
             const int rows = min(TQ, sg.qo_len - sg.t0) * g;
-            const int row = r & ((128 >> copies_log2(rows)) - 1);
-            const bool live = row < rows;
-            const int tok = live ? row / g : 0, hh = live ? row - tok * g : 0;
-            const size_t off = ((size_t)(sg.qo0 + sg.t0 + tok) * p.num_qo_heads + (size_t)sg.hk * g + hh) * DH;
-            const bool q1 = p.q_pieces == 1 && !k2;  // an fp8 query as it is
-            constexpr int NV = DH / 8;               // 16-byte loads of a 2-byte row
-            uint4 raw[NV];
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) + off * (q1 ? 1 : 2));
-#pragma unroll
-            for (int i = 0; i < NV; ++i) raw[i] = live && (i < NV / 2 || !q1) ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-            if (!wait_all(tQEmpty + buf, (uint32_t)((use + 1) & 1))) return false;
+            const int cl = copies_log2(rows), rp = 128 >> cl;
+            constexpr int LPR = DH / 8, RPI = 32 / LPR;  // lanes a row, rows a warp's round
+            const int e = lane % LPR, row0 = (warp - 8) * RPI + lane / LPR;
+            const bool q1 = !k2 && p.q_pieces == 1;      // an fp8 query as it is
+            const size_t head0 = (size_t)(sg.qo0 + sg.t0) * p.num_qo_heads + (size_t)sg.hk * g;
             const uint32_t dst = base + L.q + (uint32_t)(buf * p.q_pieces) * kTile;
-            float fac = 1.f;
-            auto put = [&](uint32_t tile, int c, const uint4& w) {  // 16-byte chunk c of this row
-                if constexpr (k2)
-                    sts128(tile + (c >> 3) * kHalf + r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4), w.x, w.y, w.z, w.w);
-                else if constexpr (DH == 128)
-                    sts128(tile + r * 128u + (uint32_t)((c ^ (r & 7)) << 4), w.x, w.y, w.z, w.w);
-                else
-                    sts128(tile + r * 64u + (uint32_t)((c ^ ((r >> 1) & 3)) << 4), w.x, w.y, w.z, w.w);
-            };
-            if (k2) {
+            const uint32_t fdst = base + L.fac + 512u * (nth & 1);
+            constexpr int kBatch = 4;  // rows in flight per lane group
+            bool ready = false;
+#pragma unroll 1
+            for (int first = row0; first - row0 < rp; first += 4 * RPI * kBatch) {
+                uint4 raw[kBatch];
 #pragma unroll
-                for (int i = 0; i < NV; ++i) put(dst, i, raw[i]);
-            } else if (q1) {
-#pragma unroll
-                for (int i = 0; i < NV / 2; ++i) put(dst, i, raw[i]);
-            } else {
-                const bool bf = p.q_dtype == PAFP8_BF16;
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
-                uint32_t top = 0;  // largest magnitude as a 16-bit pattern
-#pragma unroll
-                for (int i = 0; i < 4 * NV; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-                const float amax = bf ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
-                // 2^e brings the largest magnitude into [128, 256).  A row with an
-                // infinity or a NaN gives NaN, as its logits would.
-                const int ex = (int)((__float_as_uint(amax) >> 23) & 0xFFu) - 127;
-                const int e = amax == 0.f ? 0 : max(-120, min(100, 7 - ex));
-                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-                fac = isfinite(amax) ? __uint_as_float((uint32_t)(127 - e) << 23) : __uint_as_float(0x7FC00000u);
-#pragma unroll
-                for (int i = 0; i < NV / 2; ++i) {  // 16 elements: one 16-byte chunk a piece
-                    uint4 out[3];
-                    uint32_t* ow = reinterpret_cast<uint32_t*>(out);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t ww = w[8 * i + k];
-                        float x, y;
-                        if (bf) {
-                            x = __uint_as_float(ww << 16);
-                            y = __uint_as_float(ww & 0xFFFF0000u);
+                for (int k = 0; k < kBatch; ++k) {
+                    const int row = first + 4 * RPI * k;
+                    raw[k] = make_uint4(0, 0, 0, 0);
+                    if (row < rows) {
+                        const int tok = row / g;
+                        const size_t at = (head0 + (size_t)tok * p.num_qo_heads + (row - tok * g)) * DH + 8 * e;
+                        if (q1) {
+                            const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.q) + at));
+                            raw[k] = make_uint4(x.x, x.y, 0, 0);
                         } else {
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww));
-                            x = f.x;
-                            y = f.y;
-                        }
-                        x *= up;
-                        y *= up;
-#pragma unroll
-                        for (int c = 0; c < 3; ++c) {
-                            const uint32_t pr = e4m3_pair(x, y);
-                            if (k & 1)
-                                ow[4 * c + (k >> 1)] |= pr << 16;
-                            else
-                                ow[4 * c + (k >> 1)] = pr;
-                            const float2 b = e4m3_back(pr);
-                            x -= b.x;
-                            y -= b.y;
+                            raw[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at));
                         }
                     }
-                    put(dst, i, out[0]);
-                    put(dst + kTile, i, out[1]);
-                    if (p.q_pieces == 3) put(dst + 2 * kTile, i, out[2]);
+                }
+                if (!ready) {  // the buffer is free once its last segment's QK has run
+                    if (!wait_all(tQEmpty + buf, (uint32_t)((use + 1) & 1))) return false;
+                    ready = true;
+                }
+#pragma unroll 1
+                for (int k = 0; k < kBatch; ++k) {
+                    const int row = first + 4 * RPI * k;
+                    if (row - lane / LPR >= rp) break;  // uniform: rp is a multiple of a round's rows
+                    const uint4 rw = k == 0 ? raw[0] : k == 1 ? raw[1] : k == 2 ? raw[2] : raw[3];
+                    if constexpr (k2) {
+                        for (int c = 0; c < 1 << cl; ++c) {
+                            const int r2 = row + c * rp;
+                            sts128(dst + (e >> 3) * kHalf + r2 * 128u + (uint32_t)(((e & 7) ^ (r2 & 7)) << 4), rw.x, rw.y, rw.z,
+                                   rw.w);
+                            if (e == 0) sts_f(fdst + 4u * r2, 1.f);
+                        }
+                        continue;
+                    }
+                    // An eight-byte element group's place in a piece's tile row.
+                    const uint32_t at = DH == 128 ? row * 128u + (uint32_t)(((e >> 1) ^ (row & 7)) << 4) + 8u * (e & 1)
+                                                  : row * 64u + (uint32_t)(((e >> 1) ^ ((row >> 1) & 3)) << 4) + 8u * (e & 1);
+                    const uint32_t copy_bytes = (uint32_t)rp * DH;
+                    float fac = 1.f;
+                    if (q1) {
+                        for (int c = 0; c < 1 << cl; ++c) sts64(dst + at + c * copy_bytes, rw.x, rw.y);
+                    } else {
+                        const bool bf = p.q_dtype == PAFP8_BF16;
+                        const uint32_t w[4] = {rw.x, rw.y, rw.z, rw.w};
+                        uint32_t top = 0;  // the row's largest magnitude as a 16-bit pattern
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+#pragma unroll
+                        for (int d = LPR / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                        const float amax = bf ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+                        // 2^ex brings the largest magnitude into [128, 256).  A row with an
+                        // infinity or a NaN gives NaN, as its logits would.
+                        const int up = 7 - ((int)((__float_as_uint(amax) >> 23) & 0xFFu) - 127);
+                        const int ex = amax == 0.f ? 0 : max(-120, min(100, up));
+                        const float mul = __uint_as_float((uint32_t)(127 + ex) << 23);
+                        fac = isfinite(amax) ? __uint_as_float((uint32_t)(127 - ex) << 23) : __uint_as_float(0x7FC00000u);
+                        float x[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (bf) {
+                                x[2 * i] = __uint_as_float(w[i] << 16) * mul;
+                                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * mul;
+                            } else {
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                                x[2 * i] = f.x * mul;
+                                x[2 * i + 1] = f.y * mul;
+                            }
+                        }
+#pragma unroll 1
+                        for (int pc = 0; pc < p.q_pieces; ++pc) {
+                            uint32_t pr[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                pr[i] = e4m3_pair(x[2 * i], x[2 * i + 1]);
+                                const float2 b = e4m3_back(pr[i]);
+                                x[2 * i] -= b.x;
+                                x[2 * i + 1] -= b.y;
+                            }
+                            for (int c = 0; c < 1 << cl; ++c)
+                                sts64(dst + pc * kTile + at + c * copy_bytes, pr[0] | (pr[1] << 16), pr[2] | (pr[3] << 16));
+                        }
+                    }
+                    if (e == 0)
+                        for (int c = 0; c < 1 << cl; ++c) sts_f(fdst + 4u * (row + c * rp), fac);
                 }
             }
-            sts_f(base + L.fac + 4u * (128 * (nth & 1) + r), fac);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
