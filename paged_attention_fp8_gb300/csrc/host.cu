@@ -1262,8 +1262,7 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
             return st;
         if ((st = encode(&tv, v_cache, d.num_pages, d.num_kv_heads, d.kv_layout, d.head_dim, d.page_size)) != PAFP8_OK)
             return st;
-        const cudaError_t e = d.head_dim == 64 ? launch_tree_d64(tp, tk, tv, plan->num_ctas, plan->num_merge, s)
-                                               : launch_tree_d128(tp, tk, tv, plan->num_ctas, plan->num_merge, s);
+        const cudaError_t e = tree_launcher(d.head_dim, plan->rows_pad)(tp, tk, tv, plan->num_ctas, plan->num_merge, s);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return fail(PAFP8_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));

@@ -256,10 +256,15 @@ inline cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tma
 }
 
 // The tree kernel over its plan's segments and, with split lines, the merge of
-// their partial states (tree_d128.cu, tree_d64.cu).
-cudaError_t launch_tree_d128(const TreeParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int num_ctas,
-                             int num_merge, cudaStream_t stream);
-cudaError_t launch_tree_d64(const TreeParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int num_ctas,
-                            int num_merge, cudaStream_t stream);
+// their partial states.  One translation unit per head size and row count.
+using TreeLaunch = cudaError_t(const TreeParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int num_ctas,
+                               int num_merge, cudaStream_t stream);
+TreeLaunch launch_tree_d128_r32, launch_tree_d128_r64, launch_tree_d128_r128;
+TreeLaunch launch_tree_d64_r32, launch_tree_d64_r64, launch_tree_d64_r128;
+// The instantiation for row tiles of up to `rows` rows (of 128).
+inline TreeLaunch* tree_launcher(int head_dim, int rows) {
+    if (head_dim == 64) return rows <= 32 ? launch_tree_d64_r32 : rows <= 64 ? launch_tree_d64_r64 : launch_tree_d64_r128;
+    return rows <= 32 ? launch_tree_d128_r32 : rows <= 64 ? launch_tree_d128_r64 : launch_tree_d128_r128;
+}
 
 }  // namespace pafp8

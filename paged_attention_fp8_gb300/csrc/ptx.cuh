@@ -235,6 +235,13 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+// Maximum over the warp's lanes (NaN ignored), in every lane.
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Three-input maximum (one instruction on sm_100 and later).
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -360,16 +367,31 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
     return d;
 }
 
-// The same for 64-byte rows under the 64-byte swizzle (an fp8 V tile of 64
-// dims): 64 one-byte elements along M or N per row, 8-row atoms 512 bytes
-// apart along K; one column block, so the leading byte offset is unused.
-__device__ __forceinline__ uint64_t sw64_mnmajor_desc(uint32_t saddr) { return sw64_kmajor_desc(saddr); }
+// An MN-major operand of W-byte rows (W = 128, 64 or 32, the swizzle of that
+// width): W bytes of consecutive elements along M or N per row, one row per K
+// index, 8-row atoms 8 W bytes apart along K, `lbo` bytes between column
+// blocks of W bytes along M or N.
+template <int W>
+__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t saddr, uint32_t lbo) {
+    static_assert(W == 128 || W == 64 || W == 32, "a swizzle width");
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;              // leading byte offset: next W bytes of columns
+    d |= (uint64_t)((8 * W) >> 4) << 32;                       // stride byte offset: next 8 K rows
+    d |= (uint64_t)1 << 46;                                    // descriptor version
+    d |= (uint64_t)(W == 128 ? 2 : W == 64 ? 4 : 6) << 61;     // SWIZZLE_128B, _64B, _32B
+    return d;
+}
 
 // Instruction descriptor: f32 accumulator, K-major A and B, M x N.
 // a_fmt/b_fmt: kind::f16 -> 0 f16, 1 bf16; kind::f8f6f4 -> 0 e4m3, 1 e5m2.
 __host__ __device__ constexpr uint32_t make_idesc(int a_fmt, int b_fmt, int m, int n) {
     return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// The same with MN-major A and B (bits 15 and 16).
+__host__ __device__ constexpr uint32_t make_idesc_mn(int a_fmt, int b_fmt, int m, int n) {
+    return make_idesc(a_fmt, b_fmt, m, n) | (1u << 15) | (1u << 16);
 }
 // The same with an MN-major B operand (bit 16: B transposed).
 __host__ __device__ constexpr uint32_t make_idesc_bmn(int a_fmt, int b_fmt, int m, int n) {
@@ -460,20 +482,39 @@ __device__ __forceinline__ void tc_mma_f8_ss_k2(uint32_t d_tmem, uint64_t a, uin
         ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accum)
         : "memory");
 }
-// kind::f8f6f4 with A in TMEM (8 columns per K step of 32 one-byte elements)
-// and an MN-major B of DH-byte rows, K = 4 x 32: a K step is 32 rows of DH
-// bytes on.
-template <int DH>
-__device__ __forceinline__ void tc_mma_f8_ts_mn_k4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                                   uint32_t accum) {
+// One MMA of a whole warp in step: every lane runs the code that leads here (so
+// that the operands sit in uniform registers), `elect` is nonzero in the one
+// that issues.  Descriptors as two words: the low one carries the address
+// (16-byte units) and the leading byte offset.
+template <bool kF8>
+__device__ __forceinline__ void tc_mma_elect(uint32_t d_tmem, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                             uint32_t idesc, uint32_t accum, uint32_t elect) {
+    if constexpr (kF8)
+        asm volatile(
+            "{\n .reg .pred p, e;\n .reg .b64 da, db;\n mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+            " setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n}\n"
+            ::"r"(d_tmem), "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accum), "r"(elect)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p, e;\n .reg .b64 da, db;\n mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+            " setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n"
+            ::"r"(d_tmem), "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accum), "r"(elect)
+            : "memory");
+}
+__device__ __forceinline__ void tc_commit_elect(uint32_t bar, uint32_t elect) {
     asm volatile(
-        "{\n .reg .pred p, t;\n .reg .b64 db;\n .reg .b32 ta;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, %4, %4;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
-        " add.u32 ta, %1, 8;\n add.s64 db, %2, %5;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [ta], db, %3, t;\n"
-        " add.u32 ta, %1, 16;\n add.s64 db, %2, %6;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [ta], db, %3, t;\n"
-        " add.u32 ta, %1, 24;\n add.s64 db, %2, %7;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [ta], db, %3, t;\n}\n"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accum), "n"(2 * DH), "n"(4 * DH), "n"(6 * DH)
+        "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(elect)
         : "memory");
+}
+// 1 in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+    return e;
 }
 #undef PAFP8_K8_SS_BODY
 #undef PAFP8_K8_SS_ARGS
@@ -627,18 +668,6 @@ __device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
           "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
-}
-
-__device__ __forceinline__ void tc_st4(uint32_t taddr, const uint32_t (&r)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
 }
 
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {

@@ -1,6 +1,6 @@
 // tree.cuh -- attention of a tree of drafted tokens over the paged KV cache on
 // the tcgen05 tensor cores (sm_103a).  Included by one translation unit per
-// head size (tree_d128.cu, tree_d64.cu).
+// head size and row count (tree_d*_r*.cu), which compile in parallel.
 //
 // What it computes: request b has T new (drafted) tokens, whose keys are the
 // last T of its L cached ones.  Drafted token u sees every key j < L - T and
@@ -9,27 +9,43 @@
 // over the keys it sees, lse = ln sum exp(logits); a row that sees no key
 // gives o = 0, lse = -inf.
 //
-// What bounds it: with R = T * group rows per KV head a key costs 2 D bytes
-// (fp8) from HBM and 4 D R flops, so up to R of about 128 the cache's bytes
+// What bounds it: with T * group rows per KV head a key costs 2 D bytes (fp8)
+// from HBM and 4 D T group flops, so up to about 128 rows the cache's bytes
 // bound it, and the tensor and softmax work per byte has to stay below that.
 // Widening an fp8 tile to 16 bits in shared memory would cost more shared
 // memory traffic than reading it once from HBM does, so nothing is widened:
-//   * S = Q K^T takes K as it landed (kind::f8f6f4).  A 2-byte query row is
+//   * S^T = K Q^T takes K as it landed (kind::f8f6f4).  A 2-byte query row is
 //     scaled by a power of two to a maximum in [128, 256) and split into
 //     e4m3 pieces (4 significant bits each: two for bf16's 8, three for f16's
-//     11) whose products accumulate in one accumulator: x = a + b (+ c), each
+//     11) whose products add up in one accumulator: x = a + b (+ c), each
 //     piece the e4m3 rounding of what the earlier ones left, exact but for
 //     elements below 2^-10 of the row's largest, which lose 2^-18 of it at
 //     most.
-//   * O += P V takes V as it landed, the MN-major B operand, and P as e4m3
-//     pieces from TMEM: P' = 2^7 p in [0, 256), hi = e4m3(P'),
-//     lo = e4m3(32 (P' - hi)), in two accumulators O_hi and O_lo (O = O_hi +
-//     O_lo / 32), so that P carries 8 significant bits (a bf16's worth, 2^-9
-//     off) down to p = 2^-16 and never less than 2^-23 of the row's largest
-//     off.  An f16 output adds a third piece, e4m3 of what lo left,
-//     accumulated with lo: 12 bits.
+//   * O^T += V^T P^T takes V as it landed and P as e4m3 pieces from shared
+//     memory: P' = 2^6 p in [0, 256], hi = e4m3(P'), lo = e4m3(32 (P' - hi)),
+//     side by side along N, so that one MMA reads V once for both and leaves
+//     O_hi and O_lo (O = O_hi + O_lo / 32) in neighbouring columns.  P then
+//     carries 8 significant bits (a bf16's worth, 2^-9 off) down to p = 2^-12
+//     and is never more than 2^-21 of the row's largest off.  An f16 output
+//     adds a third piece, e4m3 of what lo left, accumulated onto O_lo: 12 bits.
 //   * A 2-byte cache of the query's dtype runs kind::f16 on Q, K and V as
 //     they are, P rounded to that type.
+//
+// Both products are transposed: keys (of K) and dims (of V) are the 128 rows of
+// the MMAs, query rows their N, so the tensor time follows the row count R (32,
+// 64 or 128, the plan's largest row tile rounded up) instead of always paying
+// for 128 rows.  With query rows as M, a 16-row draft spent 1400 cycles of the
+// tensor pipe per 128-key tile, as much as the tile's HBM time; transposed it
+// is about 500 at R = 32 and 700 at R = 64.  A softmax thread then owns a key
+// and half of the rows, every lane is busy whatever R is, and P is written to
+// shared memory, which frees S right away.
+//
+// The running maximum: a row's maximum over a tile lies across 128 lanes, so it
+// is not taken per tile.  P' is formed with the row's reference maximum, and
+// only when some P' would pass 2^8, four times that maximum's (a vote per tile,
+// its latency hidden behind the exponentials and the stores of P), are the
+// column maxima taken (redux), O and l rescaled and the tile's P redone; the
+// first tile of a segment always takes them.
 //
 // Work: the plan lays the 128-key tiles of all (request, row tile of 128 /
 // group tokens) lines end to end, cuts them into equal ranges, and gives each
@@ -38,23 +54,16 @@
 // is a segment; a segment that is not its whole line writes a partial state,
 // and a merge kernel (a programmatic dependent) joins them.
 //
-// An MMA has 128 rows whatever R is.  When a row tile has at most 64 or 32
-// rows, the 128 lanes hold 2 or 4 copies of them, copy c taking the softmax of
-// its share of each tile's keys (its P is zero elsewhere, its maximum, sum and
-// accumulators its own), and the epilogue joins the copies like split-KV
-// states: the softmax work per tile, which would otherwise fall on R lanes,
-// stays spread over all threads.
-//
-// Roles (512 threads):
-//   warps 0-7   softmax: lane r of TMEM is owned by threads r (first half of
-//               the row's columns) and r + 128 (second half); the halves agree
-//               on the maximum through shared memory;
+// Roles (512 threads; setmaxnreg moves registers to the softmax warps):
+//   warps 0-7   softmax: thread = key 32 (w % 4) + lane of the tile, rows of
+//               half w / 4;
 //   warps 8-11  helpers: build the next segment's Q pieces, then the finished
-//               segment's epilogue;
+//               segment's epilogue (lane = dim);
 //   warps 12, 14, 15  TMA producers;  warp 13  MMA issuer and TMEM owner.
-// TMEM columns: S / P buffers 0-127 and 128-255 (tile parity), O_hi from 256,
-// O_lo from 256 + D.  MMA order: QK(j + 1) before PV(j), across segments, so
-// the softmax of a tile overlaps the tensor work of its neighbours.
+// TMEM columns: a ring of S^T buffers (R columns each), then O^T buffers
+// (2 R columns, R with a 2-byte cache).  QK runs ahead of PV by up to two
+// tiles, into the next segment too, and a second O buffer lets the next
+// segment start while the epilogue reads the last one.
 // All waits are bounded; on expiry a status bit is set and the CTA winds down.
 #pragma once
 #include "../../include/pafp8.h"
@@ -67,13 +76,11 @@ namespace {
 using namespace ptx;
 
 constexpr int kTreeThreads = 512;
-constexpr uint32_t kColO = 256;
 constexpr int kMaxStages = 8;
-// O is rescaled when a row's maximum rises by more than 2^kHead; P' is at most
-// 2^(kShift + kHead).
+// Reference maxima rise when some P' would pass 2^(kShift + kHead).
 template <int KT>
-struct PShift {  // fp8 pieces: P' < 2^8, e4m3 reaches 448
-    static constexpr float kShift = 7.f, kHead = 1.f;
+struct PShift {  // fp8 pieces: P' <= 2^8, e4m3 reaches 448
+    static constexpr float kShift = 6.f, kHead = 2.f;
 };
 template <>
 struct PShift<PAFP8_BF16> {
@@ -83,39 +90,68 @@ template <>
 struct PShift<PAFP8_F16> {
     static constexpr float kShift = 0.f, kHead = 8.f;
 };
+// kShift - m of a row that has seen no key: any logit passes the bound.
+constexpr float kUnseen = 1e30f;
 
-// Shared memory: [Q buffers][K stages][V stages][staging][state rings][barriers].
-struct TreeSmem {
-    uint32_t q, k, v, stage, ml, fac, xmax, bars, tmem_slot, abort_flag, bytes;
+// Sizes of one instantiation.  R: rows of a row tile, a power of two >= 32.
+template <int KT, int NP, int DH, int R>
+struct TreeDims {
+    static constexpr bool k2 = KT == PAFP8_BF16 || KT == PAFP8_F16;
+    static constexpr int ES = k2 ? 2 : 1;
+    static constexpr uint32_t kTile = kTileKeys * DH * ES;  // a K or V tile
+    static constexpr uint32_t kHalf = kTileKeys * 128;      // a 64-dim half of a 2-byte tile
+    static constexpr int NH = DH / 64;                      // halves of a 2-byte row
+    static constexpr uint32_t kQPiece = R * DH * ES;        // 2-byte: [half][R rows][128 B]
+    // P: per piece [128 keys][R] as blocks of W-byte rows.
+    static constexpr int W = R * ES < 128 ? R * ES : 128;
+    static constexpr uint32_t kPBlock = 128 * W;
+    static constexpr uint32_t kPPiece = 128 * R * ES;
+    static constexpr int NPB = R == 128 ? 1 : 2;            // P buffers
+    static constexpr int NOB = R == 128 && !k2 ? 1 : 2;     // O buffers
+    static constexpr int OC = k2 ? R : 2 * R;               // columns of an O buffer
+    static constexpr uint32_t kColO = 2 * R;                // after two S buffers
+    static constexpr uint32_t kCols = kColO + NOB * OC <= 128 ? 128 : kColO + NOB * OC <= 256 ? 256 : 512;
+    static constexpr int NCOL = R / 2;                      // rows of a softmax thread
+    static constexpr int NC = NCOL < 32 ? NCOL : 32;        // of them at a time
+    static_assert(kColO + NOB * OC <= kCols, "TMEM columns");
 };
-constexpr int kStageRow = 36;  // floats: 32 dims of a row, 16-byte aligned, 8 rows on distinct banks
+
+struct TreeSmem {
+    uint32_t q, k, v, p, sc, neg, wmax, lsum, mst, wt, vote, bars, tmem_slot, abort_flag, bytes;
+};
 enum TreeBar : int {
-    tQFull = 0,                  // [2]
-    tQEmpty = 2,                 // [2]
-    tInfo = 4,                   // [2] row factors of a segment written
-    tState = 6,                  // [2] m and l of a segment written
-    tSFull = 8,                  // [2]
-    tPFull = 10,                 // [2]
-    tOFull = 12, tOEmpty = 13,
-    tXmax = 14,                  // [4] quadrants
-    tStage = 18,                 // helpers' staging
-    tDrain = 19,
-    tKFull = 20,
+    tQFull = 0,              // [2]
+    tQEmpty = 2,             // [2]
+    tInfo = 4,               // [2] row scales of a segment written
+    tState = 6,              // [2] m and l of a segment written
+    tSFull = 8,              // [2]
+    tPFull = 16,             // [2]
+    tOFull = 18,             // [2]
+    tOEmpty = 20,            // [2]
+    tHalf = 22,              // [2] the four softmax warps of a row half
+    tHelp = 24,              // the helper warps
+    tDrain = 25,
+    tKFull = 26,
     tKEmpty = tKFull + kMaxStages,
     tVFull = tKEmpty + kMaxStages,
     tVEmpty = tVFull + kMaxStages,
     tNumBars = tVEmpty + kMaxStages
 };
-__host__ __device__ inline TreeSmem tree_smem(uint32_t q_bytes, uint32_t tile_bytes, int stages) {
+template <typename D, int R, int NP>
+__host__ __device__ inline TreeSmem tree_smem(int q_tiles, int stages) {
     TreeSmem s{};
     s.q = 0;
-    s.k = q_bytes;
-    s.v = s.k + (uint32_t)stages * tile_bytes;
-    s.stage = s.v + (uint32_t)stages * tile_bytes;
-    s.ml = s.stage + 128 * kStageRow * 4;          // [2][3][128] floats: m, l of either half
-    s.fac = s.ml + 2 * 3 * 128 * 4;                // [2][128] floats
-    s.xmax = s.fac + 2 * 128 * 4;                  // [2][2][128] floats
-    s.bars = s.xmax + 2 * 2 * 128 * 4;
+    s.k = (uint32_t)q_tiles * D::kQPiece;
+    s.v = s.k + (uint32_t)stages * D::kTile;
+    s.p = s.v + (uint32_t)stages * D::kTile;
+    s.sc = s.p + D::NPB * NP * D::kPPiece;  // [2][R] floats: log2 scale of each row
+    s.neg = s.sc + 2 * R * 4;               // [8 warps][NCOL]: kShift - reference maximum
+    s.wmax = s.neg + 8 * D::NCOL * 4;       // [2][half][4 quadrants][NC]
+    s.lsum = s.wmax + 2 * 2 * 4 * D::NC * 4;  // [2][4][R]
+    s.mst = s.lsum + 2 * 4 * R * 4;         // [2][R]
+    s.wt = s.mst + 2 * R * 4;               // [2][R]
+    s.vote = s.wt + 2 * R * 4;              // [half][2] words
+    s.bars = s.vote + 16;
     s.tmem_slot = s.bars + 8 * tNumBars;
     s.abort_flag = s.tmem_slot + 4;
     s.bytes = s.abort_flag + 4;
@@ -127,6 +163,11 @@ __device__ __forceinline__ float lds_f(uint32_t a) {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t lds_u(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ float4 lds_f4(uint32_t a) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
@@ -134,26 +175,33 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
 }
 __device__ __forceinline__ void sts_f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 
-__device__ __forceinline__ void tree_abort(uint32_t flag, uint32_t* status) {
-    asm volatile("st.shared.u32 [%0], 1;" ::"r"(flag) : "memory");
-    atomicOr(status, kStatusTimeout);
-}
-// Bounded wait that gives up once another role has; a bound below the default
-// polls without suspending (try_wait could outlast it).
-__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, uint32_t flag, uint32_t* status, long long limit) {
-    const bool shortened = limit < kWaitCyclesDefault;
-    if (shortened ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!(shortened ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
-        uint32_t v;
-        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(flag) : "memory");
-        if (v != 0) return false;
-        if (clock64() - t0 > limit) {
-            tree_abort(flag, status);
-            return false;
-        }
-    }
-    return true;
+// Bounded wait that gives up once another role has (`flag`), and past `limit`
+// cycles sets the flag and the status bit itself.  The loop is one compact asm
+// block: some thirty waits are inlined, and the instruction cache holds little
+// more than the tile loops.  `hint` is how long (ns) one try may suspend the
+// thread: waiting warps that poll take issue slots from the working ones.
+// With hint 0 (a shortened limit, which a suspended try could outlast) it only
+// tests.
+__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, uint32_t flag, uint32_t* status, long long limit,
+                                          uint32_t hint) {
+    if (mbar_test_wait(bar, parity)) return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 t, u;\n .reg .b32 f;\n"
+        " setp.eq.u32 q, %6, 0;\n mov.u64 t, %%clock64;\n"
+        "LOOP:\n"
+        " @q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " @!q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %6;\n @p bra DONE;\n"
+        " ld.volatile.shared.u32 f, [%3];\n setp.ne.u32 p, f, 0;\n @p bra FAIL;\n"
+        " mov.u64 u, %%clock64;\n sub.s64 u, u, t;\n setp.le.s64 p, u, %5;\n @p bra LOOP;\n"
+        " st.shared.u32 [%3], 1;\n red.global.or.b32 [%4], %7;\n"
+        "FAIL:\n mov.u32 %0, 0;\n bra END;\n"
+        "DONE:\n mov.u32 %0, 1;\n"
+        "END:\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(flag), "l"(status), "l"(limit), "r"(hint), "n"((int)kStatusTimeout)
+        : "memory");
+    return ok != 0;
 }
 
 // One segment: key tiles [tile0, tile1) of a line (request, KV head, row tile).
@@ -166,8 +214,6 @@ __device__ __forceinline__ Seg load_seg(const int* segs, int i) {
     const int4 a = __ldg(r), b = __ldg(r + 1), c = __ldg(r + 2);
     return Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x};
 }
-// log2 of the copies a row tile of `rows` rows is held in.
-__device__ __forceinline__ int copies_log2(int rows) { return rows <= 32 ? 2 : rows <= 64 ? 1 : 0; }
 
 // 32 bits of mask row `row` from bit u0 on (bits below 0: keys of the context,
 // seen; bits from T on: none).
@@ -189,200 +235,83 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
     return d;
 }
-__device__ __forceinline__ float2 e4m3_back(uint32_t pair) {
+__device__ __forceinline__ __half2 half2_of_e4m3(uint32_t pair) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)pair));
-    return __half22float2(*reinterpret_cast<__half2*>(&h));
+    return *reinterpret_cast<__half2*>(&h);
+}
+__device__ __forceinline__ uint32_t e4m3_of_half2(__half2 x) {
+    unsigned short d;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(*reinterpret_cast<uint32_t*>(&x)));
+    return d;
+}
+
+// Four P' (at most 2^8) as e4m3 pieces: hi = e4m3(P'), lo = e4m3(32 (P' - hi)),
+// and with NP = 3 e4m3 of what lo left; four codes a word.  P' is first
+// rounded to f16 (11 bits, 2^-12 off: half a step of the finest result, 12
+// bits), in which the differences are exact.
+template <int NP>
+__device__ __forceinline__ void e4m3_pieces(const float* x, uint32_t& hi, uint32_t& lo, uint32_t& lo2) {
+    uint32_t a[2], b[2], c[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
+        a[k] = e4m3_of_half2(h);
+        const __half2 r = __hmul2(__hsub2(h, half2_of_e4m3(a[k])), __float2half2_rn(32.f));
+        b[k] = e4m3_of_half2(r);
+        if constexpr (NP == 3) c[k] = e4m3_of_half2(__hsub2(r, half2_of_e4m3(b[k])));
+    }
+    hi = prmt(a[0], a[1], 0x5410u);
+    lo = prmt(b[0], b[1], 0x5410u);
+    if constexpr (NP == 3) lo2 = prmt(c[0], c[1], 0x5410u);
 }
 
 template <int NC>
-__device__ __forceinline__ void ld_cols(uint32_t t, uint32_t (&v)[NC]) {
+__device__ __forceinline__ void ld_cols(uint32_t t, float (&v)[NC]) {
     if constexpr (NC == 16) {
-        tc_ld16(t, v);
+        tc_ld16(t, reinterpret_cast<uint32_t(&)[16]>(v));
     } else {
 #pragma unroll
         for (int c = 0; c < NC / 32; ++c) tc_ld32(t + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
     }
-}
-template <int N>
-__device__ __forceinline__ void st_cols(uint32_t t, const uint32_t (&v)[N]) {
-    if constexpr (N == 4) tc_st4(t, v);
-    if constexpr (N == 8) tc_st8(t, v);
-    if constexpr (N == 16) tc_st16(t, v);
-    if constexpr (N == 32) tc_st32(t, v);
-}
-
-// What a softmax thread keeps of its row over a segment.
-struct RowState {
-    float m, l;  // running maximum (log2 units), sum of P' over this thread's columns
-};
-
-struct TileArgs {
-    uint32_t tS, tO;          // this warp's S / P buffer and O_hi, lane base added
-    uint32_t xmax, xbar;      // exchange slots [half][128] and barrier of this tile
-    uint32_t xphase;
-    uint32_t prev_bar, prev_phase;  // completes when the previous tile's PV has
-    uint32_t pbar;
-    uint32_t flag;
-    uint32_t* status;
-    long long limit;
-    const uint32_t* mrow;     // mask row
-    int words, T, u0;         // u0: mask bit of this thread's first column (negative: context)
-    int r, half, copy;
-    bool first;               // first tile of the segment
-    float scale;
-};
-
-// One tile's softmax on NC columns of this thread's row: maximum, rescale of O
-// when it rose, P pieces into TMEM.  Warp-collective; false when a wait gave up.
-template <int KT, int NP, int DH, int NC>
-__device__ __forceinline__ bool softmax_tile(RowState& st, const TileArgs& a) {
-    constexpr bool k2 = KT == PAFP8_BF16 || KT == PAFP8_F16;
-    constexpr int C = 64 / NC;  // copies
-    constexpr float kShift = PShift<KT>::kShift, kHead = PShift<KT>::kHead;
-    const int col0 = a.copy * (128 / C) + a.half * NC;
-    uint32_t v[NC];
-    ld_cols<NC>(a.tS + col0, v);
     tc_wait_ld();
-    if (a.u0 + NC > 0) {  // some of these keys are drafted tokens (or lie behind the last)
-#pragma unroll
-        for (int c = 0; c < NC; c += 32) {
-            const uint32_t bits = mask_bits(a.mrow, a.u0 + c, a.words, a.T);
-#pragma unroll
-            for (int i = 0; i < 32 && c + i < NC; ++i)
-                if (!((bits >> i) & 1u)) v[c + i] = 0xFF800000u;  // -inf
-        }
-    }
-    float pm[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) pm[k] = __uint_as_float(v[k]);
-#pragma unroll
-    for (int i = 4; i < NC; i += 2)
-        pm[(i >> 1) & 3] = max3(pm[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-    float mx = fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]);
-    sts_f(a.xmax + 4u * (128 * a.half + a.r), mx);
-    warp_arrive(a.xbar);
-    if (!__all_sync(0xFFFFFFFFu, tree_wait(a.xbar, a.xphase, a.flag, a.status, a.limit))) return false;
-    mx = fmaxf(mx, lds_f(a.xmax + 4u * (128 * (a.half ^ 1) + a.r)));
-    const float m_new = fmaxf(st.m, mx * a.scale);
-    float m_use = st.m;
-    bool rescale = false;
-    if (a.first) {
-        m_use = m_new;
-    } else if (m_new > st.m + kHead) {
-        m_use = m_new;
-        rescale = true;
-    }
-    if (__any_sync(0xFFFFFFFFu, rescale)) {
-        // Every O update of the earlier tiles has to be complete.
-        if (!__all_sync(0xFFFFFFFFu, tree_wait(a.prev_bar, a.prev_phase, a.flag, a.status, a.limit))) return false;
-        tc_fence_after();
-        const float alpha = rescale ? ex2(st.m - m_use) : 1.f;
-        const f32x2 alpha2 = make_f32x2(alpha, alpha);
-        st.l *= alpha;
-        // The two threads of a row take half of its O columns each.
-        constexpr int kCols = k2 ? DH / 2 : DH;
-#pragma unroll 1
-        for (int c = 0; c < kCols / 32; ++c) {
-            uint32_t o[32];
-            const uint32_t at = a.tO + a.half * kCols + 32 * c;
-            tc_ld32(at, o);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float x, y;
-                split_f32x2(mul2(make_f32x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), alpha2), x, y);
-                o[2 * i] = __float_as_uint(x);
-                o[2 * i + 1] = __float_as_uint(y);
-            }
-            tc_st32(at, o);
-        }
-        tc_wait_st();
-    }
-    st.m = m_use;
-    // A row that has seen no key yet keeps m = -inf; its P is exp2(-inf) = 0.
-    const float neg = m_use == -INFINITY ? 0.f : kShift - m_use;
-    const f32x2 scale2 = make_f32x2(a.scale, a.scale), neg2 = make_f32x2(neg, neg);
-    f32x2 ps[2] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
-    constexpr int W = NC / (k2 ? 2 : 4);  // words of one P piece
-    uint32_t p0[W], p1[k2 ? 1 : W], p2[NP == 3 ? W : 1];
-#pragma unroll
-    for (int i = 0; i < NC / 2; ++i) {
-        float x, y;
-        split_f32x2(fma2(make_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), scale2, neg2), x, y);
-        const f32x2 e = make_f32x2(ex2(x), ex2(y));
-        ps[i & 1] = add2(ps[i & 1], e);
-        split_f32x2(e, x, y);
-        if constexpr (KT == PAFP8_BF16) {
-            p0[i] = pack_bf162(x, y);
-        } else if constexpr (KT == PAFP8_F16) {
-            p0[i] = pack_half2(x, y);
-        } else {
-            const uint32_t hi = e4m3_pair(x, y);
-            const float2 hb = e4m3_back(hi);
-            const f32x2 rest = mul2(fma2(make_f32x2(hb.x, hb.y), make_f32x2(-1.f, -1.f), e), make_f32x2(32.f, 32.f));
-            split_f32x2(rest, x, y);
-            const uint32_t lo = e4m3_pair(x, y);
-            uint32_t lo2 = 0;
-            if constexpr (NP == 3) {
-                const float2 lb = e4m3_back(lo);
-                split_f32x2(fma2(make_f32x2(lb.x, lb.y), make_f32x2(-1.f, -1.f), rest), x, y);
-                lo2 = e4m3_pair(x, y);
-            }
-            if (i & 1) {
-                p0[i >> 1] = prmt(p0[i >> 1], hi, 0x5410u);
-                p1[i >> 1] = prmt(p1[i >> 1], lo, 0x5410u);
-                if constexpr (NP == 3) p2[i >> 1] = prmt(p2[i >> 1], lo2, 0x5410u);
-            } else {
-                p0[i >> 1] = hi;
-                p1[i >> 1] = lo;
-                if constexpr (NP == 3) p2[i >> 1] = lo2;
-            }
-        }
-    }
-    {
-        float x, y, z, w;
-        split_f32x2(ps[0], x, y);
-        split_f32x2(ps[1], z, w);
-        st.l += (x + y) + (z + w);
-    }
-    // P over S (both halves have read it): piece i in 32 (fp8) or 64 columns
-    // from 32 i on; the other copies' keys have P = 0.
-    constexpr int kPer = (k2 ? 64 : 32) / C;  // columns of one copy
-    uint32_t zero[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) zero[i] = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const uint32_t at = a.tS + c * kPer + a.half * W;
-        const bool mine = c == a.copy;
-        if (C == 1 || mine) {
-            st_cols<W>(at, p0);
-            if constexpr (!k2) st_cols<W>(at + 32, p1);
-            if constexpr (NP == 3) st_cols<W>(at + 64, p2);
-        } else {
-            st_cols<W>(at, zero);
-            if constexpr (!k2) st_cols<W>(at + 32, zero);
-            if constexpr (NP == 3) st_cols<W>(at + 64, zero);
-        }
-    }
-    tc_wait_st();
-    tc_fence_before();
-    return true;
 }
 
-template <int KT, int NP, int DH>
+// Sums of v[c] over the warp's lanes: lane l returns column l's (of 32; of 16,
+// column l % 16's).
+template <int N>
+__device__ __forceinline__ float column_sum(const float* v, int lane) {
+    float a[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = v[i];
+    if constexpr (N == 16) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xFFFFFFFFu, a[i], 16);
+    }
+#pragma unroll
+    for (int d = N / 2; d > 0; d >>= 1) {
+        const bool up = (lane & d) != 0;
+#pragma unroll
+        for (int i = 0; i < d; ++i) {
+            const float keep = up ? a[i + d] : a[i], send = up ? a[i] : a[i + d];
+            a[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, d);
+        }
+    }
+    return a[0];
+}
+
+template <int KT, int NP, int DH, int R>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
-    constexpr bool k2 = KT == PAFP8_BF16 || KT == PAFP8_F16;
-    constexpr int ES = k2 ? 2 : 1;
-    constexpr uint32_t kTile = kTileKeys * DH * ES;   // one K, V or Q-piece tile
-    constexpr uint32_t kHalf = kTileKeys * 128;       // a 64-dim half of a 2-byte tile
-    constexpr int NH = DH / 64;                       // halves of a 2-byte row
+    using D = TreeDims<KT, NP, DH, R>;
+    constexpr bool k2 = D::k2;
+    constexpr uint32_t kTile = D::kTile, kHalf = D::kHalf;
+    constexpr int NH = D::NH, NCOL = D::NCOL, NPB = D::NPB, NOB = D::NOB;
+    constexpr float kShift = PShift<KT>::kShift, kHead = PShift<KT>::kHead;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const TreeSmem L = tree_smem((uint32_t)(p.q_buffers * p.q_pieces) * kTile, kTile, p.stages);
+    const TreeSmem L = tree_smem<D, R, NP>(p.q_buffers * p.q_pieces, p.stages);
     auto bar = [&](int i) -> uint32_t { return base + L.bars + 8u * (uint32_t)i; };
     const uint32_t flag = base + L.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -392,7 +321,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int s_end = __ldg(meta + meta[kMetaOffCtaSeg] + blockIdx.x + 1);
     const int* segs = meta + meta[kMetaOffSeg];
     const int g = p.group, TQ = kTileRows / g;
-    auto wait = [&](int b, uint32_t parity) { return tree_wait(bar(b), parity, flag, p.status, p.wait_cycles); };
+    const uint32_t hint = p.wait_cycles < kWaitCyclesDefault ? 0u : 20000u;
+    auto wait = [&](int b, uint32_t parity) { return tree_wait(bar(b), parity, flag, p.status, p.wait_cycles, hint); };
     auto wait_all = [&](int b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
 
     if (threadIdx.x == 0) {
@@ -403,11 +333,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(bar(tState + i), 8);   // softmax warps
             mbar_init(bar(tSFull + i), 1);
             mbar_init(bar(tPFull + i), 8);
+            mbar_init(bar(tOFull + i), 1);
+            mbar_init(bar(tOEmpty + i), 4);
+            mbar_init(bar(tHalf + i), 4);
         }
-        mbar_init(bar(tOFull), 1);
-        mbar_init(bar(tOEmpty), 4);
-        for (int i = 0; i < 4; ++i) mbar_init(bar(tXmax + i), 2);
-        mbar_init(bar(tStage), 4);
+        mbar_init(bar(tHelp), 4);
         mbar_init(bar(tDrain), 1);
         for (int i = 0; i < NS; ++i) {
             mbar_init(bar(tKFull + i), 3);  // producer warps
@@ -415,18 +345,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(bar(tVFull + i), 3);
             mbar_init(bar(tVEmpty + i), 1);
         }
+        for (int i = 0; i < 4; ++i) sts32(base + L.vote + 4 * i, 0);
         asm volatile("st.shared.u32 [%0], 0;" ::"r"(flag) : "memory");
         mbar_init_fence();
     }
-    if (warp == 13) tc_alloc(base + L.tmem_slot, 512);
+    if (warp == 13) tc_alloc(base + L.tmem_slot, D::kCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    uint32_t tmem;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(base + L.tmem_slot) : "memory");
+    const uint32_t tmem = lds_u(base + L.tmem_slot);
 
-    if (warp == 12 || warp >= 14) {
+    if (warp >= 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+      if (warp != 13) {
         // ----------------------------------------------------------- producers
         // A box holds the 16 tokens of one (sub-)page, and a warp's box takes it
         // about 130 cycles to issue, 16 boxes a tile 2100: more than the tile's
@@ -440,7 +372,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         constexpr int kBoxes = 8 * (k2 ? NH : 1);      // boxes of a K or V tile: (half, sub-page)
         const int box = 3 * lane + pw, i8 = box & 7;   // this lane's box
         constexpr uint32_t kBoxBytes = k2 ? 2048u : (uint32_t)(kPageSize * DH);
-        long long n = 0;  // tiles issued
+        int n = 0;  // tiles issued
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true, k_only = false;
@@ -497,216 +429,370 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         if (lane == 0) {
             // Every copy lands before the CTA may exit.
-            const long long nk = n + (k_only ? 1 : 0);
+            const int nk = n + (k_only ? 1 : 0);
             for (int s = 0; s < NS; ++s) {
                 if (s < nk) mbar_wait(bar(tKFull + s), (uint32_t)(((nk - 1 - s) / NS) & 1));
                 if (s < n) mbar_wait(bar(tVFull + s), (uint32_t)(((n - 1 - s) / NS) & 1));
             }
         }
         __syncwarp();
-    } else if (warp == 13) {
+      } else {
         // ----------------------------------------------------------------- MMA
-        if (lane == 0 && s_begin < s_end) {
-            const int kvf = k2 ? (KT == PAFP8_BF16 ? 1 : 0) : (p.kv_dtype == PAFP8_E5M2 ? 1 : 0);
-            const int qf = k2 ? kvf : (p.q_dtype == PAFP8_E5M2 ? 1 : 0);
-            const uint32_t idesc_qk = make_idesc(qf, kvf, 128, 128);
-            const uint32_t idesc_pv = make_idesc_bmn(k2 ? kvf : 0, kvf, 128, DH);
-            bool ok = true, issued = false;
-            // QK cursor: segment qs, tile qt, tile count qn so far; PV cursor alike.
-            int qs = s_begin, qn = 0;
-            int kstage = 0, vstage = 0;
-            uint32_t kphase = 0, vphase = 0;
-            Seg qg = load_seg(segs, qs);
-            int qt = qg.tile0;
-            auto qk = [&]() -> bool {
-                const int nth = qs - s_begin, buf = NQB == 2 ? nth & 1 : 0;
-                if (qt == qg.tile0) {
-                    if (!wait(tQFull + buf, (uint32_t)((NQB == 2 ? nth >> 1 : nth) & 1))) return false;
-                }
-                if (!wait(tKFull + kstage, kphase)) return false;
-                tc_fence_after();
-                const uint32_t d = tmem + 128u * (qn & 1);
-                const uint32_t qa = base + L.q + (uint32_t)(buf * p.q_pieces) * kTile;
-                const uint32_t ka = base + L.k + (uint32_t)kstage * kTile;
-                if constexpr (k2) {
-                    const uint64_t dq = sw128_kmajor_desc(qa), dk = sw128_kmajor_desc(ka);
-                    if constexpr (DH == 128)
-                        tc_mma_f16_ss_k8<kHalf, kHalf>(d, dq, dk, idesc_qk, 0u);
-                    else
-                        tc_mma_f16_ss_k4(d, dq, dk, idesc_qk, 0u);
-                } else {
-                    for (int i = 0; i < p.q_pieces; ++i) {
-                        if constexpr (DH == 128)
-                            tc_mma_f8_ss_k4(d, sw128_kmajor_desc(qa + i * kTile), sw128_kmajor_desc(ka), idesc_qk, i > 0);
-                        else
-                            tc_mma_f8_ss_k2(d, sw64_kmajor_desc(qa + i * kTile), sw64_kmajor_desc(ka), idesc_qk, i > 0);
+        // The whole warp walks the loop in step and one lane issues: with the
+        // loop under `if (lane == 0)` every operand went through vector
+        // registers, some 800 instructions a tile, and the issuing thread, not
+        // the tensor pipe, set the tile's time.
+        const uint32_t elect = elect_one();
+        const int kvf = k2 ? (KT == PAFP8_BF16 ? 1 : 0) : (p.kv_dtype == PAFP8_E5M2 ? 1 : 0);
+        const int qf = k2 ? kvf : (p.q_dtype == PAFP8_E5M2 ? 1 : 0);
+        const uint32_t idesc_qk = make_idesc(kvf, qf, 128, R);
+        const uint32_t idesc_pv = make_idesc_mn(kvf, k2 ? kvf : 0, 128, D::OC);
+        const uint32_t idesc_p3 = make_idesc_mn(kvf, 0, 128, R);
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const int sb0 = __shfl_sync(0xFFFFFFFFu, s_begin, 0), sb1 = __shfl_sync(0xFFFFFFFFu, s_end, 0);
+        auto tiles_of = [&](int si) -> int {
+            const int2 t = __ldg(reinterpret_cast<const int2*>(segs + kTreeSegWords * (long long)si + 2));
+            return __shfl_sync(0xFFFFFFFFu, t.y - t.x, 0);
+        };
+        // Descriptors: the constant halves, and the words of the tiles at offset 0.
+        constexpr uint64_t kQKd = (k2 || DH == 128) ? 1 : 0;  // 128-byte rows, else 64
+        const uint64_t qk_proto = kQKd ? sw128_kmajor_desc(0) : sw64_kmajor_desc(0);
+        const uint64_t v_proto = k2 ? mnmajor_desc<128>(0, DH == 128 ? kHalf : kTile) : mnmajor_desc<(k2 ? 128 : DH)>(0, kTile);
+        const uint64_t p_proto = mnmajor_desc<D::W>(0, k2 ? D::kPBlock : D::kPPiece);
+        const uint32_t qk_hi = (uint32_t)(qk_proto >> 32), v_hi = (uint32_t)(v_proto >> 32), p_hi = (uint32_t)(p_proto >> 32);
+        const uint32_t k_lo = (uint32_t)qk_proto + ((base + L.k) >> 4), q_lo = (uint32_t)qk_proto + ((base + L.q) >> 4);
+        const uint32_t v_lo = (uint32_t)v_proto + ((base + L.v) >> 4), p_lo = (uint32_t)p_proto + ((base + L.p) >> 4);
+        bool ok = true;
+        int qs = sb0, qn = 0, qbuf = 0;  // QK's segment, tile count and Q buffer
+        uint32_t qphase = 0;
+        int kstage = 0, vstage = 0;
+        uint32_t kphase = 0, vphase = 0;
+        int qleft = qs < sb1 ? tiles_of(qs) : 0;
+        bool qfirst = true;
+        int pn = 0;
+        for (int ps = sb0; ps < sb1 && ok; ++ps) {
+            const int nth = ps - sb0, ob = nth % NOB;
+            const int nt = tiles_of(ps);
+            for (int t = 0; t < nt; ++t, ++pn) {
+                // QK(j + 1) goes before PV(j), into the next segment at most (the Q of
+                // the one after is built only when this one's epilogue is done).  So
+                // QK(j) follows PV(j - 2), which waited for P(j - 2): S(j - 2) has been
+                // read, and once S(j) is complete so is PV(j - 2), P's buffer free.
+                while (qs < sb1 && qn <= pn + 1 && qs <= ps + 1) {
+                    const int sb = qn & 1;
+                    if (qfirst) {
+                        if (!(ok = wait_all(tQFull + qbuf, qphase))) break;
+                        qfirst = false;
                     }
-                }
-                issued = true;
-                tc_commit(bar(tSFull + (qn & 1)));
-                tc_commit(bar(tKEmpty + kstage));
-                if (++kstage == NS) {
-                    kstage = 0;
-                    kphase ^= 1u;
-                }
-                ++qn;
-                if (++qt == qg.tile1) {
-                    tc_commit(bar(tQEmpty + buf));
-                    if (++qs < s_end) {
-                        qg = load_seg(segs, qs);
-                        qt = qg.tile0;
-                    }
-                }
-                return true;
-            };
-            ok = qk();
-            int pn = 0;
-            for (int ps = s_begin; ps < s_end && ok; ++ps) {
-                const Seg pg = load_seg(segs, ps);
-                for (int t = pg.tile0; t < pg.tile1; ++t, ++pn) {
-                    if (qs < s_end && !(ok = qk())) break;
-                    // O of the segment before has been read by its epilogue.
-                    if (t == pg.tile0 && ps > s_begin && !(ok = wait(tOEmpty, (uint32_t)((ps - s_begin - 1) & 1)))) break;
-                    if (!(ok = wait(tVFull + vstage, vphase))) break;
-                    if (!(ok = wait(tPFull + (pn & 1), (uint32_t)((pn >> 1) & 1)))) break;
+                    if (!(ok = wait_all(tKFull + kstage, kphase))) break;
                     tc_fence_after();
-                    const uint32_t acc = t > pg.tile0 ? 1u : 0u;
-                    const uint32_t pa = tmem + 128u * (pn & 1);
-                    const uint32_t va = base + L.v + (uint32_t)vstage * kTile;
+                    // S^T = K Q^T: A = K (keys), B = Q (rows), both K-major.
+                    const uint32_t d = tm + (uint32_t)(R * sb);
+                    const uint32_t ka = k_lo + (uint32_t)kstage * (kTile >> 4);
+                    uint32_t qa = q_lo + (uint32_t)(qbuf * p.q_pieces) * (D::kQPiece >> 4);
                     if constexpr (k2) {
-                        tc_mma_f16_ts_mn_k8(tmem + kColO, pa, sw128_mnmajor_desc(va, DH == 128 ? kHalf : 16u), idesc_pv, acc);
+#pragma unroll
+                        for (int i = 0; i < DH / 16; ++i)  // K = 16: 32 bytes on, then the other 64-dim half
+                            tc_mma_elect<false>(d, ka + (i >> 2) * (kHalf >> 4) + 2 * (i & 3), qk_hi,
+                                                qa + (i >> 2) * (R * 128 >> 4) + 2 * (i & 3), qk_hi, idesc_qk, i > 0, elect);
                     } else {
-                        const uint64_t dv = DH == 128 ? sw128_mnmajor_desc(va, 16u) : sw64_mnmajor_desc(va);
-                        tc_mma_f8_ts_mn_k4<DH>(tmem + kColO, pa, dv, idesc_pv, acc);
-                        tc_mma_f8_ts_mn_k4<DH>(tmem + kColO + DH, pa + 32, dv, idesc_pv, acc);
-                        if constexpr (NP == 3) tc_mma_f8_ts_mn_k4<DH>(tmem + kColO + DH, pa + 64, dv, idesc_pv, 1u);
+                        for (int pc = 0; pc < p.q_pieces; ++pc, qa += D::kQPiece >> 4) {
+#pragma unroll
+                            for (int i = 0; i < DH / 32; ++i)
+                                tc_mma_elect<true>(d, ka + 2 * i, qk_hi, qa + 2 * i, qk_hi, idesc_qk, pc > 0 || i > 0, elect);
+                        }
                     }
-                    tc_commit(bar(tVEmpty + vstage));
-                    if (t + 1 == pg.tile1) tc_commit(bar(tOFull));
-                    if (++vstage == NS) {
-                        vstage = 0;
-                        vphase ^= 1u;
+                    tc_commit_elect(bar(tSFull + sb), elect);
+                    tc_commit_elect(bar(tKEmpty + kstage), elect);
+                    if (++kstage == NS) {
+                        kstage = 0;
+                        kphase ^= 1u;
+                    }
+                    ++qn;
+                    if (--qleft == 0) {
+                        tc_commit_elect(bar(tQEmpty + qbuf), elect);
+                        if (++qbuf == NQB) {
+                            qbuf = 0;
+                            qphase ^= 1u;
+                        }
+                        qfirst = true;
+                        if (++qs < sb1) qleft = tiles_of(qs);
                     }
                 }
-            }
-            if (issued) {  // every MMA completes before TMEM is freed
-                tc_commit(bar(tDrain));
-                mbar_wait(bar(tDrain), 0);
+                if (!ok) break;
+                // O of the segment that last used this buffer has been read.
+                if (t == 0 && nth >= NOB && !(ok = wait_all(tOEmpty + ob, (uint32_t)((nth / NOB + 1) & 1)))) break;
+                if (!(ok = wait_all(tVFull + vstage, vphase))) break;
+                if (!(ok = wait_all(tPFull + pn % NPB, (uint32_t)((pn / NPB) & 1)))) break;
+                tc_fence_after();
+                // O^T += V^T P^T: A = V (dims), B = P (rows), both MN-major.  64 dims
+                // fill half of M = 128: the other half reads the shared memory one
+                // tile on and its lanes of O are never used.
+                const uint32_t d = tm + D::kColO + (uint32_t)(D::OC * ob);
+                const uint32_t va = v_lo + (uint32_t)vstage * (kTile >> 4);
+                const uint32_t pa = p_lo + (uint32_t)(pn % NPB) * (NP * D::kPPiece >> 4);
+                constexpr int W = D::W;
+                if constexpr (k2) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)  // K = 16 keys
+                        tc_mma_elect<false>(d, va + 128 * i, v_hi, pa + W * i, p_hi, idesc_pv, t > 0 || i > 0, elect);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)  // K = 32 keys
+                        tc_mma_elect<true>(d, va + 2 * DH * i, v_hi, pa + 2 * W * i, p_hi, idesc_pv, t > 0 || i > 0, elect);
+                    if constexpr (NP == 3) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tc_mma_elect<true>(d + R, va + 2 * DH * i, v_hi, pa + (2 * D::kPPiece >> 4) + 2 * W * i, p_hi, idesc_p3,
+                                               1u, elect);
+                    }
+                }
+                tc_commit_elect(bar(tVEmpty + vstage), elect);
+                if (t + 1 == nt) tc_commit_elect(bar(tOFull + ob), elect);
+                if (++vstage == NS) {
+                    vstage = 0;
+                    vphase ^= 1u;
+                }
             }
         }
+        if (qn > 0) {  // every MMA completes before TMEM is freed
+            tc_commit_elect(bar(tDrain), elect);
+            mbar_wait(bar(tDrain), 0);
+        }
         __syncwarp();
+      }
     } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory");
         // ------------------------------------------------------------- softmax
+        constexpr int NC = D::NC, NSUB = NCOL / NC;  // NSUB passes of NC rows a tile
         const int quad = warp & 3, half = warp >> 2;
-        const int r = 32 * quad + lane;
+        const int krow = 32 * quad + lane;    // this thread's key in a tile
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
-        const uint32_t tO = lane_base + kColO;
-        int j = 0;  // tiles so far
-        int stage = 0;
-        uint32_t sphase = 0;  // phase of V stage `stage`
+        const uint32_t votes = base + L.vote + 8u * half;
+        const int hbar = tHalf + half;
+        int j = 0;                              // tiles so far
+        int stage = 0;                          // V stage of tile j
+        uint32_t vphase = 0;
+        uint32_t hphase = 0, wbuf = 0, ballots = 0;
         bool ok = true;
         for (int si = s_begin; si < s_end && ok; ++si) {
             const Seg sg = load_seg(segs, si);
             const int nth = si - s_begin;
-            const int ntok = min(TQ, sg.qo_len - sg.t0), rows = ntok * g;
-            const int cl = copies_log2(rows);
-            const int rp = 128 >> cl, row = r & (rp - 1), copy = r >> (7 - cl);
-            const int tok = min(row / g, ntok - 1);
+            const int ntok = min(TQ, sg.qo_len - sg.t0);
             const int ctx = sg.kv_len - sg.qo_len;
-            const uint32_t* mrow = p.tree_mask + (long long)(sg.qo0 + sg.t0 + tok) * p.mask_words;
+            const uint32_t tO = lane_base + D::kColO + (uint32_t)(D::OC * (nth % NOB));
+            f32x2 l[NCOL / 2];
+#pragma unroll
+            for (int i = 0; i < NCOL / 2; ++i) l[i] = make_f32x2(0.f, 0.f);
             if (!(ok = wait_all(tInfo + (nth & 1), (uint32_t)((nth >> 1) & 1)))) break;
-            float scale = p.sm_scale_log2;
-            if (p.k_scales != nullptr) {
-                const int qh = sg.hk * g + row % g;
-                scale = fold_scale_log2(p.sm_scale, p.q_scales != nullptr ? __ldg(p.q_scales + qh) : 1.0f,
-                                        __ldg(p.k_scales + sg.hk));
-            }
-            scale *= lds_f(base + L.fac + 4u * (128 * (nth & 1) + r));
-            RowState st{-INFINITY, 0.f};
-            for (int t = sg.tile0; t < sg.tile1; ++t, ++j) {
-                if (!(ok = wait_all(tSFull + (j & 1), (uint32_t)((j >> 1) & 1)))) break;
+            for (int t = sg.tile0; t < sg.tile1 && ok; ++t, ++j) {
+                const bool first = t == sg.tile0;
+                const int sb = j & 1;
+                if (!(ok = wait_all(tSFull + sb, (uint32_t)((j >> 1) & 1)))) break;
                 tc_fence_after();
-                TileArgs a;
-                a.tS = lane_base + 128u * (j & 1);
-                a.tO = tO;
-                a.xmax = base + L.xmax + 1024u * (j & 1);
-                a.xbar = bar(tXmax + quad);
-                a.xphase = (uint32_t)(j & 1);
-                a.prev_bar = bar(tVEmpty + (stage == 0 ? NS - 1 : stage - 1));
-                a.prev_phase = stage == 0 ? sphase ^ 1u : sphase;
-                a.flag = flag;
-                a.status = p.status;
-                a.limit = p.wait_cycles;
-                a.mrow = mrow;
-                a.words = p.mask_words;
-                a.T = sg.qo_len;
-                a.u0 = t * kTileKeys + copy * rp + half * (rp >> 1) - ctx;
-                a.r = r;
-                a.half = half;
-                a.copy = copy;
-                a.first = t == sg.tile0;
-                a.scale = scale;
-                if (cl == 0)
-                    ok = softmax_tile<KT, NP, DH, 64>(st, a);
-                else if (cl == 1)
-                    ok = softmax_tile<KT, NP, DH, 32>(st, a);
-                else
-                    ok = softmax_tile<KT, NP, DH, 16>(st, a);
+                const uint32_t pb = base + L.p + (uint32_t)(j % NPB) * (NP * D::kPPiece);
+#pragma unroll
+                for (int sub = 0; sub < NSUB; ++sub) {
+                    const int cb = half * NCOL + sub * NC;  // first row of this pass
+                    const uint32_t tS = lane_base + (uint32_t)(R * sb + cb);
+                    const uint32_t sct = base + L.sc + (uint32_t)((nth & 1) * R + cb) * 4u;
+                    const uint32_t negt = base + L.neg + (uint32_t)(warp * NCOL + sub * NC) * 4u;
+                    float v[NC];
+                    // The logits; those of keys that a row does not see become -inf.  Lane i
+                    // fetches 32 keys' mask bits of row i's token.
+                    auto load = [&]() {
+                        ld_cols<NC>(tS, v);
+                        if ((t + 1) * kTileKeys <= ctx) return;
+                        const int tok = min((cb + lane) / g, ntok - 1);
+                        const uint32_t bits = mask_bits(p.tree_mask + (long long)(sg.qo0 + sg.t0 + tok) * p.mask_words,
+                                                        t * kTileKeys + 32 * quad - ctx, p.mask_words, sg.qo_len);
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+                            if (!((__shfl_sync(0xFFFFFFFFu, bits, c) >> lane) & 1u)) v[c] = -INFINITY;
+                    };
+                    // P' in place of the logits.  The vote on the reference maxima is cast
+                    // before the exponentials and read after P is stored, so its
+                    // latency passes meanwhile; a raised reference redoes the pass.
+                    bool rise = first;
+#pragma unroll 1
+                    while (true) {
+                        load();
+                        if (rise) {
+                            // Column maxima of the tile: over this warp's lanes, then over the
+                            // four warps of the half.  Lane i settles row i.
+                            float cm = 0.f;
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) {
+                                const float m = warp_max(v[c]);
+                                if (lane == c) cm = m;
+                            }
+                            const uint32_t wm = base + L.wmax + (uint32_t)((wbuf * 2 + half) * 4 * NC) * 4u;
+                            wbuf ^= 1u;
+                            if (lane < NC) sts_f(wm + 4u * (quad * NC + lane), cm);
+                            warp_arrive(bar(hbar));
+                            if (!(ok = wait_all(hbar, hphase))) break;
+                            hphase ^= 1u;
+                            const int c = min(lane, NC - 1);
+                            const float top = fmaxf(max3(lds_f(wm + 4u * c), lds_f(wm + 4u * (NC + c)), lds_f(wm + 4u * (2 * NC + c))),
+                                                    lds_f(wm + 4u * (3 * NC + c))) * lds_f(sct + 4u * c);
+                            const float was = first ? kUnseen : lds_f(negt + 4u * c);
+                            const float m_old = was >= kUnseen ? -INFINITY : kShift - was;
+                            const float m_new = fmaxf(m_old, top);
+                            const float alpha = m_old == -INFINITY ? 0.f : ex2(m_old - m_new);
+                            __syncwarp();
+                            if (lane < NC) sts_f(negt + 4u * c, m_new == -INFINITY ? kUnseen : kShift - m_new);
+                            __syncwarp();
+                            if (!first) {
+                                // Every O update of the earlier tiles has to be complete.
+                                if (!(ok = wait_all(tVEmpty + (stage == 0 ? NS - 1 : stage - 1), stage == 0 ? vphase ^ 1u : vphase)))
+                                    break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int i = 0; i < NC; i += 2)
+                                    l[(sub * NC + i) / 2] =
+                                        mul2(l[(sub * NC + i) / 2], make_f32x2(__shfl_sync(0xFFFFFFFFu, alpha, i),
+                                                                             __shfl_sync(0xFFFFFFFFu, alpha, i + 1)));
+#pragma unroll 1
+                                for (int at = 0; at < (k2 ? NC : 2 * NC); at += 16) {  // O_hi, then O_lo
+                                    const int c0 = at & (NC - 1);
+                                    const uint32_t to = tO + (uint32_t)((at >= NC ? R : 0) + cb + c0);
+                                    uint32_t o[16];
+                                    tc_ld16(to, o);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xFFFFFFFFu, alpha, c0 + i));
+                                    tc_st16(to, o);
+                                }
+                                tc_wait_st();
+                            }
+                        }
+                        // x = s * scale + (kShift - m)
+#pragma unroll
+                        for (int c = 0; c < NC; c += 4) {
+                            const float4 sc = lds_f4(sct + 4u * c), ng = lds_f4(negt + 4u * c);
+                            split_f32x2(fma2(make_f32x2(v[c], v[c + 1]), make_f32x2(sc.x, sc.y), make_f32x2(ng.x, ng.y)), v[c],
+                                        v[c + 1]);
+                            split_f32x2(fma2(make_f32x2(v[c + 2], v[c + 3]), make_f32x2(sc.z, sc.w), make_f32x2(ng.z, ng.w)),
+                                        v[c + 2], v[c + 3]);
+                        }
+                        const uint32_t slot = votes + 4u * (ballots & 1u);
+                        if (!rise) {
+                            float pm[2] = {v[0], v[1]};
+#pragma unroll
+                            for (int c = 2; c < NC; c += 2) pm[(c >> 1) & 1] = max3(pm[(c >> 1) & 1], v[c], v[c + 1]);
+                            ++ballots;
+                            if (__any_sync(0xFFFFFFFFu, fmaxf(pm[0], pm[1]) > kShift + kHead) && lane == 0) sts32(slot, ballots);
+                            warp_arrive(bar(hbar));
+                        }
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) v[c] = ex2(v[c]);
+                        // P into shared memory.  Of two buffers the one to write is free (its
+                        // product was complete before S was); a single one is free when the
+                        // tile before has been multiplied.
+                        if (NPB == 1 && sub == 0 && j > 0 &&
+                            !(ok = wait_all(tVEmpty + (stage == 0 ? NS - 1 : stage - 1), stage == 0 ? vphase ^ 1u : vphase)))
+                            break;
+                        constexpr int W = D::W;
+                        constexpr int kElems = 16 / D::ES;  // rows a 16-byte chunk
+                        const uint32_t swz = W == 128 ? krow & 7 : W == 64 ? (krow >> 1) & 3 : (krow >> 2) & 1;
+#pragma unroll
+                        for (int c = 0; c < NC; c += kElems) {
+                            const int byte0 = (cb + c) * D::ES;  // in the key's row of all blocks
+                            const uint32_t at = pb + (uint32_t)(byte0 / W) * D::kPBlock + (uint32_t)krow * W +
+                                                ((((uint32_t)(byte0 % W) >> 4) ^ swz) << 4);
+                            uint32_t w0[4], w1[4], w2[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if constexpr (KT == PAFP8_BF16) {
+                                    w0[i] = pack_bf162(v[c + 2 * i], v[c + 2 * i + 1]);
+                                } else if constexpr (KT == PAFP8_F16) {
+                                    w0[i] = pack_half2(v[c + 2 * i], v[c + 2 * i + 1]);
+                                } else {
+                                    e4m3_pieces<NP>(v + c + 4 * i, w0[i], w1[i], w2[i]);
+                                }
+                            }
+                            sts128(at, w0[0], w0[1], w0[2], w0[3]);
+                            if constexpr (!k2) sts128(at + D::kPPiece, w1[0], w1[1], w1[2], w1[3]);
+                            if constexpr (NP == 3) sts128(at + 2 * D::kPPiece, w2[0], w2[1], w2[2], w2[3]);
+                        }
+                        if (rise) break;
+                        if (!(ok = wait_all(hbar, hphase))) break;
+                        hphase ^= 1u;
+                        if (lds_u(slot) != ballots) break;
+                        rise = true;
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < NC / 2; ++i)
+                        l[sub * NC / 2 + i] = add2(l[sub * NC / 2 + i], make_f32x2(v[2 * i], v[2 * i + 1]));
+                }
                 if (!ok) break;
-                // Key rows behind the request's end (the tail of its last page and
+                // Value rows behind the request's end (the tail of its last page and
                 // rows no page filled) hold anything: zero them, P = 0 there must
                 // not meet a NaN.
                 const int valid = sg.kv_len - t * kTileKeys;
                 if (valid < kTileKeys) {
-                    if (!(ok = wait_all(tVFull + stage, sphase))) break;
-                    if (half == 0 && r >= valid) {
-                        const uint32_t vrow = base + L.v + (uint32_t)stage * kTile + (uint32_t)r * (k2 ? 128u : (uint32_t)DH);
+                    if (!(ok = wait_all(tVFull + stage, vphase))) break;
+                    if (half == 0 && krow >= valid) {
+                        const uint32_t vrow = base + L.v + (uint32_t)stage * kTile + (uint32_t)krow * (k2 ? 128u : (uint32_t)DH);
 #pragma unroll
                         for (int c = 0; c < (k2 ? 8 : DH / 16); ++c) {
                             sts128(vrow + 16u * c, 0u, 0u, 0u, 0u);
                             if (k2 && NH == 2) sts128(vrow + kHalf + 16u * c, 0u, 0u, 0u, 0u);
                         }
                     }
-                    fence_async_smem();
                 }
-                warp_arrive(bar(tPFull + (j & 1)));
+                fence_async_smem();
+                tc_fence_before();
+                warp_arrive(bar(tPFull + j % NPB));
                 if (++stage == NS) {
                     stage = 0;
-                    sphase ^= 1u;
+                    vphase ^= 1u;
                 }
             }
             if (!ok) break;
-            const uint32_t ml = base + L.ml + 1536u * (nth & 1);
-            if (half == 0) sts_f(ml + 4u * r, st.m);
-            sts_f(ml + 512u * (1 + half) + 4u * r, st.l);
+            // The segment's sums (over this warp's keys) and maxima for the epilogue.
+#pragma unroll
+            for (int sub = 0; sub < NSUB; ++sub) {
+                float ls[NC];
+#pragma unroll
+                for (int i = 0; i < NC / 2; ++i) split_f32x2(l[sub * NC / 2 + i], ls[2 * i], ls[2 * i + 1]);
+                const float sum = column_sum<NC>(ls, lane);
+                if (lane < NC) {
+                    const int row = half * NCOL + sub * NC + lane;
+                    sts_f(base + L.lsum + 4u * (((nth & 1) * 4 + quad) * R + row), sum);
+                    const float ng = lds_f(base + L.neg + (uint32_t)(warp * NCOL + sub * NC + lane) * 4u);
+                    if (quad == 0) sts_f(base + L.mst + 4u * ((nth & 1) * R + row), ng >= kUnseen ? -INFINITY : kShift - ng);
+                }
+            }
             warp_arrive(bar(tState + (nth & 1)));
         }
-    } else if (warp < 12) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ------------------------------------------------- Q pieces, epilogues
-        const int r = threadIdx.x - 256;
-        const uint32_t tO = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
-        uint32_t stage_phase = 0;
+        const int d = threadIdx.x - 256;  // the dim (TMEM lane) this thread writes out
+        uint32_t help_phase = 0;
         bool ok = true;
         // Segment si's Q rows into its buffer: DH / 8 lanes a row, eight elements
-        // a lane, each row stored to all its copies.  A compact loop: unrolled
-        // over whole rows the code ran once a segment and spent 10 us on
-        // instruction fetches.
+        // a lane; rows of no token are zero.  A compact loop: unrolled over whole
+        // rows the code ran once a segment and spent 10 us on instruction fetches.
         auto build_q = [&](int si) -> bool {
             const Seg sg = load_seg(segs, si);
             const int nth = si - s_begin, buf = NQB == 2 ? nth & 1 : 0;
             const int use = NQB == 2 ? nth >> 1 : nth;  // earlier uses of this buffer
             const int rows = min(TQ, sg.qo_len - sg.t0) * g;
-            const int cl = copies_log2(rows), rp = 128 >> cl;
             constexpr int LPR = DH / 8, RPI = 32 / LPR;  // lanes a row, rows a warp's round
             const int e = lane % LPR, row0 = (warp - 8) * RPI + lane / LPR;
             const bool q1 = !k2 && p.q_pieces == 1;      // an fp8 query as it is
             const size_t head0 = (size_t)(sg.qo0 + sg.t0) * p.num_qo_heads + (size_t)sg.hk * g;
-            const uint32_t dst = base + L.q + (uint32_t)(buf * p.q_pieces) * kTile;
-            const uint32_t fdst = base + L.fac + 512u * (nth & 1);
+            const uint32_t dst = base + L.q + (uint32_t)(buf * p.q_pieces) * D::kQPiece;
+            const uint32_t fdst = base + L.sc + (uint32_t)((nth & 1) * R) * 4u;
+            const float ks = p.k_scales != nullptr ? __ldg(p.k_scales + sg.hk) : 0.f;
             constexpr int kBatch = 4;  // rows in flight per lane group
             bool ready = false;
 #pragma unroll 1
-            for (int first = row0; first - row0 < rp; first += 4 * RPI * kBatch) {
+            for (int first = row0; first - row0 < R; first += 4 * RPI * kBatch) {
                 uint4 raw[kBatch];
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
@@ -730,24 +816,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
                 for (int k = 0; k < kBatch; ++k) {
                     const int row = first + 4 * RPI * k;
-                    if (row - lane / LPR >= rp) break;  // uniform: rp is a multiple of a round's rows
+                    if (row - lane / LPR >= R) break;  // uniform: R is a multiple of a round's rows
                     const uint4 rw = k == 0 ? raw[0] : k == 1 ? raw[1] : k == 2 ? raw[2] : raw[3];
+                    // log2 scale of this row's logits, but for the pieces' power of two.
+                    float scale = p.sm_scale_log2;
+                    if (p.k_scales != nullptr) {
+                        const int qh = sg.hk * g + row % g;
+                        scale = fold_scale_log2(p.sm_scale, p.q_scales != nullptr ? __ldg(p.q_scales + qh) : 1.0f, ks);
+                    }
                     if constexpr (k2) {
-                        for (int c = 0; c < 1 << cl; ++c) {
-                            const int r2 = row + c * rp;
-                            sts128(dst + (e >> 3) * kHalf + r2 * 128u + (uint32_t)(((e & 7) ^ (r2 & 7)) << 4), rw.x, rw.y, rw.z,
-                                   rw.w);
-                            if (e == 0) sts_f(fdst + 4u * r2, 1.f);
-                        }
+                        sts128(dst + (e >> 3) * (R * 128u) + row * 128u + (uint32_t)(((e & 7) ^ (row & 7)) << 4), rw.x, rw.y, rw.z,
+                               rw.w);
+                        if (e == 0) sts_f(fdst + 4u * row, scale);
                         continue;
                     }
                     // An eight-byte element group's place in a piece's tile row.
                     const uint32_t at = DH == 128 ? row * 128u + (uint32_t)(((e >> 1) ^ (row & 7)) << 4) + 8u * (e & 1)
                                                   : row * 64u + (uint32_t)(((e >> 1) ^ ((row >> 1) & 3)) << 4) + 8u * (e & 1);
-                    const uint32_t copy_bytes = (uint32_t)rp * DH;
                     float fac = 1.f;
                     if (q1) {
-                        for (int c = 0; c < 1 << cl; ++c) sts64(dst + at + c * copy_bytes, rw.x, rw.y);
+                        sts64(dst + at, rw.x, rw.y);
                     } else {
                         const bool bf = p.q_dtype == PAFP8_BF16;
                         const uint32_t w[4] = {rw.x, rw.y, rw.z, rw.w};
@@ -781,16 +869,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 pr[i] = e4m3_pair(x[2 * i], x[2 * i + 1]);
-                                const float2 b = e4m3_back(pr[i]);
+                                const float2 b = __half22float2(half2_of_e4m3(pr[i]));
                                 x[2 * i] -= b.x;
                                 x[2 * i + 1] -= b.y;
                             }
-                            for (int c = 0; c < 1 << cl; ++c)
-                                sts64(dst + pc * kTile + at + c * copy_bytes, pr[0] | (pr[1] << 16), pr[2] | (pr[3] << 16));
+                            sts64(dst + pc * D::kQPiece + at, pr[0] | (pr[1] << 16), pr[2] | (pr[3] << 16));
                         }
                     }
-                    if (e == 0)
-                        for (int c = 0; c < 1 << cl; ++c) sts_f(fdst + 4u * (row + c * rp), fac);
+                    // A scale that underflows to zero would turn -inf (unseen) into NaN.
+                    const float sf = scale * fac;
+                    if (e == 0) sts_f(fdst + 4u * row, sf < 1.2e-38f ? 1.2e-38f : sf);
                 }
             }
             fence_async_smem();
@@ -801,117 +889,83 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             return true;
         };
-        if (s_begin < s_end) ok = build_q(s_begin);
-        for (int si = s_begin; si < s_end && ok; ++si) {
-            if (si + 1 < s_end && !(ok = build_q(si + 1))) break;
+        for (int sq = s_begin; sq <= s_end && s_begin < s_end; ++sq) {  // Q of segment sq, epilogue of the one before
+            if (sq < s_end && !(ok = build_q(sq))) break;
+            if (sq == s_begin) continue;
+            const int si = sq - 1;
             const Seg sg = load_seg(segs, si);
-            const int nth = si - s_begin;
+            const int nth = si - s_begin, ob = nth % NOB;
             const int rows = min(TQ, sg.qo_len - sg.t0) * g;
-            const int cl = copies_log2(rows), rp = 128 >> cl, C = 1 << cl;
-            const float vsc = p.v_scales != nullptr ? __ldg(p.v_scales + sg.hk) : p.v_scale;
-            if (!(ok = wait_all(tState + (nth & 1), (uint32_t)((nth >> 1) & 1)))) break;
-            const uint32_t ml = base + L.ml + 1536u * (nth & 1);
-            auto state_m = [&](int x) { return lds_f(ml + 4u * x); };
-            auto state_l = [&](int x) { return lds_f(ml + 512u + 4u * x) + lds_f(ml + 1024u + 4u * x); };
-            // Row `row` over its copies: the largest maximum M, the sum L at M.
-            auto joined = [&](int row, float& M, float& Lsum) {
-                M = state_m(row);
-                for (int c = 1; c < C; ++c) M = fmaxf(M, state_m(row + c * rp));
-                Lsum = 0.f;
-                const float m0 = M == -INFINITY ? 0.f : M;
-                for (int c = 0; c < C; ++c) Lsum += ex2(state_m(row + c * rp) - m0) * state_l(row + c * rp);
-            };
-            float M, Ls;
-            joined(r & (rp - 1), M, Ls);
-            const float m0 = M == -INFINITY ? 0.f : M;
             const bool whole = sg.slot < 0;
-            // Weight of this lane's O: its copy's share, 1 / L, v_scale in the end.
-            const float wgt = Ls == 0.f ? 0.f : ex2(state_m(r) - m0) / Ls * (whole ? vsc : 1.f);
-            if (!(ok = wait_all(tOFull, (uint32_t)(nth & 1)))) break;
+            const float vsc = p.v_scales != nullptr ? __ldg(p.v_scales + sg.hk) : p.v_scale;
+            const size_t head0 = (size_t)(sg.qo0 + sg.t0) * p.num_qo_heads + (size_t)sg.hk * g;
+            const size_t prow0 = (size_t)max(sg.slot, 0) * p.rows_pad;
+            const uint32_t wt = base + L.wt + (uint32_t)((nth & 1) * R) * 4u;
+            if (!(ok = wait_all(tState + (nth & 1), (uint32_t)((nth >> 1) & 1)))) break;
+            if (d < R) {  // row d's sum and weight
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum += lds_f(base + L.lsum + 4u * (((nth & 1) * 4 + i) * R + d));
+                sts_f(wt + 4u * d, sum == 0.f ? 0.f : (whole ? vsc : 1.f) / sum);
+                if (d < rows) {
+                    const float lse2 = sum == 0.f ? -INFINITY : lds_f(base + L.mst + 4u * ((nth & 1) * R + d)) - kShift + __log2f(sum);
+                    if (!whole)
+                        p.part_lse[prow0 + d] = lse2;
+                    else if (p.lse != nullptr)
+                        p.lse[head0 + (size_t)(d / g) * p.num_qo_heads + d % g] = lse2 * 0.69314718055994531f;
+                }
+            }
+            warp_arrive(bar(tHelp));
+            if (!(ok = wait_all(tHelp, help_phase))) break;
+            help_phase ^= 1u;
+            if (!(ok = wait_all(tOFull + ob, (uint32_t)((nth / NOB) & 1)))) break;
             tc_fence_after();
-            const int row_o = r >> cl;  // the row this thread writes out, and its dims of each 32
-            const int nd = 32 >> cl, d0 = (r & (C - 1)) * nd;
-            const bool live = row_o < rows;
-            const int tok = live ? row_o / g : 0, hh = live ? row_o - tok * g : 0;
-            const size_t orow = (size_t)(sg.qo0 + sg.t0 + tok) * p.num_qo_heads + (size_t)sg.hk * g + hh;
-            const size_t prow = (size_t)max(sg.slot, 0) * p.rows_pad + (live ? row_o : 0);
+            const uint32_t tO = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + D::kColO + (uint32_t)(D::OC * ob);
+            // Rows 16 at a time, a warp writing 32 dims of each: 64 bytes of o, or 128
+            // of a partial state.
+            int hh = 0;
+            uint16_t* dst = static_cast<uint16_t*>(p.o) + head0 * DH + d;
+            float* part = p.part_o + prow0 * DH + d;
 #pragma unroll 1
-            for (int c = 0; c < DH / 32; ++c) {
-                uint32_t hi[32];
-                tc_ld32(tO + 32 * c, hi);
+            for (int r0 = 0; r0 < rows; r0 += 16) {
+                uint32_t o[16];
+                tc_ld16(tO + r0, o);
                 if constexpr (!k2) {
-                    uint32_t lo[32];
-                    tc_ld32(tO + DH + 32 * c, lo);
+                    uint32_t lo[16];
+                    tc_ld16(tO + R + r0, lo);
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        hi[i] = __float_as_uint(fmaf(__uint_as_float(lo[i]), 1.f / 32.f, __uint_as_float(hi[i])));
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = __float_as_uint(fmaf(__uint_as_float(lo[i]), 1.f / 32.f, __uint_as_float(o[i])));
                 } else {
                     tc_wait_ld();
                 }
-                if (c + 1 == DH / 32) {  // O is read: the next segment may write it
+                if (r0 + 16 >= rows) {  // O is read: another segment may write the buffer
                     tc_fence_before();
-                    warp_arrive(bar(tOEmpty));
+                    warp_arrive(bar(tOEmpty + ob));
                 }
+                if (DH == 64 && d >= 64) continue;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) hi[i] = Ls == 0.f ? 0u : __float_as_uint(__uint_as_float(hi[i]) * wgt);
-                if (C > 1) {
-                    // The copies meet in shared memory: every row's 32 dims of each,
-                    // then each thread sums its 32 / C dims of one row.
-                    const uint32_t stg = base + L.stage;
+                for (int i4 = 0; i4 < 4; ++i4) {
+                    const float4 w4 = lds_f4(wt + 4u * (r0 + 4 * i4));
+                    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        sts128(stg + (uint32_t)(r * kStageRow + 4 * i) * 4u, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                    warp_arrive(bar(tStage));
-                    if (!(ok = wait_all(tStage, stage_phase))) break;
-                    stage_phase ^= 1u;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {  // up to 16 dims, four at a time
-                        if (4 * q < nd) {
-                            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                            for (int k = 0; k < C; ++k) {
-                                const float4 x = lds_f4(stg + (uint32_t)((row_o + k * rp) * kStageRow + d0 + 4 * q) * 4u);
-                                s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+                    for (int i = 0; i < 4; ++i) {
+                        if (r0 + 4 * i4 + i >= rows) break;
+                        const float x = w[i] == 0.f ? 0.f : __uint_as_float(o[4 * i4 + i]) * w[i];
+                        if (whole) {
+                            *dst = (uint16_t)(pack_out2(x, 0.f, p.o_dtype) & 0xFFFFu);
+                            dst += DH;
+                            if (++hh == g) {
+                                hh = 0;
+                                dst += (size_t)(p.num_qo_heads - g) * DH;
                             }
-                            hi[4 * q] = __float_as_uint(s.x), hi[4 * q + 1] = __float_as_uint(s.y);
-                            hi[4 * q + 2] = __float_as_uint(s.z), hi[4 * q + 3] = __float_as_uint(s.w);
+                        } else {
+                            *part = x;
+                            part += DH;
                         }
                     }
-                    warp_arrive(bar(tStage));  // staging may be written again
-                    if (!(ok = wait_all(tStage, stage_phase))) break;
-                    stage_phase ^= 1u;
                 }
-                if (live) {
-                    const int d = 32 * c + d0;
-                    if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * DH + d);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (8 * i < nd) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    w[k] = pack_out2(__uint_as_float(hi[8 * i + 2 * k]), __uint_as_float(hi[8 * i + 2 * k + 1]),
-                                                     p.o_dtype);
-                                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * DH + d);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (4 * i < nd) dst[i] = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                    }
-                }
-            }
-            if (!ok) break;
-            if (live && d0 == 0) {
-                float Mo, Lo;
-                joined(row_o, Mo, Lo);
-                const float lse2 = Lo == 0.f ? -INFINITY : Mo - PShift<KT>::kShift + __log2f(Lo);
-                if (!whole)
-                    p.part_lse[prow] = lse2;
-                else if (p.lse != nullptr)
-                    p.lse[orow] = lse2 * 0.69314718055994531f;
             }
         }
     }
@@ -921,7 +975,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     __syncthreads();
     if (warp == 13) {
         tc_fence_after();
-        tc_dealloc(tmem, 512);
+        tc_dealloc(tmem, D::kCols);
     }
 }
 
@@ -983,21 +1037,20 @@ __global__ void __launch_bounds__(32 * kTreeMergeWarps) tree_merge_kernel(const 
     if (lane == 0 && p.lse != nullptr) p.lse[orow] = (m + __log2f(sum)) * 0.69314718055994531f;
 }
 
-template <int KT, int NP, int DH>
+template <int KT, int NP, int DH, int R>
 cudaError_t launch_tree_t(TreeParams p, const CUtensorMap& tk, const CUtensorMap& tv, int num_ctas, int num_merge,
                           cudaStream_t stream) {
-    constexpr bool k2 = KT == PAFP8_BF16 || KT == PAFP8_F16;
-    constexpr uint32_t tile = kTileKeys * DH * (k2 ? 2 : 1);
-    // Two Q buffers (the next segment's Q is built during the current one)
-    // unless three pieces of 16 KB leave too little for the K and V ring.
-    p.q_buffers = p.q_pieces * tile > 40960 ? 1 : 2;
-    const uint32_t q_bytes = (uint32_t)(p.q_buffers * p.q_pieces) * tile;
+    using D = TreeDims<KT, NP, DH, R>;
     constexpr uint32_t budget = 232448 - 1024;
+    // Two Q buffers (the next segment's Q is built during the current one) if
+    // the ring keeps three stages of K and V, or two of a 2-byte cache.
+    p.q_buffers = tree_smem<D, R, NP>(2 * p.q_pieces, D::k2 ? 2 : 3).bytes <= budget ? 2 : 1;
     int stages = 2;
-    while (stages < kMaxStages && tree_smem(q_bytes, tile, stages + 1).bytes <= budget) ++stages;
+    while (stages < kMaxStages && tree_smem<D, R, NP>(p.q_buffers * p.q_pieces, stages + 1).bytes <= budget) ++stages;
     p.stages = stages;
-    const size_t smem = 1024 + tree_smem(q_bytes, tile, stages).bytes;
-    auto kern = tree_kernel<KT, NP, DH>;
+    const size_t smem = 1024 + tree_smem<D, R, NP>(p.q_buffers * p.q_pieces, stages).bytes;
+    if (smem > 232448) return cudaErrorInvalidValue;
+    auto kern = tree_kernel<KT, NP, DH, R>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kern<<<num_ctas, kTreeThreads, smem, stream>>>(p, tk, tv);
@@ -1014,17 +1067,17 @@ cudaError_t launch_tree_t(TreeParams p, const CUtensorMap& tk, const CUtensorMap
     return cudaLaunchKernelEx(&cfg, tree_merge_kernel<DH>, p);
 }
 
-template <int DH>
-cudaError_t launch_tree_head(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int num_ctas,
+template <int DH, int R>
+cudaError_t launch_tree_rows(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int num_ctas,
                              int num_merge, cudaStream_t stream) {
     switch (p.kv_dtype) {
-        case PAFP8_F16: return launch_tree_t<PAFP8_F16, 1, DH>(p, tk, tv, num_ctas, num_merge, stream);
-        case PAFP8_BF16: return launch_tree_t<PAFP8_BF16, 1, DH>(p, tk, tv, num_ctas, num_merge, stream);
+        case PAFP8_F16: return launch_tree_t<PAFP8_F16, 1, DH, R>(p, tk, tv, num_ctas, num_merge, stream);
+        case PAFP8_BF16: return launch_tree_t<PAFP8_BF16, 1, DH, R>(p, tk, tv, num_ctas, num_merge, stream);
         default: break;
     }
     // An f16 output keeps 11 bits: three pieces of P.
-    return p.o_dtype == PAFP8_F16 ? launch_tree_t<PAFP8_E4M3FN, 3, DH>(p, tk, tv, num_ctas, num_merge, stream)
-                                  : launch_tree_t<PAFP8_E4M3FN, 2, DH>(p, tk, tv, num_ctas, num_merge, stream);
+    return p.o_dtype == PAFP8_F16 ? launch_tree_t<PAFP8_E4M3FN, 3, DH, R>(p, tk, tv, num_ctas, num_merge, stream)
+                                  : launch_tree_t<PAFP8_E4M3FN, 2, DH, R>(p, tk, tv, num_ctas, num_merge, stream);
 }
 
 }  // namespace
