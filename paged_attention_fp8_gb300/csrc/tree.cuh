@@ -77,6 +77,7 @@ using namespace ptx;
 
 constexpr int kTreeThreads = 512;
 constexpr int kMaxStages = 8;
+constexpr int kSegCache = 32;  // segment records kept in shared memory
 // Reference maxima rise when some P' would pass 2^(kShift + kHead).
 template <int KT>
 struct PShift {  // fp8 pieces: P' <= 2^8, e4m3 reaches 448
@@ -117,7 +118,7 @@ struct TreeDims {
 };
 
 struct TreeSmem {
-    uint32_t q, k, v, p, sc, neg, wmax, lsum, mst, wt, vote, bars, tmem_slot, abort_flag, bytes;
+    uint32_t q, k, v, p, sc, neg, wmax, alpha, lsum, mst, wt, seg, vote, bars, tmem_slot, abort_flag, bytes;
 };
 enum TreeBar : int {
     tQFull = 0,              // [2]
@@ -147,10 +148,12 @@ __host__ __device__ inline TreeSmem tree_smem(int q_tiles, int stages) {
     s.sc = s.p + D::NPB * NP * D::kPPiece;  // [2][R] floats: log2 scale of each row
     s.neg = s.sc + 2 * R * 4;               // [8 warps][NCOL]: kShift - reference maximum
     s.wmax = s.neg + 8 * D::NCOL * 4;       // [2][half][4 quadrants][NC]
-    s.lsum = s.wmax + 2 * 2 * 4 * D::NC * 4;  // [2][4][R]
+    s.alpha = s.wmax + 2 * 2 * 4 * D::NC * 4;  // [8 warps][NC]
+    s.lsum = s.alpha + 8 * D::NC * 4;       // [2][4][R]
     s.mst = s.lsum + 2 * 4 * R * 4;         // [2][R]
     s.wt = s.mst + 2 * R * 4;               // [2][R]
-    s.vote = s.wt + 2 * R * 4;              // [half][2] words
+    s.seg = s.wt + 2 * R * 4;               // the CTA's first kSegCache segment records
+    s.vote = s.seg + kSegCache * kTreeSegWords * 4;  // [half][2] words
     s.bars = s.vote + 16;
     s.tmem_slot = s.bars + 8 * tNumBars;
     s.abort_flag = s.tmem_slot + 4;
@@ -209,9 +212,21 @@ struct Seg {
     int hk, t0, tile0, tile1, slot;  // slot: partial state, or -1 for a whole line
     int qo0, qo_len, kv_len, page0;
 };
-__device__ __forceinline__ Seg load_seg(const int* segs, int i) {
-    const int4* r = reinterpret_cast<const int4*>(segs + kTreeSegWords * (long long)i);
-    const int4 a = __ldg(r), b = __ldg(r + 1), c = __ldg(r + 2);
+// The CTA's segment i (of its own list): from shared memory, or from global
+// memory behind the first kSegCache.  A record is at the head of every role's
+// work on a segment; from L2 each cost about a microsecond there.
+__device__ __forceinline__ Seg load_seg(const int* segs, uint32_t cache, int i) {
+    int4 a, b, c;
+    if (i < kSegCache) {
+        const uint32_t r = cache + (uint32_t)(kTreeSegWords * 4 * i);
+        const uint4 x = lds128(r), y = lds128(r + 16), z = lds128(r + 32);
+        a = make_int4((int)x.x, (int)x.y, (int)x.z, (int)x.w);
+        b = make_int4((int)y.x, (int)y.y, (int)y.z, (int)y.w);
+        c = make_int4((int)z.x, 0, 0, 0);
+    } else {
+        const int4* r = reinterpret_cast<const int4*>(segs + kTreeSegWords * (long long)i);
+        a = __ldg(r), b = __ldg(r + 1), c = __ldg(r + 2);
+    }
     return Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x};
 }
 
@@ -266,6 +281,7 @@ __device__ __forceinline__ void e4m3_pieces(const float* x, uint32_t& hi, uint32
     if constexpr (NP == 3) lo2 = prmt(c[0], c[1], 0x5410u);
 }
 
+// 16 or 32 columns of this thread's TMEM lane; the values are there after tc_wait_ld.
 template <int NC>
 __device__ __forceinline__ void ld_cols(uint32_t t, float (&v)[NC]) {
     if constexpr (NC == 16) {
@@ -274,7 +290,15 @@ __device__ __forceinline__ void ld_cols(uint32_t t, float (&v)[NC]) {
 #pragma unroll
         for (int c = 0; c < NC / 32; ++c) tc_ld32(t + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
     }
-    tc_wait_ld();
+}
+template <int NC>
+__device__ __forceinline__ void st_cols(uint32_t t, const float (&v)[NC]) {
+    if constexpr (NC == 16) {
+        tc_st16(t, reinterpret_cast<const uint32_t(&)[16]>(v));
+    } else {
+#pragma unroll
+        for (int c = 0; c < NC / 32; ++c) tc_st32(t + 32 * c, *reinterpret_cast<const uint32_t(*)[32]>(v + 32 * c));
+    }
 }
 
 // Sums of v[c] over the warp's lanes: lane l returns column l's (of 32; of 16,
@@ -317,9 +341,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int NS = p.stages, NQB = p.q_buffers;
     const int* meta = p.meta;
-    const int s_begin = __ldg(meta + meta[kMetaOffCtaSeg] + blockIdx.x);
-    const int s_end = __ldg(meta + meta[kMetaOffCtaSeg] + blockIdx.x + 1);
-    const int* segs = meta + meta[kMetaOffSeg];
+    const int s_first = __ldg(meta + meta[kMetaOffCtaSeg] + blockIdx.x);
+    const int n_seg = __ldg(meta + meta[kMetaOffCtaSeg] + blockIdx.x + 1) - s_first;
+    const int* segs = meta + meta[kMetaOffSeg] + kTreeSegWords * (long long)s_first;
+    const uint32_t seg_cache = base + L.seg;
     const int g = p.group, TQ = kTileRows / g;
     const uint32_t hint = p.wait_cycles < kWaitCyclesDefault ? 0u : 20000u;
     auto wait = [&](int b, uint32_t parity) { return tree_wait(bar(b), parity, flag, p.status, p.wait_cycles, hint); };
@@ -349,12 +374,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         asm volatile("st.shared.u32 [%0], 0;" ::"r"(flag) : "memory");
         mbar_init_fence();
     }
+    for (int i = threadIdx.x; i < min(n_seg, kSegCache) * kTreeSegWords; i += kTreeThreads)
+        sts32(seg_cache + 4u * i, (uint32_t)__ldg(segs + i));
     if (warp == 13) tc_alloc(base + L.tmem_slot, D::kCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t tmem = lds_u(base + L.tmem_slot);
+    const uint32_t tmem = lds_u(base + L.tmem_slot);  // (the records and barriers above are visible from here on)
 
     if (warp >= 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
@@ -376,8 +403,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true, k_only = false;
-        for (int si = s_begin; si < s_end && ok; ++si) {
-            const Seg sg = load_seg(segs, si);
+        for (int si = 0; si < n_seg && ok; ++si) {
+            const Seg sg = load_seg(segs, seg_cache, si);
             const int m = p.page_mult;
             const int nsub = (sg.kv_len + kPageSize - 1) / kPageSize;  // 16-token sub-pages of the request
             const int* idx = p.kv_indices + sg.page0;
@@ -449,10 +476,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t idesc_pv = make_idesc_mn(kvf, k2 ? kvf : 0, 128, D::OC);
         const uint32_t idesc_p3 = make_idesc_mn(kvf, 0, 128, R);
         const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-        const int sb0 = __shfl_sync(0xFFFFFFFFu, s_begin, 0), sb1 = __shfl_sync(0xFFFFFFFFu, s_end, 0);
+        const int n_seg_u = __shfl_sync(0xFFFFFFFFu, n_seg, 0);
         auto tiles_of = [&](int si) -> int {
-            const int2 t = __ldg(reinterpret_cast<const int2*>(segs + kTreeSegWords * (long long)si + 2));
-            return __shfl_sync(0xFFFFFFFFu, t.y - t.x, 0);
+            const Seg sg = load_seg(segs, seg_cache, si);
+            return __shfl_sync(0xFFFFFFFFu, sg.tile1 - sg.tile0, 0);
         };
         // Descriptors: the constant halves, and the words of the tiles at offset 0.
         constexpr uint64_t kQKd = (k2 || DH == 128) ? 1 : 0;  // 128-byte rows, else 64
@@ -463,22 +490,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t k_lo = (uint32_t)qk_proto + ((base + L.k) >> 4), q_lo = (uint32_t)qk_proto + ((base + L.q) >> 4);
         const uint32_t v_lo = (uint32_t)v_proto + ((base + L.v) >> 4), p_lo = (uint32_t)p_proto + ((base + L.p) >> 4);
         bool ok = true;
-        int qs = sb0, qn = 0, qbuf = 0;  // QK's segment, tile count and Q buffer
+        int qs = 0, qn = 0, qbuf = 0;  // QK's segment, tile count and Q buffer
         uint32_t qphase = 0;
         int kstage = 0, vstage = 0;
         uint32_t kphase = 0, vphase = 0;
-        int qleft = qs < sb1 ? tiles_of(qs) : 0;
+        int qleft = n_seg_u > 0 ? tiles_of(0) : 0;
         bool qfirst = true;
         int pn = 0;
-        for (int ps = sb0; ps < sb1 && ok; ++ps) {
-            const int nth = ps - sb0, ob = nth % NOB;
+        for (int ps = 0; ps < n_seg_u && ok; ++ps) {
+            const int nth = ps, ob = nth % NOB;
             const int nt = tiles_of(ps);
             for (int t = 0; t < nt; ++t, ++pn) {
                 // QK(j + 1) goes before PV(j), into the next segment at most (the Q of
                 // the one after is built only when this one's epilogue is done).  So
                 // QK(j) follows PV(j - 2), which waited for P(j - 2): S(j - 2) has been
                 // read, and once S(j) is complete so is PV(j - 2), P's buffer free.
-                while (qs < sb1 && qn <= pn + 1 && qs <= ps + 1) {
+                while (qs < n_seg_u && qn <= pn + 1 && qs <= ps + 1) {
                     const int sb = qn & 1;
                     if (qfirst) {
                         if (!(ok = wait_all(tQFull + qbuf, qphase))) break;
@@ -516,7 +543,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             qphase ^= 1u;
                         }
                         qfirst = true;
-                        if (++qs < sb1) qleft = tiles_of(qs);
+                        if (++qs < n_seg_u) qleft = tiles_of(qs);
                     }
                 }
                 if (!ok) break;
@@ -575,15 +602,30 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         uint32_t vphase = 0;
         uint32_t hphase = 0, wbuf = 0, ballots = 0;
         bool ok = true;
-        for (int si = s_begin; si < s_end && ok; ++si) {
-            const Seg sg = load_seg(segs, si);
-            const int nth = si - s_begin;
+        for (int si = 0; si < n_seg && ok; ++si) {
+            const Seg sg = load_seg(segs, seg_cache, si);
+            const int nth = si;
             const int ntok = min(TQ, sg.qo_len - sg.t0);
             const int ctx = sg.kv_len - sg.qo_len;
             const uint32_t tO = lane_base + D::kColO + (uint32_t)(D::OC * (nth % NOB));
             f32x2 l[NCOL / 2];
 #pragma unroll
             for (int i = 0; i < NCOL / 2; ++i) l[i] = make_f32x2(0.f, 0.f);
+            // Mask bits of this warp's 32 keys of a tile, lane i holding those of row
+            // i's token, fetched a tile ahead.
+            const uint32_t* mrow[NSUB];
+#pragma unroll
+            for (int i = 0; i < NSUB; ++i)
+                mrow[i] = p.tree_mask + (long long)(sg.qo0 + sg.t0 + min((half * NCOL + i * NC + lane) / g, ntok - 1)) * p.mask_words;
+            uint32_t bits[NSUB];
+            auto fetch_bits = [&](int t) {
+#pragma unroll
+                for (int i = 0; i < NSUB; ++i)
+                    bits[i] = (t + 1) * kTileKeys > ctx
+                                  ? mask_bits(mrow[i], t * kTileKeys + 32 * quad - ctx, p.mask_words, sg.qo_len)
+                                  : 0xFFFFFFFFu;
+            };
+            fetch_bits(sg.tile0);
             if (!(ok = wait_all(tInfo + (nth & 1), (uint32_t)((nth >> 1) & 1)))) break;
             for (int t = sg.tile0; t < sg.tile1 && ok; ++t, ++j) {
                 const bool first = t == sg.tile0;
@@ -598,25 +640,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     const uint32_t sct = base + L.sc + (uint32_t)((nth & 1) * R + cb) * 4u;
                     const uint32_t negt = base + L.neg + (uint32_t)(warp * NCOL + sub * NC) * 4u;
                     float v[NC];
-                    // The logits; those of keys that a row does not see become -inf.  Lane i
-                    // fetches 32 keys' mask bits of row i's token.
-                    auto load = [&]() {
-                        ld_cols<NC>(tS, v);
-                        if ((t + 1) * kTileKeys <= ctx) return;
-                        const int tok = min((cb + lane) / g, ntok - 1);
-                        const uint32_t bits = mask_bits(p.tree_mask + (long long)(sg.qo0 + sg.t0 + tok) * p.mask_words,
-                                                        t * kTileKeys + 32 * quad - ctx, p.mask_words, sg.qo_len);
-#pragma unroll
-                        for (int c = 0; c < NC; ++c)
-                            if (!((__shfl_sync(0xFFFFFFFFu, bits, c) >> lane) & 1u)) v[c] = -INFINITY;
-                    };
                     // P' in place of the logits.  The vote on the reference maxima is cast
                     // before the exponentials and read after P is stored, so its
                     // latency passes meanwhile; a raised reference redoes the pass.
                     bool rise = first;
 #pragma unroll 1
                     while (true) {
-                        load();
+                        ld_cols<NC>(tS, v);
+                        tc_wait_ld();
+                        if ((t + 1) * kTileKeys > ctx) {  // keys that a row does not see become -inf
+#pragma unroll
+                            for (int c = 0; c < NC; ++c)
+                                if (!((__shfl_sync(0xFFFFFFFFu, bits[sub], c) >> lane) & 1u)) v[c] = -INFINITY;
+                        }
                         if (rise) {
                             // Column maxima of the tile: over this warp's lanes, then over the
                             // four warps of the half.  Lane i settles row i.
@@ -639,30 +675,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             const float m_old = was >= kUnseen ? -INFINITY : kShift - was;
                             const float m_new = fmaxf(m_old, top);
                             const float alpha = m_old == -INFINITY ? 0.f : ex2(m_old - m_new);
-                            __syncwarp();
-                            if (lane < NC) sts_f(negt + 4u * c, m_new == -INFINITY ? kUnseen : kShift - m_new);
+                            const uint32_t alt = base + L.alpha + (uint32_t)(warp * NC) * 4u;
+                            if (lane < NC) {
+                                sts_f(alt + 4u * c, alpha);
+                                sts_f(negt + 4u * c, m_new == -INFINITY ? kUnseen : kShift - m_new);
+                            }
                             __syncwarp();
                             if (!first) {
                                 // Every O update of the earlier tiles has to be complete.
                                 if (!(ok = wait_all(tVEmpty + (stage == 0 ? NS - 1 : stage - 1), stage == 0 ? vphase ^ 1u : vphase)))
                                     break;
                                 tc_fence_after();
-#pragma unroll
-                                for (int i = 0; i < NC; i += 2)
-                                    l[(sub * NC + i) / 2] =
-                                        mul2(l[(sub * NC + i) / 2], make_f32x2(__shfl_sync(0xFFFFFFFFu, alpha, i),
-                                                                             __shfl_sync(0xFFFFFFFFu, alpha, i + 1)));
 #pragma unroll 1
-                                for (int at = 0; at < (k2 ? NC : 2 * NC); at += 16) {  // O_hi, then O_lo
-                                    const int c0 = at & (NC - 1);
-                                    const uint32_t to = tO + (uint32_t)((at >= NC ? R : 0) + cb + c0);
-                                    uint32_t o[16];
-                                    tc_ld16(to, o);
+                                for (int part = 0; part < (k2 ? 1 : 2); ++part) {  // O_hi, then O_lo
+                                    const uint32_t to = tO + (uint32_t)(part * R + cb);
+                                    float o[NC];
+                                    ld_cols<NC>(to, o);
                                     tc_wait_ld();
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xFFFFFFFFu, alpha, c0 + i));
-                                    tc_st16(to, o);
+                                    for (int i = 0; i < NC; i += 4) {
+                                        const float4 a = lds_f4(alt + 4u * i);
+                                        o[i] *= a.x, o[i + 1] *= a.y, o[i + 2] *= a.z, o[i + 3] *= a.w;
+                                    }
+                                    st_cols<NC>(to, o);
+                                }
+#pragma unroll
+                                for (int i = 0; i < NC; i += 4) {
+                                    const float4 a = lds_f4(alt + 4u * i);
+                                    l[(sub * NC + i) / 2] = mul2(l[(sub * NC + i) / 2], make_f32x2(a.x, a.y));
+                                    l[(sub * NC + i) / 2 + 1] = mul2(l[(sub * NC + i) / 2 + 1], make_f32x2(a.z, a.w));
                                 }
                                 tc_wait_st();
                             }
@@ -728,6 +769,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         l[sub * NC / 2 + i] = add2(l[sub * NC / 2 + i], make_f32x2(v[2 * i], v[2 * i + 1]));
                 }
                 if (!ok) break;
+                if (t + 1 < sg.tile1) fetch_bits(t + 1);
                 // Value rows behind the request's end (the tail of its last page and
                 // rows no page filled) hold anything: zero them, P = 0 there must
                 // not meet a NaN.
@@ -778,8 +820,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // a lane; rows of no token are zero.  A compact loop: unrolled over whole
         // rows the code ran once a segment and spent 10 us on instruction fetches.
         auto build_q = [&](int si) -> bool {
-            const Seg sg = load_seg(segs, si);
-            const int nth = si - s_begin, buf = NQB == 2 ? nth & 1 : 0;
+            const Seg sg = load_seg(segs, seg_cache, si);
+            const int nth = si, buf = NQB == 2 ? nth & 1 : 0;
             const int use = NQB == 2 ? nth >> 1 : nth;  // earlier uses of this buffer
             const int rows = min(TQ, sg.qo_len - sg.t0) * g;
             constexpr int LPR = DH / 8, RPI = 32 / LPR;  // lanes a row, rows a warp's round
@@ -889,12 +931,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             return true;
         };
-        for (int sq = s_begin; sq <= s_end && s_begin < s_end; ++sq) {  // Q of segment sq, epilogue of the one before
-            if (sq < s_end && !(ok = build_q(sq))) break;
-            if (sq == s_begin) continue;
+        for (int sq = 0; sq <= n_seg && n_seg > 0; ++sq) {  // Q of segment sq, epilogue of the one before
+            if (sq < n_seg && !(ok = build_q(sq))) break;
+            if (sq == 0) continue;
             const int si = sq - 1;
-            const Seg sg = load_seg(segs, si);
-            const int nth = si - s_begin, ob = nth % NOB;
+            const Seg sg = load_seg(segs, seg_cache, si);
+            const int nth = si, ob = nth % NOB;
             const int rows = min(TQ, sg.qo_len - sg.t0) * g;
             const bool whole = sg.slot < 0;
             const float vsc = p.v_scales != nullptr ? __ldg(p.v_scales + sg.hk) : p.v_scale;
