@@ -134,6 +134,7 @@ struct pafp8_plan {
     int page_mult = 1;
     std::vector<int32_t> vptr;
     int num_ctas = 0, num_partials = 0, num_merge = 0;
+    int tile_rows = 0;   // tree: rows a row tile may have (32 or 64)
     int rows_pad = 0;    // tree: rows of the largest row tile
     int mask_words = 0;  // tree: words the longest draft needs
     size_t meta_bytes = 0, part_o_off = 0, part_lse_off = 0, status_off = 0, ws_bytes = 0;
@@ -472,32 +473,36 @@ void build_prefill_meta(pafp8_plan* pl) {
     pl->num_merge = 0;
 }
 
-// Tree partition.  A line is a (request, row tile of 128 / group tokens) pair,
-// its cost its 128-key tiles plus kTreeSegCost for starting it.  Heads are
-// dealt to CTAs in blocks of hb (a divisor of the KV heads): the lines, laid
-// end to end once per head block, are cut into num_ctas / hb ranges of equal
-// cost, and CTA i * hb + h takes range i for head h of the block, so the CTAs
-// reading the heads of one token-major page run at the same time.  hb is the
-// largest divisor whose busiest CTA is within 3 % of the best one's.  A
-// segment that is not its whole line has a slot for its partial state; a
-// split line's slots are consecutive.
+// Tree partition.  A line is a (request, row tile) pair -- the request's rows
+// (token, head of the group) cut into tiles of tile_rows --, its cost its
+// 128-key tiles plus kTreeSegCost for starting it.  Heads are dealt to CTAs in
+// blocks of hb (a divisor of the KV heads): the lines, laid end to end once per
+// head block, are cut into num_ctas / hb ranges of equal cost, and CTA i * hb +
+// h takes range i for head h of the block, so the CTAs reading the heads of one
+// token-major page run at the same time.  hb is the largest divisor whose
+// busiest CTA is within 3 % of the best one's.  A segment that is not its whole
+// line has a slot for its partial state; a split line's slots are consecutive.
 constexpr int kTreeSegCost = 1;
 void build_tree_meta(pafp8_plan* pl) {
     const int B = pl->desc.batch, hkv = pl->desc.num_kv_heads, g = pl->group;
-    const int TQ = kTileRows / g;
-    struct Line { int32_t b, t0, nt; };
+    struct Line { int32_t b, r0, nt; };
     std::vector<Line> lines;
     int64_t cost = 0;
-    pl->rows_pad = 0;
+    int most = 0;
+    for (int b = 0; b < B; ++b) most = std::max(most, pl->qo_indptr[b + 1] - pl->qo_indptr[b]);
+    pl->mask_words = (most + 31) / 32;
+    // (rows as 64 bits: a draft of millions of tokens times the group)
+    const int64_t most_rows = (int64_t)most * g;
+    const int RT = tree_tile_rows((int)std::min<int64_t>(most_rows, 1 << 20));
+    pl->tile_rows = RT;
+    pl->rows_pad = (int)std::min<int64_t>(most_rows, RT);
     for (int b = 0; b < B; ++b) {
-        const int qo = pl->qo_indptr[b + 1] - pl->qo_indptr[b];
+        const int64_t rows = (int64_t)(pl->qo_indptr[b + 1] - pl->qo_indptr[b]) * g;
         const int32_t n = pl->kv_indptr[b + 1] - pl->kv_indptr[b];
         const int64_t kv = n > 0 ? (int64_t)(n - 1) * pl->desc.page_size + pl->last_page_len[b] : 0;
-        pl->mask_words = std::max(pl->mask_words, (qo + 31) / 32);
-        for (int t0 = 0; t0 < qo; t0 += TQ) {
-            lines.push_back({b, t0, (int32_t)((kv + kTileKeys - 1) / kTileKeys)});
+        for (int64_t r0 = 0; r0 < rows; r0 += RT) {
+            lines.push_back({b, (int32_t)r0, (int32_t)((kv + kTileKeys - 1) / kTileKeys)});
             cost += lines.back().nt + kTreeSegCost;
-            pl->rows_pad = std::max(pl->rows_pad, std::min(TQ, qo - t0) * g);
         }
     }
     int hb = 1;
@@ -563,8 +568,8 @@ void build_tree_meta(pafp8_plan* pl) {
             const int qo = pl->qo_indptr[ln.b + 1] - pl->qo_indptr[ln.b];
             for (int32_t i = 0; i < n; ++i) slot0[k + i] = nslot + i;  // head h of the block: + h n
             for (int h = 0; h < hb; ++h) {
-                const int32_t rec[8] = {nslot + h * n, nslot + (h + 1) * n, pl->qo_indptr[ln.b] + ln.t0,
-                                        parts[k].block * hb + h, std::min(TQ, qo - ln.t0) * g, n, 0, 0};
+                const int32_t rec[8] = {nslot + h * n, nslot + (h + 1) * n, pl->qo_indptr[ln.b], parts[k].block * hb + h,
+                                        std::min(RT, qo * g - ln.r0), ln.r0, 0, 0};
                 merges.insert(merges.end(), rec, rec + 8);
                 ++nmerge;
             }
@@ -581,7 +586,7 @@ void build_tree_meta(pafp8_plan* pl) {
     m[kMetaHeadBlocks] = nhb;
     m[kMetaHeadsPerCta] = hb;
     m[kMetaGroup] = g;
-    m[kMetaTileRows] = TQ;
+    m[kMetaTileRows] = RT;
     const int G = parts.empty() ? 0 : (int)(groups * hb);
     m[kMetaNumCtas] = G;
     m[kMetaNumPartials] = nslot;
@@ -605,7 +610,7 @@ void build_tree_meta(pafp8_plan* pl) {
                     slot = slot0[k] + h * (int32_t)(e - a + 1);
                 }
                 const int32_t n = pl->kv_indptr[ln.b + 1] - pl->kv_indptr[ln.b];
-                const int32_t rec[kTreeSegWords] = {pt.block * hb + h, ln.t0, pt.a, pt.e, slot, pl->qo_indptr[ln.b],
+                const int32_t rec[kTreeSegWords] = {pt.block * hb + h, ln.r0, pt.a, pt.e, slot, pl->qo_indptr[ln.b],
                                                     pl->qo_indptr[ln.b + 1] - pl->qo_indptr[ln.b],
                                                     (n - 1) * pl->desc.page_size + pl->last_page_len[ln.b],
                                                     pl->kv_indptr[ln.b], 0, 0, 0};
@@ -977,6 +982,9 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
                 return fail(PAFP8_ERR_SHAPE, "qo_indptr[0] is %d, not 0", (int)qo_indptr_h[0]);
             const int64_t qo = (int64_t)qo_indptr_h[b + 1] - qo_indptr_h[b];
             const int64_t kv = n > 0 ? (n - 1) * d.page_size + last_page_len_h[b] : 0;
+            if (d.mode == PAFP8_MODE_TREE && qo * group > INT32_MAX)
+                return fail(PAFP8_ERR_UNSUPPORTED, "request %d has %lld rows of %d heads: their product must stay below 2^31",
+                            b, (long long)qo, group);
             if (qo < 0)
                 return fail(PAFP8_ERR_SHAPE, "qo_indptr decreases at request %d (%d -> %d)", b,
                             (int)qo_indptr_h[b], (int)qo_indptr_h[b + 1]);
@@ -1262,7 +1270,7 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
             return st;
         if ((st = encode(&tv, v_cache, d.num_pages, d.num_kv_heads, d.kv_layout, d.head_dim, d.page_size)) != PAFP8_OK)
             return st;
-        const cudaError_t e = tree_launcher(d.head_dim, plan->rows_pad)(tp, tk, tv, plan->num_ctas, plan->num_merge, s);
+        const cudaError_t e = tree_launcher(d.head_dim, plan->tile_rows)(tp, tk, tv, plan->num_ctas, plan->num_merge, s);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return fail(PAFP8_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));

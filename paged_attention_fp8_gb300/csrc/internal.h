@@ -14,7 +14,7 @@ constexpr int kHeadDim = 128;   // head_dim served by this library
 constexpr int kPageSize = 16;   // page_size served by this library
 constexpr int kMaxGroupDecode = 8;
 constexpr int kMaxGroupPrefill = 16;
-constexpr int kMaxGroupTree = 128;  // a row tile holds at least one token
+constexpr int kMaxGroupTree = 128;
 constexpr int kTileRows = 128;   // prefill query rows (token x head) per tile
 constexpr int kTileKeys = 128;   // prefill keys per KV tile (8 pages)
 // Default bound of a kernel's pipeline waits, in SM clock cycles (~1 s).
@@ -38,14 +38,14 @@ enum MetaHeader : int {
     kMetaOffReqKvLen,    // int32[batch]   kv_len of the request
     kMetaOffCtaSeg,      // int32[num_ctas+1] CSR of segments per CTA
     kMetaOffSeg,         // int32[4*num_segs] (row, page_begin, page_end, out_slot); tree: [kTreeSegWords*num_segs]
-                         // hk, t0, tile_begin, tile_end, slot, qo_begin, qo_len, kv_len, page_begin, 0, 0, 0
+                         // hk, first row, tile_begin, tile_end, slot, qo_begin, qo_len, kv_len, page_begin, 0, 0, 0
     kMetaOffMergePtr,    // int32[num_merge+1]
     kMetaOffMergeRow,    // int32[num_merge]
     kMetaOffMergeSlot,   // int32[num_partials]
     kMetaOffReqQo,       // int32[batch+1] qo_indptr (prefill)
     kMetaNumTiles,       // prefill tiles
     kMetaOffTile,        // int32[8*num_tiles] prefill items: b, hk, t0, nkv, qo_begin, qo_len, kv_len, page_begin;
-                         // tree: int32[8*num_merge] split lines: slot0, slot1, first query row, hk, rows, 0, 0, 0
+                         // tree: int32[8*num_merge] split lines: slot0, slot1, qo_begin, hk, rows, first row, 0, 0
     kMetaTileRows,       // packed query rows per prefill tile
     kMetaOffRowMerge,    // int32[rows] merge entry of each decode row, or -1
     kMetaNumChunks,      // decode pages handed out at run time, in chunks
@@ -259,12 +259,13 @@ inline cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tma
 // their partial states.  One translation unit per head size and row count.
 using TreeLaunch = cudaError_t(const TreeParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int num_ctas,
                                int num_merge, cudaStream_t stream);
-TreeLaunch launch_tree_d128_r32, launch_tree_d128_r64, launch_tree_d128_r128;
-TreeLaunch launch_tree_d64_r32, launch_tree_d64_r64, launch_tree_d64_r128;
-// The instantiation for row tiles of up to `rows` rows (of 128).
-inline TreeLaunch* tree_launcher(int head_dim, int rows) {
-    if (head_dim == 64) return rows <= 32 ? launch_tree_d64_r32 : rows <= 64 ? launch_tree_d64_r64 : launch_tree_d64_r128;
-    return rows <= 32 ? launch_tree_d128_r32 : rows <= 64 ? launch_tree_d128_r64 : launch_tree_d128_r128;
+TreeLaunch launch_tree_d128_r32, launch_tree_d128_r64, launch_tree_d64_r32, launch_tree_d64_r64;
+// Rows of a row tile: 32 when every draft fits, else 64 (of which a draft may
+// take several).
+inline int tree_tile_rows(int most_rows) { return most_rows <= 32 ? 32 : 64; }
+inline TreeLaunch* tree_launcher(int head_dim, int tile_rows) {
+    if (head_dim == 64) return tile_rows == 32 ? launch_tree_d64_r32 : launch_tree_d64_r64;
+    return tile_rows == 32 ? launch_tree_d128_r32 : launch_tree_d128_r64;
 }
 
 }  // namespace pafp8

@@ -22,48 +22,56 @@
 //     elements below 2^-10 of the row's largest, which lose 2^-18 of it at
 //     most.
 //   * O^T += V^T P^T takes V as it landed and P as e4m3 pieces from shared
-//     memory: P' = 2^6 p in [0, 256], hi = e4m3(P'), lo = e4m3(32 (P' - hi)),
+//     memory: P' = 2^5 p in [0, 256], hi = e4m3(P'), lo = e4m3(32 (P' - hi)),
 //     side by side along N, so that one MMA reads V once for both and leaves
 //     O_hi and O_lo (O = O_hi + O_lo / 32) in neighbouring columns.  P then
-//     carries 8 significant bits (a bf16's worth, 2^-9 off) down to p = 2^-12
-//     and is never more than 2^-21 of the row's largest off.  An f16 output
+//     carries 8 significant bits (a bf16's worth, 2^-9 off) down to p = 2^-11
+//     and is never more than 2^-20 of the row's largest off.  An f16 output
 //     adds a third piece, e4m3 of what lo left, accumulated onto O_lo: 12 bits.
 //   * A 2-byte cache of the query's dtype runs kind::f16 on Q, K and V as
 //     they are, P rounded to that type.
 //
 // Both products are transposed: keys (of K) and dims (of V) are the 128 rows of
-// the MMAs, query rows their N, so the tensor time follows the row count R (32,
-// 64 or 128, the plan's largest row tile rounded up) instead of always paying
-// for 128 rows.  With query rows as M, a 16-row draft spent 1400 cycles of the
-// tensor pipe per 128-key tile, as much as the tile's HBM time; transposed it
-// is about 500 at R = 32 and 700 at R = 64.  A softmax thread then owns a key
-// and half of the rows, every lane is busy whatever R is, and P is written to
-// shared memory, which frees S right away.
+// the MMAs, query rows their N, so the tensor time follows the row count R (32
+// or 64) instead of always paying for 128 rows.  With query rows as M, a
+// 16-row draft spent 1400 cycles of the tensor pipe per 128-key tile, as much
+// as the tile's HBM time; transposed it is about 500 at R = 32 and 700 at
+// R = 64.  A softmax thread then owns a key, every lane is busy whatever R is,
+// and P is written to shared memory, which frees S right away.  Drafts of more
+// than 64 rows are cut into row tiles of 64: 128 rows at once would take as
+// long as two such tiles.
+//
+// One tile's softmax is a chain of some 2000 cycles (wait, load, scale, exp,
+// convert, store, vote, hand on), longer than a tile's HBM time (1400).  So two
+// groups of four warps take turns, one the even tiles, one the odd ones, each
+// with its own accumulator in TMEM, maxima and sums: nothing passes between
+// them, and the epilogue joins the two states.
 //
 // The running maximum: a row's maximum over a tile lies across 128 lanes, so it
 // is not taken per tile.  P' is formed with the row's reference maximum, and
-// only when some P' would pass 2^8, four times that maximum's (a vote per tile,
+// only when some P' would pass 2^8, eight times that maximum's (a vote per tile,
 // its latency hidden behind the exponentials and the stores of P), are the
 // column maxima taken (redux), O and l rescaled and the tile's P redone; the
 // first tile of a segment always takes them.
 //
-// Work: the plan lays the 128-key tiles of all (request, row tile of 128 /
-// group tokens) lines end to end, cuts them into equal ranges, and gives each
-// range to a group of CTAs, one a KV head, so that the CTAs that read the
-// heads of one token-major page run side by side.  A range's part of a line
-// is a segment; a segment that is not its whole line writes a partial state,
-// and a merge kernel (a programmatic dependent) joins them.
+// Work: the plan lays the 128-key tiles of all (request, row tile) lines end to
+// end, cuts them into equal ranges, and gives each range to a group of CTAs,
+// one a KV head, so that the CTAs that read the heads of one token-major page
+// run side by side.  A range's part of a line is a segment; a segment that is
+// not its whole line writes a partial state, and a merge kernel (a
+// programmatic dependent) joins them.
 //
 // Roles (512 threads; setmaxnreg moves registers to the softmax warps):
-//   warps 0-7   softmax: thread = key 32 (w % 4) + lane of the tile, rows of
-//               half w / 4;
+//   warps 0-3, 4-7  softmax of the even and of the odd tiles: thread = key
+//               32 (w % 4) + lane of the tile;
 //   warps 8-11  helpers: build the next segment's Q pieces, then the finished
 //               segment's epilogue (lane = dim);
 //   warps 12, 14, 15  TMA producers;  warp 13  MMA issuer and TMEM owner.
-// TMEM columns: a ring of S^T buffers (R columns each), then O^T buffers
-// (2 R columns, R with a 2-byte cache).  QK runs ahead of PV by up to two
-// tiles, into the next segment too, and a second O buffer lets the next
-// segment start while the epilogue reads the last one.
+// TMEM columns: a ring of three S^T buffers (R columns each), then the O^T
+// accumulators of the two groups (2 R columns each, R with a 2-byte cache),
+// twice where there is room, so that the next segment may start while the
+// epilogue reads the last one.  QK runs two tiles ahead of PV, into the next
+// segment too.
 // All waits are bounded; on expiry a status bit is set and the CTA winds down.
 #pragma once
 #include "../../include/pafp8.h"
@@ -81,7 +89,7 @@ constexpr int kSegCache = 32;  // segment records kept in shared memory
 // Reference maxima rise when some P' would pass 2^(kShift + kHead).
 template <int KT>
 struct PShift {  // fp8 pieces: P' <= 2^8, e4m3 reaches 448
-    static constexpr float kShift = 6.f, kHead = 2.f;
+    static constexpr float kShift = 5.f, kHead = 3.f;
 };
 template <>
 struct PShift<PAFP8_BF16> {
@@ -94,7 +102,7 @@ struct PShift<PAFP8_F16> {
 // kShift - m of a row that has seen no key: any logit passes the bound.
 constexpr float kUnseen = 1e30f;
 
-// Sizes of one instantiation.  R: rows of a row tile, a power of two >= 32.
+// Sizes of one instantiation.  R: rows of a row tile, 32 or 64.
 template <int KT, int NP, int DH, int R>
 struct TreeDims {
     static constexpr bool k2 = KT == PAFP8_BF16 || KT == PAFP8_F16;
@@ -103,36 +111,32 @@ struct TreeDims {
     static constexpr uint32_t kHalf = kTileKeys * 128;      // a 64-dim half of a 2-byte tile
     static constexpr int NH = DH / 64;                      // halves of a 2-byte row
     static constexpr uint32_t kQPiece = R * DH * ES;        // 2-byte: [half][R rows][128 B]
-    // P: per piece [128 keys][R] as blocks of W-byte rows.
-    static constexpr int W = R * ES < 128 ? R * ES : 128;
-    static constexpr uint32_t kPBlock = 128 * W;
-    static constexpr uint32_t kPPiece = 128 * R * ES;
-    static constexpr int NPB = R == 128 ? 1 : 2;            // P buffers
-    static constexpr int NOB = R == 128 && !k2 ? 1 : 2;     // O buffers
-    static constexpr int OC = k2 ? R : 2 * R;               // columns of an O buffer
-    static constexpr uint32_t kColO = 2 * R;                // after two S buffers
-    static constexpr uint32_t kCols = kColO + NOB * OC <= 128 ? 128 : kColO + NOB * OC <= 256 ? 256 : 512;
-    static constexpr int NCOL = R / 2;                      // rows of a softmax thread
-    static constexpr int NC = NCOL < 32 ? NCOL : 32;        // of them at a time
-    static_assert(kColO + NOB * OC <= kCols, "TMEM columns");
+    static constexpr int W = R * ES;                        // bytes of a key's row of a P piece
+    static constexpr uint32_t kPPiece = 128 * W;            // [128 keys][R]
+    static constexpr int OC = k2 ? R : 2 * R;               // columns of an accumulator
+    static constexpr int NOB = 3 * R + 4 * OC <= 512 ? 2 : 1;  // accumulators of a group
+    static constexpr uint32_t kColO = 3 * R;                // [NOB][group]
+    static constexpr uint32_t kCols = kColO + NOB * 2 * OC <= 256 ? 256 : 512;
+    static_assert(R == 32 || R == 64, "row tiles");
+    static_assert(kColO + NOB * 2 * OC <= kCols, "TMEM columns");
 };
 
 struct TreeSmem {
-    uint32_t q, k, v, p, sc, neg, wmax, alpha, lsum, mst, wt, seg, vote, bars, tmem_slot, abort_flag, bytes;
+    uint32_t q, k, v, p, sc, neg, alpha, wmax, lsum, mst, wt, seg, vote, bars, tmem_slot, abort_flag, bytes;
 };
 enum TreeBar : int {
     tQFull = 0,              // [2]
     tQEmpty = 2,             // [2]
     tInfo = 4,               // [2] row scales of a segment written
     tState = 6,              // [2] m and l of a segment written
-    tSFull = 8,              // [2]
-    tPFull = 16,             // [2]
-    tOFull = 18,             // [2]
-    tOEmpty = 20,            // [2]
-    tHalf = 22,              // [2] the four softmax warps of a row half
-    tHelp = 24,              // the helper warps
-    tDrain = 25,
-    tKFull = 26,
+    tSFull = 8,              // [3]
+    tPFull = 11,             // [3]
+    tOFull = 14,             // [2]
+    tOEmpty = 16,            // [2 buffers][2 groups]
+    tVote = 20,              // [2] the four warps of a group
+    tHelp = 22,              // the helper warps
+    tDrain = 23,
+    tKFull = 24,
     tKEmpty = tKFull + kMaxStages,
     tVFull = tKEmpty + kMaxStages,
     tVEmpty = tVFull + kMaxStages,
@@ -145,15 +149,15 @@ __host__ __device__ inline TreeSmem tree_smem(int q_tiles, int stages) {
     s.k = (uint32_t)q_tiles * D::kQPiece;
     s.v = s.k + (uint32_t)stages * D::kTile;
     s.p = s.v + (uint32_t)stages * D::kTile;
-    s.sc = s.p + D::NPB * NP * D::kPPiece;  // [2][R] floats: log2 scale of each row
-    s.neg = s.sc + 2 * R * 4;               // [8 warps][NCOL]: kShift - reference maximum
-    s.wmax = s.neg + 8 * D::NCOL * 4;       // [2][half][4 quadrants][NC]
-    s.alpha = s.wmax + 2 * 2 * 4 * D::NC * 4;  // [8 warps][NC]
-    s.lsum = s.alpha + 8 * D::NC * 4;       // [2][4][R]
-    s.mst = s.lsum + 2 * 4 * R * 4;         // [2][R]
-    s.wt = s.mst + 2 * R * 4;               // [2][R]
-    s.seg = s.wt + 2 * R * 4;               // the CTA's first kSegCache segment records
-    s.vote = s.seg + kSegCache * kTreeSegWords * 4;  // [half][2] words
+    s.sc = s.p + 3 * NP * D::kPPiece;       // [2][R] floats: log2 scale of each row
+    s.neg = s.sc + 2 * R * 4;               // [8 warps][R]: kShift - reference maximum
+    s.alpha = s.neg + 8 * R * 4;            // [8 warps][R]
+    s.wmax = s.alpha + 8 * R * 4;           // [2][group][4 quadrants][32]
+    s.lsum = s.wmax + 2 * 2 * 4 * 32 * 4;   // [2][8 warps][R]
+    s.mst = s.lsum + 2 * 8 * R * 4;         // [2][group][R]
+    s.wt = s.mst + 2 * 2 * R * 4;           // [2][group][R]
+    s.seg = s.wt + 2 * 2 * R * 4;           // the CTA's first kSegCache segment records
+    s.vote = s.seg + kSegCache * kTreeSegWords * 4;  // [group][2] words
     s.bars = s.vote + 16;
     s.tmem_slot = s.bars + 8 * tNumBars;
     s.abort_flag = s.tmem_slot + 4;
@@ -208,8 +212,10 @@ __device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, uint32_
 }
 
 // One segment: key tiles [tile0, tile1) of a line (request, KV head, row tile).
+// Row i of the tile is query head (r0 + i) % group of drafted token (r0 + i) /
+// group.
 struct Seg {
-    int hk, t0, tile0, tile1, slot;  // slot: partial state, or -1 for a whole line
+    int hk, r0, tile0, tile1, slot;  // slot: partial state, or -1 for a whole line
     int qo0, qo_len, kv_len, page0;
 };
 // The CTA's segment i (of its own list): from shared memory, or from global
@@ -301,19 +307,10 @@ __device__ __forceinline__ void st_cols(uint32_t t, const float (&v)[NC]) {
     }
 }
 
-// Sums of v[c] over the warp's lanes: lane l returns column l's (of 32; of 16,
-// column l % 16's).
-template <int N>
-__device__ __forceinline__ float column_sum(const float* v, int lane) {
-    float a[N];
+// Sums of v[0 .. 31] over the warp's lanes: lane l returns column l's.
+__device__ __forceinline__ float column_sum(float (&a)[32], int lane) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) a[i] = v[i];
-    if constexpr (N == 16) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xFFFFFFFFu, a[i], 16);
-    }
-#pragma unroll
-    for (int d = N / 2; d > 0; d >>= 1) {
+    for (int d = 16; d > 0; d >>= 1) {
         const bool up = (lane & d) != 0;
 #pragma unroll
         for (int i = 0; i < d; ++i) {
@@ -331,7 +328,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     using D = TreeDims<KT, NP, DH, R>;
     constexpr bool k2 = D::k2;
     constexpr uint32_t kTile = D::kTile, kHalf = D::kHalf;
-    constexpr int NH = D::NH, NCOL = D::NCOL, NPB = D::NPB, NOB = D::NOB;
+    constexpr int NH = D::NH, NOB = D::NOB;
     constexpr float kShift = PShift<KT>::kShift, kHead = PShift<KT>::kHead;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -345,7 +342,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int n_seg = __ldg(meta + meta[kMetaOffCtaSeg] + blockIdx.x + 1) - s_first;
     const int* segs = meta + meta[kMetaOffSeg] + kTreeSegWords * (long long)s_first;
     const uint32_t seg_cache = base + L.seg;
-    const int g = p.group, TQ = kTileRows / g;
+    const int g = p.group;
     const uint32_t hint = p.wait_cycles < kWaitCyclesDefault ? 0u : 20000u;
     auto wait = [&](int b, uint32_t parity) { return tree_wait(bar(b), parity, flag, p.status, p.wait_cycles, hint); };
     auto wait_all = [&](int b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
@@ -356,12 +353,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(bar(tQEmpty + i), 1);  // commit
             mbar_init(bar(tInfo + i), 4);
             mbar_init(bar(tState + i), 8);   // softmax warps
-            mbar_init(bar(tSFull + i), 1);
-            mbar_init(bar(tPFull + i), 8);
             mbar_init(bar(tOFull + i), 1);
-            mbar_init(bar(tOEmpty + i), 4);
-            mbar_init(bar(tHalf + i), 4);
+            mbar_init(bar(tVote + i), 4);
         }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(bar(tSFull + i), 1);
+            mbar_init(bar(tPFull + i), 4);   // a group's warps
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(bar(tOEmpty + i), 4);
         mbar_init(bar(tHelp), 4);
         mbar_init(bar(tDrain), 1);
         for (int i = 0; i < NS; ++i) {
@@ -485,7 +484,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         constexpr uint64_t kQKd = (k2 || DH == 128) ? 1 : 0;  // 128-byte rows, else 64
         const uint64_t qk_proto = kQKd ? sw128_kmajor_desc(0) : sw64_kmajor_desc(0);
         const uint64_t v_proto = k2 ? mnmajor_desc<128>(0, DH == 128 ? kHalf : kTile) : mnmajor_desc<(k2 ? 128 : DH)>(0, kTile);
-        const uint64_t p_proto = mnmajor_desc<D::W>(0, k2 ? D::kPBlock : D::kPPiece);
+        const uint64_t p_proto = mnmajor_desc<D::W>(0, D::kPPiece);
         const uint32_t qk_hi = (uint32_t)(qk_proto >> 32), v_hi = (uint32_t)(v_proto >> 32), p_hi = (uint32_t)(p_proto >> 32);
         const uint32_t k_lo = (uint32_t)qk_proto + ((base + L.k) >> 4), q_lo = (uint32_t)qk_proto + ((base + L.q) >> 4);
         const uint32_t v_lo = (uint32_t)v_proto + ((base + L.v) >> 4), p_lo = (uint32_t)p_proto + ((base + L.p) >> 4);
@@ -494,19 +493,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         uint32_t qphase = 0;
         int kstage = 0, vstage = 0;
         uint32_t kphase = 0, vphase = 0;
+        int sbuf = 0, pbuf = 0;        // ring of three: S of QK's tile, P of PV's
+        uint32_t pphase = 0;
         int qleft = n_seg_u > 0 ? tiles_of(0) : 0;
         bool qfirst = true;
         int pn = 0;
         for (int ps = 0; ps < n_seg_u && ok; ++ps) {
-            const int nth = ps, ob = nth % NOB;
+            const int ob = ps % NOB;
             const int nt = tiles_of(ps);
             for (int t = 0; t < nt; ++t, ++pn) {
-                // QK(j + 1) goes before PV(j), into the next segment at most (the Q of
+                // QK(j + 2) goes before PV(j), into the next segment at most (the Q of
                 // the one after is built only when this one's epilogue is done).  So
-                // QK(j) follows PV(j - 2), which waited for P(j - 2): S(j - 2) has been
-                // read, and once S(j) is complete so is PV(j - 2), P's buffer free.
-                while (qs < n_seg_u && qn <= pn + 1 && qs <= ps + 1) {
-                    const int sb = qn & 1;
+                // QK(j) follows PV(j - 3), which waited for P(j - 3): S(j - 3) has been
+                // read, and once S(j) is complete so is PV(j - 3) and P's buffer free.
+                while (qs < n_seg_u && qn <= pn + 2 && qs <= ps + 1) {
                     if (qfirst) {
                         if (!(ok = wait_all(tQFull + qbuf, qphase))) break;
                         qfirst = false;
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     if (!(ok = wait_all(tKFull + kstage, kphase))) break;
                     tc_fence_after();
                     // S^T = K Q^T: A = K (keys), B = Q (rows), both K-major.
-                    const uint32_t d = tm + (uint32_t)(R * sb);
+                    const uint32_t d = tm + (uint32_t)(R * sbuf);
                     const uint32_t ka = k_lo + (uint32_t)kstage * (kTile >> 4);
                     uint32_t qa = q_lo + (uint32_t)(qbuf * p.q_pieces) * (D::kQPiece >> 4);
                     if constexpr (k2) {
@@ -529,12 +529,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                 tc_mma_elect<true>(d, ka + 2 * i, qk_hi, qa + 2 * i, qk_hi, idesc_qk, pc > 0 || i > 0, elect);
                         }
                     }
-                    tc_commit_elect(bar(tSFull + sb), elect);
+                    tc_commit_elect(bar(tSFull + sbuf), elect);
                     tc_commit_elect(bar(tKEmpty + kstage), elect);
                     if (++kstage == NS) {
                         kstage = 0;
                         kphase ^= 1u;
                     }
+                    if (++sbuf == 3) sbuf = 0;
                     ++qn;
                     if (--qleft == 0) {
                         tc_commit_elect(bar(tQEmpty + qbuf), elect);
@@ -547,26 +548,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     }
                 }
                 if (!ok) break;
-                // O of the segment that last used this buffer has been read.
-                if (t == 0 && nth >= NOB && !(ok = wait_all(tOEmpty + ob, (uint32_t)((nth / NOB + 1) & 1)))) break;
+                // O of the segment that last used this accumulator has been read.
+                const int gr = pn & 1;
+                if (t < 2 && ps >= NOB && !(ok = wait_all(tOEmpty + 2 * ob + gr, (uint32_t)((ps / NOB + 1) & 1)))) break;
                 if (!(ok = wait_all(tVFull + vstage, vphase))) break;
-                if (!(ok = wait_all(tPFull + pn % NPB, (uint32_t)((pn / NPB) & 1)))) break;
+                if (!(ok = wait_all(tPFull + pbuf, pphase))) break;
                 tc_fence_after();
                 // O^T += V^T P^T: A = V (dims), B = P (rows), both MN-major.  64 dims
                 // fill half of M = 128: the other half reads the shared memory one
                 // tile on and its lanes of O are never used.
-                const uint32_t d = tm + D::kColO + (uint32_t)(D::OC * ob);
+                const uint32_t d = tm + D::kColO + (uint32_t)(D::OC * (2 * ob + gr));
                 const uint32_t va = v_lo + (uint32_t)vstage * (kTile >> 4);
-                const uint32_t pa = p_lo + (uint32_t)(pn % NPB) * (NP * D::kPPiece >> 4);
+                const uint32_t pa = p_lo + (uint32_t)pbuf * (NP * D::kPPiece >> 4);
                 constexpr int W = D::W;
                 if constexpr (k2) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)  // K = 16 keys
-                        tc_mma_elect<false>(d, va + 128 * i, v_hi, pa + W * i, p_hi, idesc_pv, t > 0 || i > 0, elect);
+                        tc_mma_elect<false>(d, va + 128 * i, v_hi, pa + W * i, p_hi, idesc_pv, t >= 2 || i > 0, elect);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)  // K = 32 keys
-                        tc_mma_elect<true>(d, va + 2 * DH * i, v_hi, pa + 2 * W * i, p_hi, idesc_pv, t > 0 || i > 0, elect);
+                        tc_mma_elect<true>(d, va + 2 * DH * i, v_hi, pa + 2 * W * i, p_hi, idesc_pv, t >= 2 || i > 0, elect);
                     if constexpr (NP == 3) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -580,6 +582,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     vstage = 0;
                     vphase ^= 1u;
                 }
+                if (++pbuf == 3) {
+                    pbuf = 0;
+                    pphase ^= 1u;
+                }
             }
         }
         if (qn > 0) {  // every MMA completes before TMEM is freed
@@ -591,127 +597,135 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory");
         // ------------------------------------------------------------- softmax
-        constexpr int NC = D::NC, NSUB = NCOL / NC;  // NSUB passes of NC rows a tile
-        const int quad = warp & 3, half = warp >> 2;
-        const int krow = 32 * quad + lane;    // this thread's key in a tile
+        const int quad = warp & 3, gr = warp >> 2;  // this group's tiles have parity gr
+        const int krow = 32 * quad + lane;          // this thread's key in a tile
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
-        const uint32_t votes = base + L.vote + 8u * half;
-        const int hbar = tHalf + half;
-        int j = 0;                              // tiles so far
-        int stage = 0;                          // V stage of tile j
-        uint32_t vphase = 0;
+        const uint32_t negt = base + L.neg + (uint32_t)(warp * R) * 4u;
+        const uint32_t alt = base + L.alpha + (uint32_t)(warp * R) * 4u;
+        const uint32_t votes = base + L.vote + 8u * gr;
+        const int vbar = tVote + gr;
+        // Ring positions of this group's current tile: V stage (and the one of its
+        // tile before), S and P buffer.
+        int stage = 0, prev_stage = 0, buf = 0;
+        uint32_t vphase = 0, prev_phase = 0, bphase = 0;
+        auto advance = [&]() {
+            if (++stage == NS) {
+                stage = 0;
+                vphase ^= 1u;
+            }
+            if (++buf == 3) {
+                buf = 0;
+                bphase ^= 1u;
+            }
+        };
+        int j = 0;  // tiles of the CTA before the next one
         uint32_t hphase = 0, wbuf = 0, ballots = 0;
         bool ok = true;
         for (int si = 0; si < n_seg && ok; ++si) {
             const Seg sg = load_seg(segs, seg_cache, si);
-            const int nth = si;
-            const int ntok = min(TQ, sg.qo_len - sg.t0);
+            const int rows = min(R, sg.qo_len * g - sg.r0);
             const int ctx = sg.kv_len - sg.qo_len;
-            const uint32_t tO = lane_base + D::kColO + (uint32_t)(D::OC * (nth % NOB));
-            f32x2 l[NCOL / 2];
+            const uint32_t tO = lane_base + D::kColO + (uint32_t)(D::OC * (2 * (si % NOB) + gr));
+            const uint32_t sct = base + L.sc + (uint32_t)((si & 1) * R) * 4u;
+            f32x2 l[R / 2];
 #pragma unroll
-            for (int i = 0; i < NCOL / 2; ++i) l[i] = make_f32x2(0.f, 0.f);
-            // Mask bits of this warp's 32 keys of a tile, lane i holding those of row
-            // i's token, fetched a tile ahead.
-            const uint32_t* mrow[NSUB];
+            for (int i = 0; i < R / 2; ++i) l[i] = make_f32x2(0.f, 0.f);
+            // Mask bits of this warp's 32 keys of a tile, lane i holding those of rows
+            // i and i + 32, fetched a tile ahead.
+            constexpr int NL = R / 32;
+            const uint32_t* mrow[NL];
 #pragma unroll
-            for (int i = 0; i < NSUB; ++i)
-                mrow[i] = p.tree_mask + (long long)(sg.qo0 + sg.t0 + min((half * NCOL + i * NC + lane) / g, ntok - 1)) * p.mask_words;
-            uint32_t bits[NSUB];
+            for (int i = 0; i < NL; ++i)
+                mrow[i] = p.tree_mask + (long long)(sg.qo0 + (sg.r0 + min(32 * i + lane, rows - 1)) / g) * p.mask_words;
+            uint32_t bits[NL];
             auto fetch_bits = [&](int t) {
 #pragma unroll
-                for (int i = 0; i < NSUB; ++i)
+                for (int i = 0; i < NL; ++i)
                     bits[i] = (t + 1) * kTileKeys > ctx
                                   ? mask_bits(mrow[i], t * kTileKeys + 32 * quad - ctx, p.mask_words, sg.qo_len)
                                   : 0xFFFFFFFFu;
             };
-            fetch_bits(sg.tile0);
-            if (!(ok = wait_all(tInfo + (nth & 1), (uint32_t)((nth >> 1) & 1)))) break;
+            const int t_first = sg.tile0 + ((j ^ gr) & 1);  // this group's first tile of the segment
+            fetch_bits(t_first);
+            if (!(ok = wait_all(tInfo + (si & 1), (uint32_t)((si >> 1) & 1)))) break;
             for (int t = sg.tile0; t < sg.tile1 && ok; ++t, ++j) {
-                const bool first = t == sg.tile0;
-                const int sb = j & 1;
-                if (!(ok = wait_all(tSFull + sb, (uint32_t)((j >> 1) & 1)))) break;
+                if ((j & 1) != gr) {
+                    advance();
+                    continue;
+                }
+                const bool first = t == t_first;
+                const uint32_t tS = lane_base + (uint32_t)(R * buf);
+                if (!(ok = wait_all(tSFull + buf, bphase))) break;
                 tc_fence_after();
-                const uint32_t pb = base + L.p + (uint32_t)(j % NPB) * (NP * D::kPPiece);
+                const uint32_t pb = base + L.p + (uint32_t)buf * (NP * D::kPPiece);
+                // 32 rows at a time: P' in place of the logits.  The vote on the reference
+                // maxima is cast before the exponentials and read after P is stored, so
+                // its latency passes meanwhile; a raised reference redoes the rows.
 #pragma unroll
-                for (int sub = 0; sub < NSUB; ++sub) {
-                    const int cb = half * NCOL + sub * NC;  // first row of this pass
-                    const uint32_t tS = lane_base + (uint32_t)(R * sb + cb);
-                    const uint32_t sct = base + L.sc + (uint32_t)((nth & 1) * R + cb) * 4u;
-                    const uint32_t negt = base + L.neg + (uint32_t)(warp * NCOL + sub * NC) * 4u;
-                    float v[NC];
-                    // P' in place of the logits.  The vote on the reference maxima is cast
-                    // before the exponentials and read after P is stored, so its
-                    // latency passes meanwhile; a raised reference redoes the pass.
+                for (int sub = 0; sub < NL; ++sub) {
+                    const uint32_t tSs = tS + 32u * sub, scs = sct + 128u * sub, ngs = negt + 128u * sub, als = alt + 128u * sub;
+                    float v[32];
                     bool rise = first;
 #pragma unroll 1
                     while (true) {
-                        ld_cols<NC>(tS, v);
+                        ld_cols<32>(tSs, v);
                         tc_wait_ld();
                         if ((t + 1) * kTileKeys > ctx) {  // keys that a row does not see become -inf
 #pragma unroll
-                            for (int c = 0; c < NC; ++c)
+                            for (int c = 0; c < 32; ++c)
                                 if (!((__shfl_sync(0xFFFFFFFFu, bits[sub], c) >> lane) & 1u)) v[c] = -INFINITY;
                         }
                         if (rise) {
                             // Column maxima of the tile: over this warp's lanes, then over the
-                            // four warps of the half.  Lane i settles row i.
+                            // group's four warps.  Lane i settles row i.
                             float cm = 0.f;
 #pragma unroll
-                            for (int c = 0; c < NC; ++c) {
+                            for (int c = 0; c < 32; ++c) {
                                 const float m = warp_max(v[c]);
                                 if (lane == c) cm = m;
                             }
-                            const uint32_t wm = base + L.wmax + (uint32_t)((wbuf * 2 + half) * 4 * NC) * 4u;
+                            const uint32_t wm = base + L.wmax + (uint32_t)((wbuf * 2 + gr) * 128 + lane) * 4u;
                             wbuf ^= 1u;
-                            if (lane < NC) sts_f(wm + 4u * (quad * NC + lane), cm);
-                            warp_arrive(bar(hbar));
-                            if (!(ok = wait_all(hbar, hphase))) break;
+                            sts_f(wm + 128u * quad, cm);
+                            warp_arrive(bar(vbar));
+                            if (!(ok = wait_all(vbar, hphase))) break;
                             hphase ^= 1u;
-                            const int c = min(lane, NC - 1);
-                            const float top = fmaxf(max3(lds_f(wm + 4u * c), lds_f(wm + 4u * (NC + c)), lds_f(wm + 4u * (2 * NC + c))),
-                                                    lds_f(wm + 4u * (3 * NC + c))) * lds_f(sct + 4u * c);
-                            const float was = first ? kUnseen : lds_f(negt + 4u * c);
+                            const float top = fmaxf(max3(lds_f(wm), lds_f(wm + 128u), lds_f(wm + 256u)), lds_f(wm + 384u)) * lds_f(scs + 4u * lane);
+                            const float was = first ? kUnseen : lds_f(ngs + 4u * lane);
                             const float m_old = was >= kUnseen ? -INFINITY : kShift - was;
                             const float m_new = fmaxf(m_old, top);
-                            const float alpha = m_old == -INFINITY ? 0.f : ex2(m_old - m_new);
-                            const uint32_t alt = base + L.alpha + (uint32_t)(warp * NC) * 4u;
-                            if (lane < NC) {
-                                sts_f(alt + 4u * c, alpha);
-                                sts_f(negt + 4u * c, m_new == -INFINITY ? kUnseen : kShift - m_new);
-                            }
+                            sts_f(als + 4u * lane, m_old == -INFINITY ? 0.f : ex2(m_old - m_new));
+                            sts_f(ngs + 4u * lane, m_new == -INFINITY ? kUnseen : kShift - m_new);
                             __syncwarp();
                             if (!first) {
-                                // Every O update of the earlier tiles has to be complete.
-                                if (!(ok = wait_all(tVEmpty + (stage == 0 ? NS - 1 : stage - 1), stage == 0 ? vphase ^ 1u : vphase)))
-                                    break;
+                                // This accumulator's last update has to be complete.
+                                if (!(ok = wait_all(tVEmpty + prev_stage, prev_phase))) break;
                                 tc_fence_after();
 #pragma unroll 1
-                                for (int part = 0; part < (k2 ? 1 : 2); ++part) {  // O_hi, then O_lo
-                                    const uint32_t to = tO + (uint32_t)(part * R + cb);
-                                    float o[NC];
-                                    ld_cols<NC>(to, o);
+                                for (int c0 = 32 * sub; c0 < D::OC; c0 += R) {  // O_hi, O_lo
+                                    float o[32];
+                                    ld_cols<32>(tO + c0, o);
                                     tc_wait_ld();
 #pragma unroll
-                                    for (int i = 0; i < NC; i += 4) {
-                                        const float4 a = lds_f4(alt + 4u * i);
+                                    for (int i = 0; i < 32; i += 4) {
+                                        const float4 a = lds_f4(als + 4u * i);
                                         o[i] *= a.x, o[i + 1] *= a.y, o[i + 2] *= a.z, o[i + 3] *= a.w;
                                     }
-                                    st_cols<NC>(to, o);
+                                    st_cols<32>(tO + c0, o);
                                 }
 #pragma unroll
-                                for (int i = 0; i < NC; i += 4) {
-                                    const float4 a = lds_f4(alt + 4u * i);
-                                    l[(sub * NC + i) / 2] = mul2(l[(sub * NC + i) / 2], make_f32x2(a.x, a.y));
-                                    l[(sub * NC + i) / 2 + 1] = mul2(l[(sub * NC + i) / 2 + 1], make_f32x2(a.z, a.w));
+                                for (int i = 0; i < 32; i += 4) {
+                                    const float4 a = lds_f4(als + 4u * i);
+                                    l[16 * sub + i / 2] = mul2(l[16 * sub + i / 2], make_f32x2(a.x, a.y));
+                                    l[16 * sub + i / 2 + 1] = mul2(l[16 * sub + i / 2 + 1], make_f32x2(a.z, a.w));
                                 }
                                 tc_wait_st();
                             }
                         }
                         // x = s * scale + (kShift - m)
 #pragma unroll
-                        for (int c = 0; c < NC; c += 4) {
-                            const float4 sc = lds_f4(sct + 4u * c), ng = lds_f4(negt + 4u * c);
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 sc = lds_f4(scs + 4u * c), ng = lds_f4(ngs + 4u * c);
                             split_f32x2(fma2(make_f32x2(v[c], v[c + 1]), make_f32x2(sc.x, sc.y), make_f32x2(ng.x, ng.y)), v[c],
                                         v[c + 1]);
                             split_f32x2(fma2(make_f32x2(v[c + 2], v[c + 3]), make_f32x2(sc.z, sc.w), make_f32x2(ng.z, ng.w)),
@@ -721,27 +735,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         if (!rise) {
                             float pm[2] = {v[0], v[1]};
 #pragma unroll
-                            for (int c = 2; c < NC; c += 2) pm[(c >> 1) & 1] = max3(pm[(c >> 1) & 1], v[c], v[c + 1]);
+                            for (int c = 2; c < 32; c += 2) pm[(c >> 1) & 1] = max3(pm[(c >> 1) & 1], v[c], v[c + 1]);
                             ++ballots;
                             if (__any_sync(0xFFFFFFFFu, fmaxf(pm[0], pm[1]) > kShift + kHead) && lane == 0) sts32(slot, ballots);
-                            warp_arrive(bar(hbar));
+                            warp_arrive(bar(vbar));
                         }
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) v[c] = ex2(v[c]);
-                        // P into shared memory.  Of two buffers the one to write is free (its
-                        // product was complete before S was); a single one is free when the
-                        // tile before has been multiplied.
-                        if (NPB == 1 && sub == 0 && j > 0 &&
-                            !(ok = wait_all(tVEmpty + (stage == 0 ? NS - 1 : stage - 1), stage == 0 ? vphase ^ 1u : vphase)))
-                            break;
+                        for (int c = 0; c < 32; ++c) v[c] = ex2(v[c]);
+                        // P into shared memory: the buffer's last product was complete before S.
                         constexpr int W = D::W;
                         constexpr int kElems = 16 / D::ES;  // rows a 16-byte chunk
                         const uint32_t swz = W == 128 ? krow & 7 : W == 64 ? (krow >> 1) & 3 : (krow >> 2) & 1;
 #pragma unroll
-                        for (int c = 0; c < NC; c += kElems) {
-                            const int byte0 = (cb + c) * D::ES;  // in the key's row of all blocks
-                            const uint32_t at = pb + (uint32_t)(byte0 / W) * D::kPBlock + (uint32_t)krow * W +
-                                                ((((uint32_t)(byte0 % W) >> 4) ^ swz) << 4);
+                        for (int c = 0; c < 32; c += kElems) {
+                            const uint32_t at = pb + (uint32_t)krow * W + (((uint32_t)((32 * sub + c) / kElems) ^ swz) << 4);
                             uint32_t w0[4], w1[4], w2[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
@@ -758,25 +765,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             if constexpr (NP == 3) sts128(at + 2 * D::kPPiece, w2[0], w2[1], w2[2], w2[3]);
                         }
                         if (rise) break;
-                        if (!(ok = wait_all(hbar, hphase))) break;
+                        if (!(ok = wait_all(vbar, hphase))) break;
                         hphase ^= 1u;
                         if (lds_u(slot) != ballots) break;
                         rise = true;
                     }
                     if (!ok) break;
 #pragma unroll
-                    for (int i = 0; i < NC / 2; ++i)
-                        l[sub * NC / 2 + i] = add2(l[sub * NC / 2 + i], make_f32x2(v[2 * i], v[2 * i + 1]));
+                    for (int i = 0; i < 16; ++i) l[16 * sub + i] = add2(l[16 * sub + i], make_f32x2(v[2 * i], v[2 * i + 1]));
                 }
                 if (!ok) break;
-                if (t + 1 < sg.tile1) fetch_bits(t + 1);
                 // Value rows behind the request's end (the tail of its last page and
                 // rows no page filled) hold anything: zero them, P = 0 there must
                 // not meet a NaN.
                 const int valid = sg.kv_len - t * kTileKeys;
                 if (valid < kTileKeys) {
                     if (!(ok = wait_all(tVFull + stage, vphase))) break;
-                    if (half == 0 && krow >= valid) {
+                    if (krow >= valid) {
                         const uint32_t vrow = base + L.v + (uint32_t)stage * kTile + (uint32_t)krow * (k2 ? 128u : (uint32_t)DH);
 #pragma unroll
                         for (int c = 0; c < (k2 ? 8 : DH / 16); ++c) {
@@ -787,28 +792,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 }
                 fence_async_smem();
                 tc_fence_before();
-                warp_arrive(bar(tPFull + j % NPB));
-                if (++stage == NS) {
-                    stage = 0;
-                    vphase ^= 1u;
-                }
+                warp_arrive(bar(tPFull + buf));
+                if (t + 2 < sg.tile1) fetch_bits(t + 2);
+                prev_stage = stage;
+                prev_phase = vphase;
+                advance();
             }
             if (!ok) break;
-            // The segment's sums (over this warp's keys) and maxima for the epilogue.
+            // The segment's sums (over this warp's keys) and this group's maxima for
+            // the epilogue; a group without a tile in it leaves an empty state.
+            const bool none = t_first >= sg.tile1;
 #pragma unroll
-            for (int sub = 0; sub < NSUB; ++sub) {
-                float ls[NC];
+            for (int i = 0; i < NL; ++i) {
+                float ls[32];
 #pragma unroll
-                for (int i = 0; i < NC / 2; ++i) split_f32x2(l[sub * NC / 2 + i], ls[2 * i], ls[2 * i + 1]);
-                const float sum = column_sum<NC>(ls, lane);
-                if (lane < NC) {
-                    const int row = half * NCOL + sub * NC + lane;
-                    sts_f(base + L.lsum + 4u * (((nth & 1) * 4 + quad) * R + row), sum);
-                    const float ng = lds_f(base + L.neg + (uint32_t)(warp * NCOL + sub * NC + lane) * 4u);
-                    if (quad == 0) sts_f(base + L.mst + 4u * ((nth & 1) * R + row), ng >= kUnseen ? -INFINITY : kShift - ng);
-                }
+                for (int c = 0; c < 16; ++c) split_f32x2(l[16 * i + c], ls[2 * c], ls[2 * c + 1]);
+                const float sum = column_sum(ls, lane);
+                const int row = 32 * i + lane;
+                sts_f(base + L.lsum + 4u * (((si & 1) * 8 + warp) * R + row), sum);
+                const float ng = lds_f(negt + 4u * row);
+                if (quad == 0)
+                    sts_f(base + L.mst + 4u * (((si & 1) * 2 + gr) * R + row), none || ng >= kUnseen ? -INFINITY : kShift - ng);
             }
-            warp_arrive(bar(tState + (nth & 1)));
+            warp_arrive(bar(tState + (si & 1)));
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
@@ -823,11 +829,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const Seg sg = load_seg(segs, seg_cache, si);
             const int nth = si, buf = NQB == 2 ? nth & 1 : 0;
             const int use = NQB == 2 ? nth >> 1 : nth;  // earlier uses of this buffer
-            const int rows = min(TQ, sg.qo_len - sg.t0) * g;
+            const int rows = min(R, sg.qo_len * g - sg.r0);
             constexpr int LPR = DH / 8, RPI = 32 / LPR;  // lanes a row, rows a warp's round
             const int e = lane % LPR, row0 = (warp - 8) * RPI + lane / LPR;
             const bool q1 = !k2 && p.q_pieces == 1;      // an fp8 query as it is
-            const size_t head0 = (size_t)(sg.qo0 + sg.t0) * p.num_qo_heads + (size_t)sg.hk * g;
+            const size_t head0 = (size_t)sg.qo0 * p.num_qo_heads + (size_t)sg.hk * g;
             const uint32_t dst = base + L.q + (uint32_t)(buf * p.q_pieces) * D::kQPiece;
             const uint32_t fdst = base + L.sc + (uint32_t)((nth & 1) * R) * 4u;
             const float ks = p.k_scales != nullptr ? __ldg(p.k_scales + sg.hk) : 0.f;
@@ -841,8 +847,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     const int row = first + 4 * RPI * k;
                     raw[k] = make_uint4(0, 0, 0, 0);
                     if (row < rows) {
-                        const int tok = row / g;
-                        const size_t at = (head0 + (size_t)tok * p.num_qo_heads + (row - tok * g)) * DH + 8 * e;
+                        const int tok = (sg.r0 + row) / g;
+                        const size_t at = (head0 + (size_t)tok * p.num_qo_heads + (sg.r0 + row - tok * g)) * DH + 8 * e;
                         if (q1) {
                             const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.q) + at));
                             raw[k] = make_uint4(x.x, x.y, 0, 0);
@@ -863,7 +869,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     // log2 scale of this row's logits, but for the pieces' power of two.
                     float scale = p.sm_scale_log2;
                     if (p.k_scales != nullptr) {
-                        const int qh = sg.hk * g + row % g;
+                        const int qh = sg.hk * g + (sg.r0 + row) % g;
                         scale = fold_scale_log2(p.sm_scale, p.q_scales != nullptr ? __ldg(p.q_scales + qh) : 1.0f, ks);
                     }
                     if constexpr (k2) {
@@ -936,65 +942,88 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (sq == 0) continue;
             const int si = sq - 1;
             const Seg sg = load_seg(segs, seg_cache, si);
-            const int nth = si, ob = nth % NOB;
-            const int rows = min(TQ, sg.qo_len - sg.t0) * g;
+            const int ob = si % NOB;
+            const int rows = min(R, sg.qo_len * g - sg.r0);
             const bool whole = sg.slot < 0;
             const float vsc = p.v_scales != nullptr ? __ldg(p.v_scales + sg.hk) : p.v_scale;
-            const size_t head0 = (size_t)(sg.qo0 + sg.t0) * p.num_qo_heads + (size_t)sg.hk * g;
+            const size_t head0 = (size_t)sg.qo0 * p.num_qo_heads + (size_t)sg.hk * g;
             const size_t prow0 = (size_t)max(sg.slot, 0) * p.rows_pad;
-            const uint32_t wt = base + L.wt + (uint32_t)((nth & 1) * R) * 4u;
-            if (!(ok = wait_all(tState + (nth & 1), (uint32_t)((nth >> 1) & 1)))) break;
-            if (d < R) {  // row d's sum and weight
-                float sum = 0.f;
+            const uint32_t wt = base + L.wt + (uint32_t)((si & 1) * 2 * R) * 4u;
+            if (!(ok = wait_all(tState + (si & 1), (uint32_t)((si >> 1) & 1)))) break;
+            if (d < R) {
+                // Row d: the groups' states joined, M and L at it, and each group's weight.
+                float m[2], sum[2] = {0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum += lds_f(base + L.lsum + 4u * (((nth & 1) * 4 + i) * R + d));
-                sts_f(wt + 4u * d, sum == 0.f ? 0.f : (whole ? vsc : 1.f) / sum);
+                for (int i = 0; i < 2; ++i) {
+                    m[i] = lds_f(base + L.mst + 4u * (((si & 1) * 2 + i) * R + d));
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) sum[i] += lds_f(base + L.lsum + 4u * (((si & 1) * 8 + 4 * i + w) * R + d));
+                }
+                const float M = fmaxf(m[0], m[1]), m0 = M == -INFINITY ? 0.f : M;
+                const float f0 = ex2(m[0] - m0), f1 = ex2(m[1] - m0);
+                // (an empty state counts for nothing; a NaN sum stays one)
+                const float L2 = (sum[0] == 0.f ? 0.f : f0 * sum[0]) + (sum[1] == 0.f ? 0.f : f1 * sum[1]);
+                const float w = L2 == 0.f ? 0.f : (whole ? vsc : 1.f) / L2;
+                sts_f(wt + 4u * d, sum[0] == 0.f ? 0.f : f0 * w);
+                sts_f(wt + 4u * (R + d), sum[1] == 0.f ? 0.f : f1 * w);
                 if (d < rows) {
-                    const float lse2 = sum == 0.f ? -INFINITY : lds_f(base + L.mst + 4u * ((nth & 1) * R + d)) - kShift + __log2f(sum);
+                    const float lse2 = L2 == 0.f ? -INFINITY : M - kShift + __log2f(L2);
+                    const int tok = (sg.r0 + d) / g;
                     if (!whole)
                         p.part_lse[prow0 + d] = lse2;
                     else if (p.lse != nullptr)
-                        p.lse[head0 + (size_t)(d / g) * p.num_qo_heads + d % g] = lse2 * 0.69314718055994531f;
+                        p.lse[head0 + (size_t)tok * p.num_qo_heads + (sg.r0 + d - tok * g)] = lse2 * 0.69314718055994531f;
                 }
             }
             warp_arrive(bar(tHelp));
             if (!(ok = wait_all(tHelp, help_phase))) break;
             help_phase ^= 1u;
-            if (!(ok = wait_all(tOFull + ob, (uint32_t)((nth / NOB) & 1)))) break;
+            if (!(ok = wait_all(tOFull + ob, (uint32_t)((si / NOB) & 1)))) break;
             tc_fence_after();
-            const uint32_t tO = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + D::kColO + (uint32_t)(D::OC * ob);
-            // Rows 16 at a time, a warp writing 32 dims of each: 64 bytes of o, or 128
-            // of a partial state.
-            int hh = 0;
-            uint16_t* dst = static_cast<uint16_t*>(p.o) + head0 * DH + d;
+            const uint32_t tO = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + D::kColO + (uint32_t)(2 * D::OC * ob);
+            // Rows eight at a time, a warp writing 32 dims of each: 64 bytes of o, or
+            // 128 of a partial state.
+            const int tok0 = sg.r0 / g;
+            int hh = sg.r0 - tok0 * g;
+            uint16_t* dst = static_cast<uint16_t*>(p.o) + (head0 + (size_t)tok0 * p.num_qo_heads + hh) * DH + d;
             float* part = p.part_o + prow0 * DH + d;
 #pragma unroll 1
-            for (int r0 = 0; r0 < rows; r0 += 16) {
-                uint32_t o[16];
-                tc_ld16(tO + r0, o);
+            for (int r0 = 0; r0 < rows; r0 += 8) {
+                uint32_t o[2][8];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) tc_ld8(tO + D::OC * i + r0, o[i]);
                 if constexpr (!k2) {
-                    uint32_t lo[16];
-                    tc_ld16(tO + R + r0, lo);
+                    uint32_t lo[2][8];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) tc_ld8(tO + D::OC * i + R + r0, lo[i]);
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[i] = __float_as_uint(fmaf(__uint_as_float(lo[i]), 1.f / 32.f, __uint_as_float(o[i])));
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            o[i][k] = __float_as_uint(fmaf(__uint_as_float(lo[i][k]), 1.f / 32.f, __uint_as_float(o[i][k])));
                 } else {
                     tc_wait_ld();
                 }
-                if (r0 + 16 >= rows) {  // O is read: another segment may write the buffer
+                if (r0 + 8 >= rows) {  // O is read: another segment may write the accumulators
                     tc_fence_before();
-                    warp_arrive(bar(tOEmpty + ob));
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(tOEmpty + 2 * ob));
+                        mbar_arrive(bar(tOEmpty + 2 * ob + 1));
+                    }
                 }
                 if (DH == 64 && d >= 64) continue;
 #pragma unroll
-                for (int i4 = 0; i4 < 4; ++i4) {
-                    const float4 w4 = lds_f4(wt + 4u * (r0 + 4 * i4));
-                    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+                for (int k4 = 0; k4 < 8; k4 += 4) {
+                    const float4 wa = lds_f4(wt + 4u * (r0 + k4)), wb = lds_f4(wt + 4u * (R + r0 + k4));
+                    const float w0[4] = {wa.x, wa.y, wa.z, wa.w}, w1[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (r0 + 4 * i4 + i >= rows) break;
-                        const float x = w[i] == 0.f ? 0.f : __uint_as_float(o[4 * i4 + i]) * w[i];
+                    for (int k = 0; k < 4; ++k) {
+                        if (r0 + k4 + k >= rows) break;
+                        // An accumulator of weight 0 may hold anything.
+                        const float x = (w0[k] == 0.f ? 0.f : __uint_as_float(o[0][k4 + k]) * w0[k]) +
+                                        (w1[k] == 0.f ? 0.f : __uint_as_float(o[1][k4 + k]) * w1[k]);
                         if (whole) {
                             *dst = (uint16_t)(pack_out2(x, 0.f, p.o_dtype) & 0xFFFFu);
                             dst += DH;
@@ -1029,7 +1058,7 @@ __global__ void __launch_bounds__(32 * kTreeMergeWarps) tree_merge_kernel(const 
     constexpr int DPL = DH / 32;
     const int* meta = p.meta;
     const int4* rec = reinterpret_cast<const int4*>(meta + meta[kMetaOffTile]) + 2 * (long long)blockIdx.x;
-    const int4 a = __ldg(rec), b = __ldg(rec + 1);  // slot0, slot1, first row of q, hk; rows
+    const int4 a = __ldg(rec), b = __ldg(rec + 1);  // slot0, slot1, the request's first token, hk; rows, first row
     const int row = blockIdx.y * kTreeMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (row >= b.x) return;
@@ -1066,7 +1095,7 @@ __global__ void __launch_bounds__(32 * kTreeMergeWarps) tree_merge_kernel(const 
         }
     }
     const float inv = sum == 0.f ? 0.f : vsc / sum;
-    const int tok = row / p.group, hh = row - tok * p.group;
+    const int tok = (b.y + row) / p.group, hh = b.y + row - tok * p.group;
     const size_t orow = (size_t)(a.z + tok) * p.num_qo_heads + (size_t)a.w * p.group + hh;
     uint32_t w[DPL / 2];
 #pragma unroll

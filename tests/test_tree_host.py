@@ -43,20 +43,20 @@ def test_every_tile_of_every_line_is_in_one_segment(seed):
     plan = _plan(kv, qo, hq=hkv * group, hkv=hkv, num_ctas=num_ctas)
     ctas, ptr, segs, merges, npart = _parts(plan)
     assert ctas <= num_ctas
-    TQ = 128 // group
-    want = {(b, hk, t0) for b in range(batch) for hk in range(hkv) for t0 in range(0, qo[b], TQ)}
+    R = 32 if max(qo + [0]) * group <= 32 else 64
+    want = {(b, hk, r0) for b in range(batch) for hk in range(hkv) for r0 in range(0, qo[b] * group, R)}
     qo0 = np.concatenate([[0], np.cumsum(qo)])
     page0 = np.concatenate([[0], np.cumsum([-(-n // 16) for n in kv])])
     got, slots = {}, {}
     first = {(int(qo0[b]), qo[b], kv[b], int(page0[b])): b for b in range(batch) if qo[b]}
     for s in segs:
-        hk, t0, a, e, slot = (int(x) for x in s[:5])
+        hk, r0, a, e, slot = (int(x) for x in s[:5])
         b = first[tuple(int(x) for x in s[5:9])]
         assert a < e
-        got.setdefault((b, hk, t0), []).append((a, e, slot))
+        got.setdefault((b, hk, r0), []).append((a, e, slot))
         if slot >= 0:
             assert slot not in slots
-            slots[slot] = (b, hk, t0, a)
+            slots[slot] = (b, hk, r0, a)
     assert set(got) == want
     split = {}
     for key, parts in got.items():
@@ -67,11 +67,11 @@ def test_every_tile_of_every_line_is_in_one_segment(seed):
             assert parts[0][2] == -1
         else:
             assert [p[2] for p in parts] == list(range(parts[0][2], parts[0][2] + len(parts)))
-            split[(int(qo0[key[0]]) + key[2], key[1])] = (parts[0][2], parts[-1][2] + 1, min(TQ, qo[key[0]] - key[2]) * group)
+            split[(int(qo0[key[0]]), key[2], key[1])] = (parts[0][2], parts[-1][2] + 1, min(R, qo[key[0]] * group - key[2]))
     assert len(slots) == npart and set(slots) == set(range(npart))
-    assert {(int(x[2]), int(x[3])): (int(x[0]), int(x[1]), int(x[4])) for x in merges} == split
+    assert {(int(x[2]), int(x[5]), int(x[3])): (int(x[0]), int(x[1]), int(x[4])) for x in merges} == split
     if npart:
-        rows = max(min(TQ, n - t0) * group for n in qo for t0 in range(0, n, TQ))
+        rows = max(min(R, n * group) for n in qo)
         assert plan.workspace_bytes >= npart * rows * (128 + 1) * 4
 
 

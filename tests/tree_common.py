@@ -154,8 +154,8 @@ class TreeBatch:
                     # exp2, the sums and the fold of the scale: 2^-20 together
                     rel = p_half + 2 * dz + 2.0 ** -20
                     # Small probabilities: half the last piece's smallest step, 2^-10 / 32 where
-                    # the row's maximum is at 2^6, i.e. 2^-21 of it (an f16's is smaller).
-                    tail = L * 2.0 ** -21 * v.abs().max() / tot.clamp(min=1.0) if self.kt in FP8 or self.kt == "f16" else 0.0
+                    # the row's maximum is at 2^5, i.e. 2^-20 of it (an f16's is smaller).
+                    tail = L * 2.0 ** -20 * v.abs().max() / tot.clamp(min=1.0) if self.kt in FP8 or self.kt == "f16" else 0.0
                     slack = (w @ v.abs()) * rel + tail
                     tol = slack + HALF[DT[self.ot]] * (ro.abs() + slack) + 2.0 ** -24
                     got = o[r0:r0 + T, h].double()
