@@ -982,8 +982,9 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
                 return fail(PAFP8_ERR_SHAPE, "qo_indptr[0] is %d, not 0", (int)qo_indptr_h[0]);
             const int64_t qo = (int64_t)qo_indptr_h[b + 1] - qo_indptr_h[b];
             const int64_t kv = n > 0 ? (n - 1) * d.page_size + last_page_len_h[b] : 0;
-            if (d.mode == PAFP8_MODE_TREE && qo * group > INT32_MAX)
-                return fail(PAFP8_ERR_UNSUPPORTED, "request %d has %lld rows of %d heads: their product must stay below 2^31",
+            if (d.mode == PAFP8_MODE_TREE && qo * group > (1 << 25))
+                return fail(PAFP8_ERR_UNSUPPORTED,
+                            "request %d has %lld drafted tokens of %d query heads per KV head: the product may be 2^25 at most",
                             b, (long long)qo, group);
             if (qo < 0)
                 return fail(PAFP8_ERR_SHAPE, "qo_indptr decreases at request %d (%d -> %d)", b,
@@ -1257,6 +1258,7 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
         tp.num_pages = d.num_pages;
         tp.page_mult = plan->page_mult;
         tp.group = plan->group;
+        tp.group_magic = plan->group == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + plan->group - 1) / plan->group);
         tp.sm_scale_log2 = sm_log2;
         tp.v_scale = v_scale;
         tp.q_scales = k_scales != nullptr ? q_scales : nullptr;

@@ -211,6 +211,7 @@ struct TreeParams {
     int q_pieces;            // e4m3 pieces of a query row (1 for an fp8 query or a 2-byte cache)
     int q_buffers, stages;   // set by the launcher from the shared memory there is
     int num_qo_heads, num_pages, page_mult, group;
+    uint32_t group_magic;    // ceil(2^32 / group) (0 for group 1): n / group is the high word of n times it, n < 2^25
     float sm_scale_log2;     // sm_scale * q_scale * k_scale * log2(e)
     float v_scale;
     const float* q_scales;   // per-head scales, as in DecodeParams

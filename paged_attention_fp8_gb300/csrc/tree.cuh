@@ -122,7 +122,7 @@ struct TreeDims {
 };
 
 struct TreeSmem {
-    uint32_t q, k, v, p, sc, neg, alpha, wmax, lsum, mst, wt, seg, vote, bars, tmem_slot, abort_flag, bytes;
+    uint32_t q, k, v, p, sc, neg, alpha, wmax, lsum, mst, wt, rowp, seg, vote, bars, tmem_slot, abort_flag, bytes;
 };
 enum TreeBar : int {
     tQFull = 0,              // [2]
@@ -156,7 +156,8 @@ __host__ __device__ inline TreeSmem tree_smem(int q_tiles, int stages) {
     s.lsum = s.wmax + 2 * 2 * 4 * 32 * 4;   // [2][8 warps][R]
     s.mst = s.lsum + 2 * 8 * R * 4;         // [2][group][R]
     s.wt = s.mst + 2 * 2 * R * 4;           // [2][group][R]
-    s.seg = s.wt + 2 * 2 * R * 4;           // the CTA's first kSegCache segment records
+    s.rowp = s.wt + 2 * 2 * R * 4;          // [2][R] byte offsets of the rows in o (64 bits)
+    s.seg = s.rowp + 2 * R * 8;             // the CTA's first kSegCache segment records
     s.vote = s.seg + kSegCache * kTreeSegWords * 4;  // [group][2] words
     s.bars = s.vote + 16;
     s.tmem_slot = s.bars + 8 * tNumBars;
@@ -343,6 +344,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int* segs = meta + meta[kMetaOffSeg] + kTreeSegWords * (long long)s_first;
     const uint32_t seg_cache = base + L.seg;
     const int g = p.group;
+    // n / group for n < 2^25 (a plan has no more rows in a request).
+    auto token_of = [&](int n) -> int { return g == 1 ? n : (int)__umulhi((uint32_t)n, p.group_magic); };
     const uint32_t hint = p.wait_cycles < kWaitCyclesDefault ? 0u : 20000u;
     auto wait = [&](int b, uint32_t parity) { return tree_wait(bar(b), parity, flag, p.status, p.wait_cycles, hint); };
     auto wait_all = [&](int b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t tmem = lds_u(base + L.tmem_slot);  // (the records and barriers above are visible from here on)
 
     if (warp >= 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
       if (warp != 13) {
         // ----------------------------------------------------------- producers
         // A box holds the 16 tokens of one (sub-)page, and a warp's box takes it
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         __syncwarp();
       }
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;" ::: "memory");
         // ------------------------------------------------------------- softmax
         const int quad = warp & 3, gr = warp >> 2;  // this group's tiles have parity gr
         const int krow = 32 * quad + lane;          // this thread's key in a tile
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const uint32_t* mrow[NL];
 #pragma unroll
             for (int i = 0; i < NL; ++i)
-                mrow[i] = p.tree_mask + (long long)(sg.qo0 + (sg.r0 + min(32 * i + lane, rows - 1)) / g) * p.mask_words;
+                mrow[i] = p.tree_mask + (long long)(sg.qo0 + token_of(sg.r0 + min(32 * i + lane, rows - 1))) * p.mask_words;
             uint32_t bits[NL];
             auto fetch_bits = [&](int t) {
 #pragma unroll
@@ -817,25 +820,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             warp_arrive(bar(tState + (si & 1)));
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
         // ------------------------------------------------- Q pieces, epilogues
         const int d = threadIdx.x - 256;  // the dim (TMEM lane) this thread writes out
         uint32_t help_phase = 0;
+        int j_base = 0;  // tiles of the segments before
         bool ok = true;
         // Segment si's Q rows into its buffer: DH / 8 lanes a row, eight elements
-        // a lane; rows of no token are zero.  A compact loop: unrolled over whole
-        // rows the code ran once a segment and spent 10 us on instruction fetches.
+        // a lane; rows of no token are zero.  A compact loop, and few instructions
+        // a row: a helper warp shares its scheduler with two softmax warps and
+        // gets one instruction in about eight cycles.
         auto build_q = [&](int si) -> bool {
             const Seg sg = load_seg(segs, seg_cache, si);
-            const int nth = si, buf = NQB == 2 ? nth & 1 : 0;
-            const int use = NQB == 2 ? nth >> 1 : nth;  // earlier uses of this buffer
+            const int buf = NQB == 2 ? si & 1 : 0;
+            const int use = NQB == 2 ? si >> 1 : si;  // earlier uses of this buffer
             const int rows = min(R, sg.qo_len * g - sg.r0);
             constexpr int LPR = DH / 8, RPI = 32 / LPR;  // lanes a row, rows a warp's round
             const int e = lane % LPR, row0 = (warp - 8) * RPI + lane / LPR;
             const bool q1 = !k2 && p.q_pieces == 1;      // an fp8 query as it is
+            const bool bf = p.q_dtype == PAFP8_BF16;
             const size_t head0 = (size_t)sg.qo0 * p.num_qo_heads + (size_t)sg.hk * g;
             const uint32_t dst = base + L.q + (uint32_t)(buf * p.q_pieces) * D::kQPiece;
-            const uint32_t fdst = base + L.sc + (uint32_t)((nth & 1) * R) * 4u;
+            const uint32_t fdst = base + L.sc + (uint32_t)((si & 1) * R) * 4u;
             const float ks = p.k_scales != nullptr ? __ldg(p.k_scales + sg.hk) : 0.f;
             constexpr int kBatch = 4;  // rows in flight per lane group
             bool ready = false;
@@ -847,7 +853,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     const int row = first + 4 * RPI * k;
                     raw[k] = make_uint4(0, 0, 0, 0);
                     if (row < rows) {
-                        const int tok = (sg.r0 + row) / g;
+                        const int tok = token_of(sg.r0 + row);
                         const size_t at = (head0 + (size_t)tok * p.num_qo_heads + (sg.r0 + row - tok * g)) * DH + 8 * e;
                         if (q1) {
                             const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.q) + at));
@@ -869,71 +875,66 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     // log2 scale of this row's logits, but for the pieces' power of two.
                     float scale = p.sm_scale_log2;
                     if (p.k_scales != nullptr) {
-                        const int qh = sg.hk * g + (sg.r0 + row) % g;
+                        const int n = sg.r0 + row, qh = sg.hk * g + (n - token_of(n) * g);
                         scale = fold_scale_log2(p.sm_scale, p.q_scales != nullptr ? __ldg(p.q_scales + qh) : 1.0f, ks);
                     }
                     if constexpr (k2) {
                         sts128(dst + (e >> 3) * (R * 128u) + row * 128u + (uint32_t)(((e & 7) ^ (row & 7)) << 4), rw.x, rw.y, rw.z,
                                rw.w);
-                        if (e == 0) sts_f(fdst + 4u * row, scale);
-                        continue;
-                    }
-                    // An eight-byte element group's place in a piece's tile row.
-                    const uint32_t at = DH == 128 ? row * 128u + (uint32_t)(((e >> 1) ^ (row & 7)) << 4) + 8u * (e & 1)
-                                                  : row * 64u + (uint32_t)(((e >> 1) ^ ((row >> 1) & 3)) << 4) + 8u * (e & 1);
-                    float fac = 1.f;
-                    if (q1) {
-                        sts64(dst + at, rw.x, rw.y);
                     } else {
-                        const bool bf = p.q_dtype == PAFP8_BF16;
-                        const uint32_t w[4] = {rw.x, rw.y, rw.z, rw.w};
-                        uint32_t top = 0;  // the row's largest magnitude as a 16-bit pattern
+                        // An eight-byte element group's place in a piece's tile row.
+                        const uint32_t at = dst + (DH == 128 ? row * 128u + (uint32_t)(((e >> 1) ^ (row & 7)) << 4) + 8u * (e & 1)
+                                                             : row * 64u + (uint32_t)(((e >> 1) ^ ((row >> 1) & 3)) << 4) + 8u * (e & 1));
+                        if (q1) {
+                            sts64(at, rw.x, rw.y);
+                        } else {
+                            const uint32_t w[4] = {rw.x, rw.y, rw.z, rw.w};
+                            // The row's largest magnitude as a 16-bit pattern.
+                            uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                                    __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+                            top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-#pragma unroll
-                        for (int d = LPR / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                        const float amax = bf ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
-                        // 2^ex brings the largest magnitude into [128, 256).  A row with an
-                        // infinity or a NaN gives NaN, as its logits would.
-                        const int up = 7 - ((int)((__float_as_uint(amax) >> 23) & 0xFFu) - 127);
-                        const int ex = amax == 0.f ? 0 : max(-120, min(100, up));
-                        const float mul = __uint_as_float((uint32_t)(127 + ex) << 23);
-                        fac = isfinite(amax) ? __uint_as_float((uint32_t)(127 - ex) << 23) : __uint_as_float(0x7FC00000u);
-                        float x[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (bf) {
-                                x[2 * i] = __uint_as_float(w[i] << 16) * mul;
-                                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * mul;
-                            } else {
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                                x[2 * i] = f.x * mul;
-                                x[2 * i + 1] = f.y * mul;
-                            }
-                        }
-#pragma unroll 1
-                        for (int pc = 0; pc < p.q_pieces; ++pc) {
-                            uint32_t pr[4];
+                            for (int x = LPR / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+                            const float amax = bf ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+                            // 2^ex brings the largest magnitude into [128, 256).  A row with an
+                            // infinity or a NaN gives NaN, as its logits would.
+                            const int up = 7 - ((int)((__float_as_uint(amax) >> 23) & 0xFFu) - 127);
+                            const int ex = amax == 0.f ? 0 : max(-120, min(100, up));
+                            const float mul = __uint_as_float((uint32_t)(127 + ex) << 23);
+                            scale *= isfinite(amax) ? __uint_as_float((uint32_t)(127 - ex) << 23) : __uint_as_float(0x7FC00000u);
+                            // In f16 from here on: below 2^8 it holds bf16's 8 bits and its own
+                            // 11 down to 2^-14, and the differences are exact.
+                            __half2 h[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                pr[i] = e4m3_pair(x[2 * i], x[2 * i + 1]);
-                                const float2 b = __half22float2(half2_of_e4m3(pr[i]));
-                                x[2 * i] -= b.x;
-                                x[2 * i + 1] -= b.y;
+                                float2 f;
+                                if (bf)
+                                    f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+                                else
+                                    f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                                h[i] = __floats2half2_rn(f.x * mul, f.y * mul);
                             }
-                            sts64(dst + pc * D::kQPiece + at, pr[0] | (pr[1] << 16), pr[2] | (pr[3] << 16));
+#pragma unroll 1
+                            for (int pc = 0; pc < p.q_pieces; ++pc) {
+                                uint32_t pr[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    pr[i] = e4m3_of_half2(h[i]);
+                                    h[i] = __hsub2(h[i], half2_of_e4m3(pr[i]));
+                                }
+                                sts64(at + pc * D::kQPiece, prmt(pr[0], pr[1], 0x5410u), prmt(pr[2], pr[3], 0x5410u));
+                            }
                         }
                     }
                     // A scale that underflows to zero would turn -inf (unseen) into NaN.
-                    const float sf = scale * fac;
-                    if (e == 0) sts_f(fdst + 4u * row, sf < 1.2e-38f ? 1.2e-38f : sf);
+                    if (e == 0) sts_f(fdst + 4u * row, scale < 1.2e-38f ? 1.2e-38f : scale);
                 }
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar(tQFull + buf));
-                mbar_arrive(bar(tInfo + (nth & 1)));
+                mbar_arrive(bar(tInfo + (si & 1)));
             }
             return true;
         };
@@ -948,7 +949,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const float vsc = p.v_scales != nullptr ? __ldg(p.v_scales + sg.hk) : p.v_scale;
             const size_t head0 = (size_t)sg.qo0 * p.num_qo_heads + (size_t)sg.hk * g;
             const size_t prow0 = (size_t)max(sg.slot, 0) * p.rows_pad;
-            const uint32_t wt = base + L.wt + (uint32_t)((si & 1) * 2 * R) * 4u;
+            const uint32_t wt = base + L.wt + (uint32_t)((si & 1) * 2 * R) * 4u, rowp = base + L.rowp + (uint32_t)((si & 1) * R) * 8u;
             if (!(ok = wait_all(tState + (si & 1), (uint32_t)((si >> 1) & 1)))) break;
             if (d < R) {
                 // Row d: the groups' states joined, M and L at it, and each group's weight.
@@ -966,13 +967,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 const float w = L2 == 0.f ? 0.f : (whole ? vsc : 1.f) / L2;
                 sts_f(wt + 4u * d, sum[0] == 0.f ? 0.f : f0 * w);
                 sts_f(wt + 4u * (R + d), sum[1] == 0.f ? 0.f : f1 * w);
+                const int tok = token_of(sg.r0 + d);
+                const size_t orow = head0 + (size_t)tok * p.num_qo_heads + (sg.r0 + d - tok * g);
+                const uint64_t at = (uint64_t)orow * (DH * 2);  // the row's place in o, in bytes
+                asm volatile("st.shared.b64 [%0], %1;" ::"r"(rowp + 8u * d), "l"(at) : "memory");
                 if (d < rows) {
                     const float lse2 = L2 == 0.f ? -INFINITY : M - kShift + __log2f(L2);
-                    const int tok = (sg.r0 + d) / g;
                     if (!whole)
                         p.part_lse[prow0 + d] = lse2;
                     else if (p.lse != nullptr)
-                        p.lse[head0 + (size_t)tok * p.num_qo_heads + (sg.r0 + d - tok * g)] = lse2 * 0.69314718055994531f;
+                        p.lse[orow] = lse2 * 0.69314718055994531f;
                 }
             }
             warp_arrive(bar(tHelp));
@@ -982,60 +986,73 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             tc_fence_after();
             const uint32_t tO = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + D::kColO + (uint32_t)(2 * D::OC * ob);
             // Rows eight at a time, a warp writing 32 dims of each: 64 bytes of o, or
-            // 128 of a partial state.
-            const int tok0 = sg.r0 / g;
-            int hh = sg.r0 - tok0 * g;
-            uint16_t* dst = static_cast<uint16_t*>(p.o) + (head0 + (size_t)tok0 * p.num_qo_heads + hh) * DH + d;
+            // 128 of a partial state.  Rows in pairs (packed fp32).
+            const bool both = sg.tile1 - sg.tile0 > 1;  // else one group's accumulator holds anything
+            const int g0 = j_base & 1;                  // the group of the segment's first tile
+            j_base += sg.tile1 - sg.tile0;
+            uint8_t* const o_base = static_cast<uint8_t*>(p.o) + 2 * d;
             float* part = p.part_o + prow0 * DH + d;
+            const f32x2 fold = make_f32x2(1.f / 32.f, 1.f / 32.f);
 #pragma unroll 1
             for (int r0 = 0; r0 < rows; r0 += 8) {
-                uint32_t o[2][8];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) tc_ld8(tO + D::OC * i + r0, o[i]);
-                if constexpr (!k2) {
-                    uint32_t lo[2][8];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) tc_ld8(tO + D::OC * i + R + r0, lo[i]);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            o[i][k] = __float_as_uint(fmaf(__uint_as_float(lo[i][k]), 1.f / 32.f, __uint_as_float(o[i][k])));
-                } else {
-                    tc_wait_ld();
-                }
-                if (r0 + 8 >= rows) {  // O is read: another segment may write the accumulators
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(tOEmpty + 2 * ob));
-                        mbar_arrive(bar(tOEmpty + 2 * ob + 1));
+                float o[8], o1[8];
+                {
+                    float lo[8], lo1[8];
+                    tc_ld8(tO + D::OC * g0 + r0, reinterpret_cast<uint32_t(&)[8]>(o));
+                    if constexpr (!k2) tc_ld8(tO + D::OC * g0 + R + r0, reinterpret_cast<uint32_t(&)[8]>(lo));
+                    if (both) {
+                        tc_ld8(tO + D::OC * (g0 ^ 1) + r0, reinterpret_cast<uint32_t(&)[8]>(o1));
+                        if constexpr (!k2) tc_ld8(tO + D::OC * (g0 ^ 1) + R + r0, reinterpret_cast<uint32_t(&)[8]>(lo1));
                     }
-                }
-                if (DH == 64 && d >= 64) continue;
-#pragma unroll
-                for (int k4 = 0; k4 < 8; k4 += 4) {
-                    const float4 wa = lds_f4(wt + 4u * (r0 + k4)), wb = lds_f4(wt + 4u * (R + r0 + k4));
-                    const float w0[4] = {wa.x, wa.y, wa.z, wa.w}, w1[4] = {wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (r0 + k4 + k >= rows) break;
-                        // An accumulator of weight 0 may hold anything.
-                        const float x = (w0[k] == 0.f ? 0.f : __uint_as_float(o[0][k4 + k]) * w0[k]) +
-                                        (w1[k] == 0.f ? 0.f : __uint_as_float(o[1][k4 + k]) * w1[k]);
-                        if (whole) {
-                            *dst = (uint16_t)(pack_out2(x, 0.f, p.o_dtype) & 0xFFFFu);
-                            dst += DH;
-                            if (++hh == g) {
-                                hh = 0;
-                                dst += (size_t)(p.num_qo_heads - g) * DH;
-                            }
-                        } else {
-                            *part = x;
-                            part += DH;
+                    tc_wait_ld();
+                    if (r0 + 8 >= rows) {  // O is read: another segment may write the accumulators
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(bar(tOEmpty + 2 * ob));
+                            mbar_arrive(bar(tOEmpty + 2 * ob + 1));
                         }
                     }
+                    if (DH == 64 && d >= 64) continue;
+                    const uint32_t wa = wt + 4u * (g0 * R + r0), wb = wt + 4u * ((g0 ^ 1) * R + r0);
+#pragma unroll
+                    for (int k = 0; k < 8; k += 4) {
+                        const float4 w = lds_f4(wa + 4u * k);
+                        f32x2 x = make_f32x2(o[k], o[k + 1]), y = make_f32x2(o[k + 2], o[k + 3]);
+                        if constexpr (!k2) {
+                            x = fma2(make_f32x2(lo[k], lo[k + 1]), fold, x);
+                            y = fma2(make_f32x2(lo[k + 2], lo[k + 3]), fold, y);
+                        }
+                        x = mul2(x, make_f32x2(w.x, w.y));
+                        y = mul2(y, make_f32x2(w.z, w.w));
+                        if (both) {
+                            const float4 u = lds_f4(wb + 4u * k);
+                            f32x2 x1 = make_f32x2(o1[k], o1[k + 1]), y1 = make_f32x2(o1[k + 2], o1[k + 3]);
+                            if constexpr (!k2) {
+                                x1 = fma2(make_f32x2(lo1[k], lo1[k + 1]), fold, x1);
+                                y1 = fma2(make_f32x2(lo1[k + 2], lo1[k + 3]), fold, y1);
+                            }
+                            x = fma2(x1, make_f32x2(u.x, u.y), x);
+                            y = fma2(y1, make_f32x2(u.z, u.w), y);
+                        }
+                        split_f32x2(x, o[k], o[k + 1]);
+                        split_f32x2(y, o[k + 2], o[k + 3]);
+                    }
+                }
+                const int n = rows - r0;
+                if (whole) {
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) {
+                        const uint32_t v2 = pack_out2(o[k], o[k + 1], p.o_dtype);
+                        const uint4 at = lds128(rowp + 8u * (r0 + k));  // two rows' places
+                        if (k < n) *reinterpret_cast<uint16_t*>(o_base + (((uint64_t)at.y << 32) | at.x)) = (uint16_t)v2;
+                        if (k + 1 < n) *reinterpret_cast<uint16_t*>(o_base + (((uint64_t)at.w << 32) | at.z)) = (uint16_t)(v2 >> 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < n) part[k * DH] = o[k];
+                    part += 8 * DH;
                 }
             }
         }
