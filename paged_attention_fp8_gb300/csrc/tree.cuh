@@ -183,6 +183,13 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
 }
 __device__ __forceinline__ void sts_f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 
+// A value that every lane holds, in a form that the compiler knows to be the
+// same in all of them.  Control flow on anything else (a loaded loop bound, a
+// warp index from threadIdx) counts as divergent, and every shuffle, vote or
+// reduction under it is then compiled with a fallback that costs hundreds of
+// cycles: a segment's column sums took 9000 cycles that way.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
 // Bounded wait that gives up once another role has (`flag`), and past `limit`
 // cycles sets the flag and the status bit itself.  The loop is one compact asm
 // block: some thirty waits are inlined, and the instruction cache holds little
@@ -234,7 +241,8 @@ __device__ __forceinline__ Seg load_seg(const int* segs, uint32_t cache, int i) 
         const int4* r = reinterpret_cast<const int4*>(segs + kTreeSegWords * (long long)i);
         a = __ldg(r), b = __ldg(r + 1), c = __ldg(r + 2);
     }
-    return Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x};
+    return Seg{uniform(a.x), uniform(a.y), uniform(a.z), uniform(a.w), uniform(b.x), uniform(b.y), uniform(b.z), uniform(b.w),
+               uniform(c.x)};
 }
 
 // 32 bits of mask row `row` from bit u0 on (bits below 0: keys of the context,
@@ -336,11 +344,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const TreeSmem L = tree_smem<D, R, NP>(p.q_buffers * p.q_pieces, p.stages);
     auto bar = [&](int i) -> uint32_t { return base + L.bars + 8u * (uint32_t)i; };
     const uint32_t flag = base + L.abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int NS = p.stages, NQB = p.q_buffers;
     const int* meta = p.meta;
     const int s_first = __ldg(meta + meta[kMetaOffCtaSeg] + blockIdx.x);
-    const int n_seg = __ldg(meta + meta[kMetaOffCtaSeg] + blockIdx.x + 1) - s_first;
+    const int n_seg = uniform(__ldg(meta + meta[kMetaOffCtaSeg] + blockIdx.x + 1) - s_first);
     const int* segs = meta + meta[kMetaOffSeg] + kTreeSegWords * (long long)s_first;
     const uint32_t seg_cache = base + L.seg;
     const int g = p.group;
@@ -477,11 +485,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t idesc_qk = make_idesc(kvf, qf, 128, R);
         const uint32_t idesc_pv = make_idesc_mn(kvf, k2 ? kvf : 0, 128, D::OC);
         const uint32_t idesc_p3 = make_idesc_mn(kvf, 0, 128, R);
-        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-        const int n_seg_u = __shfl_sync(0xFFFFFFFFu, n_seg, 0);
+        const uint32_t tm = (uint32_t)uniform((int)tmem);
         auto tiles_of = [&](int si) -> int {
             const Seg sg = load_seg(segs, seg_cache, si);
-            return __shfl_sync(0xFFFFFFFFu, sg.tile1 - sg.tile0, 0);
+            return sg.tile1 - sg.tile0;
         };
         // Descriptors: the constant halves, and the words of the tiles at offset 0.
         constexpr uint64_t kQKd = (k2 || DH == 128) ? 1 : 0;  // 128-byte rows, else 64
@@ -498,10 +505,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         uint32_t kphase = 0, vphase = 0;
         int sbuf = 0, pbuf = 0;        // ring of three: S of QK's tile, P of PV's
         uint32_t pphase = 0;
-        int qleft = n_seg_u > 0 ? tiles_of(0) : 0;
+        int qleft = n_seg > 0 ? tiles_of(0) : 0;
         bool qfirst = true;
         int pn = 0;
-        for (int ps = 0; ps < n_seg_u && ok; ++ps) {
+        for (int ps = 0; ps < n_seg && ok; ++ps) {
             const int ob = ps % NOB;
             const int nt = tiles_of(ps);
             for (int t = 0; t < nt; ++t, ++pn) {
@@ -509,7 +516,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 // the one after is built only when this one's epilogue is done).  So
                 // QK(j) follows PV(j - 3), which waited for P(j - 3): S(j - 3) has been
                 // read, and once S(j) is complete so is PV(j - 3) and P's buffer free.
-                while (qs < n_seg_u && qn <= pn + 2 && qs <= ps + 1) {
+                while (qs < n_seg && qn <= pn + 2 && qs <= ps + 1) {
                     if (qfirst) {
                         if (!(ok = wait_all(tQFull + qbuf, qphase))) break;
                         qfirst = false;
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             qphase ^= 1u;
                         }
                         qfirst = true;
-                        if (++qs < n_seg_u) qleft = tiles_of(qs);
+                        if (++qs < n_seg) qleft = tiles_of(qs);
                     }
                 }
                 if (!ok) break;
@@ -630,9 +637,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const int ctx = sg.kv_len - sg.qo_len;
             const uint32_t tO = lane_base + D::kColO + (uint32_t)(D::OC * (2 * (si % NOB) + gr));
             const uint32_t sct = base + L.sc + (uint32_t)((si & 1) * R) * 4u;
-            f32x2 l[R / 2];
+            // Sums of P' over this thread's keys, rows 0-31 and 32-63.
+            f32x2 l[R / 32][16];
 #pragma unroll
-            for (int i = 0; i < R / 2; ++i) l[i] = make_f32x2(0.f, 0.f);
+            for (int i = 0; i < 16; ++i) l[0][i] = l[R / 32 - 1][i] = make_f32x2(0.f, 0.f);
             // Mask bits of this warp's 32 keys of a tile, lane i holding those of rows
             // i and i + 32, fetched a tile ahead.
             constexpr int NL = R / 32;
@@ -663,12 +671,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 const uint32_t pb = base + L.p + (uint32_t)buf * (NP * D::kPPiece);
                 // 32 rows at a time: P' in place of the logits.  The vote on the reference
                 // maxima is cast before the exponentials and read after P is stored, so
-                // its latency passes meanwhile; a raised reference redoes the rows.
-#pragma unroll
+                // its latency passes meanwhile; a raised reference redoes the rows.  Rolled:
+                // with two copies of this code the rare path was never in the
+                // instruction cache and cost 6000 cycles each time.
+#pragma unroll 1
                 for (int sub = 0; sub < NL; ++sub) {
                     const uint32_t tSs = tS + 32u * sub, scs = sct + 128u * sub, ngs = negt + 128u * sub, als = alt + 128u * sub;
                     float v[32];
-                    bool rise = first;
+                    int rise = first;
 #pragma unroll 1
                     while (true) {
                         ld_cols<32>(tSs, v);
@@ -676,7 +686,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         if ((t + 1) * kTileKeys > ctx) {  // keys that a row does not see become -inf
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                if (!((__shfl_sync(0xFFFFFFFFu, bits[sub], c) >> lane) & 1u)) v[c] = -INFINITY;
+                                if (!((__shfl_sync(0xFFFFFFFFu, sub == 0 ? bits[0] : bits[NL - 1], c) >> lane) & 1u)) v[c] = -INFINITY;
                         }
                         if (rise) {
                             // Column maxima of the tile: over this warp's lanes, then over the
@@ -717,10 +727,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                     st_cols<32>(tO + c0, o);
                                 }
 #pragma unroll
-                                for (int i = 0; i < 32; i += 4) {
-                                    const float4 a = lds_f4(als + 4u * i);
-                                    l[16 * sub + i / 2] = mul2(l[16 * sub + i / 2], make_f32x2(a.x, a.y));
-                                    l[16 * sub + i / 2 + 1] = mul2(l[16 * sub + i / 2 + 1], make_f32x2(a.z, a.w));
+                                for (int i = 0; i < 16; i += 2) {
+                                    const float4 a = lds_f4(als + 8u * i);
+                                    const f32x2 a0 = make_f32x2(a.x, a.y), a1 = make_f32x2(a.z, a.w);
+                                    if (sub == 0) {
+                                        l[0][i] = mul2(l[0][i], a0);
+                                        l[0][i + 1] = mul2(l[0][i + 1], a1);
+                                    } else {
+                                        l[NL - 1][i] = mul2(l[NL - 1][i], a0);
+                                        l[NL - 1][i + 1] = mul2(l[NL - 1][i + 1], a1);
+                                    }
                                 }
                                 tc_wait_st();
                             }
@@ -751,7 +767,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         const uint32_t swz = W == 128 ? krow & 7 : W == 64 ? (krow >> 1) & 3 : (krow >> 2) & 1;
 #pragma unroll
                         for (int c = 0; c < 32; c += kElems) {
-                            const uint32_t at = pb + (uint32_t)krow * W + (((uint32_t)((32 * sub + c) / kElems) ^ swz) << 4);
+                            const uint32_t at = pb + (uint32_t)krow * W + (((uint32_t)(32 / kElems * sub + c / kElems) ^ swz) << 4);
                             uint32_t w0[4], w1[4], w2[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
@@ -770,12 +786,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         if (rise) break;
                         if (!(ok = wait_all(vbar, hphase))) break;
                         hphase ^= 1u;
-                        if (lds_u(slot) != ballots) break;
-                        rise = true;
+                        if (!__any_sync(0xFFFFFFFFu, lds_u(slot) == ballots)) break;
+                        rise = 1;
                     }
                     if (!ok) break;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) l[16 * sub + i] = add2(l[16 * sub + i], make_f32x2(v[2 * i], v[2 * i + 1]));
+                    for (int i = 0; i < 16; ++i) {
+                        const f32x2 e = make_f32x2(v[2 * i], v[2 * i + 1]);
+                        if (sub == 0)
+                            l[0][i] = add2(l[0][i], e);
+                        else
+                            l[NL - 1][i] = add2(l[NL - 1][i], e);
+                    }
                 }
                 if (!ok) break;
                 // Value rows behind the request's end (the tail of its last page and
@@ -805,11 +827,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             // The segment's sums (over this warp's keys) and this group's maxima for
             // the epilogue; a group without a tile in it leaves an empty state.
             const bool none = t_first >= sg.tile1;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < NL; ++i) {
                 float ls[32];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) split_f32x2(l[16 * i + c], ls[2 * c], ls[2 * c + 1]);
+                for (int c = 0; c < 16; ++c) split_f32x2(i == 0 ? l[0][c] : l[NL - 1][c], ls[2 * c], ls[2 * c + 1]);
                 const float sum = column_sum(ls, lane);
                 const int row = 32 * i + lane;
                 sts_f(base + L.lsum + 4u * (((si & 1) * 8 + warp) * R + row), sum);
