@@ -375,9 +375,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_init(bar(tHelp), 4);
         mbar_init(bar(tDrain), 1);
         for (int i = 0; i < NS; ++i) {
-            mbar_init(bar(tKFull + i), 3);  // producer warps
+            mbar_init(bar(tKFull + i), 1);  // the tile's producer warp
             mbar_init(bar(tKEmpty + i), 1);
-            mbar_init(bar(tVFull + i), 3);
+            mbar_init(bar(tVFull + i), 1);
             mbar_init(bar(tVEmpty + i), 1);
         }
         for (int i = 0; i < 4; ++i) sts32(base + L.vote + 4 * i, 0);
@@ -397,79 +397,80 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
       if (warp != 13) {
         // ----------------------------------------------------------- producers
-        // A box holds the 16 tokens of one (sub-)page, and a warp's box takes it
-        // about 130 cycles to issue, 16 boxes a tile 2100: more than the tile's
-        // time at full bandwidth (1400).  So three warps share the boxes, every
-        // third one each, and each warp expects its own bytes.
+        // A box holds the 16 tokens of one (sub-)page; a warp takes about 130 cycles
+        // to issue one, 16 a tile 2100, more than the tile's time at full bandwidth
+        // (1400).  So three warps take every third tile each.  A warp that waits
+        // for a V slot (freed by the tile's softmax and PV) holds up none of the
+        // next two tiles' K.  With two stages only two warps take part: a wait
+        // names its phase by parity, so it has to follow the completion of the
+        // phase two before, that is, of tile n - 2 stages; the warp's tile before,
+        // n - step, vouches for tile n - step - stages, which is enough when step
+        // <= stages.
         const int pw = warp == 12 ? 0 : warp - 13;
+        const int step = min(3, NS);
         if (lane == 0) {
             prefetch_tmap(&tmk);
             prefetch_tmap(&tmv);
         }
-        constexpr int kBoxes = 8 * (k2 ? NH : 1);      // boxes of a K or V tile: (half, sub-page)
-        const int box = 3 * lane + pw, i8 = box & 7;   // this lane's box
+        constexpr int kBoxes = 8 * (k2 ? NH : 1);  // boxes of a K or V tile, one a lane: (half, sub-page)
         constexpr uint32_t kBoxBytes = k2 ? 2048u : (uint32_t)(kPageSize * DH);
-        int n = 0;  // tiles issued
-        int stage = 0;
-        uint32_t phase = 0;
+        const int m = p.page_mult;
+        int n = pw < step ? pw : 1 << 30, total = 0;  // this warp's next tile; tiles of the segments so far
+        int stage = pw % NS;
+        uint32_t phase = (uint32_t)(pw / NS) & 1u;
         bool ok = true, k_only = false;
         for (int si = 0; si < n_seg && ok; ++si) {
             const Seg sg = load_seg(segs, seg_cache, si);
-            const int m = p.page_mult;
             const int nsub = (sg.kv_len + kPageSize - 1) / kPageSize;  // 16-token sub-pages of the request
             const int* idx = p.kv_indices + sg.page0;
             auto fetch = [&](int tile) -> int {  // the page entry of this lane's sub-page
-                const int v = tile * (kTileKeys / kPageSize) + i8;
+                const int v = tile * (kTileKeys / kPageSize) + (lane & 7);
                 return v < nsub ? __ldg(idx + (m == 1 ? v : v / m)) : 0;
             };
-            int next = fetch(sg.tile0);
-            for (int t = sg.tile0; t < sg.tile1 && ok; ++t) {
+            int t = min(sg.tile0 + (n - total), sg.tile1 + 8);
+            total += sg.tile1 - sg.tile0;
+            int next = t < sg.tile1 ? fetch(t) : 0;
+            for (; t < sg.tile1; t += step, n += step) {
                 int page = next;
-                if (t + 1 < sg.tile1) next = fetch(t + 1);
-                const int sub = t * (kTileKeys / kPageSize) + i8;
-                const bool mine = box < kBoxes && sub < nsub;
-                const bool bad = mine && (page < 0 || page >= p.num_pages);
-                if (bad) {
+                if (t + step < sg.tile1) next = fetch(t + step);
+                const int sub = t * (kTileKeys / kPageSize) + (lane & 7);
+                const bool mine = lane < kBoxes && sub < nsub;
+                if (mine && (page < 0 || page >= p.num_pages)) {
                     page = 0;
                     atomicOr(p.status, kStatusBounds);
                 }
                 const int slot = m == 1 ? 0 : (sub % m) * kPageSize;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, mine)) * kBoxBytes;
                 for (int kv = 0; kv < 2; ++kv) {
-                    const int full = (kv ? tVFull : tKFull) + stage, empty = (kv ? tVEmpty : tKEmpty) + stage;
-                    if (lane == 0) {
-                        ok = wait(empty, phase ^ 1u);
-                        if (ok) mbar_arrive_expect_tx(bar(full), bytes);
-                    }
-                    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-                    if (!ok) {
+                    const int full = (kv ? tVFull : tKFull) + stage;
+                    if (!(ok = wait_all((kv ? tVEmpty : tKEmpty) + stage, phase ^ 1u))) {
                         k_only = kv == 1;
                         break;
                     }
+                    if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
+                    __syncwarp();
                     const CUtensorMap* map = kv ? &tmv : &tmk;
-                    const uint32_t dst = base + (kv ? L.v : L.k) + (uint32_t)stage * kTile + (uint32_t)box * kBoxBytes;
+                    const uint32_t dst = base + (kv ? L.v : L.k) + (uint32_t)stage * kTile + (uint32_t)lane * kBoxBytes;
                     if (mine) {
                         if constexpr (k2)
-                            tma_load_5d(dst, map, bar(full), 0, box >> 3, slot, sg.hk, page);
+                            tma_load_5d(dst, map, bar(full), 0, lane >> 3, slot, sg.hk, page);
                         else
                             tma_load_4d(dst, map, bar(full), 0, sg.hk, slot, page);
                     }
                     __syncwarp();
                 }
                 if (!ok) break;
-                ++n;
-                if (++stage == NS) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                for (stage += step; stage >= NS; stage -= NS) phase ^= 1u;
             }
         }
         if (lane == 0) {
-            // Every copy lands before the CTA may exit.
-            const int nk = n + (k_only ? 1 : 0);
-            for (int s = 0; s < NS; ++s) {
-                if (s < nk) mbar_wait(bar(tKFull + s), (uint32_t)(((nk - 1 - s) / NS) & 1));
-                if (s < n) mbar_wait(bar(tVFull + s), (uint32_t)(((n - 1 - s) / NS) & 1));
+            // Every copy of this warp lands before the CTA may exit: its tiles that are
+            // the last on their stage (after an abort, its last ones).
+            const int end = ok ? total : n + 1;
+            if (!ok && k_only) mbar_wait(bar(tKFull + n % NS), (uint32_t)((n / NS) & 1));
+            for (int x = n - step; pw < step && x >= 0 && x + NS >= end; x -= step) {
+                mbar_wait(bar(tKFull + x % NS), (uint32_t)((x / NS) & 1));
+                mbar_wait(bar(tVFull + x % NS), (uint32_t)((x / NS) & 1));
             }
         }
         __syncwarp();
