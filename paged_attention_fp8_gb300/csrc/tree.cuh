@@ -122,7 +122,7 @@ struct TreeDims {
 };
 
 struct TreeSmem {
-    uint32_t q, k, v, p, sc, neg, alpha, wmax, lsum, mst, wt, rowp, seg, vote, bars, tmem_slot, abort_flag, bytes;
+    uint32_t q, k, v, p, sc, neg, alpha, wmax, lsum, mst, wt, rowp, seg, bars, tmem_slot, abort_flag, bytes;
 };
 enum TreeBar : int {
     tQFull = 0,              // [2]
@@ -133,10 +133,9 @@ enum TreeBar : int {
     tPFull = 11,             // [3]
     tOFull = 14,             // [2]
     tOEmpty = 16,            // [2 buffers][2 groups]
-    tVote = 20,              // [2] the four warps of a group
-    tHelp = 22,              // the helper warps
-    tDrain = 23,
-    tKFull = 24,
+    tHelp = 20,              // the helper warps
+    tDrain = 21,
+    tKFull = 22,
     tKEmpty = tKFull + kMaxStages,
     tVFull = tKEmpty + kMaxStages,
     tVEmpty = tVFull + kMaxStages,
@@ -158,8 +157,7 @@ __host__ __device__ inline TreeSmem tree_smem(int q_tiles, int stages) {
     s.wt = s.mst + 2 * 2 * R * 4;           // [2][group][R]
     s.rowp = s.wt + 2 * 2 * R * 4;          // [2][R] byte offsets of the rows in o (64 bits)
     s.seg = s.rowp + 2 * R * 8;             // the CTA's first kSegCache segment records
-    s.vote = s.seg + kSegCache * kTreeSegWords * 4;  // [group][2] words
-    s.bars = s.vote + 16;
+    s.bars = s.seg + kSegCache * kTreeSegWords * 4;
     s.tmem_slot = s.bars + 8 * tNumBars;
     s.abort_flag = s.tmem_slot + 4;
     s.bytes = s.abort_flag + 4;
@@ -316,6 +314,20 @@ __device__ __forceinline__ void st_cols(uint32_t t, const float (&v)[NC]) {
     }
 }
 
+// The 128 threads of a softmax group meet; true if any of them says so.  A
+// hardware barrier and not an mbarrier: the votes of an mbarrier's waiters came
+// 400 cycles late.  It has no bound, so every warp of a group goes through the
+// same barriers whatever its own waits did, and the group leaves together.
+__device__ __forceinline__ bool group_any(int id, bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)mine)
+        : "memory");
+    return __any_sync(0xFFFFFFFFu, r != 0);
+}
+
 // Sums of v[0 .. 31] over the warp's lanes: lane l returns column l's.
 __device__ __forceinline__ float column_sum(float (&a)[32], int lane) {
 #pragma unroll
@@ -365,7 +377,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(bar(tInfo + i), 4);
             mbar_init(bar(tState + i), 8);   // softmax warps
             mbar_init(bar(tOFull + i), 1);
-            mbar_init(bar(tVote + i), 4);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(bar(tSFull + i), 1);
@@ -380,7 +391,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(bar(tVFull + i), 1);
             mbar_init(bar(tVEmpty + i), 1);
         }
-        for (int i = 0; i < 4; ++i) sts32(base + L.vote + 4 * i, 0);
         asm volatile("st.shared.u32 [%0], 0;" ::"r"(flag) : "memory");
         mbar_init_fence();
     }
@@ -613,8 +623,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
         const uint32_t negt = base + L.neg + (uint32_t)(warp * R) * 4u;
         const uint32_t alt = base + L.alpha + (uint32_t)(warp * R) * 4u;
-        const uint32_t votes = base + L.vote + 8u * gr;
-        const int vbar = tVote + gr;
+        const int vbar = 1 + gr;                    // the group's hardware barrier
         // Ring positions of this group's current tile: V stage (and the one of its
         // tile before), S and P buffer.
         int stage = 0, prev_stage = 0, buf = 0;
@@ -630,9 +639,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
         };
         int j = 0;  // tiles of the CTA before the next one
-        uint32_t hphase = 0, wbuf = 0, ballots = 0;
-        bool ok = true;
-        for (int si = 0; si < n_seg && ok; ++si) {
+        uint32_t wbuf = 0;
+        // Whether one of this warp's waits gave up: it goes on (its results no
+        // longer matter) until the group's next vote, where all four leave.
+        bool dead = false, out = false;
+        for (int si = 0; si < n_seg && !out; ++si) {
             const Seg sg = load_seg(segs, seg_cache, si);
             const int rows = min(R, sg.qo_len * g - sg.r0);
             const int ctx = sg.kv_len - sg.qo_len;
@@ -659,20 +670,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             };
             const int t_first = sg.tile0 + ((j ^ gr) & 1);  // this group's first tile of the segment
             fetch_bits(t_first);
-            if (!(ok = wait_all(tInfo + (si & 1), (uint32_t)((si >> 1) & 1)))) break;
-            for (int t = sg.tile0; t < sg.tile1 && ok; ++t, ++j) {
+            dead |= !wait_all(tInfo + (si & 1), (uint32_t)((si >> 1) & 1));
+            for (int t = sg.tile0; t < sg.tile1 && !out; ++t, ++j) {
                 if ((j & 1) != gr) {
                     advance();
                     continue;
                 }
                 const bool first = t == t_first;
                 const uint32_t tS = lane_base + (uint32_t)(R * buf);
-                if (!(ok = wait_all(tSFull + buf, bphase))) break;
+                dead |= !wait_all(tSFull + buf, bphase);
                 tc_fence_after();
                 const uint32_t pb = base + L.p + (uint32_t)buf * (NP * D::kPPiece);
-                // 32 rows at a time: P' in place of the logits.  The vote on the reference
-                // maxima is cast before the exponentials and read after P is stored, so
-                // its latency passes meanwhile; a raised reference redoes the rows.  Rolled:
+                // 32 rows at a time: P' in place of the logits.  After P is stored the group
+                // votes on the reference maxima; a raised one redoes the rows.  Rolled:
                 // with two copies of this code the rare path was never in the
                 // instruction cache and cost 6000 cycles each time.
 #pragma unroll 1
@@ -701,9 +711,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             const uint32_t wm = base + L.wmax + (uint32_t)((wbuf * 2 + gr) * 128 + lane) * 4u;
                             wbuf ^= 1u;
                             sts_f(wm + 128u * quad, cm);
-                            warp_arrive(bar(vbar));
-                            if (!(ok = wait_all(vbar, hphase))) break;
-                            hphase ^= 1u;
+                            group_any(vbar, false);
                             const float top = fmaxf(max3(lds_f(wm), lds_f(wm + 128u), lds_f(wm + 256u)), lds_f(wm + 384u)) * lds_f(scs + 4u * lane);
                             const float was = first ? kUnseen : lds_f(ngs + 4u * lane);
                             const float m_old = was >= kUnseen ? -INFINITY : kShift - was;
@@ -713,7 +721,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             __syncwarp();
                             if (!first) {
                                 // This accumulator's last update has to be complete.
-                                if (!(ok = wait_all(tVEmpty + prev_stage, prev_phase))) break;
+                                dead |= !wait_all(tVEmpty + prev_stage, prev_phase);
                                 tc_fence_after();
 #pragma unroll 1
                                 for (int c0 = 32 * sub; c0 < D::OC; c0 += R) {  // O_hi, O_lo
@@ -751,15 +759,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             split_f32x2(fma2(make_f32x2(v[c + 2], v[c + 3]), make_f32x2(sc.z, sc.w), make_f32x2(ng.z, ng.w)),
                                         v[c + 2], v[c + 3]);
                         }
-                        const uint32_t slot = votes + 4u * (ballots & 1u);
-                        if (!rise) {
-                            float pm[2] = {v[0], v[1]};
+                        float pm[2] = {v[0], v[1]};
 #pragma unroll
-                            for (int c = 2; c < 32; c += 2) pm[(c >> 1) & 1] = max3(pm[(c >> 1) & 1], v[c], v[c + 1]);
-                            ++ballots;
-                            if (__any_sync(0xFFFFFFFFu, fmaxf(pm[0], pm[1]) > kShift + kHead) && lane == 0) sts32(slot, ballots);
-                            warp_arrive(bar(vbar));
-                        }
+                        for (int c = 2; c < 32; c += 2) pm[(c >> 1) & 1] = max3(pm[(c >> 1) & 1], v[c], v[c + 1]);
 #pragma unroll
                         for (int c = 0; c < 32; ++c) v[c] = ex2(v[c]);
                         // P into shared memory: the buffer's last product was complete before S.
@@ -784,13 +786,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             if constexpr (!k2) sts128(at + D::kPPiece, w1[0], w1[1], w1[2], w1[3]);
                             if constexpr (NP == 3) sts128(at + 2 * D::kPPiece, w2[0], w2[1], w2[2], w2[3]);
                         }
-                        if (rise) break;
-                        if (!(ok = wait_all(vbar, hphase))) break;
-                        hphase ^= 1u;
-                        if (!__any_sync(0xFFFFFFFFu, lds_u(slot) == ballots)) break;
+                        if (!group_any(vbar, dead || (!rise && fmaxf(pm[0], pm[1]) > kShift + kHead))) break;
+                        if (group_any(vbar, dead)) {
+                            out = true;
+                            break;
+                        }
                         rise = 1;
                     }
-                    if (!ok) break;
+                    if (out) break;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const f32x2 e = make_f32x2(v[2 * i], v[2 * i + 1]);
@@ -800,13 +803,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             l[NL - 1][i] = add2(l[NL - 1][i], e);
                     }
                 }
-                if (!ok) break;
+                if (out) break;
                 // Value rows behind the request's end (the tail of its last page and
                 // rows no page filled) hold anything: zero them, P = 0 there must
                 // not meet a NaN.
                 const int valid = sg.kv_len - t * kTileKeys;
                 if (valid < kTileKeys) {
-                    if (!(ok = wait_all(tVFull + stage, vphase))) break;
+                    dead |= !wait_all(tVFull + stage, vphase);
                     if (krow >= valid) {
                         const uint32_t vrow = base + L.v + (uint32_t)stage * kTile + (uint32_t)krow * (k2 ? 128u : (uint32_t)DH);
 #pragma unroll
@@ -824,7 +827,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 prev_phase = vphase;
                 advance();
             }
-            if (!ok) break;
+            if (out) break;
             // The segment's sums (over this warp's keys) and this group's maxima for
             // the epilogue; a group without a tile in it leaves an empty state.
             const bool none = t_first >= sg.tile1;
