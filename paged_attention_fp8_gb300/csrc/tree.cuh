@@ -192,9 +192,11 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, 
 // cycles sets the flag and the status bit itself.  The loop is one compact asm
 // block: some thirty waits are inlined, and the instruction cache holds little
 // more than the tile loops.  `hint` is how long (ns) one try may suspend the
-// thread: waiting warps that poll take issue slots from the working ones.
-// With hint 0 (a shortened limit, which a suspended try could outlast) it only
+// thread; NAP, how long it sleeps between tries: a warp that polls takes issue
+// slots from the working ones (eight polling warps took a fifth of them), so the
+// roles that run ahead or wait long sleep.  With hint 0 (a shortened limit, which a suspended try could outlast) it only
 // tests.
+template <int NAP>
 __device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, uint32_t flag, uint32_t* status, long long limit,
                                           uint32_t hint) {
     if (mbar_test_wait(bar, parity)) return true;
@@ -206,13 +208,14 @@ __device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, uint32_
         " @q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " @!q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %6;\n @p bra DONE;\n"
         " ld.volatile.shared.u32 f, [%3];\n setp.ne.u32 p, f, 0;\n @p bra FAIL;\n"
+        " nanosleep.u32 %8;\n"
         " mov.u64 u, %%clock64;\n sub.s64 u, u, t;\n setp.le.s64 p, u, %5;\n @p bra LOOP;\n"
         " st.shared.u32 [%3], 1;\n red.global.or.b32 [%4], %7;\n"
         "FAIL:\n mov.u32 %0, 0;\n bra END;\n"
         "DONE:\n mov.u32 %0, 1;\n"
         "END:\n}\n"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(flag), "l"(status), "l"(limit), "r"(hint), "n"((int)kStatusTimeout)
+        : "r"(bar), "r"(parity), "r"(flag), "l"(status), "l"(limit), "r"(hint), "n"((int)kStatusTimeout), "n"(NAP)
         : "memory");
     return ok != 0;
 }
@@ -367,8 +370,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // n / group for n < 2^25 (a plan has no more rows in a request).
     auto token_of = [&](int n) -> int { return g == 1 ? n : (int)__umulhi((uint32_t)n, p.group_magic); };
     const uint32_t hint = p.wait_cycles < kWaitCyclesDefault ? 0u : 20000u;
-    auto wait = [&](int b, uint32_t parity) { return tree_wait(bar(b), parity, flag, p.status, p.wait_cycles, hint); };
-    auto wait_all = [&](int b, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(b, parity)); };
+    auto wait_all = [&](int b, uint32_t parity) {
+        return (bool)__all_sync(0xFFFFFFFFu, tree_wait<0>(bar(b), parity, flag, p.status, p.wait_cycles, hint));
+    };
+    auto wait_idle = [&](int b, uint32_t parity) {  // for the roles that may come a little late
+        return (bool)__all_sync(0xFFFFFFFFu, tree_wait<100>(bar(b), parity, flag, p.status, p.wait_cycles, hint));
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -453,7 +460,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, mine)) * kBoxBytes;
                 for (int kv = 0; kv < 2; ++kv) {
                     const int full = (kv ? tVFull : tKFull) + stage;
-                    if (!(ok = wait_all((kv ? tVEmpty : tKEmpty) + stage, phase ^ 1u))) {
+                    if (!(ok = wait_idle((kv ? tVEmpty : tKEmpty) + stage, phase ^ 1u))) {
                         k_only = kv == 1;
                         break;
                     }
@@ -890,7 +897,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     }
                 }
                 if (!ready) {  // the buffer is free once its last segment's QK has run
-                    if (!wait_all(tQEmpty + buf, (uint32_t)((use + 1) & 1))) return false;
+                    if (!wait_idle(tQEmpty + buf, (uint32_t)((use + 1) & 1))) return false;
                     ready = true;
                 }
 #pragma unroll 1
@@ -976,7 +983,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const size_t head0 = (size_t)sg.qo0 * p.num_qo_heads + (size_t)sg.hk * g;
             const size_t prow0 = (size_t)max(sg.slot, 0) * p.rows_pad;
             const uint32_t wt = base + L.wt + (uint32_t)((si & 1) * 2 * R) * 4u, rowp = base + L.rowp + (uint32_t)((si & 1) * R) * 8u;
-            if (!(ok = wait_all(tState + (si & 1), (uint32_t)((si >> 1) & 1)))) break;
+            if (!(ok = wait_idle(tState + (si & 1), (uint32_t)((si >> 1) & 1)))) break;
             if (d < R) {
                 // Row d: the groups' states joined, M and L at it, and each group's weight.
                 float m[2], sum[2] = {0.f, 0.f};
