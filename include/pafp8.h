@@ -309,9 +309,10 @@ pafp8_status pafp8_run_head_scales(const pafp8_plan *plan, int32_t q_dtype, cons
  * prefill plan (fp8 cache with any query, 2-byte cache of the query's own
  * dtype), head_dim 128 or 64, both layouts, up to 128 query heads per KV
  * head.  A 2-byte query over an fp8 cache is multiplied exactly to 2^-18 of
- * its row's largest magnitude; probabilities are rounded to 8 significant
- * bits for a bf16 output over an fp8 cache, 12 for an f16 one, and to the
- * cache's type over a 2-byte cache.  A NaN or infinity in the value row of a
+ * its row's largest magnitude; probabilities are rounded to a bf16's 8
+ * significant bits for a bf16 output over an fp8 cache (those below 2^-11 of
+ * the row's largest to 2^-19 of it), an f16's 11 for an f16 output (2^-20 of
+ * it), and to the cache's type over a 2-byte cache.  A NaN or infinity in the value row of a
  * cached token reaches every drafted token of its request, whether its mask
  * shows that token or not. */
 pafp8_status pafp8_run_tree(const pafp8_plan *plan, int32_t q_dtype, const void *q, int32_t k_dtype,

@@ -475,14 +475,13 @@ void build_prefill_meta(pafp8_plan* pl) {
 
 // Tree partition.  A line is a (request, row tile) pair -- the request's rows
 // (token, head of the group) cut into tiles of tile_rows --, its cost its
-// 128-key tiles plus kTreeSegCost for starting it.  Heads are dealt to CTAs in
+// 128-key tiles plus seg_cost for starting it.  Heads are dealt to CTAs in
 // blocks of hb (a divisor of the KV heads): the lines, laid end to end once per
 // head block, are cut into num_ctas / hb ranges of equal cost, and CTA i * hb +
 // h takes range i for head h of the block, so the CTAs reading the heads of one
 // token-major page run at the same time.  hb is the largest divisor whose
 // busiest CTA is within 3 % of the best one's.  A segment that is not its whole
 // line has a slot for its partial state; a split line's slots are consecutive.
-constexpr int kTreeSegCost = 1;
 void build_tree_meta(pafp8_plan* pl) {
     const int B = pl->desc.batch, hkv = pl->desc.num_kv_heads, g = pl->group;
     struct Line { int32_t b, r0, nt; };
@@ -496,13 +495,19 @@ void build_tree_meta(pafp8_plan* pl) {
     const int RT = tree_tile_rows((int)std::min<int64_t>(most_rows, 1 << 20));
     pl->tile_rows = RT;
     pl->rows_pad = (int)std::min<int64_t>(most_rows, RT);
+    // What starting a segment costs, in tiles: its first maxima, the sums at its
+    // end and its epilogue take 64 rows of an fp8 cache about five tiles' time
+    // (64 requests of 512-4096 keys: 94.9 us at cost 1, 89.4 at 4 and 6, 90.4 at
+    // 8, before P's second piece shared the first's accumulator); 32 rows, or the longer tiles of a 2-byte cache, about two (60.0 us at
+    // 1 and 3, 63.3 at 6).
+    const int seg_cost = RT == 64 && is_fp8(pl->desc.kv_dtype) ? 5 : 2;
     for (int b = 0; b < B; ++b) {
         const int64_t rows = (int64_t)(pl->qo_indptr[b + 1] - pl->qo_indptr[b]) * g;
         const int32_t n = pl->kv_indptr[b + 1] - pl->kv_indptr[b];
         const int64_t kv = n > 0 ? (int64_t)(n - 1) * pl->desc.page_size + pl->last_page_len[b] : 0;
         for (int64_t r0 = 0; r0 < rows; r0 += RT) {
             lines.push_back({b, (int32_t)r0, (int32_t)((kv + kTileKeys - 1) / kTileKeys)});
-            cost += lines.back().nt + kTreeSegCost;
+            cost += lines.back().nt + seg_cost;
         }
     }
     int hb = 1;
@@ -518,7 +523,7 @@ void build_tree_meta(pafp8_plan* pl) {
                 else if (100 * busiest <= 103 * best)
                     hb = d;
             }
-        groups = std::max<int64_t>(1, std::min<int64_t>(pl->desc.num_ctas / hb, (int64_t)(hkv / hb) * (cost - (int64_t)lines.size() * kTreeSegCost)));
+        groups = std::max<int64_t>(1, std::min<int64_t>(pl->desc.num_ctas / hb, (int64_t)(hkv / hb) * (cost - (int64_t)lines.size() * seg_cost)));
     }
     const int nhb = hkv / hb;
     const int64_t total = cost * nhb;
@@ -532,11 +537,11 @@ void build_tree_meta(pafp8_plan* pl) {
         auto end_of = [&](int64_t k) { return (k + 1) * total / groups; };
         for (int blk = 0; blk < nhb; ++blk)
             for (size_t l = 0; l < lines.size(); ++l) {
-                const int64_t c = lines[l].nt + kTreeSegCost;
+                const int64_t c = lines[l].nt + seg_cost;
                 int64_t a = 0;  // tiles of this line placed
                 while (a < lines[l].nt) {
                     // Tiles of this line that end inside range i.
-                    int64_t e = i + 1 >= groups ? lines[l].nt : std::min<int64_t>(lines[l].nt, end_of(i) - at - kTreeSegCost);
+                    int64_t e = i + 1 >= groups ? lines[l].nt : std::min<int64_t>(lines[l].nt, end_of(i) - at - seg_cost);
                     if (e > a) {
                         parts.push_back({blk, (int32_t)l, (int32_t)a, (int32_t)e});
                         a = e;

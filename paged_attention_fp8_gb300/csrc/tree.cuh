@@ -21,13 +21,19 @@
 //     piece the e4m3 rounding of what the earlier ones left, exact but for
 //     elements below 2^-10 of the row's largest, which lose 2^-18 of it at
 //     most.
-//   * O^T += V^T P^T takes V as it landed and P as e4m3 pieces from shared
-//     memory: P' = 2^5 p in [0, 256], hi = e4m3(P'), lo = e4m3(32 (P' - hi)),
-//     side by side along N, so that one MMA reads V once for both and leaves
-//     O_hi and O_lo (O = O_hi + O_lo / 32) in neighbouring columns.  P then
-//     carries 8 significant bits (a bf16's worth, 2^-9 off) down to p = 2^-11
-//     and is never more than 2^-20 of the row's largest off.  An f16 output
-//     adds a third piece, e4m3 of what lo left, accumulated onto O_lo: 12 bits.
+//   * O^T += V^T P^T takes V as it landed and P' = 2^5 p in [0, 256] as two fp8
+//     pieces from shared memory: hi = e4m3(P') and lo = e5m2(P' - hi), whose
+//     products add up in one accumulator.  P is then 2^-8
+//     off at most, as a bf16 is, down to p = 2^-11, and below that never more
+//     than 2^-19 of the row's largest.  e5m2 reaches low enough that lo needs
+//     no scale of its own and so no second accumulator: an e4m3 lo is off by
+//     half as much, but its accumulator's reads and TMEM columns made
+//     64 requests of 512-4096 keys take 89.4 us instead of 85.0.
+//   * An f16 output takes three: hi, lo = e4m3(32 (P' - hi)) and e4m3 of what lo
+//     left, which is P' rounded to f16 (2^-11 off) down to p = 2^-9 and never
+//     more than 2^-20 of the row's largest off below.  hi and lo lie side by side along N, so that one MMA reads V
+//     once for both and leaves O_hi and O_lo (O = O_hi + O_lo / 32) in
+//     neighbouring columns; the third piece is accumulated onto O_lo.
 //   * A 2-byte cache of the query's dtype runs kind::f16 on Q, K and V as
 //     they are, P rounded to that type.
 //
@@ -68,8 +74,8 @@
 //               segment's epilogue (lane = dim);
 //   warps 12, 14, 15  TMA producers;  warp 13  MMA issuer and TMEM owner.
 // TMEM columns: a ring of three S^T buffers (R columns each), then the O^T
-// accumulators of the two groups (2 R columns each, R with a 2-byte cache),
-// twice where there is room, so that the next segment may start while the
+// accumulators of the two groups (R columns each, 2 R for an f16 output over an
+// fp8 cache), twice where there is room, so that the next segment may start while the
 // epilogue reads the last one.  QK runs two tiles ahead of PV, into the next
 // segment too.
 // All waits are bounded; on expiry a status bit is set and the CTA winds down.
@@ -113,7 +119,8 @@ struct TreeDims {
     static constexpr uint32_t kQPiece = R * DH * ES;        // 2-byte: [half][R rows][128 B]
     static constexpr int W = R * ES;                        // bytes of a key's row of a P piece
     static constexpr uint32_t kPPiece = 128 * W;            // [128 keys][R]
-    static constexpr int OC = k2 ? R : 2 * R;               // columns of an accumulator
+    static constexpr bool kTwo = NP == 3;                   // O_hi and O_lo
+    static constexpr int OC = kTwo ? 2 * R : R;             // columns of an accumulator
     static constexpr int NOB = 3 * R + 4 * OC <= 512 ? 2 : 1;  // accumulators of a group
     static constexpr uint32_t kColO = 3 * R;                // [NOB][group]
     static constexpr uint32_t kCols = kColO + NOB * 2 * OC <= 256 ? 256 : 512;
@@ -277,23 +284,29 @@ __device__ __forceinline__ uint32_t e4m3_of_half2(__half2 x) {
     return d;
 }
 
-// Four P' (at most 2^8) as e4m3 pieces: hi = e4m3(P'), lo = e4m3(32 (P' - hi)),
-// and with NP = 3 e4m3 of what lo left; four codes a word.  P' is first
-// rounded to f16 (11 bits, 2^-12 off: half a step of the finest result, 12
-// bits), in which the differences are exact.
+// Four P' (at most 2^8) as fp8 pieces, four codes a word: hi = e4m3(P'), and
+// lo = e5m2(P' - hi), an e5m2 code being the high byte of the f16 of equal
+// value (rounded half up: adding half a step to the bits); with NP = 3
+// lo = e4m3(32 (P' - hi)) and lo2 = e4m3 of what lo left.  P' is first rounded
+// to f16 (2^-11 off), in which the differences are exact.
 template <int NP>
-__device__ __forceinline__ void e4m3_pieces(const float* x, uint32_t& hi, uint32_t& lo, uint32_t& lo2) {
+__device__ __forceinline__ void p_pieces(const float* x, uint32_t& hi, uint32_t& lo, uint32_t& lo2) {
     uint32_t a[2], b[2], c[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
         a[k] = e4m3_of_half2(h);
-        const __half2 r = __hmul2(__hsub2(h, half2_of_e4m3(a[k])), __float2half2_rn(32.f));
-        b[k] = e4m3_of_half2(r);
-        if constexpr (NP == 3) c[k] = e4m3_of_half2(__hsub2(r, half2_of_e4m3(b[k])));
+        const __half2 d = __hsub2(h, half2_of_e4m3(a[k]));
+        if constexpr (NP == 3) {
+            const __half2 r = __hmul2(d, __float2half2_rn(32.f));
+            b[k] = e4m3_of_half2(r);
+            c[k] = e4m3_of_half2(__hsub2(r, half2_of_e4m3(b[k])));
+        } else {
+            b[k] = *reinterpret_cast<const uint32_t*>(&d) + 0x00800080u;
+        }
     }
     hi = prmt(a[0], a[1], 0x5410u);
-    lo = prmt(b[0], b[1], 0x5410u);
+    lo = prmt(b[0], b[1], NP == 3 ? 0x5410u : 0x7531u);
     if constexpr (NP == 3) lo2 = prmt(c[0], c[1], 0x5410u);
 }
 
@@ -502,7 +515,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int qf = k2 ? kvf : (p.q_dtype == PAFP8_E5M2 ? 1 : 0);
         const uint32_t idesc_qk = make_idesc(kvf, qf, 128, R);
         const uint32_t idesc_pv = make_idesc_mn(kvf, k2 ? kvf : 0, 128, D::OC);
-        const uint32_t idesc_p3 = make_idesc_mn(kvf, 0, 128, R);
+        const uint32_t idesc_p2 = make_idesc_mn(kvf, D::kTwo ? 0 : 1, 128, R);  // the last piece
         const uint32_t tm = (uint32_t)uniform((int)tmem);
         auto tiles_of = [&](int si) -> int {
             const Seg sg = load_seg(segs, seg_cache, si);
@@ -597,12 +610,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)  // K = 32 keys
                         tc_mma_elect<true>(d, va + 2 * DH * i, v_hi, pa + 2 * W * i, p_hi, idesc_pv, t >= 2 || i > 0, elect);
-                    if constexpr (NP == 3) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tc_mma_elect<true>(d + R, va + 2 * DH * i, v_hi, pa + (2 * D::kPPiece >> 4) + 2 * W * i, p_hi, idesc_p3,
-                                               1u, elect);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        tc_mma_elect<true>(D::kTwo ? d + R : d, va + 2 * DH * i, v_hi,
+                                           pa + ((NP - 1) * D::kPPiece >> 4) + 2 * W * i, p_hi, idesc_p2, 1u, elect);
                 }
                 tc_commit_elect(bar(tVEmpty + vstage), elect);
                 if (t + 1 == nt) tc_commit_elect(bar(tOFull + ob), elect);
@@ -786,7 +797,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                 } else if constexpr (KT == PAFP8_F16) {
                                     w0[i] = pack_half2(v[c + 2 * i], v[c + 2 * i + 1]);
                                 } else {
-                                    e4m3_pieces<NP>(v + c + 4 * i, w0[i], w1[i], w2[i]);
+                                    p_pieces<NP>(v + c + 4 * i, w0[i], w1[i], w2[i]);
                                 }
                             }
                             sts128(at, w0[0], w0[1], w0[2], w0[3]);
@@ -1032,10 +1043,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 {
                     float lo[8], lo1[8];
                     tc_ld8(tO + D::OC * g0 + r0, reinterpret_cast<uint32_t(&)[8]>(o));
-                    if constexpr (!k2) tc_ld8(tO + D::OC * g0 + R + r0, reinterpret_cast<uint32_t(&)[8]>(lo));
+                    if constexpr (D::kTwo) tc_ld8(tO + D::OC * g0 + R + r0, reinterpret_cast<uint32_t(&)[8]>(lo));
                     if (both) {
                         tc_ld8(tO + D::OC * (g0 ^ 1) + r0, reinterpret_cast<uint32_t(&)[8]>(o1));
-                        if constexpr (!k2) tc_ld8(tO + D::OC * (g0 ^ 1) + R + r0, reinterpret_cast<uint32_t(&)[8]>(lo1));
+                        if constexpr (D::kTwo) tc_ld8(tO + D::OC * (g0 ^ 1) + R + r0, reinterpret_cast<uint32_t(&)[8]>(lo1));
                     }
                     tc_wait_ld();
                     if (r0 + 8 >= rows) {  // O is read: another segment may write the accumulators
@@ -1052,7 +1063,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     for (int k = 0; k < 8; k += 4) {
                         const float4 w = lds_f4(wa + 4u * k);
                         f32x2 x = make_f32x2(o[k], o[k + 1]), y = make_f32x2(o[k + 2], o[k + 3]);
-                        if constexpr (!k2) {
+                        if constexpr (D::kTwo) {
                             x = fma2(make_f32x2(lo[k], lo[k + 1]), fold, x);
                             y = fma2(make_f32x2(lo[k + 2], lo[k + 3]), fold, y);
                         }
@@ -1061,7 +1072,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         if (both) {
                             const float4 u = lds_f4(wb + 4u * k);
                             f32x2 x1 = make_f32x2(o1[k], o1[k + 1]), y1 = make_f32x2(o1[k + 2], o1[k + 3]);
-                            if constexpr (!k2) {
+                            if constexpr (D::kTwo) {
                                 x1 = fma2(make_f32x2(lo1[k], lo1[k + 1]), fold, x1);
                                 y1 = fma2(make_f32x2(lo1[k + 2], lo1[k + 3]), fold, y1);
                             }

@@ -78,8 +78,9 @@ def test_every_tile_of_every_line_is_in_one_segment(seed):
 def test_equal_requests_are_balanced():
     plan = _plan([4096] * 64, [16] * 64, hq=32, hkv=8)
     ctas, ptr, segs, _, _ = _parts(plan)
-    tiles = [int((segs[ptr[i]:ptr[i + 1], 3] - segs[ptr[i]:ptr[i + 1], 2]).sum()) for i in range(ctas)]
-    assert ctas == 152 and max(tiles) <= 1.02 * sum(tiles) / ctas
+    # tiles, and five for each segment's start
+    cost = [int((segs[ptr[i]:ptr[i + 1], 3] - segs[ptr[i]:ptr[i + 1], 2] + 5).sum()) for i in range(ctas)]
+    assert ctas == 152 and max(cost) <= 1.02 * sum(cost) / ctas
     # the heads of one range are neighbours
     assert [int(segs[ptr[i], 0]) for i in range(8)] == list(range(8))
 
@@ -133,3 +134,25 @@ def test_tree_and_other_plans_do_not_mix():
     ph = pa.pod_phase(tree.handle, A, A, A, A, A, 1 << 20)
     assert L.pafp8_run_pod(ctypes.byref(ph), ctypes.byref(ph), pa.BF16, pa.E4M3FN, A, pa.E4M3FN, A, 1.0, 1.0, 1.0, pa.BF16,
                            None) == 3
+
+
+def test_pieces_of_the_probabilities():
+    """Every f16 in (0, 256], the largest at 2^5 or above: what its fp8 pieces leave."""
+    import torch
+
+    def e4m3(x):
+        return x.to(torch.float8_e4m3fn).float()
+
+    half = torch.arange(1, 0x5C01, dtype=torch.int32).to(torch.int16).view(torch.float16)
+    x = half.float()
+    hi = e4m3(x)
+    left = (x - hi).half()
+    assert torch.equal(left.float(), x - hi)
+    bits = (left.view(torch.int16).int() + 0x80) & 0xFF00
+    lo = torch.where(bits > 0x7FFF, bits - 0x10000, bits).to(torch.int16).view(torch.float16).float()
+    two = (x - hi - lo).abs()
+    assert (two <= torch.where(x >= 2.0 ** -6, x * 2.0 ** -8, torch.tensor(2.0 ** -14))).all()
+    scaled = 32 * (x - hi)
+    l1 = e4m3(scaled)
+    three = (x - hi - (l1 + e4m3(scaled - l1)) / 32).abs()
+    assert (three <= torch.where(x >= 2.0 ** -4, 0.0, 2.0 ** -15)).all()

@@ -122,8 +122,10 @@ class TreeBatch:
         g = self.hq // self.hkv
         sm = 1 / math.sqrt(self.d)
         pieces = 1 if self.qt in FP8 or self.kt not in FP8 else 2 if self.qt == "bf16" else 3
-        # One rounding of P: two or three e4m3 pieces, or the cache's type.
-        p_half = HALF[DT[self.kt]] if self.kt not in FP8 else 2.0 ** -12 if self.ot == "f16" else 2.0 ** -8
+        # P's rounding: f16's (2^-11), which three e4m3 pieces hold exactly and of which
+        # two leave 2^-8 (hi leaves up to 2^-4 of its binade, whose e5m2 below that
+        # value has steps of 2^-7), or the cache's type.
+        p_half = HALF[DT[self.kt]] if self.kt not in FP8 else 2.0 ** -11 if self.ot == "f16" else 2.0 ** -8 + 2.0 ** -11
         for b, (L, T) in enumerate(zip(self.kv_lens, self.qo_lens)):
             if T == 0:
                 continue
@@ -153,9 +155,14 @@ class TreeBatch:
                     dz = torch.where(vis, dz, 0.0).amax(1, keepdim=True)
                     # exp2, the sums and the fold of the scale: 2^-20 together
                     rel = p_half + 2 * dz + 2.0 ** -20
-                    # Small probabilities: half the last piece's smallest step, 2^-10 / 32 where
-                    # the row's maximum is at 2^5, i.e. 2^-20 of it (an f16's is smaller).
-                    tail = L * 2.0 ** -20 * v.abs().max() / tot.clamp(min=1.0) if self.kt in FP8 or self.kt == "f16" else 0.0
+                    # Small probabilities, the row's maximum being at 2^5: half the last
+                    # piece's smallest step, e4m3's 2^-10 / 32 (2^-20 of it; e5m2's 2^-17
+                    # and an f16's are smaller).  With two pieces hi is a multiple of
+                    # 2^-9 below 2^-6 and leaves less than 2^-10, whose e5m2 steps are
+                    # 2^-13: 2^-14 off, 2^-19 of it.
+                    tail = L * 2.0 ** (-19 if p_half > 2.0 ** -8 else -20) * v.abs().max() / tot.clamp(min=1.0)
+                    if self.kt == "bf16":
+                        tail = 0.0
                     slack = (w @ v.abs()) * rel + tail
                     tol = slack + HALF[DT[self.ot]] * (ro.abs() + slack) + 2.0 ** -24
                     got = o[r0:r0 + T, h].double()
