@@ -316,8 +316,9 @@ def pafp8_run_tree(handle: int, q, k_cache, v_cache, kv_indices, tree_mask, o, l
     """Attention of a tree of drafted tokens (a plan of mode "tree"): tree_mask
     [nnz_qo, words] of int32 (bits), as StepTables holds it; per-head scale
     tensors instead of the per-tensor ones when k_scales is given."""
+    dev = _device_of(q, "q")
     if tree_mask.dim() != 2 or tree_mask.element_size() != 4 or not tree_mask.is_contiguous() or \
-            tree_mask.shape[0] < q.shape[0] or tree_mask.get_device() != q.get_device():
+            tree_mask.shape[0] < q.shape[0] or tree_mask.get_device() != dev:
         raise ValueError(f"tree_mask {tuple(tree_mask.shape)} of {tree_mask.dtype} on {tree_mask.device} is not a "
                          f"contiguous int32 [{q.shape[0]}, words] tensor on the query's device")
     _check(lib().pafp8_run_tree(
@@ -326,7 +327,7 @@ def pafp8_run_tree(handle: int, q, k_cache, v_cache, kv_indices, tree_mask, o, l
         dtype_code(v_dtype if v_dtype is not None else v_cache.dtype), _ptr(v_cache),
         _ptr(kv_indices), _ptr(tree_mask), tree_mask.shape[1], q_scale, k_scale, v_scale, _ptr(q_scales), _ptr(k_scales),
         _ptr(v_scales), dtype_code(o_dtype if o_dtype is not None else o.dtype), _ptr(o), _ptr(lse),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_on(dev, stream)))
 
 
 def pafp8_device_status(handle: int, workspace, stream=None) -> None:
@@ -404,6 +405,15 @@ def _addr(t, name, n, dtype, dev) -> int:
     return t.data_ptr()
 
 
+def _stream_on(dev, stream) -> Optional[int]:
+    """`stream`, or the current stream of device `dev`: _stream without the
+    torch.cuda.Stream object that it makes, a tenth of a small step's call."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return getattr(stream, "cuda_stream", stream)
+
+
 def _device_of(t, name) -> int:
     """The current CUDA device, which `t` must be on."""
     import torch
@@ -428,6 +438,21 @@ def pafp8_build_tables(cached_lens, new_lens, block_table, free_pages, free_used
         if tree_mask.dim() != 2:
             raise ValueError(f"tree_mask has shape {tuple(tree_mask.shape)}, not [tokens, words]")
         words = tree_mask.shape[1]
+    _build_tables(
+        dev, cached_lens, new_lens, block_table, free_pages, free_used, parents,
+        (_addr(free_used_out, "free_used_out", 1, i32, dev), _addr(kv_indptr, "kv_indptr", batch + 1, i32, dev),
+         _addr(last_page_len, "last_page_len", batch, i32, dev), _addr(kv_indices, "kv_indices", 0, i32, dev),
+         _addr(qo_indptr, "qo_indptr", batch + 1, i32, dev), _addr(batch_indices, "batch_indices", tokens, i32, dev),
+         _addr(positions, "positions", tokens, i32, dev), _addr(slots, "slots", tokens, _I64, dev)),
+        (_addr(rope_positions, "rope_positions", tokens, i32, dev),
+         _addr(tree_mask, "tree_mask", tokens * words, i32, dev), _addr(status, "status", 1, i32, dev)),
+        kv_indices.numel(), tokens, words, page_size, num_pages, stream)
+
+
+def _build_tables(dev, cached_lens, new_lens, block_table, free_pages, free_used, parents, outs, tree_outs, max_pages,
+                  tokens, words, page_size, num_pages, stream) -> None:
+    """The call itself, its outputs given as addresses."""
+    i32, batch = _I32(), cached_lens.numel()
     rows, width = block_table.shape
     if rows < batch or block_table.dtype is not i32 or block_table.get_device() != dev or \
             (width > 1 and block_table.stride(1) != 1):
@@ -436,14 +461,9 @@ def pafp8_build_tables(cached_lens, new_lens, block_table, free_pages, free_used
     _check(lib().pafp8_build_tables(_TABLES.pack(
         _addr(cached_lens, "cached_lens", batch, i32, dev), _addr(new_lens, "new_lens", batch, i32, dev),
         block_table.data_ptr(), _addr(free_pages, "free_pages", 0, i32, dev), _addr(free_used, "free_used", 1, i32, dev),
-        _addr(free_used_out, "free_used_out", 1, i32, dev), _addr(kv_indptr, "kv_indptr", batch + 1, i32, dev),
-        _addr(last_page_len, "last_page_len", batch, i32, dev), _addr(kv_indices, "kv_indices", 0, i32, dev),
-        _addr(qo_indptr, "qo_indptr", batch + 1, i32, dev), _addr(batch_indices, "batch_indices", tokens, i32, dev),
-        _addr(positions, "positions", tokens, i32, dev), _addr(slots, "slots", tokens, _I64, dev),
-        _addr(parents, "parents", tokens, i32, dev), _addr(rope_positions, "rope_positions", tokens, i32, dev),
-        _addr(tree_mask, "tree_mask", tokens * words, i32, dev), _addr(status, "status", 1, i32, dev),
-        block_table.stride(0) if rows > 1 else width, kv_indices.numel(), tokens, batch, page_size, num_pages,
-        free_pages.numel(), width, words), _stream(stream)))
+        *outs, _addr(parents, "parents", tokens, i32, dev), *tree_outs,
+        block_table.stride(0) if rows > 1 else width, max_pages, tokens, batch, page_size, num_pages, free_pages.numel(),
+        width, words), _stream_on(dev, stream)))
 
 
 def pafp8_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slots, q_out, k_cache, v_cache, *,
@@ -455,41 +475,46 @@ def pafp8_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slot
     token stride); positions is int32 [n] or [axes, n], slots int64 [n],
     cos_sin float32 [max_position, rot_dim].  Types come from the tensors."""
     i32 = _I32()
-    n, hq, d = q.shape
-    hkv = k.shape[1]
-    dt = q.dtype
-    layout = _LAYOUTS[kv_layout] if isinstance(kv_layout, str) else int(kv_layout)
-    if k.shape != (n, hkv, d) or v.shape != k.shape or q_out.shape != q.shape:
+    shape, kshape, cshape, dt = q.shape, k.shape, k_cache.shape, q.dtype
+    n, hq, d = shape
+    _, hkv, _ = kshape
+    layout = _LAYOUTS[kv_layout] if kv_layout in _LAYOUTS else int(kv_layout)
+    if kshape != (n, hkv, d) or v.shape != kshape or q_out.shape != shape:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} and q_out {tuple(q_out.shape)} are "
                          "not [n, Hq, D], [n, Hkv, D], [n, Hkv, D] and [n, Hq, D]")
     if k.dtype is not dt or v.dtype is not dt:
         raise ValueError(f"q, k and v have different dtypes ({dt}, {k.dtype}, {v.dtype})")
     dev = _device_of(q, "q")
-    qs, ks, vs = q.stride(), k.stride(), v.stride()
-    if k.get_device() != dev or v.get_device() != dev or qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or \
-            (hq > 1 and qs[1] != d) or (hkv > 1 and (ks[1] != d or vs[1] != d)):
-        raise ValueError(f"q, k and v (on {q.device}, {k.device}, {v.device}; strides {qs}, {ks}, {vs}) must lie on the "
-                         "current CUDA device with the heads of a token contiguous")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
+    (qs, qh, q1), (ks, kh, k1), (vs, vh, v1) = q.stride(), k.stride(), v.stride()
+    if k.get_device() != dev or v.get_device() != dev or q1 != 1 or k1 != 1 or v1 != 1 or \
+            (hq > 1 and qh != d) or (hkv > 1 and (kh != d or vh != d)):
+        raise ValueError(f"q, k and v (on {q.device}, {k.device}, {v.device}; strides {q.stride()}, {k.stride()}, "
+                         f"{v.stride()}) must lie on the current CUDA device with the heads of a token contiguous")
+    axes, stride = 1, n
+    if positions.dim() == 2:
+        axes = positions.shape[0]
+        if axes > 1:
+            stride = positions.stride(0)
     if positions.dtype is not i32 or positions.get_device() != dev or positions.dim() > 2 or \
             positions.shape[-1] != n or (n > 1 and positions.stride(-1) != 1):
         raise ValueError(f"positions {tuple(positions.shape)} of {positions.dtype} on {positions.device} is not an int32 "
                          f"[{n}] or [axes, {n}] device tensor with contiguous rows")
     limit, rot = cos_sin.shape
-    pages, a, b, _ = k_cache.shape
-    ps, heads = (b, a) if layout == LAYOUT_HND else (a, b)
-    if heads != hkv or k_cache.shape[3] != d or v_cache.shape != k_cache.shape:
+    pages, ps, heads, cd = cshape
+    if layout == LAYOUT_HND:
+        ps, heads = heads, ps
+    if heads != hkv or cd != d or v_cache.shape != cshape:
         raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} do not hold {hkv} heads of "
                          f"{d} in layout {kv_layout}")
-    kt = k_cache.dtype
+    kt, qt = k_cache.dtype, q_out.dtype
     _check(lib().pafp8_norm_rope_append(_ROPE.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_weight, "q_weight", d, dt, dev),
         _addr(k_weight, "k_weight", d, dt, dev), _addr(cos_sin, "cos_sin", 0, _F32, dev), positions.data_ptr(),
         _addr(pair_axis, "pair_axis", rot // 2, _U8, dev), _addr(slots, "slots", n, _I64, dev),
-        _addr(q_out, "q_out", 0, q_out.dtype, dev), _addr(k_cache, "k_cache", 0, kt, dev),
-        _addr(v_cache, "v_cache", 0, kt, dev), _addr(status, "status", 1, i32, dev), n, qs[0], ks[0], vs[0],
-        positions.stride(0) if axes > 1 else n, dtype_code(dt), dtype_code(q_out.dtype), dtype_code(kt), layout, hq, hkv,
-        d, rot, 1 if interleaved else 0, axes, limit, pages, ps, eps, q_scale, k_scale, v_scale), _stream(stream)))
+        _addr(q_out, "q_out", 0, qt, dev), _addr(k_cache, "k_cache", 0, kt, dev), _addr(v_cache, "v_cache", 0, kt, dev),
+        _addr(status, "status", 1, i32, dev), n, qs, ks, vs, stride, dtype_code(dt), dtype_code(qt), dtype_code(kt),
+        layout, hq, hkv, d, rot, 1 if interleaved else 0, axes, limit, pages, ps, eps, q_scale, k_scale, v_scale),
+        _stream_on(dev, stream)))
 
 
 class StepTables:
@@ -498,32 +523,37 @@ class StepTables:
     kv_indptr, last_page_len, kv_indices, qo_indptr, batch_indices, positions,
     slots, free_used, and, with mask_words > 0, rope_positions and tree_mask
     (int32 words).  The arrays keep their addresses, so a step that uses them
-    can be captured into a graph."""
+    can be captured into a graph; they cannot be replaced by others."""
 
     def __init__(self, *, batch: int, max_pages: int, max_tokens: int, page_size: int, num_pages: int,
                  mask_words: int = 0, device="cuda"):
         import torch
-        self.page_size, self.num_pages = int(page_size), int(num_pages)
-
         def ints(*shape, dtype=torch.int32):
             return torch.zeros(shape, dtype=dtype, device=device)
 
-        self.kv_indptr, self.qo_indptr, self.last_page_len = ints(batch + 1), ints(batch + 1), ints(batch)
-        self.kv_indices, self.free_used = ints(max_pages), ints(1)
-        self.batch_indices, self.positions = ints(max_tokens), ints(max_tokens)
-        self.slots = ints(max_tokens, dtype=torch.int64)
-        self.rope_positions = ints(max_tokens) if mask_words > 0 else None
-        self.tree_mask = ints(max_tokens, mask_words) if mask_words > 0 else None
-        self.status = ints(1)
+        own = dict(free_used=ints(1), kv_indptr=ints(batch + 1), last_page_len=ints(batch), kv_indices=ints(max_pages),
+                   qo_indptr=ints(batch + 1), batch_indices=ints(max_tokens), positions=ints(max_tokens),
+                   slots=ints(max_tokens, dtype=torch.int64))
+        tree = dict(rope_positions=ints(max_tokens) if mask_words > 0 else None,
+                    tree_mask=ints(max_tokens, mask_words) if mask_words > 0 else None, status=ints(1))
+        addresses = [tuple(0 if t is None else t.data_ptr() for t in d.values()) for d in (own, tree)]
+        self.__dict__.update(own, **tree, page_size=int(page_size), num_pages=int(num_pages), _batch=batch,
+                             _dev=own["slots"].get_device(), _addresses=addresses,
+                             _sizes=(int(max_pages), int(max_tokens), max(0, int(mask_words))))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name}: a StepTables keeps the arrays that it was made with")
 
     def build(self, cached_lens, new_lens, block_table, free_pages, free_used, *, parents=None, stream=None) -> None:
         """Fill the arrays (and block_table's new entries) for these lengths;
         self.free_used holds the free list's entries taken after the step."""
-        pafp8_build_tables(cached_lens, new_lens, block_table, free_pages, free_used, self.free_used, self.kv_indptr,
-                           self.last_page_len, self.kv_indices, self.qo_indptr, self.batch_indices, self.positions,
-                           self.slots, page_size=self.page_size, num_pages=self.num_pages, parents=parents,
-                           rope_positions=self.rope_positions, tree_mask=self.tree_mask, status=self.status,
-                           stream=stream)
+        dev = _device_of(cached_lens, "cached_lens")
+        if dev != self._dev:
+            _refuse(self.slots, "this StepTables", self.slots.dtype, dev)
+        if cached_lens.numel() > self._batch:
+            raise ValueError(f"{cached_lens.numel()} requests in a StepTables made for {self._batch}")
+        _build_tables(dev, cached_lens, new_lens, block_table, free_pages, free_used, parents, *self._addresses,
+                      *self._sizes, self.page_size, self.num_pages, stream)
 
 
 # ---- convenience owner of a plan ---------------------------------------

@@ -96,3 +96,14 @@ def test_packed_descriptions_are_the_structures():
         d = cls.from_buffer_copy(raw.ljust(ctypes.sizeof(cls), b"\0"))
         assert [getattr(d, n) for n, _ in cls._fields_] == vals
         assert ctypes.sizeof(cls) == fmt.size
+
+
+def test_step_tables_keep_their_arrays():
+    import torch
+
+    t = pa.StepTables(batch=2, max_pages=4, max_tokens=8, page_size=16, num_pages=4, mask_words=1, device="cpu")
+    with pytest.raises(AttributeError, match="slots"):
+        t.slots = torch.zeros(8, dtype=torch.int64)
+    with pytest.raises(AttributeError, match="batch"):
+        t.batch = 3
+    assert t.tree_mask.shape == (8, 1) and t.slots.dtype is torch.int64

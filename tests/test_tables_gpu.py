@@ -162,3 +162,11 @@ def test_row_stride_and_graph_replay_with_new_lengths(cuda_device):
                              max_pages=pages, max_tokens=tokens)
         _check(t, table, want, 0)
     assert bool((wide[:, width:] == -7).all())
+
+
+def test_more_requests_than_made_for_are_refused():
+    t = pa.StepTables(batch=2, max_pages=8, max_tokens=8, page_size=16, num_pages=8)
+    i = dict(dtype=torch.int32, device="cuda")
+    three = torch.ones(3, **i)
+    with pytest.raises(ValueError, match="3 requests"):
+        t.build(three, three, torch.zeros(3, 1, **i), torch.zeros(8, **i), torch.zeros(1, **i))
