@@ -167,3 +167,19 @@ def test_byte_equal_to_append_kv(cuda_device):
                        k_scale=c.ks, v_scale=c.vs, kv_layout="HND")
     assert torch.equal(kc.view(torch.uint8), c.kc.view(torch.uint8))
     assert torch.equal(vc.view(torch.uint8), c.vc.view(torch.uint8))
+
+
+@pytest.mark.parametrize("variant", [dict(), dict(axes=3, layout="HND", page_size=48), dict(rot=32, interleaved=True, hq=9)])
+def test_skipped_tokens_among_many(cuda_device, variant):
+    """More tokens than blocks: what a skipped token leaves must not reach the next one of its block."""
+    c = Case(**{**dict(n=6001, hq=3, hkv=1, d=128, src=BF, kv=E4, q_out=BF, seed=3), **variant})
+    before = c.out.clone()
+    skip = torch.arange(6001) % 7 == 2
+    lost = torch.arange(6001) % 11 == 5
+    c.slots[skip] = -1
+    good = c.pos.clone()
+    c.pos[0, lost] = 513
+    c.run()
+    c.pos = good
+    c.check(~(skip | lost))
+    assert int(c.status) == 1 and torch.equal(c.out[(skip | lost).cuda()], before[(skip | lost).cuda()])
