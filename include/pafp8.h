@@ -114,7 +114,7 @@ enum { PAFP8_LAYOUT_NHD = 0, PAFP8_LAYOUT_HND = 1 };
  *              16-bit output).  DEFAULT means q_dtype for a 2-byte query and
  *              BF16 for an fp8 query.
  * sm_scale     softmax scale applied to q.k; <= 0 means 1/sqrt(head_dim).
- * Split-KV options (decode; prefill ignores them):
+ * Split-KV options (decode; prefill and tree plans ignore them):
  *   fixed_split_pages > 0  every request is cut into chunks of that many pages;
  *   disable_split_kv != 0  one chunk per request;
  *   otherwise              balanced: the concatenated pages of all
@@ -314,7 +314,10 @@ pafp8_status pafp8_run_head_scales(const pafp8_plan *plan, int32_t q_dtype, cons
  * the row's largest to 2^-19 of it), an f16's 11 for an f16 output (2^-20 of
  * it), and to the cache's type over a 2-byte cache.  A NaN or infinity in the value row of a
  * cached token reaches every drafted token of its request, whether its mask
- * shows that token or not. */
+ * shows that token or not.  A request's drafted tokens times the query heads
+ * per KV head may be 2^25 at most.  The workspace holds partial states during
+ * the call, as a decode plan's does: calls (and graph replays) on one
+ * workspace must follow one another. */
 pafp8_status pafp8_run_tree(const pafp8_plan *plan, int32_t q_dtype, const void *q, int32_t k_dtype,
                             const void *k_cache, int32_t v_dtype, const void *v_cache,
                             const int32_t *kv_indices, const uint32_t *tree_mask, int32_t mask_words,

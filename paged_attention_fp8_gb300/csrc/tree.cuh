@@ -268,11 +268,6 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int u0, int w
     return s == 0 ? lo : __funnelshift_r(lo, mask_word(row, w + 1, words, T), s);
 }
 
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-    unsigned short d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-    return d;
-}
 __device__ __forceinline__ __half2 half2_of_e4m3(uint32_t pair) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)pair));
@@ -310,24 +305,10 @@ __device__ __forceinline__ void p_pieces(const float* x, uint32_t& hi, uint32_t&
     if constexpr (NP == 3) lo2 = prmt(c[0], c[1], 0x5410u);
 }
 
-// 16 or 32 columns of this thread's TMEM lane; the values are there after tc_wait_ld.
-template <int NC>
-__device__ __forceinline__ void ld_cols(uint32_t t, float (&v)[NC]) {
-    if constexpr (NC == 16) {
-        tc_ld16(t, reinterpret_cast<uint32_t(&)[16]>(v));
-    } else {
-#pragma unroll
-        for (int c = 0; c < NC / 32; ++c) tc_ld32(t + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
-    }
-}
-template <int NC>
-__device__ __forceinline__ void st_cols(uint32_t t, const float (&v)[NC]) {
-    if constexpr (NC == 16) {
-        tc_st16(t, reinterpret_cast<const uint32_t(&)[16]>(v));
-    } else {
-#pragma unroll
-        for (int c = 0; c < NC / 32; ++c) tc_st32(t + 32 * c, *reinterpret_cast<const uint32_t(*)[32]>(v + 32 * c));
-    }
+// 32 columns of this thread's TMEM lane; loaded values are there after tc_wait_ld.
+__device__ __forceinline__ void ld_cols(uint32_t t, float (&v)[32]) { tc_ld32(t, reinterpret_cast<uint32_t(&)[32]>(v)); }
+__device__ __forceinline__ void st_cols(uint32_t t, const float (&v)[32]) {
+    tc_st32(t, reinterpret_cast<const uint32_t(&)[32]>(v));
 }
 
 // The 128 threads of a softmax group meet; true if any of them says so.  A
@@ -710,7 +691,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     int rise = first;
 #pragma unroll 1
                     while (true) {
-                        ld_cols<32>(tSs, v);
+                        ld_cols(tSs, v);
                         tc_wait_ld();
                         if ((t + 1) * kTileKeys > ctx) {  // keys that a row does not see become -inf
 #pragma unroll
@@ -744,14 +725,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
                                 for (int c0 = 32 * sub; c0 < D::OC; c0 += R) {  // O_hi, O_lo
                                     float o[32];
-                                    ld_cols<32>(tO + c0, o);
+                                    ld_cols(tO + c0, o);
                                     tc_wait_ld();
 #pragma unroll
                                     for (int i = 0; i < 32; i += 4) {
                                         const float4 a = lds_f4(als + 4u * i);
                                         o[i] *= a.x, o[i + 1] *= a.y, o[i + 2] *= a.z, o[i + 3] *= a.w;
                                     }
-                                    st_cols<32>(tO + c0, o);
+                                    st_cols(tO + c0, o);
                                 }
 #pragma unroll
                                 for (int i = 0; i < 16; i += 2) {
