@@ -278,6 +278,22 @@ __device__ __forceinline__ uint32_t e4m3_of_half2(__half2 x) {
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(*reinterpret_cast<uint32_t*>(&x)));
     return d;
 }
+// Four f16 values to e4m3 codes (returned), and what the codes leave of them, in
+// place (exact).  In one asm block the 16-bit codes need no widening (64 requests
+// of 512-4096 keys: 85.3 -> 83.6 us).
+__device__ __forceinline__ uint32_t e4m3_quad(uint32_t& h0, uint32_t& h1) {
+    uint32_t w;
+    asm("{\n .reg .b16 a, b;\n .reg .b32 x, y;\n"
+        " cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n"
+        " cvt.rn.f16x2.e4m3x2 x, a;\n cvt.rn.f16x2.e4m3x2 y, b;\n mov.b32 %0, {a, b};\n"
+        " sub.rn.f16x2 %1, %1, x;\n sub.rn.f16x2 %2, %2, y;\n}\n"
+        : "=&r"(w), "+r"(h0), "+r"(h1));
+    return w;
+}
+__device__ __forceinline__ uint32_t times32(uint32_t h) {
+    const __half2 x = __hmul2(*reinterpret_cast<__half2*>(&h), __float2half2_rn(32.f));
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
 
 // Four P' (at most 2^8) as fp8 pieces, four codes a word: hi = e4m3(P'), and
 // lo = e5m2(P' - hi), an e5m2 code being the high byte of the f16 of equal
@@ -286,23 +302,15 @@ __device__ __forceinline__ uint32_t e4m3_of_half2(__half2 x) {
 // to f16 (2^-11 off), in which the differences are exact.
 template <int NP>
 __device__ __forceinline__ void p_pieces(const float* x, uint32_t& hi, uint32_t& lo, uint32_t& lo2) {
-    uint32_t a[2], b[2], c[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
-        a[k] = e4m3_of_half2(h);
-        const __half2 d = __hsub2(h, half2_of_e4m3(a[k]));
-        if constexpr (NP == 3) {
-            const __half2 r = __hmul2(d, __float2half2_rn(32.f));
-            b[k] = e4m3_of_half2(r);
-            c[k] = e4m3_of_half2(__hsub2(r, half2_of_e4m3(b[k])));
-        } else {
-            b[k] = *reinterpret_cast<const uint32_t*>(&d) + 0x00800080u;
-        }
+    uint32_t h0 = pack_half2(x[0], x[1]), h1 = pack_half2(x[2], x[3]);
+    hi = e4m3_quad(h0, h1);
+    if constexpr (NP == 3) {
+        h0 = times32(h0), h1 = times32(h1);
+        lo = e4m3_quad(h0, h1);
+        lo2 = e4m3_quad(h0, h1);
+    } else {
+        lo = prmt(h0 + 0x00800080u, h1 + 0x00800080u, 0x7531u);
     }
-    hi = prmt(a[0], a[1], 0x5410u);
-    lo = prmt(b[0], b[1], NP == 3 ? 0x5410u : 0x7531u);
-    if constexpr (NP == 3) lo2 = prmt(c[0], c[1], 0x5410u);
 }
 
 // 32 columns of this thread's TMEM lane; loaded values are there after tc_wait_ld.
