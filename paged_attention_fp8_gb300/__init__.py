@@ -152,15 +152,16 @@ def lib() -> ctypes.CDLL:
     return L
 
 
-_I64 = _F32 = _U8 = None  # torch's dtype objects, once torch is in use
+_T = None  # the torch module, once a step call has used it: importing this module does not import torch
 
 
-def _I32():
-    """torch.int32 (imports torch on the first call: the module itself does not)."""
-    global _I64, _F32, _U8
-    import torch
-    _I64, _F32, _U8 = torch.int64, torch.float32, torch.uint8
-    return torch.int32
+def _torch():
+    """torch (an import statement in every call would cost it half a microsecond)."""
+    global _T
+    if _T is None:
+        import torch
+        _T = torch
+    return _T
 
 
 _OBJ_CODES = {}  # dtype objects seen before -> code (the run calls pass torch dtypes)
@@ -409,15 +410,13 @@ def _stream_on(dev, stream) -> Optional[int]:
     """`stream`, or the current stream of device `dev`: _stream without the
     torch.cuda.Stream object that it makes, a tenth of a small step's call."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _torch()._C._cuda_getCurrentRawStream(dev)
     return getattr(stream, "cuda_stream", stream)
 
 
 def _device_of(t, name) -> int:
     """The current CUDA device, which `t` must be on."""
-    import torch
-    dev = torch.cuda.current_device() if t.is_cuda else -2
+    dev = _torch().cuda.current_device() if t.is_cuda else -2
     if t.get_device() != dev:
         _refuse(t, name, t.dtype, dev)
     return dev
@@ -430,7 +429,7 @@ def pafp8_build_tables(cached_lens, new_lens, block_table, free_pages, free_used
     device (see include/pafp8.h; StepTables owns the outputs).  Arrays are
     contiguous device int32 tensors, slots int64; block_table is
     [batch, width] with contiguous rows; tree_mask is [tokens, words]."""
-    i32 = _I32()
+    i32 = _torch().int32
     dev = _device_of(cached_lens, "cached_lens")
     batch, tokens = cached_lens.numel(), slots.numel()
     words = 0
@@ -443,7 +442,7 @@ def pafp8_build_tables(cached_lens, new_lens, block_table, free_pages, free_used
         (_addr(free_used_out, "free_used_out", 1, i32, dev), _addr(kv_indptr, "kv_indptr", batch + 1, i32, dev),
          _addr(last_page_len, "last_page_len", batch, i32, dev), _addr(kv_indices, "kv_indices", 0, i32, dev),
          _addr(qo_indptr, "qo_indptr", batch + 1, i32, dev), _addr(batch_indices, "batch_indices", tokens, i32, dev),
-         _addr(positions, "positions", tokens, i32, dev), _addr(slots, "slots", tokens, _I64, dev)),
+         _addr(positions, "positions", tokens, i32, dev), _addr(slots, "slots", tokens, _T.int64, dev)),
         (_addr(rope_positions, "rope_positions", tokens, i32, dev),
          _addr(tree_mask, "tree_mask", tokens * words, i32, dev), _addr(status, "status", 1, i32, dev)),
         kv_indices.numel(), tokens, words, page_size, num_pages, stream)
@@ -452,7 +451,7 @@ def pafp8_build_tables(cached_lens, new_lens, block_table, free_pages, free_used
 def _build_tables(dev, cached_lens, new_lens, block_table, free_pages, free_used, parents, outs, tree_outs, max_pages,
                   tokens, words, page_size, num_pages, stream) -> None:
     """The call itself, its outputs given as addresses."""
-    i32, batch = _I32(), cached_lens.numel()
+    i32, batch = _torch().int32, cached_lens.numel()
     rows, width = block_table.shape
     if rows < batch or block_table.dtype is not i32 or block_table.get_device() != dev or \
             (width > 1 and block_table.stride(1) != 1):
@@ -474,7 +473,8 @@ def pafp8_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slot
     include/pafp8.h).  q, k and v may be slices of one packed projection (any
     token stride); positions is int32 [n] or [axes, n], slots int64 [n],
     cos_sin float32 [max_position, rot_dim].  Types come from the tensors."""
-    i32 = _I32()
+    T = _torch()
+    i32 = T.int32
     shape, kshape, cshape, dt = q.shape, k.shape, k_cache.shape, q.dtype
     n, hq, d = shape
     _, hkv, _ = kshape
@@ -507,14 +507,18 @@ def pafp8_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slot
         raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} do not hold {hkv} heads of "
                          f"{d} in layout {kv_layout}")
     kt, qt = k_cache.dtype, q_out.dtype
+    # (the shapes of these four are known by now)
+    for t, name, dtype in ((cos_sin, "cos_sin", T.float32), (q_out, "q_out", qt), (k_cache, "k_cache", kt),
+                           (v_cache, "v_cache", kt)):
+        if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+            _refuse(t, name, dtype, dev)
     _check(lib().pafp8_norm_rope_append(_ROPE.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_weight, "q_weight", d, dt, dev),
-        _addr(k_weight, "k_weight", d, dt, dev), _addr(cos_sin, "cos_sin", 0, _F32, dev), positions.data_ptr(),
-        _addr(pair_axis, "pair_axis", rot // 2, _U8, dev), _addr(slots, "slots", n, _I64, dev),
-        _addr(q_out, "q_out", 0, qt, dev), _addr(k_cache, "k_cache", 0, kt, dev), _addr(v_cache, "v_cache", 0, kt, dev),
-        _addr(status, "status", 1, i32, dev), n, qs, ks, vs, stride, dtype_code(dt), dtype_code(qt), dtype_code(kt),
-        layout, hq, hkv, d, rot, 1 if interleaved else 0, axes, limit, pages, ps, eps, q_scale, k_scale, v_scale),
-        _stream_on(dev, stream)))
+        _addr(k_weight, "k_weight", d, dt, dev), cos_sin.data_ptr(), positions.data_ptr(),
+        _addr(pair_axis, "pair_axis", rot // 2, T.uint8, dev), _addr(slots, "slots", n, T.int64, dev), q_out.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), _addr(status, "status", 1, i32, dev), n, qs, ks, vs, stride, dtype_code(dt),
+        dtype_code(qt), dtype_code(kt), layout, hq, hkv, d, rot, 1 if interleaved else 0, axes, limit, pages, ps, eps,
+        q_scale, k_scale, v_scale), _stream_on(dev, stream)))
 
 
 class StepTables:
