@@ -48,9 +48,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kMaxThreads = 64;  // of a block
-constexpr int kBlocks = 8;       // resident ones an SM
-constexpr int kHeads = 4;        // of a thread
+constexpr int kWarps = 16;  // resident warps an SM
+constexpr int kHeads = 4;   // of a thread
 
 // Four 16-bit elements in fp32.
 template <bool kBF>
@@ -104,7 +103,7 @@ __device__ __forceinline__ void store_fp8(uint8_t* dst, const f32x2 (&x)[2], flo
 }
 
 template <bool kBF, int DH, bool kPairs>  // kPairs: neighbouring dims rotate together
-__global__ void __launch_bounds__(kMaxThreads, kBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(64, kWarps / 2) rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int TPR = DH / 8;  // threads per head
     const int g = blockIdx.y * blockDim.x + threadIdx.x, c = g % TPR, u = g / TPR;
     const int half = p.rot_dim >> 1;
@@ -322,14 +321,14 @@ __global__ void __launch_bounds__(kMaxThreads, kBlocks) rope_kernel(const __grid
 template <bool kBF, int DH>
 cudaError_t launch_d(const RopeParams& p, cudaStream_t stream) {
     const auto kernel = p.interleaved ? rope_kernel<kBF, DH, true> : rope_kernel<kBF, DH, false>;
-    // The threads of a token are cut into columns of equal size, of kMaxThreads
-    // at most; a block takes the tokens blockIdx.x, blockIdx.x + gridDim.x, ...
-    // of one column.
+    // A token's warps go two to a block if they are even (8838 tokens of 6 warps:
+    // 37.2 us, 38.1 with one), else one (5003 tokens of 3 warps: 16.4 us, 18.4
+    // with two, one of which would idle); a block takes the tokens blockIdx.x,
+    // blockIdx.x + gridDim.x, ...
     const long long units = (p.num_qo_heads + kHeads - 1) / kHeads + 2 * ((p.num_kv_heads + kHeads - 1) / kHeads);
-    const long long lanes = units * (DH / 8), columns = (lanes + kMaxThreads - 1) / kMaxThreads;
-    const int threads = (int)(((lanes + columns - 1) / columns + 31) / 32 * 32);
-    const long long blocks = std::max<long long>(1, 152LL * kBlocks * kMaxThreads / threads / columns);
-    kernel<<<dim3((unsigned)std::min<long long>(p.nnz, blocks), (unsigned)columns), threads, 0, stream>>>(p);
+    const long long warps = (units * (DH / 8) + 31) / 32, per_block = warps % 2 == 0 ? 2 : 1;
+    const long long blocks = std::min<long long>(p.nnz, std::max<long long>(1, 152 * kWarps / warps));
+    kernel<<<dim3((unsigned)blocks, (unsigned)(warps / per_block)), (unsigned)(32 * per_block), 0, stream>>>(p);
     return cudaGetLastError();
 }
 
