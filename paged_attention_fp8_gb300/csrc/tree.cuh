@@ -78,6 +78,12 @@
 // fp8 cache), twice where there is room, so that the next segment may start while the
 // epilogue reads the last one.  QK runs two tiles ahead of PV, into the next
 // segment too.
+// Measured (152 CTAs, L2 evicted): 8 requests of 32768 keys, 4 drafted tokens of
+// 8 heads a KV head, f16 over e5m2: 98 us, 81 % of the copy rate.  64 requests of
+// 512-4096 keys, 64 rows: 83.5 us, where the cache's bytes take 46: the softmax
+// warps bound it, some 650 issue slots a 64-row tile each, two tiles at a time, and
+// each of a CTA's four or so segments starts and ends at about five tiles' cost.
+//
 // All waits are bounded; on expiry a status bit is set and the CTA winds down.
 #pragma once
 #include "../../include/pafp8.h"
