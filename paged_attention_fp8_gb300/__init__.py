@@ -318,7 +318,12 @@ def pafp8_run_tree(handle: int, q, k_cache, v_cache, kv_indices, tree_mask, o, l
     [nnz_qo, words] of int32 (bits), as StepTables holds it; per-head scale
     tensors instead of the per-tensor ones when k_scales is given."""
     dev = _device_of(q, "q")
-    if tree_mask.dim() != 2 or tree_mask.element_size() != 4 or not tree_mask.is_contiguous() or \
+    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (kv_indices, "kv_indices"), (o, "o"),
+                    (lse, "lse"), (workspace, "workspace")):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            _refuse(t, name, t.dtype, dev)
+    if tree_mask.dim() != 2 or tree_mask.element_size() != 4 or tree_mask.is_floating_point() or \
+            not tree_mask.is_contiguous() or \
             tree_mask.shape[0] < q.shape[0] or tree_mask.get_device() != dev:
         raise ValueError(f"tree_mask {tuple(tree_mask.shape)} of {tree_mask.dtype} on {tree_mask.device} is not a "
                          f"contiguous int32 [{q.shape[0]}, words] tensor on the query's device")

@@ -1590,8 +1590,10 @@ pafp8_status pafp8_run_pod(const pafp8_pod_phase* prefill, const pafp8_pod_phase
         return fail(PAFP8_ERR_ARG, "both phases and their plans are required");
     const pafp8_plan_desc& a = prefill->plan->desc;
     const pafp8_plan_desc& b = decode->plan->desc;
-    if (a.mode != PAFP8_MODE_PREFILL) return fail(PAFP8_ERR_ARG, "the prefill phase's plan is a decode plan");
-    if (b.mode != PAFP8_MODE_DECODE) return fail(PAFP8_ERR_ARG, "the decode phase's plan is a prefill plan");
+    if (a.mode != PAFP8_MODE_PREFILL)
+        return fail(PAFP8_ERR_ARG, "the prefill phase's plan is a %s plan", a.mode == PAFP8_MODE_DECODE ? "decode" : "tree");
+    if (b.mode != PAFP8_MODE_DECODE)
+        return fail(PAFP8_ERR_ARG, "the decode phase's plan is a %s plan", b.mode == PAFP8_MODE_PREFILL ? "prefill" : "tree");
     if (a.num_pages != b.num_pages || a.page_size != b.page_size || a.num_kv_heads != b.num_kv_heads ||
         a.head_dim != b.head_dim || a.kv_layout != b.kv_layout)
         return fail(PAFP8_ERR_SHAPE,

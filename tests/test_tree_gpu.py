@@ -161,3 +161,19 @@ def test_expired_wait_is_reported_and_the_context_stays_usable(cuda_device, monk
     b.call()
     b.plan.device_status(b.ws)
     assert torch.equal(b.o[:b.n].cpu(), o) and torch.equal(b.lse[:b.n].cpu(), lse)
+
+
+def test_arrays_that_cannot_be_read_as_they_are_refused(cuda_device):
+    b = TreeBatch([100, 60], [4, 4], 8, 2, seed=14)
+    b.run()
+    good = (b.dq, b.kc, b.vc, b.ids, b.mask, b.o, b.lse, b.ws)
+    for at, bad, match in ((0, b.dq.transpose(0, 1), "q .*not contiguous"), (0, b.dq.cpu(), "q is on cpu"),
+                           (1, b.kc.cpu(), "k_cache is on cpu"), (3, b.ids.cpu(), "kv_indices is on cpu"),
+                           (4, b.mask.float(), "tree_mask"), (4, b.mask.t(), "tree_mask"), (4, b.mask[:3], "tree_mask"),
+                           (5, b.o.transpose(0, 1), "o .*not contiguous"), (6, b.lse.t(), "lse .*not contiguous")):
+        args = list(good)
+        args[at] = bad
+        with pytest.raises(ValueError, match=match):
+            b.plan.run_tree(*args, k_scale=b.ks, v_scale=b.vs)
+    b.plan.run_tree(*good[:6], None, b.ws, k_scale=b.ks, v_scale=b.vs)  # lse may be left out
+    b.plan.device_status(b.ws)

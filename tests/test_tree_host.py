@@ -134,6 +134,7 @@ def test_tree_and_other_plans_do_not_mix():
     ph = pa.pod_phase(tree.handle, A, A, A, A, A, 1 << 20)
     assert L.pafp8_run_pod(ctypes.byref(ph), ctypes.byref(ph), pa.BF16, pa.E4M3FN, A, pa.E4M3FN, A, 1.0, 1.0, 1.0, pa.BF16,
                            None) == 3
+    assert "is a tree plan" in pa.pafp8_last_error()
 
 
 def test_pieces_of_the_probabilities():
