@@ -156,7 +156,7 @@ enum TreeBar : int {
     tNumBars = tVEmpty + kMaxStages
 };
 template <typename D, int R, int NP>
-__host__ __device__ inline TreeSmem tree_smem(int q_tiles, int stages) {
+__host__ __device__ constexpr TreeSmem tree_smem(int q_tiles, int stages) {
     TreeSmem s{};
     s.q = 0;
     s.k = (uint32_t)q_tiles * D::kQPiece;
@@ -176,6 +176,27 @@ __host__ __device__ inline TreeSmem tree_smem(int q_tiles, int stages) {
     s.abort_flag = s.tmem_slot + 4;
     s.bytes = s.abort_flag + 4;
     return s;
+}
+// Q buffers and K / V stages of a launch.  Two Q buffers (the next segment's Q
+// is built during the current one) if the ring keeps three stages of K and V,
+// or two of a 2-byte cache.
+constexpr uint32_t kSmemBudget = 232448 - 1024;
+struct TreeRing {
+    int q_buffers, stages;
+};
+template <typename D, int R, int NP>
+__host__ __device__ constexpr TreeRing tree_ring(int q_pieces) {
+    TreeRing r{tree_smem<D, R, NP>(2 * q_pieces, D::k2 ? 2 : 3).bytes <= kSmemBudget ? 2 : 1, 2};
+    while (r.stages < kMaxStages && tree_smem<D, R, NP>(r.q_buffers * q_pieces, r.stages + 1).bytes <= kSmemBudget) ++r.stages;
+    return r;
+}
+// Whether some query type leaves an instantiation two stages (a 2-byte cache at
+// head_dim 128).
+template <typename D, int R, int NP>
+__host__ __device__ constexpr bool two_stages() {
+    for (int q_pieces = 1; q_pieces <= (D::k2 ? 1 : 3); ++q_pieces)
+        if (tree_ring<D, R, NP>(q_pieces).stages < 3) return true;
+    return false;
 }
 
 __device__ __forceinline__ float lds_f(uint32_t a) {
@@ -820,9 +841,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (out) break;
                 // Value rows behind the request's end (the tail of its last page and
                 // rows no page filled) hold anything: zero them, P = 0 there must
-                // not meet a NaN.
+                // not meet a NaN.  The wait for V names its phase by parity, so the
+                // phase before it, V of tile j - NS, has to be known complete: S(j)
+                // vouches for PV(j - 3), which with two stages says nothing of
+                // V(j - 2): the wait could pass before that had landed, and the zeros
+                // go into that tile's rows.  So with two stages PV(j - 2) is waited for
+                // first (a phase that follows PV(j - 4), for which S(j) does vouch; it
+                // always ends, this group's P(j - 2) being given).
                 const int valid = sg.kv_len - t * kTileKeys;
                 if (valid < kTileKeys) {
+                    if constexpr (two_stages<D, R, NP>()) dead |= !wait_all(tVEmpty + stage, vphase ^ 1u);
                     dead |= !wait_all(tVFull + stage, vphase);
                     if (krow >= valid) {
                         const uint32_t vrow = base + L.v + (uint32_t)stage * kTile + (uint32_t)krow * (k2 ? 128u : (uint32_t)DH);
@@ -1169,14 +1197,10 @@ template <int KT, int NP, int DH, int R>
 cudaError_t launch_tree_t(TreeParams p, const CUtensorMap& tk, const CUtensorMap& tv, int num_ctas, int num_merge,
                           cudaStream_t stream) {
     using D = TreeDims<KT, NP, DH, R>;
-    constexpr uint32_t budget = 232448 - 1024;
-    // Two Q buffers (the next segment's Q is built during the current one) if
-    // the ring keeps three stages of K and V, or two of a 2-byte cache.
-    p.q_buffers = tree_smem<D, R, NP>(2 * p.q_pieces, D::k2 ? 2 : 3).bytes <= budget ? 2 : 1;
-    int stages = 2;
-    while (stages < kMaxStages && tree_smem<D, R, NP>(p.q_buffers * p.q_pieces, stages + 1).bytes <= budget) ++stages;
-    p.stages = stages;
-    const size_t smem = 1024 + tree_smem<D, R, NP>(p.q_buffers * p.q_pieces, stages).bytes;
+    const TreeRing ring = tree_ring<D, R, NP>(p.q_pieces);
+    p.q_buffers = ring.q_buffers;
+    p.stages = ring.stages;
+    const size_t smem = 1024 + tree_smem<D, R, NP>(p.q_buffers * p.q_pieces, p.stages).bytes;
     if (smem > 232448) return cudaErrorInvalidValue;
     auto kern = tree_kernel<KT, NP, DH, R>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
