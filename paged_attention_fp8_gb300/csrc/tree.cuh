@@ -90,6 +90,7 @@
 #include "../../include/pafp8.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "ring.h"
 
 namespace pafp8 {
 namespace {
@@ -136,7 +137,7 @@ struct TreeDims {
 };
 
 struct TreeSmem {
-    uint32_t q, k, v, p, sc, neg, alpha, wmax, lsum, mst, wt, rowp, seg, bars, tmem_slot, abort_flag, bytes;
+    uint32_t q, k, v, p, sc, neg, alpha, wmax, lsum, mst, wt, rowp, seg, bars, next, tmem_slot, abort_flag, bytes;
 };
 enum TreeBar : int {
     tQFull = 0,              // [2]
@@ -172,7 +173,8 @@ __host__ __device__ constexpr TreeSmem tree_smem(int q_tiles, int stages) {
     s.rowp = s.wt + 2 * 2 * R * 4;          // [2][R] byte offsets of the rows in o (64 bits)
     s.seg = s.rowp + 2 * R * 8;             // the CTA's first kSegCache segment records
     s.bars = s.seg + kSegCache * kTreeSegWords * 4;
-    s.tmem_slot = s.bars + 8 * tNumBars;
+    s.next = s.bars + 8 * tNumBars;         // [K, V][3 producers]: one past the last tile loaded
+    s.tmem_slot = s.next + 2 * 3 * 4;
     s.abort_flag = s.tmem_slot + 4;
     s.bytes = s.abort_flag + 4;
     return s;
@@ -510,15 +512,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 for (stage += step; stage >= NS; stage -= NS) phase ^= 1u;
             }
         }
+        // Every copy lands before the CTA may exit: the last one of each slot.  After
+        // an expired wait another warp may have filled a slot once more, so the warps
+        // meet first (each comes here, its waits being bounded) and say how far they got.
         if (lane == 0) {
-            // Every copy of this warp lands before the CTA may exit: its tiles that are
-            // the last on their stage (after an abort, its last ones).
-            const int end = ok ? total : n + 1;
-            if (!ok && k_only) mbar_wait(bar(tKFull + n % NS), (uint32_t)((n / NS) & 1));
-            for (int x = n - step; pw < step && x >= 0 && x + NS >= end; x -= step) {
-                mbar_wait(bar(tKFull + x % NS), (uint32_t)((x / NS) & 1));
-                mbar_wait(bar(tVFull + x % NS), (uint32_t)((x / NS) & 1));
-            }
+            sts32(base + L.next + 4u * pw, (uint32_t)(pw < step ? n + (!ok && k_only) : 0));
+            sts32(base + L.next + 12u + 4u * pw, (uint32_t)(pw < step ? n : 0));
+        }
+        asm volatile("barrier.cta.sync 3, 96;" ::: "memory");
+        if (pw == 0 && lane < 2 * NS) {
+            const int kv = lane >= NS, slot = lane - (kv ? NS : 0);
+            const uint32_t at = base + L.next + 12u * kv;
+            const int next[3] = {(int)lds_u(at), (int)lds_u(at + 4u), (int)lds_u(at + 8u)};
+            const int x = ring_last_load(next, step, NS, slot);
+            if (x >= 0) mbar_wait(bar((kv ? tVFull : tKFull) + slot), (uint32_t)((x / NS) & 1));
         }
         __syncwarp();
       } else {
