@@ -308,8 +308,9 @@ pafp8_status pafp8_run_head_scales(const pafp8_plan *plan, int32_t q_dtype, cons
  * Every other argument and check is pafp8_run's.  Served: the dtypes of a
  * prefill plan (fp8 cache with any query, 2-byte cache of the query's own
  * dtype), head_dim 128 or 64, both layouts, up to 128 query heads per KV
- * head.  A 2-byte query over an fp8 cache is multiplied exactly to 2^-18 of
- * its row's largest magnitude; probabilities are rounded to a bf16's 8
+ * head.  A 2-byte query over an fp8 cache is multiplied exactly but for
+ * elements below 2^-9 (bf16) or 2^-6 (f16) of its row's largest magnitude, which
+ * lose 2^-17 of it at most; probabilities are rounded to a bf16's 8
  * significant bits for a bf16 output over an fp8 cache (those below 2^-11 of
  * the row's largest to 2^-19 of it), an f16's 11 for an f16 output (2^-20 of
  * it), and to the cache's type over a 2-byte cache.  A NaN or infinity in the value row of a

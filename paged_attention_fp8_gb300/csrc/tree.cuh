@@ -18,9 +18,10 @@
 //     scaled by a power of two to a maximum in [128, 256) and split into
 //     e4m3 pieces (4 significant bits each: two for bf16's 8, three for f16's
 //     11) whose products add up in one accumulator: x = a + b (+ c), each
-//     piece the e4m3 rounding of what the earlier ones left, exact but for
-//     elements below 2^-10 of the row's largest, which lose 2^-18 of it at
-//     most.
+//     piece the e4m3 rounding of what the earlier ones left.  e4m3's smallest
+//     step is 2^-9, so at most 2^-10 is lost (2^-17 of a largest magnitude of
+//     128), and that only of elements with bits below the step: under 2^-2
+//     (bf16; 2^-9 of the largest) or 2 (f16; 2^-6).
 //   * O^T += V^T P^T takes V as it landed and P' = 2^5 p in [0, 256] as two fp8
 //     pieces from shared memory: hi = e4m3(P') and lo = e5m2(P' - hi), whose
 //     products add up in one accumulator.  P is then 2^-8
