@@ -316,24 +316,30 @@ def pafp8_run_tree(handle: int, q, k_cache, v_cache, kv_indices, tree_mask, o, l
                    v_dtype=None, o_dtype=None, stream=None) -> None:
     """Attention of a tree of drafted tokens (a plan of mode "tree"): tree_mask
     [nnz_qo, words] of int32 (bits), as StepTables holds it; per-head scale
-    tensors instead of the per-tensor ones when k_scales is given."""
+    tensors (device float32: q_scales [Hq] or None, k_scales and v_scales
+    [Hkv]) instead of the per-tensor ones when k_scales is given.  Arrays are
+    contiguous; kv_indices is int32, lse float32 or None."""
+    T = _torch()
     dev = _device_of(q, "q")
-    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (kv_indices, "kv_indices"), (o, "o"),
-                    (lse, "lse"), (workspace, "workspace")):
-        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            _refuse(t, name, t.dtype, dev)
-    if tree_mask.dim() != 2 or tree_mask.element_size() != 4 or tree_mask.is_floating_point() or \
-            not tree_mask.is_contiguous() or \
-            tree_mask.shape[0] < q.shape[0] or tree_mask.get_device() != dev:
+    qt, kt, vt, ot, i32, f32 = q.dtype, k_cache.dtype, v_cache.dtype, o.dtype, T.int32, T.float32
+    for t, name, dtype in ((q, "q", qt), (k_cache, "k_cache", kt), (v_cache, "v_cache", vt), (kv_indices, "kv_indices", i32),
+                           (o, "o", ot), (lse, "lse", f32), (workspace, "workspace", workspace.dtype)):
+        if t is not None and (t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous()):
+            _refuse(t, name, dtype, dev)
+    scales = (0, 0, 0) if q_scales is k_scales is v_scales is None else (
+        _addr(q_scales, "q_scales", 0, f32, dev), _addr(k_scales, "k_scales", 0, f32, dev),
+        _addr(v_scales, "v_scales", 0, f32, dev))
+    rows, words = tree_mask.shape if tree_mask.dim() == 2 else (-1, 0)
+    if rows < q.shape[0] or tree_mask.get_device() != dev or not tree_mask.is_contiguous() or \
+            (tree_mask.dtype is not i32 and (tree_mask.element_size() != 4 or tree_mask.is_floating_point())):
         raise ValueError(f"tree_mask {tuple(tree_mask.shape)} of {tree_mask.dtype} on {tree_mask.device} is not a "
                          f"contiguous int32 [{q.shape[0]}, words] tensor on the query's device")
     _check(lib().pafp8_run_tree(
-        handle, dtype_code(q_dtype if q_dtype is not None else q.dtype), _ptr(q),
-        dtype_code(k_dtype if k_dtype is not None else k_cache.dtype), _ptr(k_cache),
-        dtype_code(v_dtype if v_dtype is not None else v_cache.dtype), _ptr(v_cache),
-        _ptr(kv_indices), _ptr(tree_mask), tree_mask.shape[1], q_scale, k_scale, v_scale, _ptr(q_scales), _ptr(k_scales),
-        _ptr(v_scales), dtype_code(o_dtype if o_dtype is not None else o.dtype), _ptr(o), _ptr(lse),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_on(dev, stream)))
+        handle, dtype_code(qt if q_dtype is None else q_dtype), q.data_ptr(),
+        dtype_code(kt if k_dtype is None else k_dtype), k_cache.data_ptr(),
+        dtype_code(vt if v_dtype is None else v_dtype), v_cache.data_ptr(), _ptr(kv_indices), tree_mask.data_ptr(), words,
+        q_scale, k_scale, v_scale, *scales, dtype_code(ot if o_dtype is None else o_dtype), o.data_ptr(), _ptr(lse),
+        workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream)))
 
 
 def pafp8_device_status(handle: int, workspace, stream=None) -> None:
