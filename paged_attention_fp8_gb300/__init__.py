@@ -225,15 +225,43 @@ def pafp8_last_error() -> str:
     return lib().pafp8_last_error().decode()
 
 
+# What pafp8_run_tree needs of its arrays, by the handles of the tree plans that
+# exist: the shapes of q and o, of the caches and of lse, page ids, mask rows, KV heads.
+_TREE_SIZES = {}
+_ITEM = {F16: 2, BF16: 2, E4M3FN: 1, E5M2: 1}  # bytes of an element; the library refuses other types
+
+
+def _tree_sizes(desc, kv_indptr, qo_indptr):
+    rows = int(qo_indptr[-1]) if desc.batch > 0 else 0
+    hq, hkv, ps, d = desc.num_qo_heads, desc.num_kv_heads, desc.page_size, desc.head_dim
+    page = (hkv, ps, d) if desc.kv_layout == LAYOUT_HND else (ps, hkv, d)
+    return (rows, hq, d), (desc.num_pages, *page), (rows, hq), int(kv_indptr[-1]) if desc.batch > 0 else 0, rows, hkv
+
+
+def _tree_fits(sizes, arrays, kv_indices, lse) -> None:
+    """ValueError for an array with fewer bytes than the plan's shapes take
+    (larger and differently shaped ones are taken as they lie), or a cache
+    whose pages are shaped otherwise.  arrays: (tensor, name, dtype code, shape)."""
+    for t, name, code, shape in (*arrays, (kv_indices, "kv_indices", None, (sizes[3],)), (lse, "lse", None, sizes[2])):
+        need = (4 if code is None else _ITEM.get(code, 0)) * int(np.prod(shape, dtype=np.int64))
+        if t is not None and t.nbytes < need:
+            raise ValueError(f"{name} {tuple(t.shape)} of {t.dtype} has {t.nbytes} bytes; the plan needs {need}")
+        if shape is sizes[1] and t.dim() == 4 and tuple(t.shape[1:]) != shape[1:]:
+            raise ValueError(f"{name} {tuple(t.shape)} has pages of {tuple(t.shape[1:])}; the plan's are {shape[1:]}")
+
+
 def pafp8_plan_create(desc: plan_desc, kv_indptr, last_page_len, qo_indptr=None) -> int:
     kv_indptr, last_page_len, qo_indptr = _i32_host(kv_indptr), _i32_host(last_page_len), _i32_host(qo_indptr)
     out = ctypes.c_void_p()
     _check(lib().pafp8_plan_create(ctypes.byref(desc), _ptr(kv_indptr), _ptr(last_page_len),
                                    _ptr(qo_indptr), ctypes.byref(out)))
+    if desc.mode == MODE_TREE:
+        _TREE_SIZES[out.value] = _tree_sizes(desc, kv_indptr, qo_indptr)
     return out.value
 
 
 def pafp8_plan_destroy(handle: int) -> None:
+    _TREE_SIZES.pop(handle, None)
     lib().pafp8_plan_destroy(handle)
 
 
@@ -326,20 +354,34 @@ def pafp8_run_tree(handle: int, q, k_cache, v_cache, kv_indices, tree_mask, o, l
                            (o, "o", ot), (lse, "lse", f32), (workspace, "workspace", workspace.dtype)):
         if t is not None and (t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous()):
             _refuse(t, name, dtype, dev)
+    code = _OBJ_CODES.get
+    qc = code(qt) or dtype_code(qt) if q_dtype is None else dtype_code(q_dtype)
+    oc = code(ot) or dtype_code(ot) if o_dtype is None else dtype_code(o_dtype)
+    kc = code(kt) or dtype_code(kt) if k_dtype is None else dtype_code(k_dtype)
+    vc = code(vt) or dtype_code(vt) if v_dtype is None else dtype_code(v_dtype)
+    sizes = _TREE_SIZES.get(handle)
+    if sizes is None:
+        hq, hkv, n_rows = 0, 0, q.shape[0]
+    else:
+        rows_of, pool, lse_of, n_index, n_rows, hkv = sizes
+        hq = rows_of[1]
+        if q.shape != rows_of or o.shape != rows_of or k_cache.shape != pool or v_cache.shape != pool or \
+                (lse is not None and lse.shape != lse_of) or (kv_indices is not None and kv_indices.numel() < n_index) or \
+                q_dtype is not None or o_dtype is not None or k_dtype is not None or v_dtype is not None:
+            _tree_fits(sizes, ((q, "q", qc, rows_of), (o, "o", oc, rows_of), (k_cache, "k_cache", kc, pool),
+                               (v_cache, "v_cache", vc, pool)), kv_indices, lse)
     scales = (0, 0, 0) if q_scales is k_scales is v_scales is None else (
-        _addr(q_scales, "q_scales", 0, f32, dev), _addr(k_scales, "k_scales", 0, f32, dev),
-        _addr(v_scales, "v_scales", 0, f32, dev))
+        _addr(q_scales, "q_scales", hq, f32, dev), _addr(k_scales, "k_scales", hkv, f32, dev),
+        _addr(v_scales, "v_scales", hkv, f32, dev))
     rows, words = tree_mask.shape if tree_mask.dim() == 2 else (-1, 0)
-    if rows < q.shape[0] or tree_mask.get_device() != dev or not tree_mask.is_contiguous() or \
+    if rows < n_rows or tree_mask.get_device() != dev or not tree_mask.is_contiguous() or \
             (tree_mask.dtype is not i32 and (tree_mask.element_size() != 4 or tree_mask.is_floating_point())):
         raise ValueError(f"tree_mask {tuple(tree_mask.shape)} of {tree_mask.dtype} on {tree_mask.device} is not a "
-                         f"contiguous int32 [{q.shape[0]}, words] tensor on the query's device")
+                         f"contiguous int32 [{n_rows}, words] tensor on the query's device")
     _check(lib().pafp8_run_tree(
-        handle, dtype_code(qt if q_dtype is None else q_dtype), q.data_ptr(),
-        dtype_code(kt if k_dtype is None else k_dtype), k_cache.data_ptr(),
-        dtype_code(vt if v_dtype is None else v_dtype), v_cache.data_ptr(), _ptr(kv_indices), tree_mask.data_ptr(), words,
-        q_scale, k_scale, v_scale, *scales, dtype_code(ot if o_dtype is None else o_dtype), o.data_ptr(), _ptr(lse),
-        workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream)))
+        handle, qc, q.data_ptr(), kc, k_cache.data_ptr(), vc, v_cache.data_ptr(), _ptr(kv_indices), tree_mask.data_ptr(), words,
+        q_scale, k_scale, v_scale, *scales, oc, o.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
+        _stream_on(dev, stream)))
 
 
 def pafp8_device_status(handle: int, workspace, stream=None) -> None:

@@ -67,3 +67,53 @@ def test_what_fits_is_passed_on(call):
 def test_types(call, kw, match):
     with pytest.raises(ValueError, match=match):
         call(**kw)
+
+
+FP8 = dict(dtype=torch.float8_e4m3fn)
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(q=torch.zeros(NNZ - 1, HQ, D, **FP8)), "q "), (dict(q=torch.zeros(NNZ, HQ // 2, D, **FP8)), "q "),
+    (dict(q=torch.zeros(NNZ, HQ, D // 2, **FP8)), "q "), (dict(o=torch.zeros(NNZ - 1, HQ, D, dtype=torch.bfloat16)), "o "),
+    (dict(o=torch.zeros(NNZ, HQ, D, dtype=torch.uint8), o_dtype="bf16"), "o "),
+    (dict(lse=torch.zeros(NNZ - 1, HQ)), "lse "), (dict(lse=torch.zeros(NNZ)), "lse "),
+    (dict(kv_indices=torch.zeros(PAGES - 1, dtype=torch.int32)), "kv_indices "),
+    (dict(k_cache=torch.zeros(POOL - 1, 16, HKV, D, **FP8)), "k_cache "),
+    (dict(v_cache=torch.zeros(POOL - 1, 16, HKV, D, **FP8)), "v_cache "),
+    (dict(v_cache=torch.zeros(POOL * 16 * HKV * D - 1, **FP8)), "v_cache "),
+    (dict(k_cache=torch.zeros(POOL, HKV, 16, D, **FP8)), "k_cache "),
+    (dict(v_cache=torch.zeros(POOL, 32, HKV // 2, D, **FP8)), "v_cache "),
+    (dict(tree_mask=torch.zeros(NNZ - 1, 1, dtype=torch.int32)), "tree_mask "),
+    (dict(tree_mask=torch.zeros(NNZ - 1, 1, dtype=torch.int32), q=torch.zeros(NNZ - 1, HQ, D, **FP8)), "(tree_mask|q) "),
+    (dict(head_scales=True, q_scales=torch.ones(HQ - 1)), "q_scales "), (dict(head_scales=True, k_scales=torch.ones(1)), "k_scales "),
+    (dict(head_scales=True, v_scales=torch.ones(1)), "v_scales ")])
+def test_sizes(call, kw, match):
+    with pytest.raises(ValueError, match="^" + match):
+        call(**kw)
+
+
+def test_larger_arrays_are_taken(call):
+    """A batch padded to more rows, a longer page list, a larger pool and wider mask rows, other shapes of as many elements."""
+    call(q=torch.zeros(NNZ + 3, HQ, D, **FP8), o=torch.zeros(NNZ + 1, HQ, D, dtype=torch.bfloat16), lse=torch.zeros(NNZ + 2, HQ),
+         tree_mask=torch.zeros(NNZ + 3, 2, dtype=torch.int32), kv_indices=torch.zeros(PAGES + 4, dtype=torch.int32),
+         k_cache=torch.zeros(POOL + 2, 16, HKV, D, **FP8), v_cache=torch.zeros(POOL + 2, 16, HKV, D, **FP8))
+    call(q=torch.zeros(NNZ, HQ * D, **FP8), o=torch.zeros(NNZ * HQ * D, dtype=torch.bfloat16), lse=torch.zeros(NNZ * HQ),
+         k_cache=torch.zeros(POOL * 16 * HKV * D, **FP8), q_dtype="e4m3fn")
+    call(q=torch.zeros(NNZ, HQ, D, dtype=torch.uint8), q_dtype="e4m3fn")
+
+
+def test_sizes_go_with_their_plan(call):
+    """A plan's handle that is destroyed takes its sizes along: the next plan may get the same address."""
+    other = pa.Plan(mode="tree", num_qo_heads=2, num_kv_heads=2, num_pages=1, kv_indptr=[0, 1], last_page_len=[5], qo_indptr=[0, 2],
+                    q_dtype="bf16", kv_dtype="bf16", num_ctas=8)
+    handle = other.handle
+    assert handle in pa._TREE_SIZES and call.plan.handle in pa._TREE_SIZES
+    pa.pafp8_plan_destroy(handle)
+    other.handle = None
+    assert handle not in pa._TREE_SIZES
+    empty = pa.Plan(mode="tree", num_qo_heads=2, num_kv_heads=2, num_pages=0, kv_indptr=[0], last_page_len=[], qo_indptr=[0],
+                    q_dtype="bf16", kv_dtype="bf16", num_ctas=8)
+    none = dict(dtype=torch.bfloat16)
+    pa.pafp8_run_tree(empty.handle, torch.zeros(0, 2, 128, **none), torch.zeros(0, 16, 2, 128, **none), torch.zeros(0, 16, 2, 128, **none),
+                      torch.zeros(0, dtype=torch.int32), torch.zeros(0, 1, dtype=torch.int32), torch.zeros(0, 2, 128, **none),
+                      torch.zeros(0, 2), torch.zeros(empty.workspace_bytes, dtype=torch.uint8), stream=1)
