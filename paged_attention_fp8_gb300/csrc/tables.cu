@@ -118,8 +118,9 @@ __global__ void __launch_bounds__(kTblThreads) tables_kernel(const TablesParams 
             bad |= page < 0 || page >= p.num_pages;
             if (base_page + j < p.max_pages) p.kv_indices[base_page + j] = page;
         }
-        // Tokens.
-        for (int u = first; u < own.fresh; u += step) {
+        // Tokens.  (Unsigned: the last step of nearly 2^31 tokens passes int's range.)
+        for (unsigned i = first; i < (unsigned)own.fresh; i += step) {
+            const int u = (int)i;
             const long long t = base_tok + u;
             if (t >= p.max_tokens) {
                 bad = true;
