@@ -316,7 +316,7 @@ pafp8_status pafp8_run_head_scales(const pafp8_plan *plan, int32_t q_dtype, cons
  * it), and to the cache's type over a 2-byte cache.  A NaN or infinity in the value row of a
  * cached token reaches every drafted token of its request, whether its mask
  * shows that token or not.  A request's drafted tokens times the query heads
- * per KV head may be 2^25 at most.  The workspace holds partial states during
+ * per KV head may be 2^25 at most, its kv_len 2^31 - 129.  The workspace holds partial states during
  * the call, as a decode plan's does: calls (and graph replays) on one
  * workspace must follow one another. */
 pafp8_status pafp8_run_tree(const pafp8_plan *plan, int32_t q_dtype, const void *q, int32_t k_dtype,

@@ -991,6 +991,10 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
                 return fail(PAFP8_ERR_UNSUPPORTED,
                             "request %d has %lld drafted tokens of %d query heads per KV head: the product may be 2^25 at most",
                             b, (long long)qo, group);
+            // The kernel counts keys in 32 bits, up to the end of the last tile.
+            if (d.mode == PAFP8_MODE_TREE && kv > INT32_MAX - kTileKeys)
+                return fail(PAFP8_ERR_UNSUPPORTED, "request %d has kv_len %lld: tree attention serves up to %d", b,
+                            (long long)kv, INT32_MAX - kTileKeys);
             if (qo < 0)
                 return fail(PAFP8_ERR_SHAPE, "qo_indptr decreases at request %d (%d -> %d)", b,
                             (int)qo_indptr_h[b], (int)qo_indptr_h[b + 1]);
