@@ -3,13 +3,15 @@
  * KV cache stored in fp8 (OCP e4m3fn or e5m2) with per-tensor scales, for
  * NVIDIA GB300 (sm_103a).
  *
- * Two workloads share one plan/run interface:
+ * Three workloads share one plan/run interface:
  *   - decode: one query row per request against its whole KV sequence; the
  *     plan splits long sequences across CTAs and a merge kernel combines the
  *     partial states by their log-sum-exp;
  *   - prefill: a ragged batch of new query rows per request, bottom-right
  *     aligned causal mask (query row i of a request with qo_len new rows and
- *     kv_len keys sees key j iff j <= i + kv_len - qo_len).
+ *     kv_len keys sees key j iff j <= i + kv_len - qo_len);
+ *   - tree: a few drafted tokens per request, which see the cached keys before
+ *     them and, among themselves, what their mask rows say.
  *
  * The plan()/run() split, o_data_type fixed at plan time and checked at run
  * time, and the scale threading follow "Enable Hopper FA3 FP8 attention in
@@ -28,7 +30,7 @@
  *     until the next failing call on this thread).  Nothing aborts.
  *   - pafp8_run neither allocates nor synchronizes, unless PAFP8_DEBUG is
  *     set in the environment (to anything but "0"): then every run call that
- *     launches (pafp8_run, _stage, _head_scales, _pod) synchronizes its
+ *     launches (pafp8_run, _stage, _head_scales, _tree, _pod) synchronizes its
  *     stream and returns the kernels' status as pafp8_device_status reports
  *     it (PAFP8_ERR_BOUNDS, PAFP8_ERR_TIMEOUT), so a bad page index or an
  *     expired wait surfaces at the call that caused it.  Not for use under
@@ -318,7 +320,9 @@ pafp8_status pafp8_run_head_scales(const pafp8_plan *plan, int32_t q_dtype, cons
  * shows that token or not.  A request's drafted tokens times the query heads
  * per KV head may be 2^25 at most, its kv_len 2^31 - 129.  The workspace holds partial states during
  * the call, as a decode plan's does: calls (and graph replays) on one
- * workspace must follow one another. */
+ * workspace must follow one another.  Lengths are the plan's: a captured call
+ * serves that one set of qo_indptr, kv_indptr and last_page_len, and for other
+ * lengths a plan is made from host arrays and uploaded. */
 pafp8_status pafp8_run_tree(const pafp8_plan *plan, int32_t q_dtype, const void *q, int32_t k_dtype,
                             const void *k_cache, int32_t v_dtype, const void *v_cache,
                             const int32_t *kv_indices, const uint32_t *tree_mask, int32_t mask_words,

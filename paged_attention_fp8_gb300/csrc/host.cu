@@ -497,9 +497,11 @@ void build_tree_meta(pafp8_plan* pl) {
     pl->rows_pad = (int)std::min<int64_t>(most_rows, RT);
     // What starting a segment costs, in tiles: its first maxima, the sums at its
     // end and its epilogue take 64 rows of an fp8 cache about five tiles' time
-    // (64 requests of 512-4096 keys: 94.9 us at cost 1, 89.4 at 4 and 6, 90.4 at
-    // 8, before P's second piece shared the first's accumulator); 32 rows, or the longer tiles of a 2-byte cache, about two (60.0 us at
-    // 1 and 3, 63.3 at 6).
+    // (64 requests of 512-4096 keys: 88.7 us at cost 1, 86.8 at 3, 83.8 at 5, 83.1
+    // at 6, 84.3 at 8; drafts of 68 to 244 rows 88.9, 79.7, 77.9, 77.1, 77.8); 32
+    // rows (8 requests of 32768 keys: 98.3 at 2, 98.9 at 5, 100.4 at 8), or the
+    // longer tiles of a 2-byte cache, about two (59.6 at 1, 59.9 at 2, 62.5 at 5,
+    // 65.0 at 8).
     const int seg_cost = RT == 64 && is_fp8(pl->desc.kv_dtype) ? 5 : 2;
     for (int b = 0; b < B; ++b) {
         const int64_t rows = (int64_t)(pl->qo_indptr[b + 1] - pl->qo_indptr[b]) * g;

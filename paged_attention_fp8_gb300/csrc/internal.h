@@ -262,10 +262,11 @@ using TreeLaunch = cudaError_t(const TreeParams& p, const CUtensorMap& tmap_k, c
                                int num_merge, cudaStream_t stream);
 TreeLaunch launch_tree_d128_r32, launch_tree_d128_r64, launch_tree_d64_r32, launch_tree_d64_r64;
 // Rows of a row tile: 32 when every draft fits, else 64 (of which a draft may
-// take several).  8 requests of 32768 keys with 32 rows take 98.6 us in tiles of
+// take several).  8 requests of 32768 keys with 32 rows take 98.2 us in tiles of
 // 32 and 119 in tiles of 64; 64 requests of 512-4096 keys with 64 rows 109 us
-// in tiles of 32 (the cache read and converted for twice as many tiles) and 83
-// in one of 64; drafts of 68 to 244 rows 91 and 75.
+// in tiles of 32 (the cache read and converted for twice as many tiles) and 83.5
+// in one of 64; drafts of 68 to 244 rows 92.5 and 78.4; up to 48 rows over a bf16
+// cache 72.8 and 59.8.  Batches of short and long drafts were not measured.
 inline int tree_tile_rows(int most_rows) { return most_rows <= 32 ? 32 : 64; }
 inline TreeLaunch* tree_launcher(int head_dim, int tile_rows) {
     if (head_dim == 64) return tile_rows == 32 ? launch_tree_d64_r32 : launch_tree_d64_r64;

@@ -18,8 +18,8 @@
 // cost less than that up to some ten thousand requests.  Long page lists are
 // split over blockIdx.y, so one request of a million tokens spreads over the
 // device too.  Bounded by latency (the length loads, the block's reductions,
-// one dependent page load): 7.5 us with everything cold for one request, 9.5
-// for 64, 15.8 for 1021 of up to 32768 tokens, whose page ids take 1.3 us at
+// one dependent page load): 7-8 us with everything cold for one request, 9
+// for 64, 15-16 for 1021 of up to 32768 tokens, whose page ids take 1.3 us at
 // the copy rate.
 #include "../../include/pafp8.h"
 #include "internal.h"

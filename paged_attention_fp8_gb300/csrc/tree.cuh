@@ -28,8 +28,9 @@
 //     off at most, as a bf16 is, down to p = 2^-11, and below that never more
 //     than 2^-19 of the row's largest.  e5m2 reaches low enough that lo needs
 //     no scale of its own and so no second accumulator: an e4m3 lo is off by
-//     half as much, but its accumulator's reads and TMEM columns made
-//     64 requests of 512-4096 keys take 89.4 us instead of 85.0.
+//     half as much, but its accumulator's reads and TMEM columns cost 64
+//     requests of 512-4096 keys 4.4 us (89.4 against 85.0, when the choice was
+//     made; they take 83-84 now).
 //   * An f16 output takes three: hi, lo = e4m3(32 (P' - hi)) and e4m3 of what lo
 //     left, which is P' rounded to f16 (2^-11 off) down to p = 2^-9 and never
 //     more than 2^-20 of the row's largest off below.  hi and lo lie side by side along N, so that one MMA reads V
@@ -45,8 +46,10 @@
 // as the tile's HBM time; transposed it is about 500 at R = 32 and 700 at
 // R = 64.  A softmax thread then owns a key, every lane is busy whatever R is,
 // and P is written to shared memory, which frees S right away.  Drafts of more
-// than 64 rows are cut into row tiles of 64: 128 rows at once would take as
-// long as two such tiles.
+// than 64 rows are cut into row tiles of 64, each of which reads the keys
+// again: in this form 128 rows at once would take as long as two such tiles.
+// (Query rows as M, a thread a row, would suit those drafts better, as in the
+// prefill kernel; that form is not built.)
 //
 // One tile's softmax is a chain of some 2000 cycles (wait, load, scale, exp,
 // convert, store, vote, hand on), longer than a tile's HBM time (1400).  So two
@@ -79,12 +82,14 @@
 // fp8 cache), twice where there is room, so that the next segment may start while the
 // epilogue reads the last one.  QK runs two tiles ahead of PV, into the next
 // segment too.
-// Measured (152 CTAs, L2 evicted): 8 requests of 32768 keys, 4 drafted tokens of
-// 8 heads a KV head, f16 over e5m2: 98 us, 81 % of the copy rate.  64 requests of
-// 512-4096 keys, 64 rows: 83.5 us, where the cache's bytes take 46: the softmax
-// warps' chain bounds it (a scheduler issues in 49 % of its cycles, the tensor pipe
-// is active in 23 %), two tiles at a time, and each of a CTA's four or so segments
-// costs about five tiles to start and end.
+// Measured (152 CTAs, caches larger than L2): 8 requests of 32768 keys, 4 drafted
+// tokens of 8 heads a KV head, f16 over e5m2: 98 us, 81 % of the copy rate.  64
+// requests of 512-4096 keys, 64 rows: 83-84 us, where the cache's bytes take 46: the
+// softmax warps' chain bounds it (a scheduler issues in 49 % of its cycles, the
+// tensor pipe is active in 23 %), two tiles at a time, and each of a CTA's four or
+// so segments costs about five tiles to start and end.  32 requests over a bf16
+// cache: 59.7 us (the bytes take 40), with two stages of K and V that leave HBM idle
+// between bursts.
 //
 // All waits are bounded; on expiry a status bit is set and the CTA winds down.
 #pragma once
