@@ -626,6 +626,129 @@ typedef struct pafp8_rope_desc {
 
 pafp8_status pafp8_norm_rope_append(const pafp8_rope_desc *desc, void *stream);
 
+/* The cache with a scale for each block of 16 tokens and KV head, in place of
+ * one scale for the tensor or the head: K and V codes lie as ever, and
+ *   k_scales, v_scales   float [num_pages, page_size / 16, num_kv_heads]
+ * (in either layout) hold the scale of token slots 16 j .. 16 j + 15 of every
+ * page and head.  pafp8_append_kv_blocks writes codes and scales,
+ * pafp8_run_block_scales attends to them, pafp8_read_kv reads them back.
+ *
+ * Quantize new tokens into such a cache.  Request b's n_b = qo_indptr[b + 1] -
+ * qo_indptr[b] new tokens go to positions cached_lens[b] .. cached_lens[b] +
+ * n_b - 1 of its sequence (the arrays that pafp8_build_tables takes and
+ * fills).  For a block that receives new tokens, with amax the largest finite
+ * magnitude among them and M the largest finite value of the type (448 or
+ * 57344):
+ *   s_new = the smallest power of two >= 2^-64 with amax <= M * s_new
+ *   s     = s_new, or max(s_old, s_new) when the block holds tokens before
+ *           position cached_lens[b]
+ *   code  = fp8(RNE, saturating)(fp32(x) * fp32(1 / s))
+ * and where s > s_old the codes of those tokens become fp8(RNE, saturating)(
+ * code * fp32(s_old / s)): exact for the powers of two this call writes, but
+ * for codes that fall below the type's normal range.  s is stored as the
+ * block's scale.  An infinite element stores the largest value with its sign,
+ * a NaN a NaN code; neither counts in amax.  Token slots behind a request's
+ * last new token keep their codes and take on the block's new scale: a token
+ * taken back (a rejected draft) is written anew by the step that reaches its
+ * position again.
+ *
+ *   src_dtype      F16, BF16 or F32: k and v
+ *   k, v           device [nnz, num_kv_heads, head_dim], heads of a token
+ *                  contiguous, tokens k_stride | v_stride elements apart;
+ *                  16-byte aligned, strides multiples of 8
+ *   nnz            rows in k and v; those from qo_indptr[batch] on are not
+ *                  read (a batch padded for a captured graph)
+ *   qo_indptr      device int32 [batch + 1], non-decreasing, from 0
+ *   cached_lens    device int32 [batch]
+ *   kv_indptr,
+ *   kv_indices     the page table, already covering the new tokens
+ *   k_cache,
+ *   v_cache        device caches of kv_dtype (E4M3FN or E5M2) in kv_layout,
+ *                  16-byte aligned
+ *   k_scales,
+ *   v_scales       device float, as above; entries of blocks that hold tokens
+ *                  are finite and > 0 (not checked), those of others are not
+ *                  read
+ *   status         device uint32 or NULL: the kernel ORs in 1 for a block that
+ *                  it did not write because its position or page lies outside
+ *                  the table or the pool, and when qo_indptr[batch] > nnz
+ * No two requests may write the same page.  Shapes served: head_dim 128 or
+ * 64, page_size a multiple of 16.  Nothing is allocated or synchronized. */
+typedef struct pafp8_block_append_desc {
+    const void *k;
+    const void *v;
+    const int32_t *qo_indptr;
+    const int32_t *cached_lens;
+    const int32_t *kv_indptr;
+    const int32_t *kv_indices;
+    void *k_cache;
+    void *v_cache;
+    float *k_scales;
+    float *v_scales;
+    uint32_t *status;
+    int64_t nnz;
+    int64_t k_stride;
+    int64_t v_stride;
+    int32_t batch;
+    int32_t src_dtype;
+    int32_t kv_dtype;
+    int32_t kv_layout;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t num_pages;
+    int32_t page_size;
+} pafp8_block_append_desc;
+
+pafp8_status pafp8_append_kv_blocks(const pafp8_block_append_desc *desc, void *stream);
+
+/* Read token ranges of an fp8 cache back into plain rows: output rows
+ * out_indptr[b] .. out_indptr[b + 1] - 1 are tokens starts[b], starts[b] + 1,
+ * ... of request b, each element fp32(code) * scale rounded once (RNE; a
+ * magnitude above the output type's range becomes an infinity).
+ *   kv_dtype       E4M3FN or E5M2
+ *   out_indptr     device int32 [batch + 1], non-decreasing, from 0
+ *   starts         device int32 [batch]
+ *   kv_indptr,
+ *   kv_indices     the page table
+ *   k_out, v_out   device [nnz, num_kv_heads, head_dim] of out_dtype (F16,
+ *                  BF16 or F32), contiguous, 16-byte aligned; rows from
+ *                  out_indptr[batch] on are left as they were
+ *   k_scales,
+ *   v_scales       device float [num_pages, page_size / 16, num_kv_heads]
+ *                  (k_scale and v_scale must then be 1), or NULL both: the
+ *                  per-tensor k_scale and v_scale apply
+ *   status         device uint32 or NULL: the kernel ORs in 1 for a row that it
+ *                  did not write because its position or page lies outside the
+ *                  table or the pool, and when out_indptr[batch] > nnz
+ * Shapes served: head_dim 128 or 64, page_size a multiple of 16.  Nothing is
+ * allocated or synchronized. */
+typedef struct pafp8_read_desc {
+    const void *k_cache;
+    const void *v_cache;
+    const int32_t *out_indptr;
+    const int32_t *starts;
+    const int32_t *kv_indptr;
+    const int32_t *kv_indices;
+    void *k_out;
+    void *v_out;
+    const float *k_scales;
+    const float *v_scales;
+    uint32_t *status;
+    int64_t nnz;
+    int32_t batch;
+    int32_t kv_dtype;
+    int32_t out_dtype;
+    int32_t kv_layout;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t num_pages;
+    int32_t page_size;
+    float k_scale;
+    float v_scale;
+} pafp8_read_desc;
+
+pafp8_status pafp8_read_kv(const pafp8_read_desc *desc, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -45,7 +45,7 @@ EXPORTS = ("pafp8_abi_version", "pafp8_last_error", "pafp8_plan_create", "pafp8_
            "pafp8_workspace_bytes", "pafp8_plan_metadata", "pafp8_plan_upload", "pafp8_run",
            "pafp8_run_stage", "pafp8_device_status", "pafp8_run_decode_noalloc", "pafp8_append_kv",
            "pafp8_run_head_scales", "pafp8_run_pod", "pafp8_host_workspace_bytes", "pafp8_run_host",
-           "pafp8_build_tables", "pafp8_norm_rope_append", "pafp8_run_tree")
+           "pafp8_build_tables", "pafp8_norm_rope_append", "pafp8_run_tree", "pafp8_append_kv_blocks", "pafp8_read_kv")
 
 
 class Pafp8Error(RuntimeError):
@@ -94,10 +94,31 @@ class rope_desc(ctypes.Structure):
         [(n, ctypes.c_float) for n in ("eps", "q_scale", "k_scale", "v_scale")]
 
 
-# The same two structures as struct formats: packing one costs a third of a
+class block_append_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k", "v", "qo_indptr", "cached_lens", "kv_indptr", "kv_indices", "k_cache", "v_cache", "k_scales", "v_scales",
+        "status")] + \
+        [(n, ctypes.c_int64) for n in ("nnz", "k_stride", "v_stride")] + \
+        [(n, ctypes.c_int32) for n in (
+            "batch", "src_dtype", "kv_dtype", "kv_layout", "num_kv_heads", "head_dim", "num_pages", "page_size")]
+
+
+class read_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k_cache", "v_cache", "out_indptr", "starts", "kv_indptr", "kv_indices", "k_out", "v_out", "k_scales", "v_scales",
+        "status")] + \
+        [("nnz", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in (
+            "batch", "kv_dtype", "out_dtype", "kv_layout", "num_kv_heads", "head_dim", "num_pages", "page_size")] + \
+        [(n, ctypes.c_float) for n in ("k_scale", "v_scale")]
+
+
+# These structures as struct formats: packing one costs a third of a
 # microsecond, filling a ctypes structure field by field five.
 _TABLES = struct.Struct("@17P3q6i")
 _ROPE = struct.Struct("@13P5q13i4f0q")
+_BLOCK_APPEND = struct.Struct("@11P3q8i")
+_READ = struct.Struct("@11Pq8i2f")
 
 _lib = None
 
@@ -145,7 +166,9 @@ def lib() -> ctypes.CDLL:
     L.pafp8_run_tree.argtypes = [vp, i32, vp, i32, vp, i32, vp, vp, vp, i32, f32, f32, f32, vp, vp, vp, i32, vp, vp, vp,
                                  sz, vp]
     L.pafp8_run_tree.restype = i32
-    # Their descriptions come packed (_TABLES, _ROPE) or as the structures above.
+    # Their descriptions come packed (_TABLES, _ROPE, ...) or as the structures above.
+    L.pafp8_append_kv_blocks.argtypes, L.pafp8_append_kv_blocks.restype = [vp, vp], i32
+    L.pafp8_read_kv.argtypes, L.pafp8_read_kv.restype = [vp, vp], i32
     L.pafp8_build_tables.argtypes, L.pafp8_build_tables.restype = [vp, vp], i32
     L.pafp8_norm_rope_append.argtypes, L.pafp8_norm_rope_append.restype = [vp, vp], i32
     _lib = L
@@ -572,6 +595,90 @@ def pafp8_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slot
         k_cache.data_ptr(), v_cache.data_ptr(), _addr(status, "status", 1, i32, dev), n, qs, ks, vs, stride, dtype_code(dt),
         dtype_code(qt), dtype_code(kt), layout, hq, hkv, d, rot, 1 if interleaved else 0, axes, limit, pages, ps, eps,
         q_scale, k_scale, v_scale), _stream_on(dev, stream)))
+
+
+def _cache_shape(k_cache, v_cache, hkv, d, layout, kv_layout, dev):
+    """(pages, page size) of two caches that hold `hkv` heads of `d` in this layout."""
+    shape, kt = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or shape[3] != d or shape[1 if layout == LAYOUT_HND else 2] != hkv:
+        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} do not hold {hkv} heads of {d} in "
+                         f"layout {kv_layout}")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.get_device() != dev or t.dtype is not kt or not t.is_contiguous():
+            _refuse(t, name, kt, dev)
+    return shape[0], shape[2 if layout == LAYOUT_HND else 1]
+
+
+def _block_scales(t, name, pages, page_size, hkv, dev) -> int:
+    """The address of a contiguous float32 [pages, page_size / 16, hkv] tensor."""
+    f32 = _torch().float32
+    if t.shape != (pages, page_size // 16, hkv):
+        raise ValueError(f"{name} {tuple(t.shape)} is not [{pages}, {page_size // 16}, {hkv}] (pages, blocks of 16 tokens, "
+                         "KV heads)")
+    return _addr(t, name, 0, f32, dev)
+
+
+def pafp8_append_kv_blocks(k_new, v_new, qo_indptr, cached_lens, kv_indptr, kv_indices, k_cache, v_cache, k_scales, v_scales,
+                           *, kv_layout="NHD", status=None, stream=None) -> None:
+    """Quantize the new tokens k_new and v_new [n, Hkv, D] into a paged fp8
+    cache with a scale for each block of 16 tokens and KV head (see
+    include/pafp8.h): rows qo_indptr[b] .. of request b from its position
+    cached_lens[b] on, k_scales and v_scales float32 [pages, page_size / 16,
+    Hkv].  k_new and v_new may be slices of one packed projection (any token
+    stride); rows from qo_indptr[batch] on are not read.  Index arrays are
+    device int32."""
+    T = _torch()
+    i32, dt = T.int32, k_new.dtype
+    if k_new.dim() != 3 or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new {tuple(k_new.shape)} and v_new {tuple(v_new.shape)} are not [n, Hkv, D] both")
+    n, hkv, d = k_new.shape
+    layout = _LAYOUTS[kv_layout] if kv_layout in _LAYOUTS else int(kv_layout)
+    dev = _device_of(k_new, "k_new")
+    (ks, kh, k1), (vs, vh, v1) = k_new.stride(), v_new.stride()
+    if v_new.dtype is not dt or v_new.get_device() != dev or k1 != 1 or v1 != 1 or (hkv > 1 and (kh != d or vh != d)):
+        raise ValueError(f"k_new and v_new ({dt} and {v_new.dtype} on {k_new.device} and {v_new.device}; strides "
+                         f"{k_new.stride()}, {v_new.stride()}) must have one dtype and lie on the current CUDA device with "
+                         "the heads of a token contiguous")
+    pages, ps = _cache_shape(k_cache, v_cache, hkv, d, layout, kv_layout, dev)
+    batch = qo_indptr.numel() - 1
+    if batch < 0:
+        raise ValueError("qo_indptr is empty (it has a request more than cached_lens)")
+    _check(lib().pafp8_append_kv_blocks(_BLOCK_APPEND.pack(
+        k_new.data_ptr(), v_new.data_ptr(), _addr(qo_indptr, "qo_indptr", 1, i32, dev),
+        _addr(cached_lens, "cached_lens", batch, i32, dev), _addr(kv_indptr, "kv_indptr", batch + 1, i32, dev),
+        _addr(kv_indices, "kv_indices", 0, i32, dev), k_cache.data_ptr(), v_cache.data_ptr(),
+        _block_scales(k_scales, "k_scales", pages, ps, hkv, dev), _block_scales(v_scales, "v_scales", pages, ps, hkv, dev),
+        _addr(status, "status", 1, i32, dev), n, ks, vs, batch, dtype_code(dt), dtype_code(k_cache.dtype), layout, hkv, d,
+        pages, ps), _stream_on(dev, stream)))
+
+
+def pafp8_read_kv(k_cache, v_cache, out_indptr, starts, kv_indptr, kv_indices, k_out, v_out, *, k_scale=1.0, v_scale=1.0,
+                  k_scales=None, v_scales=None, kv_layout="NHD", status=None, stream=None) -> None:
+    """Read token ranges of a paged fp8 cache into plain rows (see
+    include/pafp8.h): rows out_indptr[b] .. of k_out and v_out [n, Hkv, D] are
+    request b's tokens from starts[b] on, times the block scales (float32
+    [pages, page_size / 16, Hkv]) or, without them, k_scale and v_scale.  Rows
+    from out_indptr[batch] on are left as they were.  Index arrays are device
+    int32."""
+    T = _torch()
+    i32, dt = T.int32, k_out.dtype
+    if k_out.dim() != 3 or v_out.shape != k_out.shape:
+        raise ValueError(f"k_out {tuple(k_out.shape)} and v_out {tuple(v_out.shape)} are not [n, Hkv, D] both")
+    n, hkv, d = k_out.shape
+    layout = _LAYOUTS[kv_layout] if kv_layout in _LAYOUTS else int(kv_layout)
+    dev = _device_of(k_out, "k_out")
+    pages, ps = _cache_shape(k_cache, v_cache, hkv, d, layout, kv_layout, dev)
+    batch = out_indptr.numel() - 1
+    if batch < 0:
+        raise ValueError("out_indptr is empty (it has a request more than starts)")
+    _check(lib().pafp8_read_kv(_READ.pack(
+        k_cache.data_ptr(), v_cache.data_ptr(), _addr(out_indptr, "out_indptr", 1, i32, dev),
+        _addr(starts, "starts", batch, i32, dev), _addr(kv_indptr, "kv_indptr", batch + 1, i32, dev),
+        _addr(kv_indices, "kv_indices", 0, i32, dev), _addr(k_out, "k_out", 0, dt, dev), _addr(v_out, "v_out", 0, dt, dev),
+        0 if k_scales is None else _block_scales(k_scales, "k_scales", pages, ps, hkv, dev),
+        0 if v_scales is None else _block_scales(v_scales, "v_scales", pages, ps, hkv, dev),
+        _addr(status, "status", 1, i32, dev), n, batch, dtype_code(k_cache.dtype), dtype_code(dt), layout, hkv, d, pages, ps,
+        k_scale, v_scale), _stream_on(dev, stream)))
 
 
 class StepTables:

@@ -1898,4 +1898,142 @@ pafp8_status pafp8_norm_rope_append(const pafp8_rope_desc* desc, void* stream) {
     return PAFP8_OK;
 }
 
+// What the block-scale entry points ask of a cache, alike.
+static pafp8_status check_block_cache(const char* what, int32_t kv_dtype, int32_t kv_layout, int64_t nnz, int32_t batch,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t num_pages, int32_t page_size) {
+    if (!is_fp8(kv_dtype))
+        return fail(PAFP8_ERR_DTYPE, "%s works on an e4m3fn or e5m2 cache, not %s", what, dtype_name(kv_dtype));
+    if (kv_layout != PAFP8_LAYOUT_NHD && kv_layout != PAFP8_LAYOUT_HND)
+        return fail(PAFP8_ERR_ARG, "kv_layout %d is neither NHD (0) nor HND (1)", (int)kv_layout);
+    if (nnz < 0 || nnz > INT32_MAX || batch < 0 || num_pages < 0)
+        return fail(PAFP8_ERR_SHAPE, "nnz %lld, batch %d and num_pages %d must not be negative, nnz below 2^31",
+                    (long long)nnz, (int)batch, (int)num_pages);
+    if (num_kv_heads <= 0 || num_kv_heads > 65536)
+        return fail(PAFP8_ERR_SHAPE, "num_kv_heads %d must be in [1, 65536]", (int)num_kv_heads);
+    if (head_dim != kHeadDim && head_dim != 64)
+        return fail(PAFP8_ERR_UNSUPPORTED, "head_dim %d is not served by this library (%d or 64)", (int)head_dim, kHeadDim);
+    if (page_size <= 0 || page_size % kPageSize != 0)
+        return fail(PAFP8_ERR_UNSUPPORTED, "page_size %d is not served by this library (a multiple of %d)", (int)page_size,
+                    kPageSize);
+    return PAFP8_OK;
+}
+
+pafp8_status pafp8_append_kv_blocks(const pafp8_block_append_desc* desc, void* stream) {
+    if (desc == nullptr) return fail(PAFP8_ERR_ARG, "the description is NULL");
+    const pafp8_block_append_desc& d = *desc;
+    if (d.src_dtype != PAFP8_F16 && d.src_dtype != PAFP8_BF16 && d.src_dtype != PAFP8_F32)
+        return fail(PAFP8_ERR_DTYPE, "new tokens of dtype %s: append_kv_blocks takes f16, bf16 or f32 rows",
+                    dtype_name(d.src_dtype));
+    const pafp8_status st = check_block_cache("append_kv_blocks", d.kv_dtype, d.kv_layout, d.nnz, d.batch, d.num_kv_heads,
+                                              d.head_dim, d.num_pages, d.page_size);
+    if (st != PAFP8_OK) return st;
+    if (d.nnz == 0) return PAFP8_OK;
+    if (d.k == nullptr || d.v == nullptr || d.qo_indptr == nullptr || d.k_cache == nullptr || d.v_cache == nullptr ||
+        d.k_scales == nullptr || d.v_scales == nullptr ||
+        (d.batch > 0 && (d.cached_lens == nullptr || d.kv_indptr == nullptr || d.kv_indices == nullptr)))
+        return fail(PAFP8_ERR_ARG,
+                    "k, v, qo_indptr, cached_lens, kv_indptr, kv_indices, k_cache, v_cache, k_scales and v_scales must "
+                    "be non-NULL");
+    const int64_t row = (int64_t)d.num_kv_heads * d.head_dim;
+    if (d.nnz > 1 && (d.k_stride < row || d.v_stride < row))
+        return fail(PAFP8_ERR_SHAPE, "token strides must cover a token's heads (k %lld and v %lld of %lld elements)",
+                    (long long)d.k_stride, (long long)d.v_stride, (long long)row);
+    if (d.nnz > 1 && (d.k_stride % 8 != 0 || d.v_stride % 8 != 0))
+        return fail(PAFP8_ERR_ARG, "token strides must be multiples of 8 elements (k %lld, v %lld)", (long long)d.k_stride,
+                    (long long)d.v_stride);
+    if (((uintptr_t)d.k | (uintptr_t)d.v | (uintptr_t)d.k_cache | (uintptr_t)d.v_cache) % 16 != 0)
+        return fail(PAFP8_ERR_ARG, "k, v, k_cache and v_cache must be 16-byte aligned");
+    if (((uintptr_t)d.qo_indptr | (uintptr_t)d.cached_lens | (uintptr_t)d.kv_indptr | (uintptr_t)d.kv_indices |
+         (uintptr_t)d.k_scales | (uintptr_t)d.v_scales | (uintptr_t)d.status) % 4 != 0)
+        return fail(PAFP8_ERR_ARG, "qo_indptr, cached_lens, kv_indptr, kv_indices, the scales and status must be 4-byte "
+                                   "aligned");
+    if (d.k_cache == d.v_cache || d.k_scales == d.v_scales)
+        return fail(PAFP8_ERR_ARG, "K and V need a cache and scales each");
+    BlockAppendParams p{};
+    p.k = d.k;
+    p.v = d.v;
+    p.qo_indptr = d.qo_indptr;
+    p.cached_lens = d.cached_lens;
+    p.kv_indptr = d.kv_indptr;
+    p.kv_indices = d.kv_indices;
+    p.k_cache = d.k_cache;
+    p.v_cache = d.v_cache;
+    p.k_scales = d.k_scales;
+    p.v_scales = d.v_scales;
+    p.status = d.status;
+    p.nnz = d.nnz;
+    p.k_stride = d.k_stride;
+    p.v_stride = d.v_stride;
+    p.batch = d.batch;
+    p.num_kv_heads = d.num_kv_heads;
+    p.head_dim = d.head_dim;
+    p.num_pages = d.num_pages;
+    p.page_size = d.page_size;
+    p.src_dtype = d.src_dtype;
+    p.kv_dtype = d.kv_dtype;
+    p.hnd = d.kv_layout == PAFP8_LAYOUT_HND;
+    const cudaError_t e = launch_append_blocks(p, (cudaStream_t)stream);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PAFP8_ERR_CUDA, "append_kv_blocks kernel launch failed: %s", cudaGetErrorString(e));
+    }
+    return PAFP8_OK;
+}
+
+pafp8_status pafp8_read_kv(const pafp8_read_desc* desc, void* stream) {
+    if (desc == nullptr) return fail(PAFP8_ERR_ARG, "the description is NULL");
+    const pafp8_read_desc& d = *desc;
+    if (d.out_dtype != PAFP8_F16 && d.out_dtype != PAFP8_BF16 && d.out_dtype != PAFP8_F32)
+        return fail(PAFP8_ERR_DTYPE, "rows of dtype %s: read_kv writes f16, bf16 or f32", dtype_name(d.out_dtype));
+    const pafp8_status st = check_block_cache("read_kv", d.kv_dtype, d.kv_layout, d.nnz, d.batch, d.num_kv_heads, d.head_dim,
+                                              d.num_pages, d.page_size);
+    if (st != PAFP8_OK) return st;
+    if (!scale_ok(d.k_scale) || !scale_ok(d.v_scale))
+        return fail(PAFP8_ERR_ARG, "scales must be finite and > 0 (k %g, v %g)", (double)d.k_scale, (double)d.v_scale);
+    if ((d.k_scales == nullptr) != (d.v_scales == nullptr))
+        return fail(PAFP8_ERR_ARG, "block scales need both k_scales and v_scales");
+    if (d.k_scales != nullptr && (d.k_scale != 1.0f || d.v_scale != 1.0f))
+        return fail(PAFP8_ERR_ARG, "block scales replace the per-tensor ones, which must then be 1 (k %g, v %g)",
+                    (double)d.k_scale, (double)d.v_scale);
+    if (d.nnz == 0) return PAFP8_OK;
+    if (d.k_cache == nullptr || d.v_cache == nullptr || d.out_indptr == nullptr || d.k_out == nullptr || d.v_out == nullptr ||
+        (d.batch > 0 && (d.starts == nullptr || d.kv_indptr == nullptr || d.kv_indices == nullptr)))
+        return fail(PAFP8_ERR_ARG,
+                    "k_cache, v_cache, out_indptr, starts, kv_indptr, kv_indices, k_out and v_out must be non-NULL");
+    if (((uintptr_t)d.k_cache | (uintptr_t)d.v_cache | (uintptr_t)d.k_out | (uintptr_t)d.v_out) % 16 != 0)
+        return fail(PAFP8_ERR_ARG, "k_cache, v_cache, k_out and v_out must be 16-byte aligned");
+    if (((uintptr_t)d.out_indptr | (uintptr_t)d.starts | (uintptr_t)d.kv_indptr | (uintptr_t)d.kv_indices |
+         (uintptr_t)d.k_scales | (uintptr_t)d.v_scales | (uintptr_t)d.status) % 4 != 0)
+        return fail(PAFP8_ERR_ARG, "out_indptr, starts, kv_indptr, kv_indices, the scales and status must be 4-byte aligned");
+    ReadParams p{};
+    p.k_cache = d.k_cache;
+    p.v_cache = d.v_cache;
+    p.out_indptr = d.out_indptr;
+    p.starts = d.starts;
+    p.kv_indptr = d.kv_indptr;
+    p.kv_indices = d.kv_indices;
+    p.k_out = d.k_out;
+    p.v_out = d.v_out;
+    p.k_scales = d.k_scales;
+    p.v_scales = d.v_scales;
+    p.status = d.status;
+    p.nnz = d.nnz;
+    p.batch = d.batch;
+    p.num_kv_heads = d.num_kv_heads;
+    p.head_dim = d.head_dim;
+    p.num_pages = d.num_pages;
+    p.page_size = d.page_size;
+    p.kv_dtype = d.kv_dtype;
+    p.out_dtype = d.out_dtype;
+    p.hnd = d.kv_layout == PAFP8_LAYOUT_HND;
+    p.k_scale = d.k_scale;
+    p.v_scale = d.v_scale;
+    const cudaError_t e = launch_read_kv(p, (cudaStream_t)stream);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PAFP8_ERR_CUDA, "read_kv kernel launch failed: %s", cudaGetErrorString(e));
+    }
+    return PAFP8_OK;
+}
+
 }  // extern "C"

@@ -170,6 +170,42 @@ struct RopeParams {
     float eps, q_inv, k_inv, v_inv;  // inv: fp32(1 / scale)
 };
 
+struct BlockAppendParams {
+    const void* k;               // [nnz, Hkv, D] of src_dtype, tokens k_stride elements apart
+    const void* v;
+    const int32_t* qo_indptr;    // [batch + 1]: rows of each request's new tokens
+    const int32_t* cached_lens;  // [batch]: position of its first new token
+    const int32_t* kv_indptr;    // [batch + 1]
+    const int32_t* kv_indices;
+    void* k_cache;
+    void* v_cache;
+    float* k_scales;             // [num_pages, page_size / 16, Hkv]
+    float* v_scales;
+    uint32_t* status;            // or nullptr
+    long long nnz, k_stride, v_stride;
+    int batch, num_kv_heads, head_dim, num_pages, page_size;
+    int src_dtype, kv_dtype, hnd;
+    int span;                    // set by the launcher: new tokens a warp looks through for its blocks
+};
+
+struct ReadParams {
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* out_indptr;   // [batch + 1]: output rows of each request
+    const int32_t* starts;       // [batch]: position of its first row
+    const int32_t* kv_indptr;
+    const int32_t* kv_indices;
+    void* k_out;                 // [nnz, Hkv, D] of out_dtype
+    void* v_out;
+    const float* k_scales;       // [num_pages, page_size / 16, Hkv], or nullptr: k_scale
+    const float* v_scales;
+    uint32_t* status;            // or nullptr
+    long long nnz;
+    int batch, num_kv_heads, head_dim, num_pages, page_size;
+    int kv_dtype, out_dtype, hnd;
+    float k_scale, v_scale;
+};
+
 struct PrefillParams {
     const void* q;           // [nnz_qo, Hq, D]
     int head_dim;            // D: 128 or 64
@@ -230,6 +266,8 @@ cudaError_t launch_decode(const DecodeParams& p, const CUtensorMap& tmap_k,
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_append_blocks(const BlockAppendParams& p, cudaStream_t stream);
+cudaError_t launch_read_kv(const ReadParams& p, cudaStream_t stream);
 // Size of the built-in scratch of the no-allocation decode entry point, and
 // the device ordinals it serves.
 constexpr size_t kNoAllocScratchBytes = PAFP8_NOALLOC_SCRATCH_BYTES;
