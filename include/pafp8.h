@@ -30,7 +30,7 @@
  *     until the next failing call on this thread).  Nothing aborts.
  *   - pafp8_run neither allocates nor synchronizes, unless PAFP8_DEBUG is
  *     set in the environment (to anything but "0"): then every run call that
- *     launches (pafp8_run, _stage, _head_scales, _tree, _pod) synchronizes its
+ *     launches (pafp8_run, _stage, _head_scales, _block_scales, _tree, _pod) synchronizes its
  *     stream and returns the kernels' status as pafp8_device_status reports
  *     it (PAFP8_ERR_BOUNDS, PAFP8_ERR_TIMEOUT), so a bad page index or an
  *     expired wait surfaces at the call that caused it.  Not for use under
@@ -173,6 +173,25 @@ const char *pafp8_last_error(void);
 pafp8_status pafp8_plan_create(const pafp8_plan_desc *desc, const int32_t *kv_indptr_h,
                                const int32_t *last_page_len_h, const int32_t *qo_indptr_h,
                                pafp8_plan **out);
+
+/* pafp8_plan_create with a sliding window and attention sinks, for a decode or
+ * prefill plan: the row at position t of its request (t = kv_len - 1 in
+ * decode, i + kv_len - qo_len for prefill row i) sees the keys j <= t with
+ * j > t - window or j < sinks -- the last `window` keys, itself among them, and
+ * the request's first `sinks` tokens.  Every run call takes such a plan
+ * (pafp8_run_pod also with one windowed phase); only the visible keys' pages
+ * are read, in decode to a granule of 16 tokens and in prefill of 128, and the
+ * split-KV options count those pages.  Values of tokens that no row of a
+ * decode request, or of a prefill item (two tiles of 128 / group new tokens
+ * and one KV head), sees are not used, whatever they hold; a NaN in the value
+ * row of any other token reaches every row of the item.
+ *   window  0: no window (sinks must then be 0); > 0: keys seen
+ *   sinks   >= 0
+ * Lengths up to 2^31 - 129 keys a request with a window; tree plans take
+ * none.  Everything else is pafp8_plan_create's. */
+pafp8_status pafp8_plan_create_window(const pafp8_plan_desc *desc, int32_t window, int32_t sinks,
+                                      const int32_t *kv_indptr_h, const int32_t *last_page_len_h,
+                                      const int32_t *qo_indptr_h, pafp8_plan **out);
 
 /* Free a plan (NULL is ignored). */
 void pafp8_plan_destroy(pafp8_plan *plan);
@@ -700,6 +719,23 @@ typedef struct pafp8_block_append_desc {
 } pafp8_block_append_desc;
 
 pafp8_status pafp8_append_kv_blocks(const pafp8_block_append_desc *desc, void *stream);
+
+/* pafp8_run over such a cache: key and value j of KV head h are their codes
+ * times k_scales | v_scales[page][slot / 16][h].  For decode and prefill plans,
+ * with a window or without, over an E4M3FN or E5M2 cache; any scales that are
+ * finite and > 0 (device memory, not checked), 2^-96 to 2^96 in prefill.
+ *   q_scale    as in pafp8_run (an fp8 query)
+ *   k_scales,
+ *   v_scales   device float [num_pages, page_size / 16, num_kv_heads]
+ * Every other argument and check is pafp8_run's.  Decode multiplies a block's
+ * product with V by its scale in fp32; prefill lets the scale ride in the
+ * exponent of the probabilities, which are rounded to f16's 11 bits (those
+ * below 2^-14 of the request's largest probability times V scale to 2^-25 of
+ * it). */
+pafp8_status pafp8_run_block_scales(const pafp8_plan *plan, int32_t q_dtype, const void *q, int32_t k_dtype,
+                                    const void *k_cache, int32_t v_dtype, const void *v_cache, const int32_t *kv_indices,
+                                    float q_scale, const float *k_scales, const float *v_scales, int32_t o_dtype, void *o,
+                                    float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Read token ranges of an fp8 cache back into plain rows: output rows
  * out_indptr[b] .. out_indptr[b + 1] - 1 are tokens starts[b], starts[b] + 1,

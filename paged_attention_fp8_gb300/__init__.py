@@ -45,7 +45,8 @@ EXPORTS = ("pafp8_abi_version", "pafp8_last_error", "pafp8_plan_create", "pafp8_
            "pafp8_workspace_bytes", "pafp8_plan_metadata", "pafp8_plan_upload", "pafp8_run",
            "pafp8_run_stage", "pafp8_device_status", "pafp8_run_decode_noalloc", "pafp8_append_kv",
            "pafp8_run_head_scales", "pafp8_run_pod", "pafp8_host_workspace_bytes", "pafp8_run_host",
-           "pafp8_build_tables", "pafp8_norm_rope_append", "pafp8_run_tree", "pafp8_append_kv_blocks", "pafp8_read_kv")
+           "pafp8_build_tables", "pafp8_norm_rope_append", "pafp8_run_tree", "pafp8_append_kv_blocks", "pafp8_read_kv",
+           "pafp8_plan_create_window", "pafp8_run_block_scales")
 
 
 class Pafp8Error(RuntimeError):
@@ -137,6 +138,10 @@ def lib() -> ctypes.CDLL:
     L.pafp8_last_error.argtypes, L.pafp8_last_error.restype = [], ctypes.c_char_p
     L.pafp8_plan_create.argtypes = [ctypes.POINTER(plan_desc), vp, vp, vp, ctypes.POINTER(vp)]
     L.pafp8_plan_create.restype = i32
+    L.pafp8_plan_create_window.argtypes = [ctypes.POINTER(plan_desc), i32, i32, vp, vp, vp, ctypes.POINTER(vp)]
+    L.pafp8_plan_create_window.restype = i32
+    L.pafp8_run_block_scales.argtypes = [vp, i32, vp, i32, vp, i32, vp, vp, f32, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.pafp8_run_block_scales.restype = i32
     L.pafp8_plan_destroy.argtypes, L.pafp8_plan_destroy.restype = [vp], None
     L.pafp8_workspace_bytes.argtypes, L.pafp8_workspace_bytes.restype = [vp], sz
     L.pafp8_plan_metadata.argtypes = [vp, ctypes.POINTER(ctypes.POINTER(ctypes.c_int32)),
@@ -251,6 +256,10 @@ def pafp8_last_error() -> str:
 # What pafp8_run_tree needs of its arrays, by the handles of the tree plans that
 # exist: the shapes of q and o, of the caches and of lse, page ids, mask rows, KV heads.
 _TREE_SIZES = {}
+# The same of the other plans, for pafp8_run_block_scales: plain numbers until
+# its first call makes the shapes of them (a plan is made anew in every step of
+# some callers).
+_SIZES = {}
 _ITEM = {F16: 2, BF16: 2, E4M3FN: 1, E5M2: 1}  # bytes of an element; the library refuses other types
 
 
@@ -259,6 +268,26 @@ def _tree_sizes(desc, kv_indptr, qo_indptr):
     hq, hkv, ps, d = desc.num_qo_heads, desc.num_kv_heads, desc.page_size, desc.head_dim
     page = (hkv, ps, d) if desc.kv_layout == LAYOUT_HND else (ps, hkv, d)
     return (rows, hq, d), (desc.num_pages, *page), (rows, hq), int(kv_indptr[-1]) if desc.batch > 0 else 0, rows, hkv
+
+
+def _note_sizes(handle, desc, kv_indptr, qo_indptr) -> None:
+    batch = desc.batch
+    last = ctypes.c_int32.from_address
+    _SIZES[handle] = (batch if qo_indptr is None or batch <= 0 else last(_ptr(qo_indptr) + 4 * batch).value,
+                      desc.num_qo_heads, desc.num_kv_heads, desc.page_size, desc.head_dim, desc.num_pages, desc.kv_layout,
+                      last(_ptr(kv_indptr) + 4 * batch).value if batch > 0 else 0)
+
+
+def _sizes(handle):
+    """The shapes of q and o, of the caches, of lse and of the block scales, and the page ids."""
+    s = _SIZES.get(handle)
+    if s is None:
+        raise ValueError("block scales need a decode or prefill plan that exists")
+    if len(s) == 8:
+        rows, hq, hkv, ps, d, pages, layout, ids = s
+        s = _SIZES[handle] = ((rows, hq, d), (pages, hkv, ps, d) if layout == LAYOUT_HND else (pages, ps, hkv, d), (rows, hq),
+                              (pages, ps // 16, hkv), ids)
+    return s
 
 
 def _tree_fits(sizes, arrays, kv_indices, lse) -> None:
@@ -280,11 +309,24 @@ def pafp8_plan_create(desc: plan_desc, kv_indptr, last_page_len, qo_indptr=None)
                                    _ptr(qo_indptr), ctypes.byref(out)))
     if desc.mode == MODE_TREE:
         _TREE_SIZES[out.value] = _tree_sizes(desc, kv_indptr, qo_indptr)
+    else:
+        _note_sizes(out.value, desc, kv_indptr, qo_indptr)
+    return out.value
+
+
+def pafp8_plan_create_window(desc: plan_desc, window: int, sinks: int, kv_indptr, last_page_len, qo_indptr=None) -> int:
+    """pafp8_plan_create with a sliding window and attention sinks (see include/pafp8.h)."""
+    kv_indptr, last_page_len, qo_indptr = _i32_host(kv_indptr), _i32_host(last_page_len), _i32_host(qo_indptr)
+    out = ctypes.c_void_p()
+    _check(lib().pafp8_plan_create_window(ctypes.byref(desc), window, sinks, _ptr(kv_indptr), _ptr(last_page_len),
+                                          _ptr(qo_indptr), ctypes.byref(out)))
+    _note_sizes(out.value, desc, kv_indptr, qo_indptr)
     return out.value
 
 
 def pafp8_plan_destroy(handle: int) -> None:
     _TREE_SIZES.pop(handle, None)
+    _SIZES.pop(handle, None)
     lib().pafp8_plan_destroy(handle)
 
 
@@ -405,6 +447,36 @@ def pafp8_run_tree(handle: int, q, k_cache, v_cache, kv_indices, tree_mask, o, l
         handle, qc, q.data_ptr(), kc, k_cache.data_ptr(), vc, v_cache.data_ptr(), _ptr(kv_indices), tree_mask.data_ptr(), words,
         q_scale, k_scale, v_scale, *scales, oc, o.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes,
         _stream_on(dev, stream)))
+
+
+def pafp8_run_block_scales(handle: int, q, k_cache, v_cache, kv_indices, o, lse, workspace, *, q_scale=1.0, k_scales,
+                           v_scales, stream=None) -> None:
+    """pafp8_run over a cache with a scale for each 16-token block and KV head:
+    k_scales and v_scales, float32 [pages, page_size / 16, Hkv].  Arrays are
+    contiguous and on the current CUDA device; kv_indices is int32, lse float32
+    or None; dtypes come from the tensors."""
+    T = _torch()
+    dev = _device_of(q, "q")
+    qt, kt, ot, i32, f32 = q.dtype, k_cache.dtype, o.dtype, T.int32, T.float32
+    for t, name, dtype in ((q, "q", qt), (k_cache, "k_cache", kt), (v_cache, "v_cache", kt), (kv_indices, "kv_indices", i32),
+                           (o, "o", ot), (lse, "lse", f32), (workspace, "workspace", workspace.dtype), (k_scales, "k_scales", f32),
+                           (v_scales, "v_scales", f32)):
+        if t is not None and (t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous()):
+            _refuse(t, name, dtype, dev)
+    rows_of, pool, lse_of, blocks, n_index = _sizes(handle)
+    if q.shape != rows_of or o.shape != rows_of or k_cache.shape != pool or v_cache.shape != pool or \
+            (lse is not None and lse.shape != lse_of) or (kv_indices is not None and kv_indices.numel() < n_index):
+        raise ValueError(f"q {tuple(q.shape)}, o {tuple(o.shape)}, k_cache {tuple(k_cache.shape)}, v_cache "
+                         f"{tuple(v_cache.shape)}, lse {lse is not None and tuple(lse.shape)} and kv_indices "
+                         f"{kv_indices is not None and kv_indices.numel()} do not fit the plan's {rows_of}, {pool}, {lse_of} "
+                         f"and {n_index} page ids")
+    if k_scales.shape != blocks or v_scales.shape != blocks:
+        raise ValueError(f"k_scales {tuple(k_scales.shape)} and v_scales {tuple(v_scales.shape)} are not {blocks} (pages, "
+                         "blocks of 16 tokens, KV heads)")
+    _check(lib().pafp8_run_block_scales(
+        handle, dtype_code(qt), q.data_ptr(), dtype_code(kt), k_cache.data_ptr(), dtype_code(kt), v_cache.data_ptr(),
+        _ptr(kv_indices), q_scale, k_scales.data_ptr(), v_scales.data_ptr(), dtype_code(ot), o.data_ptr(), _ptr(lse),
+        workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream)))
 
 
 def pafp8_device_status(handle: int, workspace, stream=None) -> None:
@@ -730,7 +802,9 @@ class Plan:
                  kv_indptr, last_page_len, qo_indptr=None, q_dtype, kv_dtype, o_dtype=None,
                  head_dim: int = 128, page_size: int = 16, sm_scale: float = 0.0,
                  fixed_split_pages: int = 0, disable_split_kv: bool = False, num_ctas: int = 0,
-                 kv_layout: str = "NHD"):
+                 kv_layout: str = "NHD", window: int = 0, sinks: int = 0):
+        """window > 0: rows see the last `window` keys and their request's
+        first `sinks` tokens (decode and prefill plans)."""
         kv_indptr_h = _i32_host(kv_indptr)
         self.desc = plan_desc(
             mode=_MODES.get(mode, MODE_PREFILL), batch=len(kv_indptr_h) - 1,
@@ -742,7 +816,8 @@ class Plan:
             disable_split_kv=int(bool(disable_split_kv)), num_ctas=int(num_ctas),
             kv_layout=_LAYOUTS[kv_layout] if isinstance(kv_layout, str) else int(kv_layout))
         self.handle = None
-        self.handle = pafp8_plan_create(self.desc, kv_indptr_h, last_page_len, qo_indptr)
+        self.handle = pafp8_plan_create(self.desc, kv_indptr_h, last_page_len, qo_indptr) if not window and not sinks else \
+            pafp8_plan_create_window(self.desc, int(window), int(sinks), kv_indptr_h, last_page_len, qo_indptr)
 
     def __del__(self):
         if getattr(self, "handle", None):
@@ -770,6 +845,9 @@ class Plan:
 
     def run_head_scales(self, q, k_cache, v_cache, kv_indices, o, lse, workspace, **kw) -> None:
         pafp8_run_head_scales(self.handle, q, k_cache, v_cache, kv_indices, o, lse, workspace, **kw)
+
+    def run_block_scales(self, q, k_cache, v_cache, kv_indices, o, lse, workspace, **kw) -> None:
+        pafp8_run_block_scales(self.handle, q, k_cache, v_cache, kv_indices, o, lse, workspace, **kw)
 
     def run_tree(self, q, k_cache, v_cache, kv_indices, tree_mask, o, lse, workspace, **kw) -> None:
         pafp8_run_tree(self.handle, q, k_cache, v_cache, kv_indices, tree_mask, o, lse, workspace, **kw)

@@ -1,0 +1,11 @@
+// The decode kernel with a scale for each 16-token block and head (the kernel is in decode.cuh).
+#include "decode.cuh"
+
+namespace pafp8 {
+
+cudaError_t launch_decode_blocks(const DecodeParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int num_ctas,
+                             int hpc, int group, int heads_per_box, cudaStream_t stream) {
+    return launch_decode_var<kVarBlocks>(p, tmap_k, tmap_v, num_ctas, hpc, group, heads_per_box, stream);
+}
+
+}  // namespace pafp8

@@ -130,8 +130,10 @@ struct pafp8_plan {
     int heads_per_cta = 1, head_blocks = 1, group = 1;
     // Pages of page_size = 16 * page_mult tokens are read as page_mult
     // consecutive 16-token sub-pages; vptr is the CSR of sub-pages per
-    // request (ceil(kv_len / 16)), the unit of the decode partition.
+    // request (ceil(kv_len / 16), less those that a window leaves out), the
+    // unit of the decode partition.
     int page_mult = 1;
+    int window = 0, sinks = 0;  // keys a row sees besides the first `sinks`; window 0: all
     std::vector<int32_t> vptr;
     int num_ctas = 0, num_partials = 0, num_merge = 0;
     int tile_rows = 0;   // tree: rows a row tile may have (32 or 64)
@@ -412,7 +414,8 @@ void build_prefill_meta(pafp8_plan* pl) {
     // A 2-byte cache at head_dim 128 runs on CTA pairs: a query tile is 2 TQ
     // tokens (TQ per CTA), an item two such tiles; the rest on single CTAs
     // (tiles of TQ).
-    const bool pair = pl->desc.head_dim == kHeadDim && is_2byte(pl->desc.kv_dtype);
+    // (A window's few tiles an item go to single CTAs as well.)
+    const bool pair = pl->desc.head_dim == kHeadDim && is_2byte(pl->desc.kv_dtype) && pl->window == 0;
     const int span = (pair ? 4 : 2) * TQ;
     struct T { int32_t b, hk, t0, nkv; };
     std::vector<T> tiles;
@@ -428,7 +431,9 @@ void build_prefill_meta(pafp8_plan* pl) {
                 // after; its KV tiles are those of its last token.
                 const int last = std::min(t0 + span, qo) - 1;
                 const int lim = last + req_kv[b] - qo;
-                const int nkv = std::min((req_kv[b] + kTileKeys - 1) / kTileKeys, lim / kTileKeys + 1);
+                int nkv = std::min((req_kv[b] + kTileKeys - 1) / kTileKeys, lim / kTileKeys + 1);
+                if (pl->window > 0)
+                    nkv -= window_units(t0 + req_kv[b] - qo - pl->window + 1, pl->sinks, kTileKeys).gap;
                 tiles.push_back({b, hk, t0, nkv});
             }
     }
@@ -917,6 +922,12 @@ const char* pafp8_last_error(void) { return g_last_error.c_str(); }
 pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv_indptr_h,
                                const int32_t* last_page_len_h, const int32_t* qo_indptr_h,
                                pafp8_plan** out) {
+    return pafp8_plan_create_window(desc_in, 0, 0, kv_indptr_h, last_page_len_h, qo_indptr_h, out);
+}
+
+pafp8_status pafp8_plan_create_window(const pafp8_plan_desc* desc_in, int32_t window, int32_t sinks,
+                                      const int32_t* kv_indptr_h, const int32_t* last_page_len_h,
+                                      const int32_t* qo_indptr_h, pafp8_plan** out) {
     if (out == nullptr) return fail(PAFP8_ERR_ARG, "out (plan pointer) is NULL");
     *out = nullptr;
     if (desc_in == nullptr) return fail(PAFP8_ERR_ARG, "plan description is NULL");
@@ -965,6 +976,12 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
     if (d.fixed_split_pages < 0)
         return fail(PAFP8_ERR_ARG, "fixed_split_pages %d is negative", (int)d.fixed_split_pages);
     if (d.num_ctas < 0) return fail(PAFP8_ERR_ARG, "num_ctas %d is negative", (int)d.num_ctas);
+    if (window < 0 || sinks < 0)
+        return fail(PAFP8_ERR_ARG, "window %d and sinks %d must not be negative", (int)window, (int)sinks);
+    if (window == 0 && sinks > 0)
+        return fail(PAFP8_ERR_ARG, "sinks %d given without a window: every key is visible already", (int)sinks);
+    if (window > 0 && d.mode == PAFP8_MODE_TREE)
+        return fail(PAFP8_ERR_UNSUPPORTED, "a tree plan takes no window (window %d)", (int)window);
     if (d.batch > 0 && (kv_indptr_h == nullptr || last_page_len_h == nullptr))
         return fail(PAFP8_ERR_ARG, "kv_indptr and last_page_len host arrays are required");
     if (d.mode == PAFP8_MODE_DECODE && qo_indptr_h != nullptr)
@@ -984,6 +1001,10 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
                         (int)last_page_len_h[b], (int)d.page_size);
         if (n > 0 && d.num_pages == 0)
             return fail(PAFP8_ERR_SHAPE, "request %d has pages but num_pages is 0", b);
+        // The windowed kernels count keys in 32 bits, up to the end of the last tile.
+        if (window > 0 && n > 0 && (n - 1) * d.page_size + last_page_len_h[b] > INT32_MAX - kTileKeys)
+            return fail(PAFP8_ERR_UNSUPPORTED, "request %d has kv_len %lld: a window goes with up to %d", b,
+                        (long long)((n - 1) * d.page_size + last_page_len_h[b]), INT32_MAX - kTileKeys);
         if (d.mode != PAFP8_MODE_DECODE) {
             if (b == 0 && qo_indptr_h[0] != 0)
                 return fail(PAFP8_ERR_SHAPE, "qo_indptr[0] is %d, not 0", (int)qo_indptr_h[0]);
@@ -1023,6 +1044,8 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
     pafp8_plan* pl = new pafp8_plan();
     pl->desc = d;
     pl->group = group;
+    pl->window = window;
+    pl->sinks = sinks;
     pl->heads_per_cta = heads_per_cta_for(d.num_kv_heads);
     pl->head_blocks = d.num_kv_heads / pl->heads_per_cta;
     if (d.batch > 0) {
@@ -1037,7 +1060,9 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc* desc_in, const int32_t* kv
     for (int b = 0; b < d.batch; ++b) {
         const int64_t n = (int64_t)pl->kv_indptr[b + 1] - pl->kv_indptr[b];
         const int64_t kv = n > 0 ? (n - 1) * d.page_size + pl->last_page_len[b] : 0;
-        pl->vptr[b + 1] = pl->vptr[b] + (int32_t)((kv + kPageSize - 1) / kPageSize);
+        int64_t units = (kv + kPageSize - 1) / kPageSize;
+        if (window > 0) units -= window_units((int)kv - window, sinks, kPageSize).gap;
+        pl->vptr[b + 1] = pl->vptr[b] + (int32_t)units;
     }
     if (d.mode != PAFP8_MODE_DECODE) {
         if (d.batch > 0)
@@ -1110,6 +1135,12 @@ struct TreeMask {
     int32_t words;
 };
 
+// The scales of pafp8_run_block_scales.
+struct BlockScales {
+    const float* k;
+    const float* v;
+};
+
 // Checks and launches of the run entry points.  Per-head scale tensors
 // (device arrays) replace the per-tensor scales when k_scales is not NULL.
 // With launch false only the checks run.
@@ -1118,7 +1149,7 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
                       const int32_t* kv_indices, float q_scale, float k_scale, float v_scale,
                       const float* q_scales, const float* k_scales, const float* v_scales,
                       int32_t o_dtype, void* o, float* lse, void* workspace, size_t workspace_bytes,
-                      void* stream, bool launch, const TreeMask* tree) {
+                      void* stream, bool launch, const TreeMask* tree, const BlockScales* blocks) {
     if (plan == nullptr) return fail(PAFP8_ERR_ARG, "plan is NULL");
     if (stage < 0 || stage > 2) return fail(PAFP8_ERR_ARG, "stage %d is not 0, 1 or 2", (int)stage);
     const pafp8_plan_desc& d = plan->desc;
@@ -1176,6 +1207,15 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
         return fail(PAFP8_ERR_ARG, "q, o, k_cache and v_cache must be 16-byte aligned");
     if ((uintptr_t)lse % 4 != 0 || (uintptr_t)kv_indices % 4 != 0)
         return fail(PAFP8_ERR_ARG, "lse and kv_indices must be 4-byte aligned");
+    if (blocks != nullptr) {
+        if (!is_fp8(k_dtype))
+            return fail(PAFP8_ERR_DTYPE, "block scales go with an e4m3fn or e5m2 cache, not %s", dtype_name(k_dtype));
+        if (plan->nnz_pages > 0 && (blocks->k == nullptr || blocks->v == nullptr))
+            return fail(PAFP8_ERR_ARG, "k_scales and v_scales (device arrays of num_pages * page_size / 16 * num_kv_heads "
+                                       "floats) are required");
+        if (((uintptr_t)blocks->k | (uintptr_t)blocks->v) % 4 != 0)
+            return fail(PAFP8_ERR_ARG, "k_scales and v_scales must be 4-byte aligned");
+    }
     if (tree != nullptr) {
         if (plan->nnz_qo > 0 && (tree->bits == nullptr || (uintptr_t)tree->bits % 4 != 0))
             return fail(PAFP8_ERR_ARG, "tree_mask must be non-NULL and 4-byte aligned");
@@ -1214,6 +1254,10 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
         pp.k_scales = k_scales;
         pp.v_scales = k_scales != nullptr ? v_scales : nullptr;
         pp.sm_scale = d.sm_scale;
+        pp.k_blocks = blocks != nullptr ? blocks->k : nullptr;
+        pp.v_blocks = blocks != nullptr ? blocks->v : nullptr;
+        pp.window = plan->window;
+        pp.sinks = plan->sinks;
         pp.wait_cycles = wait_cycles();
         CUtensorMap tq, tk, tv;
         if ((st = encode_q_map(&tq, q, (int)plan->nnz_qo, d.num_qo_heads, plan->group,
@@ -1240,7 +1284,7 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
         if ((st = encode_q_map(&to, o, (int)plan->nnz_qo, d.num_qo_heads, plan->group, pp.tile_tokens,
                                false, d.head_dim)) != PAFP8_OK)
             return st;
-        cudaError_t e = launch_prefill(pp, tq, tk, tv, to, plan->num_ctas, s);
+        cudaError_t e = prefill_launcher(pp)(pp, tq, tk, tv, to, plan->num_ctas, s);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return fail(PAFP8_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
@@ -1313,6 +1357,10 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
     p.k_scales = k_scales;
     p.v_scales = k_scales != nullptr ? v_scales : nullptr;
     p.sm_scale = d.sm_scale;
+    p.k_blocks = blocks != nullptr ? blocks->k : nullptr;
+    p.v_blocks = blocks != nullptr ? blocks->v : nullptr;
+    p.window = plan->window;
+    p.sinks = plan->sinks;
     p.wait_cycles = wait_cycles();
 
     cudaError_t e = cudaSuccess;
@@ -1352,10 +1400,11 @@ pafp8_status run_impl(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
                       const int32_t* kv_indices, float q_scale, float k_scale, float v_scale,
                       const float* q_scales, const float* k_scales, const float* v_scales,
                       int32_t o_dtype, void* o, float* lse, void* workspace, size_t workspace_bytes,
-                      void* stream, bool launch = true, const TreeMask* tree = nullptr) {
+                      void* stream, bool launch = true, const TreeMask* tree = nullptr,
+                      const BlockScales* blocks = nullptr) {
     const pafp8_status st = run_body(plan, stage, q_dtype, q, k_dtype, k_cache, v_dtype, v_cache, kv_indices,
                                      q_scale, k_scale, v_scale, q_scales, k_scales, v_scales, o_dtype, o, lse,
-                                     workspace, workspace_bytes, stream, launch, tree);
+                                     workspace, workspace_bytes, stream, launch, tree, blocks);
     if (st != PAFP8_OK || !launch || !debug_sync()) return st;
     return pafp8_device_status(plan, workspace, stream);
 }
@@ -1458,6 +1507,17 @@ pafp8_status pafp8_run_tree(const pafp8_plan* plan, int32_t q_dtype, const void*
     const TreeMask mask{tree_mask, mask_words};
     return run_impl(plan, 0, q_dtype, q, k_dtype, k_cache, v_dtype, v_cache, kv_indices, q_scale, k_scale, v_scale,
                     q_scales, k_scales, v_scales, o_dtype, o, lse, workspace, workspace_bytes, stream, true, &mask);
+}
+
+pafp8_status pafp8_run_block_scales(const pafp8_plan* plan, int32_t q_dtype, const void* q, int32_t k_dtype,
+                                    const void* k_cache, int32_t v_dtype, const void* v_cache, const int32_t* kv_indices,
+                                    float q_scale, const float* k_scales, const float* v_scales, int32_t o_dtype, void* o,
+                                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (plan != nullptr && plan->desc.mode == PAFP8_MODE_TREE)
+        return fail(PAFP8_ERR_UNSUPPORTED, "block scales are served by decode and prefill plans, not by tree plans");
+    const BlockScales blocks{k_scales, v_scales};
+    return run_impl(plan, 0, q_dtype, q, k_dtype, k_cache, v_dtype, v_cache, kv_indices, q_scale, 1.0f, 1.0f, nullptr,
+                    nullptr, nullptr, o_dtype, o, lse, workspace, workspace_bytes, stream, true, nullptr, &blocks);
 }
 
 pafp8_status pafp8_device_status(const pafp8_plan* plan, void* workspace, void* stream) {
@@ -1564,6 +1624,8 @@ pafp8_status pafp8_run_decode_noalloc(const pafp8_plan* plan, int32_t q_dtype, c
     p.sm_scale_log2 = (float)((double)d.sm_scale * (is_fp8(q_dtype) ? (double)q_scale : 1.0) *
                               (double)k_scale * 1.4426950408889634);
     p.v_scale = v_scale;
+    p.window = plan->window;
+    p.sinks = plan->sinks;
     p.wait_cycles = wait_cycles();
     if (plan->num_ctas > 0) {
         CUtensorMap tk, tv;

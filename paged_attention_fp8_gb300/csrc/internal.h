@@ -95,6 +95,27 @@ __device__ __forceinline__ SubPageAt sub_page(const int32_t* idx, int vp, int m,
     return SubPageAt{(vp - e * m) * kPageSize, bad ? 0 : pg};
 }
 
+// The keys that a row at position p sees under a window of w keys and s first
+// tokens that stay visible: j <= p with j < s or j > p - w.  In units of `unit`
+// keys a batch item reads units 0 .. head - 1 (the sinks') and, gap units
+// further, those from its first window key on; they are numbered without the
+// gap, unit u standing for u + gap from head on.  first_key: the first key in
+// the window of the item's first row (negative: the window reaches past the
+// start).  Without a window gap is 0.
+struct WindowUnits {
+    int head, gap;
+    __host__ __device__ int at(int u) const { return u < head ? u : u + gap; }
+};
+__host__ __device__ inline WindowUnits window_units(int first_key, int sinks, int unit) {
+    const int head = sinks > 0 ? (sinks - 1) / unit + 1 : 0;
+    const int from = first_key > 0 ? first_key / unit : 0;
+    return WindowUnits{head, from > head ? from - head : 0};
+}
+
+// Variants of the decode and prefill kernels, beside the plain one: a sliding
+// window, and block scales (with or without a window).
+constexpr int kVarPlain = 0, kVarWindow = 1, kVarBlocks = 2;
+
 // Status word bits written by the kernels into the workspace.
 enum : uint32_t {
     kStatusBounds = 1u,   // a page index outside [0, num_pages)
@@ -123,6 +144,11 @@ struct DecodeParams {
     const float* k_scales;
     const float* v_scales;
     float sm_scale;
+    // Scales of 16-token blocks, [num_pages, page_mult, Hkv], when not null
+    // (sm_scale_log2 then holds no k_scale, and v_scale is 1).
+    const float* k_blocks;
+    const float* v_blocks;
+    int window, sinks;       // keys a row sees besides the first `sinks`; window 0: all
     long long wait_cycles;   // bound of a pipeline wait (SM clock cycles)
 };
 
@@ -228,6 +254,11 @@ struct PrefillParams {
     const float* k_scales;
     const float* v_scales;
     float sm_scale;
+    // Scales of 16-token blocks, [num_pages, page_mult, Hkv], when not null
+    // (sm_scale_log2 then holds no k_scale, and v_scale is 1).
+    const float* k_blocks;
+    const float* v_blocks;
+    int window, sinks;       // keys a row sees besides the first `sinks`; window 0: all
     long long wait_cycles;   // bound of a pipeline wait (SM clock cycles)
 };
 
@@ -257,12 +288,12 @@ struct TreeParams {
     long long wait_cycles;   // bound of a pipeline wait (SM clock cycles)
 };
 
-// Launchers (decode.cu, prefill_d128.cu / prefill_d64.cu).  Return the launch's cudaError_t.
+// Launchers (decode*.cu, prefill_d128.cu / prefill_d64.cu).  Return the launch's cudaError_t.
 // heads_per_box: KV heads covered by one TMA box of the cache maps (the
 // whole head block when the page-wide map could be encoded, else 1).
-cudaError_t launch_decode(const DecodeParams& p, const CUtensorMap& tmap_k,
-                          const CUtensorMap& tmap_v, int num_ctas, int heads_per_cta,
-                          int group, int heads_per_box, cudaStream_t stream);
+using DecodeLaunch = cudaError_t(const DecodeParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v, int num_ctas,
+                                 int heads_per_cta, int group, int heads_per_box, cudaStream_t stream);
+DecodeLaunch launch_decode, launch_decode_window, launch_decode_blocks;  // the first picks among the variants
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
@@ -281,17 +312,14 @@ cudaError_t launch_merge(const DecodeParams& p, int num_merge, int heads_per_cta
 // tmap_o: map over o with the 2-byte query tile's box (the fp8-query kernel
 // writes full output tiles with bulk tensor stores through it).  One
 // translation unit per head size (prefill_d128.cu, prefill_d64.cu).
-cudaError_t launch_prefill_d128(const PrefillParams& p, const CUtensorMap& tmap_q,
-                                const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
-                                const CUtensorMap& tmap_o, int num_ctas, cudaStream_t stream);
-cudaError_t launch_prefill_d64(const PrefillParams& p, const CUtensorMap& tmap_q,
-                               const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
-                               const CUtensorMap& tmap_o, int num_ctas, cudaStream_t stream);
-inline cudaError_t launch_prefill(const PrefillParams& p, const CUtensorMap& tmap_q,
-                                  const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
-                                  const CUtensorMap& tmap_o, int num_ctas, cudaStream_t stream) {
-    return p.head_dim == 64 ? launch_prefill_d64(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream)
-                            : launch_prefill_d128(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
+using PrefillLaunch = cudaError_t(const PrefillParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
+                                  const CUtensorMap& tmap_v, const CUtensorMap& tmap_o, int num_ctas, cudaStream_t stream);
+PrefillLaunch launch_prefill_d128, launch_prefill_d64, launch_prefill_window_d128, launch_prefill_window_d64,
+    launch_prefill_blocks_d128, launch_prefill_blocks_d64;
+inline PrefillLaunch* prefill_launcher(const PrefillParams& p) {
+    if (p.k_blocks != nullptr) return p.head_dim == 64 ? launch_prefill_blocks_d64 : launch_prefill_blocks_d128;
+    if (p.window > 0) return p.head_dim == 64 ? launch_prefill_window_d64 : launch_prefill_window_d128;
+    return p.head_dim == 64 ? launch_prefill_d64 : launch_prefill_d128;
 }
 
 // The tree kernel over its plan's segments and, with split lines, the merge of

@@ -58,6 +58,22 @@
 // sub-page j is at token slot 16 j of its page, which covers both layouts.
 // That path (kSlots) is its own instantiation so that the 16-token path keeps
 // a producer loop without the division by m.
+//
+// Variants (VAR, each its own instantiations).
+// Window: an item reads the KV tiles of the sinks and, a gap further, those
+// from the first key that its first row sees on; tile numbers j count without
+// the gap (WindowUnits).  Softmax rows mask keys between the sinks and their
+// own first one, and a row whose tiles so far showed it nothing keeps its
+// maximum at -inf, so that its first visible key sets it.
+// Block scales: with s = ks_c q.k (ks_c the K scale of 16-key block c, folded
+// with the softmax scale) and vs_c the block's V scale, P' = 2^(s + log2 vs_c -
+// m) and m the running maximum of s + log2 vs_c: the V scale rides in the
+// exponent, so that O = sum P' code needs no product of its own and P' keeps
+// f16's range whatever the scales are, and l = sum_c (sum of P' over block c) /
+// vs_c is the softmax's sum.  That costs eight 16-byte shared-memory reads and
+// some 20 instructions a 128-key row and pass beside the plain kernel.  Warp 14,
+// idle otherwise, looks the scales up four tiles at a time and hands them over
+// through a ring of kScaleSlots tiles.
 #pragma once
 #include "../../include/pafp8.h"
 #include "internal.h"
@@ -86,7 +102,10 @@ struct Dims {
 template <int DH>
 __device__ __forceinline__ uint32_t col_o(int x) { return 256u + (uint32_t)DH * (uint32_t)x; }  // O_X
 
-template <bool kF8, bool k2, int DH>
+constexpr int kScaleSlots = 8;                                    // tiles in the ring of block scales
+constexpr uint32_t kScaleTile = kTileKeys / kPageSize * 16;      // (K scale, log2 of V's, 1 / V's, 0) a block
+
+template <bool kF8, bool k2, int DH, int VAR = kVarPlain>
 struct Layout {
     using Dm = Dims<DH>;
     // The 2-byte-query path spends its shared memory on two f16 K tiles (the
@@ -109,7 +128,9 @@ struct Layout {
     // fp8 query: a 16 KB staging half per query tile for the output's bulk
     // tensor stores (64 dims of 128 rows, 128-byte rows swizzled).
     static constexpr uint32_t ostage = v16 + NV16 * Dm::kF16Tile;
-    static constexpr uint32_t bars = ostage + (kF8 ? 2 * kHalfTile : 0);
+    static constexpr int NSC = VAR == kVarBlocks ? kScaleSlots : 0;
+    static constexpr uint32_t scales = ostage + (kF8 ? 2 * kHalfTile : 0);
+    static constexpr uint32_t bars = scales + NSC * kScaleTile;
     // barrier indices (8 bytes each)
     static constexpr int bQFull = 0, bQReady = 1, bQEmpty = 2;
     static constexpr int bKrFull = 3, bKrEmpty = bKrFull + NKR;
@@ -123,7 +144,8 @@ struct Layout {
     static constexpr int bStageFree = bOEmpty + 2;    // [2]
     static constexpr int bStageReady = bStageFree + 2;  // [2]
     static constexpr int bDrain = bStageReady + 2;
-    static constexpr int nBars = bDrain + 1;
+    static constexpr int bScFull = bDrain + 1, bScEmpty = bScFull + NSC;
+    static constexpr int nBars = bScEmpty + NSC;
     static constexpr uint32_t tmem_slot = bars + 8 * nBars;
     static constexpr uint32_t abort_flag = tmem_slot + 4;
     static constexpr uint32_t bytes = abort_flag + 4;
@@ -134,6 +156,9 @@ static_assert(1024 + Layout<false, true, 128>::bytes <= 232448, "shared memory b
 static_assert(1024 + Layout<false, false, 64>::bytes <= 232448, "shared memory budget (2-byte query, D 64)");
 static_assert(1024 + Layout<true, false, 64>::bytes <= 232448, "shared memory budget (fp8 query, D 64)");
 static_assert(1024 + Layout<false, true, 64>::bytes <= 232448, "shared memory budget (2-byte cache, D 64)");
+static_assert(1024 + Layout<false, false, 128, kVarBlocks>::bytes <= 232448 &&
+                  1024 + Layout<true, false, 128, kVarBlocks>::bytes <= 232448,
+              "shared memory budget (block scales)");
 // Swizzled tiles start on 1024-byte boundaries (the 128-byte swizzle's atom).
 static_assert(Layout<true, false, 64>::kr % 1024 == 0 && Layout<true, false, 64>::v16 % 1024 == 0 &&
                   Layout<false, false, 64>::v16 % 1024 == 0 && Layout<false, true, 64>::v16 % 1024 == 0,
@@ -164,13 +189,21 @@ __device__ __forceinline__ Item load_item(const int* items, int t) {
 
 // KV tiles that query tile `x` (0 = A, 1 = B) of an item needs: its last
 // token's causal limit, capped by the request's own key tiles; 0 if the tile
-// has no rows.
-__device__ __forceinline__ int tile_nkv(int t0, int x, int TQ, int qo_len, int kv_len) {
+// has no rows.  gap: tiles that a window leaves out before its last.
+__device__ __forceinline__ int tile_nkv(int t0, int x, int TQ, int qo_len, int kv_len, int gap = 0) {
     const int first = t0 + x * TQ;
     if (first >= qo_len) return 0;
     const int last = min(first + TQ, qo_len) - 1;
     const int lim = last + kv_len - qo_len;
-    return min((kv_len + kTileKeys - 1) / kTileKeys, lim / kTileKeys + 1);
+    return min((kv_len + kTileKeys - 1) / kTileKeys, lim / kTileKeys + 1) - gap;
+}
+
+// The item's KV tiles under a window, as its plan record counts them.
+template <int VAR>
+__device__ __forceinline__ WindowUnits item_units(const PrefillParams& p, const Item& it) {
+    if constexpr (VAR != kVarPlain)
+        if (p.window > 0) return window_units(it.t0 + it.kv_len - it.qo_len - p.window + 1, p.sinks, kTileKeys);
+    return WindowUnits{0, 0};
 }
 
 // The item that persistent worker i of G takes in round r.  Items are sorted
@@ -214,7 +247,7 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uin
     return true;
 }
 
-template <bool kF8, int KT, bool kDiag, int DH, bool kSlots>
+template <bool kF8, int KT, bool kDiag, int DH, bool kSlots, int VAR>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmq,
                    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -224,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A bf16 query on an fp8 cache is brought into f16 range (per row, by the
     // softmax warps) before the QK MMAs; every other path multiplies Q as loaded.
     const bool fit_q = !kF8 && !k2 && p.q_dtype == PAFP8_BF16;
-    using L = Layout<kF8, k2, DH>;
+    using L = Layout<kF8, k2, DH, VAR>;
     using Dm = Dims<DH>;
     constexpr int NH = Dm::NH;
     extern __shared__ uint8_t smem_raw[];
@@ -267,6 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(L::bStageReady + x), 128);
         }
         mbar_init(bar(L::bDrain), 1);
+        for (int i = 0; i < L::NSC; ++i) {
+            mbar_init(bar(L::bScFull + i), kTileKeys / kPageSize);  // the lanes that hold the tile's scales
+            mbar_init(bar(L::bScEmpty + i), 8);                     // the softmax warps
+        }
         asm volatile("st.shared.u32 [%0], 0;" ::"r"(flag_addr) : "memory");
         mbar_init_fence();
     }
@@ -327,17 +364,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int m = p.page_mult;
             const int npages = (kv_len + kPageSize - 1) / kPageSize;
             const int* idx = p.kv_indices + it.page0;
+            const WindowUnits units = item_units<VAR>(p, it);
+            auto tile_page = [&](int j) { return (VAR != kVarPlain ? units.at(j) : j) * (kTileKeys / kPageSize); };
             int page_next = 0;
             {
-                const int np0 = min(kTileKeys / kPageSize, npages);
-                if (lane < np0) page_next = __ldg(idx + (m == 1 ? lane : lane / m));
+                const int pg0 = tile_page(0);
+                const int np0 = min(kTileKeys / kPageSize, npages - pg0);
+                if (lane < np0) page_next = __ldg(idx + (m == 1 ? pg0 + lane : (pg0 + lane) / m));
             }
             for (int j = 0; j < it.nkv && ok; ++j) {
-                const int pg0 = j * (kTileKeys / kPageSize);
+                const int pg0 = tile_page(j);
                 const int np = min(kTileKeys / kPageSize, npages - pg0);
                 int page = page_next;
                 if (j + 1 < it.nkv) {
-                    const int pg1 = pg0 + kTileKeys / kPageSize;
+                    const int pg1 = tile_page(j + 1);
                     const int np1 = min(kTileKeys / kPageSize, npages - pg1);
                     page_next = lane < np1 ? __ldg(idx + (m == 1 ? pg1 + lane : (pg1 + lane) / m)) : 0;
                 }
@@ -490,8 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Item it = load_item(items, t);
                 const int qo_len = it.qo_len;
                 const int kv_len = it.kv_len;
-                const int nA = tile_nkv(it.t0, 0, TQ, qo_len, kv_len);
-                const int nB = tile_nkv(it.t0, 1, TQ, qo_len, kv_len);
+                const int gap = item_units<VAR>(p, it).gap;
+                const int nA = tile_nkv(it.t0, 0, TQ, qo_len, kv_len, gap);
+                const int nB = tile_nkv(it.t0, 1, TQ, qo_len, kv_len, gap);
                 const int n = it.nkv;
                 ok = wait_or_abort<kDiag>(bar(fit_q ? L::bQReady : L::bQFull), qphase, flag_addr, p.status, p.wait_cycles);
                 qphase ^= 1u;
@@ -544,6 +585,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
+      } else if (VAR == kVarBlocks && warp == 14) {
+        // -------------------------------------------------- block scales
+        // Lane 8 k + i looks up block i of tile j0 + k.
+        const int k = lane >> 3, i = lane & 7, m = p.page_mult;
+        int count = 0;  // tiles handed over so far
+        bool ok = true;
+        for (int rnd = 0, t = blockIdx.x; t < n_items && ok; t = item_at(++rnd, blockIdx.x, gridDim.x)) {
+            const Item it = load_item(items, t);
+            const WindowUnits units = item_units<VAR>(p, it);
+            const int npages = (it.kv_len + kPageSize - 1) / kPageSize;
+            const int* idx = p.kv_indices + it.page0;
+            for (int j0 = 0; j0 < it.nkv && ok; j0 += 4) {
+                const int j = j0 + k;
+                float ks = 1.f, lv = 0.f, rv = 1.f;  // blocks past the request's end: all their keys are masked
+                const int vp = units.at(j) * (kTileKeys / kPageSize) + i;
+                if (j < it.nkv && vp < npages) {
+                    bool bad;  // (the producer reports it)
+                    const SubPageAt at = sub_page(idx, vp, m, p.num_pages, bad);
+                    const size_t e = ((size_t)at.page * m + at.slot / kPageSize) * p.num_kv_heads + it.hk;
+                    const float v = __ldg(p.v_blocks + e);
+                    ks = p.sm_scale_log2 * __ldg(p.k_blocks + e);
+                    lv = __log2f(v);
+                    rv = __frcp_rn(v);
+                }
+                const int tile = count + k, slot = tile % kScaleSlots;
+                if (j < it.nkv) {
+                    ok = wait_or_abort<kDiag>(bar(L::bScEmpty + slot), (uint32_t)((tile / kScaleSlots) & 1) ^ 1u, flag_addr,
+                                              p.status, p.wait_cycles);
+                    if (ok) {
+                        sts128(base + L::scales + slot * kScaleTile + i * 16, __float_as_uint(ks), __float_as_uint(lv),
+                               __float_as_uint(rv), 0u);
+                        mbar_arrive(bar(L::bScFull + slot));
+                    }
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                count += min(4, it.nkv - j0);
+            }
+        }
       }
     } else if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
@@ -555,7 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // under the 128-byte swizzle (the layout a 2-byte tile lands in), keys
         // `valid` and beyond zeroed.  K serves as the K-major B operand of Q K^T,
         // V as the MN-major B operand of P V.
-        auto widen = [&](uint32_t src, uint32_t dst, int valid) {
+        // (Under a window so are keys hide .. show - 1 of a V tile.)
+        auto widen = [&](uint32_t src, uint32_t dst, int valid, int hide, int show) {
+            auto gone = [&](int row) { return row >= valid || (VAR != kVarPlain && row >= hide && row < show); };
             if constexpr (k2) {
                 return;  // a 2-byte cache has no fp8 tile
             } else if constexpr (DH == 128) {
@@ -565,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int row = (combo >> 1) * 8 + e;
                     const int c = (combo & 1) * 4 + q8;
                     uint4 w = lds128(src + row * 128 + ((c ^ e) << 4));
-                    if (row >= valid) w = make_uint4(0u, 0u, 0u, 0u);
+                    if (gone(row)) w = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t hb = dst + (c >> 2) * kHalfTile + row * 128;
                     sts128(hb + (((2 * q8) ^ e) << 4), fp8x2_lo<KT>(w.x), fp8x2_hi<KT>(w.x), fp8x2_lo<KT>(w.y),
                            fp8x2_hi<KT>(w.y));
@@ -579,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 4; ++i) {
                     const int row = (wd * 4 + i) * 8 + e, c = q8;
                     uint4 w = lds128(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
-                    if (row >= valid) w = make_uint4(0u, 0u, 0u, 0u);
+                    if (gone(row)) w = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t hb = dst + row * 128;
                     sts128(hb + (((2 * c) ^ e) << 4), fp8x2_lo<KT>(w.x), fp8x2_hi<KT>(w.x), fp8x2_lo<KT>(w.y),
                            fp8x2_hi<KT>(w.y));
@@ -591,13 +672,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int rnd = 0, t = blockIdx.x; t < n_items && ok; t = item_at(++rnd, blockIdx.x, gridDim.x)) {
             const Item it = load_item(items, t);
             const int kv_len = it.kv_len;
+            const WindowUnits units = item_units<VAR>(p, it);
+            // No row of the item sees keys p.sinks .. first - 1.
+            const int first = VAR != kVarPlain && p.window > 0 ? it.t0 + kv_len - it.qo_len - p.window + 1 : 0;
             for (int j = 0; j < it.nkv && ok; ++j) {
-                const int valid = min(kTileKeys, kv_len - j * kTileKeys);
+                const int key0 = (VAR != kVarPlain ? units.at(j) : j) * kTileKeys;
+                const int valid = min(kTileKeys, kv_len - key0);
+                const int hide = VAR != kVarPlain ? p.sinks - key0 : 0, show = VAR != kVarPlain ? first - key0 : 0;
                 if constexpr (!kF8 && !k2) {
                     ok = wait_or_abort<kDiag>(bar(L::bKrFull + kr.idx), kr.phase, flag_addr, p.status, p.wait_cycles) &&
                          wait_or_abort<kDiag>(bar(L::bK16Empty + k16.idx), k16.phase ^ 1u, flag_addr, p.status, p.wait_cycles);
                     if (!ok) break;
-                    widen(base + L::kr + kr.idx * Dm::kRawTile, base + L::k16 + k16.idx * Dm::kF16Tile, kTileKeys);
+                    widen(base + L::kr + kr.idx * Dm::kRawTile, base + L::k16 + k16.idx * Dm::kF16Tile, kTileKeys, 0, 0);
                     fence_async_smem();
                     mbar_arrive(bar(L::bK16Full + k16.idx));
                     mbar_arrive(bar(L::bKrEmpty + kr.idx));
@@ -619,11 +705,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t off = (uint32_t)q * 16u;  // [half][key][128 B]
                         const int row = (q >> 3) & (kTileKeys - 1);
                         uint4 w = lds128(src + off);
-                        if (row >= valid) w = make_uint4(0u, 0u, 0u, 0u);
+                        if (row >= valid || (VAR != kVarPlain && row >= hide && row < show)) w = make_uint4(0u, 0u, 0u, 0u);
                         sts128(dst + off, w.x, w.y, w.z, w.w);
                     }
                 } else {
-                    widen(src, dst, valid);
+                    widen(src, dst, valid, hide, show);
                 }
                 fence_async_smem();
                 mbar_arrive(bar(L::bV16Full + v16.idx));
@@ -640,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t tS = lane_base + col_s(x), tO = lane_base + col_o<DH>(x);
         uint32_t qphase = 0, sphase = 0, ophase = 0;
+        [[maybe_unused]] int sc_count = 0;  // tiles of block scales read so far
         uint32_t stage_round = 0;  // staging rounds of this tile so far (fp8 query)
         const bool issuer = (threadIdx.x & 127) == 0;
         const bool o_32b = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;  // rows are 256 B apart
@@ -699,13 +786,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int qo_len = it.qo_len;
             const int kv_len = it.kv_len;
             const int t0 = it.t0 + x * TQ;
-            const int nX = tile_nkv(it.t0, x, TQ, qo_len, kv_len);
+            const WindowUnits units = item_units<VAR>(p, it);
+            const int nX = tile_nkv(it.t0, x, TQ, qo_len, kv_len, units.gap);
             const int tok = r / g, hh = r - tok * g;
             const bool valid_row = (tok < TQ) && (t0 + tok < qo_len);
             const int limit = valid_row ? t0 + tok + kv_len - qo_len : -1;
-            float scale = p.sm_scale_log2 * up_next;
+            // Keys p.sinks .. low - 1 lie before the row's window.
+            const int low = VAR != kVarPlain && p.window > 0 ? limit - p.window + 1 : 0;
+            float scale = (VAR == kVarBlocks ? 1.f : p.sm_scale_log2) * up_next;
             float vsc = p.v_scale;
-            if (p.k_scales != nullptr) {  // per-head scale tensors
+            if (VAR != kVarBlocks && p.k_scales != nullptr) {  // per-head scale tensors
                 const int qh = it.hk * g + min(hh, g - 1);
                 scale = fold_scale_log2(p.sm_scale, p.q_scales != nullptr ? __ldg(p.q_scales + qh) : 1.0f,
                                         __ldg(p.k_scales + it.hk)) *
@@ -718,8 +808,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sphase ^= 1u;
                 if (!ok) break;
                 tc_fence_after();
-                const int key0 = j * kTileKeys;
-                const bool need_mask = key0 + kTileKeys - 1 > limit;
+                const int key0 = (VAR != kVarPlain ? units.at(j) : j) * kTileKeys;
+                const bool below = VAR != kVarPlain && key0 < low && key0 + kTileKeys > p.sinks;
+                const bool need_mask = key0 + kTileKeys - 1 > limit || below;
                 // The whole S row (128 columns) in registers, one wait.
                 uint32_t v[128];
 #pragma unroll
@@ -732,16 +823,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         if (i > lim) v[i] = __float_as_uint(-INFINITY);
+                    if (below) {
+                        const int hide = p.sinks - key0, show = low - key0;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (i >= hide && i < show) v[i] = __float_as_uint(-INFINITY);
+                    }
                 }
-                // Four independent three-input maxima keep the chain short.
-                float pm[4];
+                float m_new;
+                const uint32_t sc_tile = base + L::scales + (sc_count % kScaleSlots) * kScaleTile;
+                if constexpr (VAR == kVarBlocks) {
+                    ok = __all_sync(0xFFFFFFFFu, wait_or_abort<kDiag>(bar(L::bScFull + sc_count % kScaleSlots),
+                                                                      (uint32_t)((sc_count / kScaleSlots) & 1), flag_addr,
+                                                                      p.status, p.wait_cycles));
+                    if (!ok) break;
+                    // Each block's maximum, then that of s + log2 of its V scale.
+                    m_new = m;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) pm[k] = __uint_as_float(v[k]);
+                    for (int c = 0; c < 8; ++c) {
+                        float a = __uint_as_float(v[16 * c]), b = __uint_as_float(v[16 * c + 1]);
 #pragma unroll
-                for (int i = 4; i < 128; i += 2)
-                    pm[(i >> 1) & 3] = max3(pm[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                const float mx = fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]);
-                const float m_new = fmaxf(m, mx * scale);
+                        for (int i = 2; i < 16; i += 4) {
+                            a = max3(a, __uint_as_float(v[16 * c + i]), __uint_as_float(v[16 * c + i + 1]));
+                            if (i + 2 < 16) b = max3(b, __uint_as_float(v[16 * c + i + 2]), __uint_as_float(v[16 * c + i + 3]));
+                        }
+                        const uint2 sc = lds64(sc_tile + 16 * c);
+                        m_new = fmaxf(m_new, fmaf(fmaxf(a, b), __uint_as_float(sc.x) * scale, __uint_as_float(sc.y)));
+                    }
+                } else {
+                    // Four independent three-input maxima keep the chain short.
+                    float pm[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) pm[k] = __uint_as_float(v[k]);
+#pragma unroll
+                    for (int i = 4; i < 128; i += 2)
+                        pm[(i >> 1) & 3] = max3(pm[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                    const float mx = fmaxf(max3(pm[0], pm[1], pm[2]), pm[3]);
+                    m_new = fmaxf(m, mx * scale);
+                }
                 float m_use = m;
                 bool rescale = false;
                 if (j == 0) {
@@ -750,7 +869,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m_use = m_new;
                     rescale = true;
                 }
-                if (m_use == -INFINITY) m_use = 0.f;  // row with no admissible key so far
+                // A row with no admissible key so far: without a window it never
+                // gets one, under a window its maximum stays at -inf.
+                const float m_keep = m_use;
+                if (m_use == -INFINITY) m_use = 0.f;
                 // tcgen05.ld/st are warp-collective: the whole warp rescales
                 // when any of its rows must (alpha = 1 for the others).
                 if (__any_sync(0xFFFFFFFFu, rescale)) {
@@ -780,36 +902,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P = exp2(s * scale - m) (masked logits are -inf: P = 0), row
                 // sum, P -> TMEM as f16 over the first half of S.  Pairs of
                 // columns go through the packed fp32 pipe.
-                const f32x2 scale2 = make_f32x2(scale, scale), negm2 = make_f32x2(-m_use, -m_use);
+                [[maybe_unused]] const f32x2 scale2 = make_f32x2(scale, scale), negm2 = make_f32x2(-m_use, -m_use);
                 // P overwrites the S values it consumed: P of columns 2i, 2i+1
                 // goes to v[i], which held column i (already used).  Two
                 // independent packed partial sums keep the chain short.
-                f32x2 ps[2] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
+                if constexpr (VAR == kVarBlocks) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    float a, b;
-                    split_f32x2(fma2(make_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), scale2,
-                                     negm2),
-                                a, b);
-                    const float e0 = ex2(a), e1 = ex2(b);
-                    const f32x2 e = make_f32x2(e0, e1);
-                    ps[i & 1] = add2(ps[i & 1], e);
-                    v[i] = kBF ? pack_bf162(e0, e1) : pack_half2(e0, e1);
-                }
-                {
-                    float a, b, c, d;
-                    split_f32x2(ps[0], a, b);
-                    split_f32x2(ps[1], c, d);
-                    l += (a + b) + (c + d);
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 sc = lds128(sc_tile + 16 * c);
+                        const float kc = __uint_as_float(sc.x) * scale, off = __uint_as_float(sc.y) - m_use;
+                        const f32x2 kc2 = make_f32x2(kc, kc), off2 = make_f32x2(off, off);
+                        f32x2 ps[2] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
+#pragma unroll
+                        for (int i = 8 * c; i < 8 * c + 8; ++i) {
+                            float a, b;
+                            split_f32x2(fma2(make_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), kc2, off2),
+                                        a, b);
+                            const float e0 = ex2(a), e1 = ex2(b);
+                            ps[i & 1] = add2(ps[i & 1], make_f32x2(e0, e1));
+                            v[i] = pack_half2(e0, e1);
+                        }
+                        float a, b;
+                        split_f32x2(add2(ps[0], ps[1]), a, b);
+                        l = fmaf(a + b, __uint_as_float(sc.z), l);
+                    }
+                    // The tile's scales are read: one arrival a warp.
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::bScEmpty + sc_count % kScaleSlots));
+                    ++sc_count;
+                } else {
+                    f32x2 ps[2] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        float a, b;
+                        split_f32x2(fma2(make_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), scale2,
+                                         negm2),
+                                    a, b);
+                        const float e0 = ex2(a), e1 = ex2(b);
+                        const f32x2 e = make_f32x2(e0, e1);
+                        ps[i & 1] = add2(ps[i & 1], e);
+                        v[i] = kBF ? pack_bf162(e0, e1) : pack_half2(e0, e1);
+                    }
+                    {
+                        float a, b, c, d;
+                        split_f32x2(ps[0], a, b);
+                        split_f32x2(ps[1], c, d);
+                        l += (a + b) + (c + d);
+                    }
                 }
                 tc_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(v));
                 tc_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(L::bPFull + x));
-                m = m_use;
+                m = VAR != kVarPlain ? m_keep : m_use;
             }
             if (!ok) break;
+            if constexpr (VAR == kVarBlocks) {
+                // Tiles that only the other query tile reads: their scales are
+                // waited for all the same, so that no warp's arrivals run ahead.
+                for (int j = nX; j < it.nkv && ok; ++j, ++sc_count) {
+                    ok = __all_sync(0xFFFFFFFFu, wait_or_abort<kDiag>(bar(L::bScFull + sc_count % kScaleSlots),
+                                                                      (uint32_t)((sc_count / kScaleSlots) & 1), flag_addr,
+                                                                      p.status, p.wait_cycles));
+                    if (ok && lane == 0) mbar_arrive(bar(L::bScEmpty + sc_count % kScaleSlots));
+                }
+                if (!ok) break;
+            }
             // The next item's record, loaded here so that its latency passes
             // during the epilogue rather than before the next item's first pass.
             {
@@ -922,45 +1081,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool kF8, int KT, bool kDiag, int DH, bool kSlots>
+template <bool kF8, int KT, bool kDiag, int DH, bool kSlots, int VAR>
 cudaError_t launch_t(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, const CUtensorMap& to, int num_ctas, cudaStream_t stream) {
-    const size_t smem = 1024 + Layout<kF8, KT == PAFP8_F16 || KT == PAFP8_BF16, DH>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<kF8, KT, kDiag, DH, kSlots>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = 1024 + Layout<kF8, KT == PAFP8_F16 || KT == PAFP8_BF16, DH, VAR>::bytes;
+    auto kern = prefill_kernel<kF8, KT, kDiag, DH, kSlots, VAR>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    prefill_kernel<kF8, KT, kDiag, DH, kSlots><<<num_ctas, kThreads, smem, stream>>>(p, tq, tk, tv, to);
+    kern<<<num_ctas, kThreads, smem, stream>>>(p, tq, tk, tv, to);
     return cudaGetLastError();
 }
 
 // The diagnostic instantiation runs only under a shortened wait bound (and
-// takes any page size); pages of 16 tokens and of 16 m tokens have one each.
-template <bool kF8, int KT, int DH>
+// takes any page size); pages of 16 tokens and of 16 m tokens have one each,
+// but for the variants, which take any page size too.
+template <bool kF8, int KT, int DH, int VAR>
 cudaError_t launch_one(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                        const CUtensorMap& tv, const CUtensorMap& to, int num_ctas, cudaStream_t stream) {
     if (p.wait_cycles < kWaitCyclesDefault)
-        return launch_t<kF8, KT, true, DH, true>(p, tq, tk, tv, to, num_ctas, stream);
-    return p.page_mult != 1 ? launch_t<kF8, KT, false, DH, true>(p, tq, tk, tv, to, num_ctas, stream)
-                            : launch_t<kF8, KT, false, DH, false>(p, tq, tk, tv, to, num_ctas, stream);
+        return launch_t<kF8, KT, true, DH, true, VAR>(p, tq, tk, tv, to, num_ctas, stream);
+    if constexpr (VAR == kVarPlain)
+        if (p.page_mult == 1) return launch_t<kF8, KT, false, DH, false, VAR>(p, tq, tk, tv, to, num_ctas, stream);
+    return launch_t<kF8, KT, false, DH, true, VAR>(p, tq, tk, tv, to, num_ctas, stream);
 }
 
-// Dispatch on the query and cache dtypes for head size DH.
-template <int DH>
+// Dispatch on the query and cache dtypes for head size DH (block scales go
+// with an fp8 cache only).
+template <int DH, int VAR = kVarPlain>
 cudaError_t launch_prefill_head(const PrefillParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
                                 const CUtensorMap& tmap_v, const CUtensorMap& tmap_o, int num_ctas,
                                 cudaStream_t stream) {
     const bool f8 = p.q_dtype == PAFP8_E4M3FN || p.q_dtype == PAFP8_E5M2;
     if (f8)
         return p.kv_dtype == PAFP8_E4M3FN
-                   ? launch_one<true, PAFP8_E4M3FN, DH>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream)
-                   : launch_one<true, PAFP8_E5M2, DH>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
-    switch (p.kv_dtype) {
-        case PAFP8_E4M3FN: return launch_one<false, PAFP8_E4M3FN, DH>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
-        case PAFP8_E5M2: return launch_one<false, PAFP8_E5M2, DH>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
-        case PAFP8_F16: return launch_one<false, PAFP8_F16, DH>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
-        case PAFP8_BF16: return launch_one<false, PAFP8_BF16, DH>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
-        default: return cudaErrorInvalidValue;
+                   ? launch_one<true, PAFP8_E4M3FN, DH, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream)
+                   : launch_one<true, PAFP8_E5M2, DH, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
+    if (p.kv_dtype == PAFP8_E4M3FN)
+        return launch_one<false, PAFP8_E4M3FN, DH, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
+    if (p.kv_dtype == PAFP8_E5M2)
+        return launch_one<false, PAFP8_E5M2, DH, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
+    if constexpr (VAR != kVarBlocks) {
+        if (p.kv_dtype == PAFP8_F16)
+            return launch_one<false, PAFP8_F16, DH, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
+        if (p.kv_dtype == PAFP8_BF16)
+            return launch_one<false, PAFP8_BF16, DH, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
     }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
