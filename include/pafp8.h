@@ -180,8 +180,8 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc *desc, const int32_t *kv_in
  * j > t - window or j < sinks -- the last `window` keys, itself among them, and
  * the request's first `sinks` tokens.  Every run call takes such a plan
  * (pafp8_run_pod also with one windowed phase); only the visible keys' pages
- * are read, in decode to a granule of 16 tokens and in prefill of 128, and the
- * split-KV options count those pages.  Values of tokens that no row of a
+ * are read, in granules of 16 tokens, and the split-KV options count those
+ * pages.  Values of tokens that no row of a
  * decode request, or of a prefill item (two tiles of 128 / group new tokens
  * and one KV head), sees are not used, whatever they hold; a NaN in the value
  * row of any other token reaches every row of the item.

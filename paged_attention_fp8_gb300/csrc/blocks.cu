@@ -34,33 +34,41 @@ namespace pafp8 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendBlocks = 6;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 // The request that owns row t, by one warp together: the last r with
-// indptr[r] <= t (32 probes a step; indptr[0] <= t < indptr[n] by the caller's
-// check).  Every index probed lies in (0, n).
-__device__ __forceinline__ int owner(const int32_t* indptr, int n, long long t) {
+// indptr[r] <= t (32 probes a step; any r for a t outside the rows), and the
+// rows it starts and ends at.  Every index probed lies in (0, n), n >= 1.
+struct Owner {
+    int r;
+    long long begin, end;
+};
+__device__ __forceinline__ Owner owner(const int32_t* indptr, int n, long long t) {
     const int lane = threadIdx.x & 31;
-    int lo = 0, hi = n;
+    int lo = 0, hi = n, at_lo = __ldg(indptr), at_hi = __ldg(indptr + n);
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const long long at = (long long)lo + (long long)(lane + 1) * step;
-        const bool below = at < hi && __ldg(indptr + at) <= t;
-        const uint32_t b = __ballot_sync(kAll, below);
+        const int v = at < hi ? __ldg(indptr + at) : 0;
+        const uint32_t b = __ballot_sync(kAll, at < hi && v <= t);
         const int steps = b == kAll ? 32 : __ffs(~b) - 1;
+        const int below = __shfl_sync(kAll, v, max(steps - 1, 0)), above = __shfl_sync(kAll, v, min(steps, 31));
+        if (steps > 0) at_lo = below;
+        if (steps < 32 && (long long)lo + (long long)(steps + 1) * step < hi) at_hi = above;
         lo += steps * step;
         hi = min(hi, lo + step);
     }
-    return lo;
+    return Owner{lo, at_lo, at_hi};
 }
 
-// Where token `pos` of request r lies: its page and the slot in it, or page -1
-// when the position or the page id is out of range.
-__device__ __forceinline__ int page_of(const int32_t* kv_indptr, const int32_t* kv_indices, int r, long long pos,
-                                       int page_size, int num_pages, int& slot) {
+// Where token `pos` of the request with page entries e0 .. e1 - 1 lies: its
+// page and the slot in it, or page -1 when the position or the page id is out
+// of range.
+__device__ __forceinline__ int page_of(const int32_t* kv_indices, int e0, int e1, long long pos, int page_size, int num_pages,
+                                       int& slot) {
     if (pos < 0) return -1;
-    const int e0 = __ldg(kv_indptr + r), e1 = __ldg(kv_indptr + r + 1);
     const long long e = e0 + pos / page_size;
     slot = (int)(pos % page_size);
     if (e0 < 0 || e >= e1) return -1;
@@ -105,9 +113,14 @@ __device__ __forceinline__ uint32_t cvt_pair(float lo, float hi) {
 
 template <int KV>
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float by) {
+    const ptx::f32x2 by2 = ptx::make_f32x2(by, by);
     uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = cvt_pair<KV>(__fmul_rn(x[2 * i], by), __fmul_rn(x[2 * i + 1], by));
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        ptx::split_f32x2(ptx::mul2(ptx::make_f32x2(x[2 * i], x[2 * i + 1]), by2), lo, hi);
+        h[i] = cvt_pair<KV>(lo, hi);
+    }
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
@@ -132,122 +145,214 @@ __device__ __forceinline__ float power_scale(uint32_t amax) {
     return __uint_as_float((uint32_t)(max(e, -64) + 127) << 23);
 }
 
-// One warp per (group of p.span new tokens, KV head, K or V): it takes the
-// blocks whose first new token lies in its group, one after the other.
+// A block's rows of K or V in one warp: lane l holds dims 8 (l % 16) .. + 7 (of
+// 128: one head of 128, or two of 64) of rows 2 i + l / 16.  Rows of earlier
+// tokens hold their 8 codes in the first two words, new rows their elements.
+// FULL: all 16 rows are new (nearly every block of a prompt), so that no row
+// needs a condition of its own.
+constexpr int kRowsPerPass = 2, kPasses = kPageSize / kRowsPerPass;
+
+template <int SRC, bool FULL>
+__device__ __forceinline__ void load_rows(Raw8<SRC> (&raw)[kPasses], const uint8_t* src, size_t stride, int s0, int m) {
+    const int sub = (threadIdx.x & 31) / 16;
+    const uint8_t* row = src + (ptrdiff_t)(sub - s0) * (ptrdiff_t)stride;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i, row += kRowsPerPass * stride) {
+        const int s = i * kRowsPerPass + sub - s0;
+        if (!FULL) {
+#pragma unroll
+            for (int k = 0; k < Raw8<SRC>::kVecs; ++k) raw[i].v[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (FULL || (s >= 0 && s < m)) {
+            const uint4* g = reinterpret_cast<const uint4*>(row);
+#pragma unroll
+            for (int k = 0; k < Raw8<SRC>::kVecs; ++k) raw[i].v[k] = __ldcs(g + k);
+        }
+    }
+}
+
+template <int SRC>
+__device__ __forceinline__ void load_codes(Raw8<SRC> (&raw)[kPasses], const uint8_t* dst, size_t row_bytes, int s0) {
+    const int sub = (threadIdx.x & 31) / 16;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int at = i * kRowsPerPass + sub;
+        if (at < s0) {
+            const uint2 c = *reinterpret_cast<const uint2*>(dst + at * row_bytes);
+            raw[i].v[0].x = c.x;
+            raw[i].v[0].y = c.y;
+        }
+    }
+}
+
+// The bits (as fp32) of this lane's largest finite magnitude among the new rows.
+template <int SRC, bool FULL>
+__device__ __forceinline__ uint32_t largest(const Raw8<SRC> (&raw)[kPasses], int s0) {
+    const int sub = (threadIdx.x & 31) / 16;
+    // Magnitudes order like their bits; a 2-byte type's two to a word.
+    constexpr uint32_t kMag = SRC == PAFP8_F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+    constexpr uint32_t kInf = SRC == PAFP8_F32 ? 0x7F800000u : SRC == PAFP8_BF16 ? 0x7F80u : 0x7C00u;
+    auto fold = [](uint32_t m) { return SRC == PAFP8_F32 ? m : max(m & 0xFFFFu, m >> 16); };
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const uint32_t keep = FULL || i * kRowsPerPass + sub >= s0 ? kMag : 0u;
+#pragma unroll
+        for (int k = 0; k < Raw8<SRC>::kVecs; ++k) {
+            const uint32_t w[4] = {raw[i].v[k].x, raw[i].v[k].y, raw[i].v[k].z, raw[i].v[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = SRC == PAFP8_F32 ? max(top, w[j] & keep) : __vmaxu2(top, w[j] & keep);
+        }
+    }
+    uint32_t best = fold(top);
+    if (best >= kInf) {  // infinities and NaN do not count: once more without them
+        best = 0;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            float x[8];
+            to_float8<SRC>(raw[i], x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t a = __float_as_uint(x[k]) & 0x7FFFFFFFu;
+                if ((FULL || i * kRowsPerPass + sub >= s0) && a < 0x7F800000u) best = max(best, a);
+            }
+        }
+        return best;
+    }
+    if constexpr (SRC == PAFP8_F32) return best;
+    else if constexpr (SRC == PAFP8_BF16) return best << 16;
+    else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)best)));
+}
+
+// Scale, earlier codes and new codes of the block whose rows are in `raw` (new
+// ones: slots s0 .. s0 + m - 1).  dst: this lane's dims of the block's first row.
+template <int SRC, int KV, int DH, bool FULL>
+__device__ __forceinline__ void write_rows(const Raw8<SRC> (&raw)[kPasses], uint8_t* dst, size_t row_bytes, float* scale,
+                                           float old, int s0, int m, bool active) {
+    const int lane = threadIdx.x & 31, sub = lane / 16;
+    uint32_t amax = largest<SRC, FULL>(raw, s0);
+    if constexpr (DH == 128) {
+        amax = __reduce_max_sync(kAll, amax);
+    } else {  // lanes l and l ^ 8 hold different heads
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1)
+            if (off != 8) amax = max(amax, __shfl_xor_sync(kAll, amax, off));
+    }
+    if (!active) return;
+    const float own = power_scale<KV>(amax);
+    const float s = !FULL && s0 != 0 && old >= own ? old : own;
+    if (!FULL && s0 != 0 && s > old) {
+        const float ratio = __fdiv_rn(old, s);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int at = i * kRowsPerPass + sub;
+            if (at < s0) {
+                float x[8];
+                values8<KV>(make_uint2(raw[i].v[0].x, raw[i].v[0].y), x);
+                *reinterpret_cast<uint2*>(dst + at * row_bytes) = codes8<KV>(x, ratio);
+            }
+        }
+    }
+    const float inv = __fdiv_rn(1.0f, s);
+    uint8_t* row = dst + sub * row_bytes;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i, row += kRowsPerPass * row_bytes) {
+        const int at = i * kRowsPerPass + sub;
+        if (FULL || (at >= s0 && at < s0 + m)) {
+            float x[8];
+            to_float8<SRC>(raw[i], x);
+            *reinterpret_cast<uint2*>(row) = codes8<KV>(x, inv);
+        }
+    }
+    if (lane % (DH / 8) == 0 && lane < 16) *scale = s;
+}
+
+// One warp per (group of p.span new tokens, K or V, 128 / DH KV heads): it
+// takes the blocks whose first new token lies in its group, one after the other.
+// A block of a 2-byte source is 4 KB in flight a warp, of fp32 8 KB.
 template <int SRC, int KV, int DH>
-__global__ void __launch_bounds__(kThreads) append_blocks_kernel(const BlockAppendParams p) {
-    constexpr int LPR = DH / 8;       // lanes per row
-    constexpr int RPP = 32 / LPR;     // rows per pass
-    constexpr int NP = kPageSize / RPP;
+__global__ void __launch_bounds__(kAppendThreads, SRC == PAFP8_F32 ? 3 : kAppendBlocks)
+    append_blocks_kernel(const BlockAppendParams p) {
+    constexpr int HPW = 128 / DH;
     constexpr int ESZ = SRC == PAFP8_F32 ? 4 : 2;
     const int lane = threadIdx.x & 31;
-    const int sub = lane / LPR, col = (lane % LPR) * 8;
-    const long long all = __ldg(p.qo_indptr + p.batch);
+    const int col = 8 * (lane & 15);
+    const int head_groups = (p.num_kv_heads + HPW - 1) / HPW;
+    const long long u = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const long long group = u / (2 * head_groups);
+    const int part = (int)(u - group * (2 * head_groups));
+    const bool is_v = part >= head_groups;
+    const int h = (is_v ? part - head_groups : part) * HPW + col / DH;  // this lane's head
+    const bool active = h < p.num_kv_heads;
+    long long t = group * p.span;
+    if (t >= p.nnz || p.batch == 0) return;
+    const long long all = __ldg(p.qo_indptr + p.batch), first_row = __ldg(p.qo_indptr);
+    const Owner who = owner(p.qo_indptr, p.batch, max(t, first_row));
     const long long rows = min(p.nnz, all);
-    if (all > p.nnz && blockIdx.x == 0 && threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
-    const long long first_row = __ldg(p.qo_indptr);
-    const long long units = (rows + p.span - 1) / p.span * (2 * p.num_kv_heads);
-    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (long long)gridDim.x * kWarps) {
-        const long long group = u / (2 * p.num_kv_heads);
-        const int hv = (int)(u - group * (2 * p.num_kv_heads));
-        const bool is_v = hv >= p.num_kv_heads;
-        const int h = is_v ? hv - p.num_kv_heads : hv;
-        const uint8_t* const src = static_cast<const uint8_t*>(is_v ? p.v : p.k) + ((size_t)h * DH + col) * ESZ;
-        const size_t stride = (size_t)(is_v ? p.v_stride : p.k_stride) * ESZ;
-        uint8_t* const cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache);
-        float* const scales = is_v ? p.v_scales : p.k_scales;
-        long long t = max(group * p.span, first_row);
-        const long long t_end = min((group + 1) * p.span, rows);
-        if (t >= t_end) continue;
-        int r = owner(p.qo_indptr, p.batch, t);
-        while (t < t_end) {
-            const long long r0 = __ldg(p.qo_indptr + r), r1 = min((long long)__ldg(p.qo_indptr + r + 1), rows);
-            if (t >= r1) {  // (requests without new tokens lie in between)
-                if (++r >= p.batch) break;
-                continue;
-            }
-            const int cached = __ldg(p.cached_lens + r);
-            const long long pos = (long long)cached + (t - r0);
-            const int s0 = (int)(pos & (kPageSize - 1));
-            const int m = (int)min((long long)(kPageSize - s0), r1 - t);
-            if (s0 != 0 && t != r0) {  // the block belongs to an earlier token's warp
-                t += m;
-                continue;
-            }
-            // The new rows: slots s0 .. s0 + m - 1 of the block.
-            Raw8<SRC> raw[NP];
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int s = i * RPP + sub - s0;
-#pragma unroll
-                for (int k = 0; k < Raw8<SRC>::kVecs; ++k) raw[i].v[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (s >= 0 && s < m) {
-                    const uint4* g = reinterpret_cast<const uint4*>(src + (size_t)(t + s) * stride);
-#pragma unroll
-                    for (int k = 0; k < Raw8<SRC>::kVecs; ++k) raw[i].v[k] = __ldcs(g + k);
-                }
-            }
-            int slot = 0;
-            const int page = cached < 0 ? -1 : page_of(p.kv_indptr, p.kv_indices, r, pos, p.page_size, p.num_pages, slot);
-            t += m;
-            if (page < 0) {
-                if (lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
-                continue;
-            }
-            slot -= s0;  // the block's first slot in the page
-            float* const scale = scales + ((size_t)page * (p.page_size / kPageSize) + slot / kPageSize) * p.num_kv_heads + h;
-            const float old = s0 != 0 ? *scale : 0.f;
-            uint32_t amax = 0;
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                float x[8];
-                to_float8<SRC>(raw[i], x);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t a = __float_as_uint(x[k]) & 0x7FFFFFFFu;
-                    amax = max(amax, a < 0x7F800000u ? a : 0u);
-                }
-            }
-            amax = __reduce_max_sync(kAll, amax);
-            const float own = power_scale<KV>(amax);
-            const float s = s0 != 0 && old >= own ? old : own;
-            const size_t row_bytes = p.hnd ? DH : (size_t)p.num_kv_heads * DH;
-            uint8_t* const dst = cache + (p.hnd ? (((size_t)page * p.num_kv_heads + h) * p.page_size + slot) * DH
-                                                : (((size_t)page * p.page_size + slot) * p.num_kv_heads + h) * DH) + col;
-            if (s0 != 0 && s > old) {
-                const float ratio = __fdiv_rn(old, s);
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int at = i * RPP + sub;
-                    if (at < s0) {
-                        uint2* const c = reinterpret_cast<uint2*>(dst + at * row_bytes);
-                        float x[8];
-                        values8<KV>(*c, x);
-                        *c = codes8<KV>(x, ratio);
-                    }
-                }
-            }
-            const float inv = __fdiv_rn(1.0f, s);
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const int at = i * RPP + sub;
-                if (at >= s0 && at < s0 + m) {
-                    float x[8];
-                    to_float8<SRC>(raw[i], x);
-                    *reinterpret_cast<uint2*>(dst + at * row_bytes) = codes8<KV>(x, inv);
-                }
-            }
-            if (lane == 0) *scale = s;
+    if (all > p.nnz && u == 0 && lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
+    const long long t_end = min(t + p.span, rows);
+    t = max(t, first_row);
+    int r = who.r;
+    long long r0 = who.begin, r1 = min(who.end, rows);
+    const uint8_t* const src = static_cast<const uint8_t*>(is_v ? p.v : p.k) + ((size_t)h * DH + col % DH) * ESZ;
+    const size_t stride = (size_t)(is_v ? p.v_stride : p.k_stride) * ESZ;
+    uint8_t* const cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache);
+    float* const scales = is_v ? p.v_scales : p.k_scales;
+    while (t < t_end) {
+        if (t >= r1) {  // (requests without new tokens lie in between)
+            if (++r >= p.batch) break;
+            r0 = __ldg(p.qo_indptr + r);
+            r1 = min((long long)__ldg(p.qo_indptr + r + 1), rows);
+            continue;
         }
+        const int cached = __ldg(p.cached_lens + r), e0 = __ldg(p.kv_indptr + r), e1 = __ldg(p.kv_indptr + r + 1);
+        const long long pos = (long long)cached + (t - r0);
+        const int s0 = (int)(pos & (kPageSize - 1));
+        const int m = (int)min((long long)(kPageSize - s0), r1 - t);
+        if (s0 != 0 && t != r0) {  // the block belongs to an earlier token's warp
+            t += m;
+            continue;
+        }
+        Raw8<SRC> raw[kPasses];
+        const uint8_t* const from = src + (size_t)t * stride;
+        // (two heads of 64 a warp: the last warp of an odd count has one)
+        const bool full = m == kPageSize && (DH == 128 || __all_sync(kAll, active));
+        if (full)
+            load_rows<SRC, true>(raw, from, stride, 0, kPageSize);
+        else
+            load_rows<SRC, false>(raw, from, stride, s0, active ? m : 0);
+        int slot = 0;
+        const int page = cached < 0 ? -1 : page_of(p.kv_indices, e0, e1, pos, p.page_size, p.num_pages, slot);
+        t += m;
+        if (page < 0) {
+            if (lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
+            continue;
+        }
+        slot -= s0;  // the block's first slot in the page
+        float* const scale = scales + ((size_t)page * (p.page_size / kPageSize) + slot / kPageSize) * p.num_kv_heads + (active ? h : 0);
+        const size_t row_bytes = p.hnd ? DH : (size_t)p.num_kv_heads * DH;
+        uint8_t* const dst = cache + (p.hnd ? (((size_t)page * p.num_kv_heads + h) * p.page_size + slot) * DH
+                                            : (((size_t)page * p.page_size + slot) * p.num_kv_heads + h) * DH) + col % DH;
+        float old = 0.f;
+        if (s0 != 0) {
+            old = *scale;
+            if (active) load_codes<SRC>(raw, dst, row_bytes, s0);
+        }
+        if (full)
+            write_rows<SRC, KV, DH, true>(raw, dst, row_bytes, scale, 0.f, 0, kPageSize, true);
+        else
+            write_rows<SRC, KV, DH, false>(raw, dst, row_bytes, scale, old, s0, m, active);
     }
 }
 
 template <int SRC, int KV, int DH>
 cudaError_t launch_append_t(BlockAppendParams p, cudaStream_t stream) {
     p.span = p.nnz <= 4LL * p.batch ? 1 : kPageSize;
-    const long long units = (p.nnz + p.span - 1) / p.span * (2LL * p.num_kv_heads);
-    const long long blocks = (units + kWarps - 1) / kWarps;
-    append_blocks_kernel<SRC, KV, DH><<<(int)min(blocks, (long long)INT32_MAX), kThreads, 0, stream>>>(p);
+    constexpr int HPW = 128 / DH, W = kAppendThreads / 32;
+    const long long units = (p.nnz + p.span - 1) / p.span * (2LL * ((p.num_kv_heads + HPW - 1) / HPW));
+    const long long blocks = (units + W - 1) / W;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    append_blocks_kernel<SRC, KV, DH><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -264,9 +369,9 @@ cudaError_t launch_append_src(const BlockAppendParams& p, cudaStream_t stream) {
 
 // ------------------------------------------------------------------ reading
 
-constexpr int kReadRows = 16;  // rows of a thread block's tile
+constexpr int kReadRows = 16;  // rows of a thread block's tile, at most
 
-// One thread block per kReadRows output rows, all heads, K and V: the first
+// One thread block per p.tile output rows, all heads, K and V: the first
 // warp looks the rows up, then every thread takes 16 codes at a time.
 template <int OUT, int KV, int DH>
 __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
@@ -276,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
     __shared__ long long s_scale[kReadRows];  // index of head 0's scale
     const long long all = __ldg(p.out_indptr + p.batch);
     const long long rows = min(p.nnz, all);
-    const long long t0 = (long long)blockIdx.x * kReadRows;
+    const long long t0 = (long long)blockIdx.x * p.tile;
     if (all > p.nnz && blockIdx.x == 0 && threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
     if (t0 >= rows) return;
     const long long head_step = p.hnd ? (long long)p.page_size * DH : DH;
@@ -284,9 +389,9 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
         const int lane = threadIdx.x;
         const long long low = __ldg(p.out_indptr);
         const long long base = max(t0, low);
-        const int r0 = base < rows ? owner(p.out_indptr, p.batch, base) : 0;
+        const int r0 = base < rows ? owner(p.out_indptr, p.batch, base).r : 0;
         const long long t = t0 + lane;
-        if (lane < kReadRows) {
+        if (lane < p.tile) {
             long long row = -1, scale = 0;
             if (t >= low && t < rows) {
                 int r = r0;
@@ -294,7 +399,9 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
                 int slot = 0;
                 const int start = __ldg(p.starts + r);
                 const long long pos = (long long)start + (t - __ldg(p.out_indptr + r));
-                const int page = start < 0 ? -1 : page_of(p.kv_indptr, p.kv_indices, r, pos, p.page_size, p.num_pages, slot);
+                const int page = start < 0 ? -1
+                                           : page_of(p.kv_indices, __ldg(p.kv_indptr + r), __ldg(p.kv_indptr + r + 1), pos,
+                                                     p.page_size, p.num_pages, slot);
                 if (page >= 0) {
                     row = p.hnd ? ((long long)page * p.num_kv_heads * p.page_size + slot) * DH
                                 : ((long long)page * p.page_size + slot) * p.num_kv_heads * DH;
@@ -309,9 +416,9 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
     }
     __syncthreads();
     const int per_row = p.num_kv_heads * CPR;
-    const int work = 2 * kReadRows * per_row;
+    const int half = p.tile * per_row, work = 2 * half;
     for (int i = threadIdx.x; i < work; i += kThreads) {
-        const int kv = i / (kReadRows * per_row), j = i - kv * (kReadRows * per_row);
+        const int kv = i >= half, j = i - kv * half;
         const int row = j / per_row, c = j - row * per_row;
         const int h = c / CPR, d = (c - h * CPR) * 16;
         if (s_row[row] < 0) continue;
@@ -342,8 +449,13 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
 }
 
 template <int OUT, int KV, int DH>
-cudaError_t launch_read_t(const ReadParams& p, cudaStream_t stream) {
-    read_kv_kernel<OUT, KV, DH><<<(unsigned)((p.nnz + kReadRows - 1) / kReadRows), kThreads, 0, stream>>>(p);
+cudaError_t launch_read_t(ReadParams p, cudaStream_t stream) {
+    // A tile's lookups are waited for once, its rows streamed after them: few
+    // rows go in small tiles over more thread blocks (about eight an SM), many
+    // in tiles of 16.
+    p.tile = 2;
+    while (p.tile < kReadRows && p.nnz > 1216LL * p.tile) p.tile *= 2;
+    read_kv_kernel<OUT, KV, DH><<<(unsigned)((p.nnz + p.tile - 1) / p.tile), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(32 * 9, 1)
             const int* idx = p.kv_indices + req_page[b];
             WindowUnits units{0, 0};
             if constexpr (VAR != kVarPlain)
-                if (p.window > 0) units = window_units(req_kv[b] - p.window, p.sinks, P);
+                if (p.window > 0) units = window_units(req_kv[b] - p.window, p.sinks);
             for (int pb = p0; pb < p1 && ok; pb += 32) {
                 const int n = min(32, p1 - pb);
                 // Pool pages and token slots of 16-token sub-pages (a page of
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(32 * 9, 1)
         if constexpr (VAR != kVarPlain) {
             if (p.window > 0) {
                 low = kv_len - p.window;
-                units = window_units(low, p.sinks, P);
+                units = window_units(low, p.sinks);
             }
         }
         // Block scales: lane i holds those of this head's sub-page i of the

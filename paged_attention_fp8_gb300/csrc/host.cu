@@ -414,10 +414,11 @@ void build_prefill_meta(pafp8_plan* pl) {
     // A 2-byte cache at head_dim 128 runs on CTA pairs: a query tile is 2 TQ
     // tokens (TQ per CTA), an item two such tiles; the rest on single CTAs
     // (tiles of TQ).
-    // (A window's few tiles an item go to single CTAs as well.)
-    const bool pair = pl->desc.head_dim == kHeadDim && is_2byte(pl->desc.kv_dtype) && pl->window == 0;
+    const bool pair = prefill_pairs(pl->desc.head_dim, pl->desc.kv_dtype, pl->window);
     const int span = (pair ? 4 : 2) * TQ;
-    struct T { int32_t b, hk, t0, nkv; };
+    // Under a window an item is one of a request without the `gap` 16-token
+    // pages between the sinks' and the first that its first row sees.
+    struct T { int32_t b, hk, t0, nkv, gap; };
     std::vector<T> tiles;
     std::vector<int32_t> req_page(B), req_kv(B);
     for (int b = 0; b < B; ++b) {
@@ -430,11 +431,13 @@ void build_prefill_meta(pafp8_plan* pl) {
                 // An item is two query tiles, A starting at t0 and B right
                 // after; its KV tiles are those of its last token.
                 const int last = std::min(t0 + span, qo) - 1;
-                const int lim = last + req_kv[b] - qo;
-                int nkv = std::min((req_kv[b] + kTileKeys - 1) / kTileKeys, lim / kTileKeys + 1);
-                if (pl->window > 0)
-                    nkv -= window_units(t0 + req_kv[b] - qo - pl->window + 1, pl->sinks, kTileKeys).gap;
-                tiles.push_back({b, hk, t0, nkv});
+                const int gap = pl->window > 0
+                                    ? window_units(t0 + req_kv[b] - qo - pl->window + 1, pl->sinks).gap
+                                    : 0;
+                const int kv = req_kv[b] - gap * kPageSize;
+                const int lim = last + kv - qo;
+                const int nkv = std::min((kv + kTileKeys - 1) / kTileKeys, lim / kTileKeys + 1);
+                tiles.push_back({b, hk, t0, nkv, gap});
             }
     }
     std::stable_sort(tiles.begin(), tiles.end(), [](const T& a, const T& c) { return a.nkv > c.nkv; });
@@ -463,13 +466,13 @@ void build_prefill_meta(pafp8_plan* pl) {
     // reads one record per item and no dependent loads.
     std::vector<int32_t> tw;
     for (auto& t : tiles) {
-        tw.push_back(t.b);
+        tw.push_back(pl->window > 0 ? t.gap : t.b);
         tw.push_back(t.hk);
         tw.push_back(t.t0);
         tw.push_back(t.nkv);
         tw.push_back(pl->qo_indptr[t.b]);
         tw.push_back(pl->qo_indptr[t.b + 1] - pl->qo_indptr[t.b]);
-        tw.push_back(req_kv[t.b]);
+        tw.push_back(req_kv[t.b] - t.gap * kPageSize);
         tw.push_back(req_page[t.b]);
     }
     put(kMetaOffTile, tw);
@@ -1061,7 +1064,7 @@ pafp8_status pafp8_plan_create_window(const pafp8_plan_desc* desc_in, int32_t wi
         const int64_t n = (int64_t)pl->kv_indptr[b + 1] - pl->kv_indptr[b];
         const int64_t kv = n > 0 ? (n - 1) * d.page_size + pl->last_page_len[b] : 0;
         int64_t units = (kv + kPageSize - 1) / kPageSize;
-        if (window > 0) units -= window_units((int)kv - window, sinks, kPageSize).gap;
+        if (window > 0) units -= window_units((int)kv - window, sinks).gap;
         pl->vptr[b + 1] = pl->vptr[b] + (int32_t)units;
     }
     if (d.mode != PAFP8_MODE_DECODE) {

@@ -44,7 +44,8 @@ enum MetaHeader : int {
     kMetaOffMergeSlot,   // int32[num_partials]
     kMetaOffReqQo,       // int32[batch+1] qo_indptr (prefill)
     kMetaNumTiles,       // prefill tiles
-    kMetaOffTile,        // int32[8*num_tiles] prefill items: b, hk, t0, nkv, qo_begin, qo_len, kv_len, page_begin;
+    kMetaOffTile,        // int32[8*num_tiles] prefill items: b, hk, t0, nkv, qo_begin, qo_len, kv_len, page_begin
+                         // (under a window: its gap of 16-token pages for b, and kv_len without them);
                          // tree: int32[8*num_merge] split lines: slot0, slot1, qo_begin, hk, rows, first row, 0, 0
     kMetaTileRows,       // packed query rows per prefill tile
     kMetaOffRowMerge,    // int32[rows] merge entry of each decode row, or -1
@@ -96,19 +97,19 @@ __device__ __forceinline__ SubPageAt sub_page(const int32_t* idx, int vp, int m,
 }
 
 // The keys that a row at position p sees under a window of w keys and s first
-// tokens that stay visible: j <= p with j < s or j > p - w.  In units of `unit`
-// keys a batch item reads units 0 .. head - 1 (the sinks') and, gap units
-// further, those from its first window key on; they are numbered without the
-// gap, unit u standing for u + gap from head on.  first_key: the first key in
-// the window of the item's first row (negative: the window reaches past the
-// start).  Without a window gap is 0.
+// tokens that stay visible: j <= p with j < s or j > p - w.  A work item reads
+// the 16-token pages 0 .. head - 1 (the sinks') and, gap pages further, those
+// from its first window key on; they are numbered without the gap, page u
+// standing for u + gap from head on.  first_key: the first key in the window of
+// the item's first row (negative: the window reaches past the start).  Without
+// a window gap is 0.
 struct WindowUnits {
     int head, gap;
     __host__ __device__ int at(int u) const { return u < head ? u : u + gap; }
 };
-__host__ __device__ inline WindowUnits window_units(int first_key, int sinks, int unit) {
-    const int head = sinks > 0 ? (sinks - 1) / unit + 1 : 0;
-    const int from = first_key > 0 ? first_key / unit : 0;
+__host__ __device__ inline WindowUnits window_units(int first_key, int sinks) {
+    const int head = sinks > 0 ? (sinks - 1) / kPageSize + 1 : 0;
+    const int from = first_key > 0 ? first_key / kPageSize : 0;
     return WindowUnits{head, from > head ? from - head : 0};
 }
 
@@ -229,6 +230,7 @@ struct ReadParams {
     long long nnz;
     int batch, num_kv_heads, head_dim, num_pages, page_size;
     int kv_dtype, out_dtype, hnd;
+    int tile;                    // set by the launcher: output rows a thread block
     float k_scale, v_scale;
 };
 
@@ -312,6 +314,18 @@ cudaError_t launch_merge(const DecodeParams& p, int num_merge, int heads_per_cta
 // tmap_o: map over o with the 2-byte query tile's box (the fp8-query kernel
 // writes full output tiles with bulk tensor stores through it).  One
 // translation unit per head size (prefill_d128.cu, prefill_d64.cu).
+// Whether a prefill plan's items are those of CTA pairs: a 2-byte cache at
+// head_dim 128, with a window of 768 keys or more if it has one.  (A prompt of
+// 16384 tokens, 32 / 8 heads: window 1000 290 us on pairs and 308 on single
+// CTAs, 700 248 and 245, 500 219 and 194, 300 167 and 142: short windows mean
+// many items of a few tiles, and a pair's item covers twice the tokens, so more
+// of its tiles lie outside each row's window.)
+constexpr int kPairWindow = 768;
+inline bool prefill_pairs(int head_dim, int kv_dtype, int window) {
+    return head_dim == kHeadDim && (kv_dtype == PAFP8_F16 || kv_dtype == PAFP8_BF16) &&
+           (window == 0 || window >= kPairWindow);
+}
+
 using PrefillLaunch = cudaError_t(const PrefillParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
                                   const CUtensorMap& tmap_v, const CUtensorMap& tmap_o, int num_ctas, cudaStream_t stream);
 PrefillLaunch launch_prefill_d128, launch_prefill_d64, launch_prefill_window_d128, launch_prefill_window_d64,

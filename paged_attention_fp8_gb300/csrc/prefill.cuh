@@ -60,20 +60,21 @@
 // a producer loop without the division by m.
 //
 // Variants (VAR, each its own instantiations).
-// Window: an item reads the KV tiles of the sinks and, a gap further, those
-// from the first key that its first row sees on; tile numbers j count without
-// the gap (WindowUnits).  Softmax rows mask keys between the sinks and their
-// own first one, and a row whose tiles so far showed it nothing keeps its
+// Window: an item reads the 16-token pages of the sinks and, `gap` pages
+// further, those from the first key that its first row sees on.  Positions and
+// tiles count without the gap -- masks, limits and lengths are those of the
+// shortened request -- and only the page lookups add it, so that the sinks cost
+// a page rather than a tile.  Softmax rows mask keys between the sinks and
+// their own first one, and a row whose tiles so far showed it nothing keeps its
 // maximum at -inf, so that its first visible key sets it.
 // Block scales: with s = ks_c q.k (ks_c the K scale of 16-key block c, folded
 // with the softmax scale) and vs_c the block's V scale, P' = 2^(s + log2 vs_c -
 // m) and m the running maximum of s + log2 vs_c: the V scale rides in the
 // exponent, so that O = sum P' code needs no product of its own and P' keeps
 // f16's range whatever the scales are, and l = sum_c (sum of P' over block c) /
-// vs_c is the softmax's sum.  That costs eight 16-byte shared-memory reads and
-// some 20 instructions a 128-key row and pass beside the plain kernel.  Warp 14,
-// idle otherwise, looks the scales up four tiles at a time and hands them over
-// through a ring of kScaleSlots tiles.
+// vs_c is the softmax's sum.  Warp 14, idle otherwise, looks the scales up four
+// tiles at a time and hands them over through a ring of kScaleSlots tiles; the
+// softmax warps read them before they wait for S.
 #pragma once
 #include "../../include/pafp8.h"
 #include "internal.h"
@@ -103,7 +104,9 @@ template <int DH>
 __device__ __forceinline__ uint32_t col_o(int x) { return 256u + (uint32_t)DH * (uint32_t)x; }  // O_X
 
 constexpr int kScaleSlots = 8;                                    // tiles in the ring of block scales
-constexpr uint32_t kScaleTile = kTileKeys / kPageSize * 16;      // (K scale, log2 of V's, 1 / V's, 0) a block
+// A tile's scales: the K scales of its 8 blocks, each twice (a packed pair),
+// log2 of the V scales, 1 / V scale twice each.
+constexpr uint32_t kScaleTile = kTileKeys / kPageSize * 20;
 
 template <bool kF8, bool k2, int DH, int VAR = kVarPlain>
 struct Layout {
@@ -176,7 +179,7 @@ struct Ring {
 };
 
 struct Item {
-    int b, hk, t0, nkv;          // nkv: KV tiles of the item (tile B's, or A's if B is empty)
+    int gap, hk, t0, nkv;        // nkv: KV tiles of the item (tile B's, or A's if B is empty)
     int qo0, qo_len, kv_len, page0;  // the request's first query row, rows, keys, first page entry
 };
 
@@ -189,21 +192,22 @@ __device__ __forceinline__ Item load_item(const int* items, int t) {
 
 // KV tiles that query tile `x` (0 = A, 1 = B) of an item needs: its last
 // token's causal limit, capped by the request's own key tiles; 0 if the tile
-// has no rows.  gap: tiles that a window leaves out before its last.
-__device__ __forceinline__ int tile_nkv(int t0, int x, int TQ, int qo_len, int kv_len, int gap = 0) {
+// has no rows.
+__device__ __forceinline__ int tile_nkv(int t0, int x, int TQ, int qo_len, int kv_len) {
     const int first = t0 + x * TQ;
     if (first >= qo_len) return 0;
     const int last = min(first + TQ, qo_len) - 1;
     const int lim = last + kv_len - qo_len;
-    return min((kv_len + kTileKeys - 1) / kTileKeys, lim / kTileKeys + 1) - gap;
+    return min((kv_len + kTileKeys - 1) / kTileKeys, lim / kTileKeys + 1);
 }
 
-// The item's KV tiles under a window, as its plan record counts them.
+// The item's 16-token pages as it numbers them: under a window the plan takes
+// the pages between the sinks' and the first that its first row sees (gap of
+// them) out of the item, whose kv_len and positions count without them.
 template <int VAR>
-__device__ __forceinline__ WindowUnits item_units(const PrefillParams& p, const Item& it) {
-    if constexpr (VAR != kVarPlain)
-        if (p.window > 0) return window_units(it.t0 + it.kv_len - it.qo_len - p.window + 1, p.sinks, kTileKeys);
-    return WindowUnits{0, 0};
+__device__ __forceinline__ int page_at(const PrefillParams& p, const Item& it, int vp) {
+    if (VAR == kVarPlain || p.window == 0) return vp;
+    return WindowUnits{p.sinks > 0 ? (p.sinks - 1) / kPageSize + 1 : 0, it.gap}.at(vp);
 }
 
 // The item that persistent worker i of G takes in round r.  Items are sorted
@@ -315,10 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(base + L::tmem_slot) : "memory");
     // Registers per thread: launched at 128; each warpgroup's branch below
     // starts by resizing: softmax 192, dequant 64, producer/MMA 64
-    // (4 x 32 x (64 + 2 x 192 + 64) = 65,536, what the block launched with).
+    // (4 x 32 x (64 + 2 x 192 + 64) = 65,536, what the block launched with);
+    // with block scales 208, 48 and 48, the same sum.
 
     if (warp >= 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+      if constexpr (VAR == kVarBlocks) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+      else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
       if (warp == 12) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
@@ -364,26 +370,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int m = p.page_mult;
             const int npages = (kv_len + kPageSize - 1) / kPageSize;
             const int* idx = p.kv_indices + it.page0;
-            const WindowUnits units = item_units<VAR>(p, it);
-            auto tile_page = [&](int j) { return (VAR != kVarPlain ? units.at(j) : j) * (kTileKeys / kPageSize); };
             int page_next = 0;
             {
-                const int pg0 = tile_page(0);
-                const int np0 = min(kTileKeys / kPageSize, npages - pg0);
-                if (lane < np0) page_next = __ldg(idx + (m == 1 ? pg0 + lane : (pg0 + lane) / m));
+                const int np0 = min(kTileKeys / kPageSize, npages), e = page_at<VAR>(p, it, lane);
+                if (lane < np0) page_next = __ldg(idx + (m == 1 ? e : e / m));
             }
             for (int j = 0; j < it.nkv && ok; ++j) {
-                const int pg0 = tile_page(j);
+                const int pg0 = j * (kTileKeys / kPageSize);
                 const int np = min(kTileKeys / kPageSize, npages - pg0);
                 int page = page_next;
                 if (j + 1 < it.nkv) {
-                    const int pg1 = tile_page(j + 1);
+                    const int pg1 = pg0 + kTileKeys / kPageSize;
                     const int np1 = min(kTileKeys / kPageSize, npages - pg1);
-                    page_next = lane < np1 ? __ldg(idx + (m == 1 ? pg1 + lane : (pg1 + lane) / m)) : 0;
+                    const int e = page_at<VAR>(p, it, pg1 + lane);
+                    page_next = lane < np1 ? __ldg(idx + (m == 1 ? e : e / m)) : 0;
                 }
                 const bool bad = lane < np && (page < 0 || page >= p.num_pages);
                 if (bad) page = 0;
-                else if (kSlots) page = page * m + (pg0 + lane) % m;
+                else if (kSlots) page = page * m + page_at<VAR>(p, it, pg0 + lane) % m;
                 if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.status, kStatusBounds);
                 // Lane i < np holds the id of the tile's sub-page i (page * m + j
                 // with kSlots; sub-page j of a page is the box at token slot 16 j
@@ -530,9 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Item it = load_item(items, t);
                 const int qo_len = it.qo_len;
                 const int kv_len = it.kv_len;
-                const int gap = item_units<VAR>(p, it).gap;
-                const int nA = tile_nkv(it.t0, 0, TQ, qo_len, kv_len, gap);
-                const int nB = tile_nkv(it.t0, 1, TQ, qo_len, kv_len, gap);
+                const int nA = tile_nkv(it.t0, 0, TQ, qo_len, kv_len);
+                const int nB = tile_nkv(it.t0, 1, TQ, qo_len, kv_len);
                 const int n = it.nkv;
                 ok = wait_or_abort<kDiag>(bar(fit_q ? L::bQReady : L::bQFull), qphase, flag_addr, p.status, p.wait_cycles);
                 qphase ^= 1u;
@@ -589,33 +592,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // -------------------------------------------------- block scales
         // Lane 8 k + i looks up block i of tile j0 + k.
         const int k = lane >> 3, i = lane & 7, m = p.page_mult;
-        int count = 0;  // tiles handed over so far
+        uint32_t count = 0;  // tiles handed over so far
         bool ok = true;
         for (int rnd = 0, t = blockIdx.x; t < n_items && ok; t = item_at(++rnd, blockIdx.x, gridDim.x)) {
             const Item it = load_item(items, t);
-            const WindowUnits units = item_units<VAR>(p, it);
             const int npages = (it.kv_len + kPageSize - 1) / kPageSize;
             const int* idx = p.kv_indices + it.page0;
             for (int j0 = 0; j0 < it.nkv && ok; j0 += 4) {
                 const int j = j0 + k;
                 float ks = 1.f, lv = 0.f, rv = 1.f;  // blocks past the request's end: all their keys are masked
-                const int vp = units.at(j) * (kTileKeys / kPageSize) + i;
+                const int vp = j * (kTileKeys / kPageSize) + i;
                 if (j < it.nkv && vp < npages) {
                     bool bad;  // (the producer reports it)
-                    const SubPageAt at = sub_page(idx, vp, m, p.num_pages, bad);
+                    const SubPageAt at = sub_page(idx, page_at<VAR>(p, it, vp), m, p.num_pages, bad);
                     const size_t e = ((size_t)at.page * m + at.slot / kPageSize) * p.num_kv_heads + it.hk;
                     const float v = __ldg(p.v_blocks + e);
                     ks = p.sm_scale_log2 * __ldg(p.k_blocks + e);
                     lv = __log2f(v);
                     rv = __frcp_rn(v);
                 }
-                const int tile = count + k, slot = tile % kScaleSlots;
+                const uint32_t tile = count + k, slot = tile % kScaleSlots;
                 if (j < it.nkv) {
-                    ok = wait_or_abort<kDiag>(bar(L::bScEmpty + slot), (uint32_t)((tile / kScaleSlots) & 1) ^ 1u, flag_addr,
+                    ok = wait_or_abort<kDiag>(bar(L::bScEmpty + slot), ((tile / kScaleSlots) & 1u) ^ 1u, flag_addr,
                                               p.status, p.wait_cycles);
                     if (ok) {
-                        sts128(base + L::scales + slot * kScaleTile + i * 16, __float_as_uint(ks), __float_as_uint(lv),
-                               __float_as_uint(rv), 0u);
+                        const uint32_t dst = base + L::scales + slot * kScaleTile;
+                        sts64(dst + i * 8, __float_as_uint(ks), __float_as_uint(ks));
+                        sts32(dst + 64 + i * 4, __float_as_uint(lv));
+                        sts64(dst + 96 + i * 8, __float_as_uint(rv), __float_as_uint(rv));
                         mbar_arrive(bar(L::bScFull + slot));
                     }
                 }
@@ -625,7 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+        if constexpr (VAR == kVarBlocks) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ---------------------------------------------------------- dequant
         const int wd = warp, q8 = lane >> 3, e = lane & 7;
         Ring kr, vr, k16, v16;
@@ -672,11 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int rnd = 0, t = blockIdx.x; t < n_items && ok; t = item_at(++rnd, blockIdx.x, gridDim.x)) {
             const Item it = load_item(items, t);
             const int kv_len = it.kv_len;
-            const WindowUnits units = item_units<VAR>(p, it);
             // No row of the item sees keys p.sinks .. first - 1.
             const int first = VAR != kVarPlain && p.window > 0 ? it.t0 + kv_len - it.qo_len - p.window + 1 : 0;
             for (int j = 0; j < it.nkv && ok; ++j) {
-                const int key0 = (VAR != kVarPlain ? units.at(j) : j) * kTileKeys;
+                const int key0 = j * kTileKeys;
                 const int valid = min(kTileKeys, kv_len - key0);
                 const int hide = VAR != kVarPlain ? p.sinks - key0 : 0, show = VAR != kVarPlain ? first - key0 : 0;
                 if constexpr (!kF8 && !k2) {
@@ -719,14 +723,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory");
+        if constexpr (VAR == kVarBlocks) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory");
         // ---------------------------------------------------------- softmax
         const int x = warp < 8 ? 0 : 1;        // query tile A or B
         const int r = threadIdx.x - 128 * (1 + x);  // row of the tile = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t tS = lane_base + col_s(x), tO = lane_base + col_o<DH>(x);
         uint32_t qphase = 0, sphase = 0, ophase = 0;
-        [[maybe_unused]] int sc_count = 0;  // tiles of block scales read so far
+        [[maybe_unused]] uint32_t sc_count = 0;  // tiles of block scales read so far
         uint32_t stage_round = 0;  // staging rounds of this tile so far (fp8 query)
         const bool issuer = (threadIdx.x & 127) == 0;
         const bool o_32b = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;  // rows are 256 B apart
@@ -786,8 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int qo_len = it.qo_len;
             const int kv_len = it.kv_len;
             const int t0 = it.t0 + x * TQ;
-            const WindowUnits units = item_units<VAR>(p, it);
-            const int nX = tile_nkv(it.t0, x, TQ, qo_len, kv_len, units.gap);
+            const int nX = tile_nkv(it.t0, x, TQ, qo_len, kv_len);
             const int tok = r / g, hh = r - tok * g;
             const bool valid_row = (tok < TQ) && (t0 + tok < qo_len);
             const int limit = valid_row ? t0 + tok + kv_len - qo_len : -1;
@@ -804,11 +808,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float m = -INFINITY, l = 0.f;  // m in scaled (log2) units
             for (int j = 0; j < nX && ok; ++j) {
+                // Block scales: here already, so read before the wait for S.
+                const uint32_t sc_tile = base + L::scales + (sc_count % kScaleSlots) * kScaleTile;
+                f32x2 kf2[8];  // per block: K scale with the softmax scale
+                float lv[8];   // log2 of the V scale
+                if constexpr (VAR == kVarBlocks) {
+                    ok = __all_sync(0xFFFFFFFFu, wait_or_abort<kDiag>(bar(L::bScFull + sc_count % kScaleSlots),
+                                                                      (sc_count / kScaleSlots) & 1u, flag_addr, p.status,
+                                                                      p.wait_cycles));
+                    if (!ok) break;
+                    const f32x2 row2 = make_f32x2(scale, scale);
+#pragma unroll
+                    for (int c = 0; c < 8; c += 2) {
+                        const uint4 w = lds128(sc_tile + 8 * c);
+                        kf2[c] = mul2(make_f32x2(__uint_as_float(w.x), __uint_as_float(w.y)), row2);
+                        kf2[c + 1] = mul2(make_f32x2(__uint_as_float(w.z), __uint_as_float(w.w)), row2);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; c += 4) {
+                        const uint4 w = lds128(sc_tile + 64 + 4 * c);
+                        lv[c] = __uint_as_float(w.x), lv[c + 1] = __uint_as_float(w.y);
+                        lv[c + 2] = __uint_as_float(w.z), lv[c + 3] = __uint_as_float(w.w);
+                    }
+                }
                 ok = __all_sync(0xFFFFFFFFu, wait_or_abort<kDiag>(bar(L::bSFull + x), sphase, flag_addr, p.status, p.wait_cycles));
                 sphase ^= 1u;
                 if (!ok) break;
                 tc_fence_after();
-                const int key0 = (VAR != kVarPlain ? units.at(j) : j) * kTileKeys;
+                const int key0 = j * kTileKeys;
                 const bool below = VAR != kVarPlain && key0 < low && key0 + kTileKeys > p.sinks;
                 const bool need_mask = key0 + kTileKeys - 1 > limit || below;
                 // The whole S row (128 columns) in registers, one wait.
@@ -831,12 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 float m_new;
-                const uint32_t sc_tile = base + L::scales + (sc_count % kScaleSlots) * kScaleTile;
                 if constexpr (VAR == kVarBlocks) {
-                    ok = __all_sync(0xFFFFFFFFu, wait_or_abort<kDiag>(bar(L::bScFull + sc_count % kScaleSlots),
-                                                                      (uint32_t)((sc_count / kScaleSlots) & 1), flag_addr,
-                                                                      p.status, p.wait_cycles));
-                    if (!ok) break;
                     // Each block's maximum, then that of s + log2 of its V scale.
                     m_new = m;
 #pragma unroll
@@ -847,8 +869,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             a = max3(a, __uint_as_float(v[16 * c + i]), __uint_as_float(v[16 * c + i + 1]));
                             if (i + 2 < 16) b = max3(b, __uint_as_float(v[16 * c + i + 2]), __uint_as_float(v[16 * c + i + 3]));
                         }
-                        const uint2 sc = lds64(sc_tile + 16 * c);
-                        m_new = fmaxf(m_new, fmaf(fmaxf(a, b), __uint_as_float(sc.x) * scale, __uint_as_float(sc.y)));
+                        float kf, again;
+                        split_f32x2(kf2[c], kf, again);
+                        m_new = fmaxf(m_new, fmaf(fmaxf(a, b), kf, lv[c]));
                     }
                 } else {
                     // Four independent three-input maxima keep the chain short.
@@ -907,24 +930,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // goes to v[i], which held column i (already used).  Two
                 // independent packed partial sums keep the chain short.
                 if constexpr (VAR == kVarBlocks) {
+                    f32x2 l2 = make_f32x2(l, 0.f);
+                    uint4 rv;  // 1 / V scale of two blocks, twice each
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        const uint4 sc = lds128(sc_tile + 16 * c);
-                        const float kc = __uint_as_float(sc.x) * scale, off = __uint_as_float(sc.y) - m_use;
-                        const f32x2 kc2 = make_f32x2(kc, kc), off2 = make_f32x2(off, off);
-                        f32x2 ps[2] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
+                        if (c % 2 == 0) rv = lds128(sc_tile + 96 + 8 * c);
+                        const float off = lv[c] - m_use;
+                        const f32x2 off2 = make_f32x2(off, off);
+                        f32x2 ps = make_f32x2(0.f, 0.f);
 #pragma unroll
                         for (int i = 8 * c; i < 8 * c + 8; ++i) {
                             float a, b;
-                            split_f32x2(fma2(make_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), kc2, off2),
+                            split_f32x2(fma2(make_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), kf2[c],
+                                             off2),
                                         a, b);
                             const float e0 = ex2(a), e1 = ex2(b);
-                            ps[i & 1] = add2(ps[i & 1], make_f32x2(e0, e1));
+                            ps = i == 8 * c ? make_f32x2(e0, e1) : add2(ps, make_f32x2(e0, e1));
                             v[i] = pack_half2(e0, e1);
                         }
+                        l2 = fma2(ps, c % 2 ? make_f32x2(__uint_as_float(rv.z), __uint_as_float(rv.w))
+                                            : make_f32x2(__uint_as_float(rv.x), __uint_as_float(rv.y)),
+                                  l2);
+                    }
+                    {
                         float a, b;
-                        split_f32x2(add2(ps[0], ps[1]), a, b);
-                        l = fmaf(a + b, __uint_as_float(sc.z), l);
+                        split_f32x2(l2, a, b);
+                        l = a + b;
                     }
                     // The tile's scales are read: one arrival a warp.
                     __syncwarp();
@@ -963,8 +994,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // waited for all the same, so that no warp's arrivals run ahead.
                 for (int j = nX; j < it.nkv && ok; ++j, ++sc_count) {
                     ok = __all_sync(0xFFFFFFFFu, wait_or_abort<kDiag>(bar(L::bScFull + sc_count % kScaleSlots),
-                                                                      (uint32_t)((sc_count / kScaleSlots) & 1), flag_addr,
-                                                                      p.status, p.wait_cycles));
+                                                                      (sc_count / kScaleSlots) & 1u, flag_addr, p.status,
+                                                                      p.wait_cycles));
                     if (ok && lane == 0) mbar_arrive(bar(L::bScEmpty + sc_count % kScaleSlots));
                 }
                 if (!ok) break;
@@ -1106,7 +1137,8 @@ cudaError_t launch_one(const PrefillParams& p, const CUtensorMap& tq, const CUte
 }
 
 // Dispatch on the query and cache dtypes for head size DH (block scales go
-// with an fp8 cache only).
+// with an fp8 cache only; a 2-byte one of head size 128 runs on pairs, but for
+// short windows).
 template <int DH, int VAR = kVarPlain>
 cudaError_t launch_prefill_head(const PrefillParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
                                 const CUtensorMap& tmap_v, const CUtensorMap& tmap_o, int num_ctas,
@@ -1120,7 +1152,7 @@ cudaError_t launch_prefill_head(const PrefillParams& p, const CUtensorMap& tmap_
         return launch_one<false, PAFP8_E4M3FN, DH, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
     if (p.kv_dtype == PAFP8_E5M2)
         return launch_one<false, PAFP8_E5M2, DH, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
-    if constexpr (VAR != kVarBlocks) {
+    if constexpr (VAR == kVarWindow || (VAR == kVarPlain && DH == 64)) {
         if (p.kv_dtype == PAFP8_F16)
             return launch_one<false, PAFP8_F16, DH, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
         if (p.kv_dtype == PAFP8_BF16)

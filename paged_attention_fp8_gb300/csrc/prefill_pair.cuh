@@ -110,7 +110,7 @@ __device__ __forceinline__ bool wait_or_abort_cl(uint32_t bar, uint32_t parity, 
     return true;
 }
 
-template <int KT, bool kDiag, bool kSlots>
+template <int KT, bool kDiag, bool kSlots, int VAR>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_pair_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmq,
                         const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int* idx = p.kv_indices + it.page0;
             int page_next = 0;
             {
-                const int np0 = min(kTileKeys / kPageSize, npages);
-                if (lane < np0) page_next = __ldg(idx + (m == 1 ? lane : lane / m));
+                const int np0 = min(kTileKeys / kPageSize, npages), e = page_at<VAR>(p, it, lane);
+                if (lane < np0) page_next = __ldg(idx + (m == 1 ? e : e / m));
             }
             for (int j = 0; j < it.nkv && ok; ++j) {
                 const int pg0 = j * (kTileKeys / kPageSize);
@@ -220,11 +220,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j + 1 < it.nkv) {
                     const int pg1 = pg0 + kTileKeys / kPageSize;
                     const int np1 = min(kTileKeys / kPageSize, npages - pg1);
-                    page_next = lane < np1 ? __ldg(idx + (m == 1 ? pg1 + lane : (pg1 + lane) / m)) : 0;
+                    const int e = page_at<VAR>(p, it, pg1 + lane);
+                    page_next = lane < np1 ? __ldg(idx + (m == 1 ? e : e / m)) : 0;
                 }
                 const bool bad = lane < np && (page < 0 || page >= p.num_pages);
                 if (bad) page = 0;
-                else if (kSlots) page = page * m + (pg0 + lane) % m;
+                else if (kSlots) page = page * m + page_at<VAR>(p, it, pg0 + lane) % m;
                 if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(p.status, kStatusBounds);
                 // TMA coordinates (token slot, page) of sub-page id v (page * m + j
                 // with kSlots: sub-page j of a page is the box at slot 16 j).
@@ -400,18 +401,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Each V tile is read by the P V MMAs as it landed.  In a request's last
         // tile the keys past its end (the tail of its last page, and rows no
         // page of this tile filled) are zeroed first -- thread t takes key row
-        // t -- so that P = 0 there never meets a stray non-finite value.  Both
-        // CTAs arrive on the leader's barrier.
+        // t -- so that P = 0 there never meets a stray non-finite value; so are
+        // the keys between the sinks and the first that the item's first row
+        // sees under a window.  Both CTAs arrive on the leader's barrier.
         Ring vr;
         bool ok = true;
         for (int rnd = 0, t = pair_id; t < n_items && ok; t = item_at(++rnd, pair_id, n_pairs)) {
             const Item it = load_item(items, t);
+            const int first = VAR != kVarPlain ? it.t0 + it.kv_len - it.qo_len - p.window + 1 : 0;
             for (int j = 0; j < it.nkv && ok; ++j) {
                 const int valid = min(kTileKeys, it.kv_len - j * kTileKeys);
+                const int hide = VAR != kVarPlain ? p.sinks - j * kTileKeys : 0;
+                const int show = VAR != kVarPlain ? first - j * kTileKeys : 0;
                 ok = wait_or_abort<kDiag>(bar(L::bVrFull + vr.idx), vr.phase, flag_addr, p.status, p.wait_cycles);
                 if (!ok) break;
-                if (valid < kTileKeys) {
-                    if ((int)threadIdx.x >= valid) {
+                if (valid < kTileKeys || (VAR != kVarPlain && show > 0 && hide < kTileKeys)) {
+                    const int key = (int)threadIdx.x;
+                    if (key >= valid || (VAR != kVarPlain && key >= hide && key < show)) {
                         const uint32_t row = base + L::vr + vr.idx * L::kRawV + threadIdx.x * 128u;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) sts128(row + 16u * c, 0u, 0u, 0u, 0u);
@@ -448,6 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tok = r / g, hh = r - tok * g;
             const bool valid_row = (tok < TQ) && (t0 + tok < qo_len);
             const int limit = valid_row ? t0 + tok + kv_len - qo_len : -1;
+            // Keys p.sinks .. low - 1 lie before the row's window.
+            const int low = VAR != kVarPlain ? limit - p.window + 1 : 0;
             float scale = p.sm_scale_log2;
             float vsc = p.v_scale;
             if (p.k_scales != nullptr) {  // per-head scale tensors
@@ -464,7 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const int key0 = j * kTileKeys;
-                const bool need_mask = key0 + kTileKeys - 1 > limit;
+                const bool below = VAR != kVarPlain && key0 < low && key0 + kTileKeys > p.sinks;
+                const bool need_mask = key0 + kTileKeys - 1 > limit || below;
                 uint32_t v[128];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
@@ -474,6 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         if (i > lim) v[i] = __float_as_uint(-INFINITY);
+                    if (below) {
+                        const int hide = p.sinks - key0, show = low - key0;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (i >= hide && i < show) v[i] = __float_as_uint(-INFINITY);
+                    }
                 }
                 float pm[4];
 #pragma unroll
@@ -491,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m_use = m_new;
                     rescale = true;
                 }
+                const float m_keep = m_use;  // (under a window -inf stays until the first visible key)
                 if (m_use == -INFINITY) m_use = 0.f;  // row with no admissible key so far
                 if (__any_sync(0xFFFFFFFFu, rescale)) {
                     // O_X += P_X V of the previous KV tile has completed (in-order
@@ -539,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_wait_st();
                 tc_fence_before();
                 warp_arrive_cluster(lbar(L::bPFull + x));
-                m = m_use;
+                m = VAR != kVarPlain ? m_keep : m_use;
             }
             if (!ok) break;
             // The next item's record, loaded here so that its latency passes
@@ -660,10 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int KT, bool kDiag, bool kSlots>
+template <int KT, bool kDiag, bool kSlots, int VAR>
 cudaError_t launch_pair_t(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& to, int num_ctas, cudaStream_t stream) {
-    auto kern = prefill_pair_kernel<KT, kDiag, kSlots>;
+    auto kern = prefill_pair_kernel<KT, kDiag, kSlots, VAR>;
     const size_t smem = 1024 + PairLayout::bytes;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -703,20 +719,23 @@ cudaError_t launch_pair_t(const PrefillParams& p, const CUtensorMap& tq, const C
 // A 2-byte cache at head_dim 128 (the query has the cache's dtype).  The
 // diagnostic instantiation runs only under a shortened wait bound; pages of
 // 16 tokens and of 16 m tokens have one each.
-template <int KT>
+template <int KT, int VAR>
 cudaError_t launch_pair_one(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const CUtensorMap& to, int num_ctas, cudaStream_t stream) {
-    if (p.wait_cycles < kWaitCyclesDefault) return launch_pair_t<KT, true, true>(p, tq, tk, tv, to, num_ctas, stream);
-    return p.page_mult != 1 ? launch_pair_t<KT, false, true>(p, tq, tk, tv, to, num_ctas, stream)
-                            : launch_pair_t<KT, false, false>(p, tq, tk, tv, to, num_ctas, stream);
+    if (p.wait_cycles < kWaitCyclesDefault)
+        return launch_pair_t<KT, true, true, VAR>(p, tq, tk, tv, to, num_ctas, stream);
+    if constexpr (VAR == kVarPlain)  // (the windowed variant takes any page size in one)
+        if (p.page_mult == 1) return launch_pair_t<KT, false, false, VAR>(p, tq, tk, tv, to, num_ctas, stream);
+    return launch_pair_t<KT, false, true, VAR>(p, tq, tk, tv, to, num_ctas, stream);
 }
 
-inline cudaError_t launch_prefill_pair(const PrefillParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
+template <int VAR = kVarPlain>
+cudaError_t launch_prefill_pair(const PrefillParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
                                        const CUtensorMap& tmap_v, const CUtensorMap& tmap_o, int num_ctas,
                                        cudaStream_t stream) {
     switch (p.kv_dtype) {
-        case PAFP8_F16: return launch_pair_one<PAFP8_F16>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
-        case PAFP8_BF16: return launch_pair_one<PAFP8_BF16>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
+        case PAFP8_F16: return launch_pair_one<PAFP8_F16, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
+        case PAFP8_BF16: return launch_pair_one<PAFP8_BF16, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
         default: return cudaErrorInvalidValue;
     }
 }

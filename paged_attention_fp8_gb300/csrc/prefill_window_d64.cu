@@ -1,5 +1,5 @@
 // Prefill kernels with a sliding window and sinks for head_dim 64 (the kernel is in
-// prefill.cuh; a 2-byte cache runs on single CTAs here).
+// prefill.cuh).
 #include "prefill.cuh"
 
 namespace pafp8 {
