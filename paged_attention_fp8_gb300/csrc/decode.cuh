@@ -406,9 +406,41 @@ __global__ void __launch_bounds__(32 * 9, 1)
             continue;
         }
 
+        // Window: token j of the request is visible when j < kv_len and not
+        // sinks <= j < low.
+        WindowUnits units{0, 0};
+        int low = 0;
+        if constexpr (VAR != kVarPlain) {
+            if (p.window > 0) {
+                low = kv_len - p.window;
+                units = window_units(low, p.sinks);
+            }
+        }
+        // Block scales: lane i holds those of this head's sub-page i of the
+        // current 32 and of the next 32, and the page id of the 32 after, so
+        // that neither lookup is waited for but at a segment's start; there the
+        // page ids' load goes before the query's, the scales' after it.
+        float bk = 1.f, bv = 1.f, bk_next = 1.f, bv_next = 1.f;
+        SubPageAt at_first{0, 0}, at_next{0, 0};
+        auto look_up = [&](int vp) {
+            if (vp >= p1) return SubPageAt{0, 0};
+            bool bad;
+            return sub_page(p.kv_indices + req_page[b], units.at(vp), p.page_mult, p.num_pages, bad);
+        };
+        auto load_scales = [&](SubPageAt at, float& k, float& v) {
+            const size_t i = ((size_t)at.page * p.page_mult + at.slot / P) * p.num_kv_heads + kvh;
+            k = __ldg(p.k_blocks + i);
+            v = __ldg(p.v_blocks + i);
+        };
+        if constexpr (VAR == kVarBlocks) {
+            at_first = look_up(p0 + lane);
+            at_next = look_up(p0 + 32 + lane);
+        }
+
         uint32_t qf[16], qlo[16];
         const size_t q_head_off = ((size_t)b * Hq + (size_t)kvh * group + g) * DH;
         const float qfactor = load_q<kBF, DH>(qf, qlo, p.q, p.q_dtype, q_head_off, g < group, t);
+        if constexpr (VAR == kVarBlocks) load_scales(at_first, bk_next, bv_next);
         const bool split_q = kBF && p.q_dtype == PAFP8_F16;
         // log2 softmax scale of heads 2t and 2t+1 (this lane's S columns).
         // Per-query-head scales exist only for an fp8 query, which a 2-byte
@@ -432,37 +464,6 @@ __global__ void __launch_bounds__(32 * 9, 1)
         float acc[NA][4];
 #pragma unroll
         for (int i = 0; i < NA; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-
-        // Window: token j of the request is visible when j < kv_len and not
-        // sinks <= j < low.
-        WindowUnits units{0, 0};
-        int low = 0;
-        if constexpr (VAR != kVarPlain) {
-            if (p.window > 0) {
-                low = kv_len - p.window;
-                units = window_units(low, p.sinks);
-            }
-        }
-        // Block scales: lane i holds those of this head's sub-page i of the
-        // current 32 and of the next 32, and the page id of the 32 after, so
-        // that neither lookup is waited for but at a segment's start.
-        float bk = 1.f, bv = 1.f, bk_next = 1.f, bv_next = 1.f;
-        SubPageAt at_next{0, 0};
-        auto look_up = [&](int vp) {
-            if (vp >= p1) return SubPageAt{0, 0};
-            bool bad;
-            return sub_page(p.kv_indices + req_page[b], units.at(vp), p.page_mult, p.num_pages, bad);
-        };
-        auto load_scales = [&](SubPageAt at, float& k, float& v) {
-            const size_t i = ((size_t)at.page * p.page_mult + at.slot / P) * p.num_kv_heads + kvh;
-            k = __ldg(p.k_blocks + i);
-            v = __ldg(p.v_blocks + i);
-        };
-        if constexpr (VAR == kVarBlocks) {
-            const SubPageAt first = look_up(p0 + lane);
-            at_next = look_up(p0 + 32 + lane);
-            load_scales(first, bk_next, bv_next);
-        }
 
         for (int pg = p0; pg < p1; ++pg) {
             float page_k = 1.f, page_v = 1.f;
