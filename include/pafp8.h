@@ -723,15 +723,16 @@ pafp8_status pafp8_append_kv_blocks(const pafp8_block_append_desc *desc, void *s
 /* pafp8_run over such a cache: key and value j of KV head h are their codes
  * times k_scales | v_scales[page][slot / 16][h].  For decode and prefill plans,
  * with a window or without, over an E4M3FN or E5M2 cache; any scales that are
- * finite and > 0 (device memory, not checked), 2^-96 to 2^96 in prefill.
+ * finite and > 0 (device memory, not checked), those of V of one request and
+ * head within 2^90 of one another and between 2^-96 and 2^96.
  *   q_scale    as in pafp8_run (an fp8 query)
  *   k_scales,
  *   v_scales   device float [num_pages, page_size / 16, num_kv_heads]
- * Every other argument and check is pafp8_run's.  Decode multiplies a block's
- * product with V by its scale in fp32; prefill lets the scale ride in the
- * exponent of the probabilities, which are rounded to f16's 11 bits (those
- * below 2^-14 of the request's largest probability times V scale to 2^-25 of
- * it). */
+ * Every other argument and check is pafp8_run's.  Decode keeps its fp32 sum in
+ * units of the current block's V scale (one rounding a block where it changes
+ * by other than a power of two); prefill lets the scale ride in the exponent of
+ * the probabilities, which are rounded to f16's 11 bits (those below 2^-14 of
+ * the request's largest probability times V scale to 2^-25 of it). */
 pafp8_status pafp8_run_block_scales(const pafp8_plan *plan, int32_t q_dtype, const void *q, int32_t k_dtype,
                                     const void *k_cache, int32_t v_dtype, const void *v_cache, const int32_t *kv_indices,
                                     float q_scale, const float *k_scales, const float *v_scales, int32_t o_dtype, void *o,

@@ -407,28 +407,32 @@ __global__ void __launch_bounds__(32 * 9, 1)
         }
 
         // Window: token j of the request is visible when j < kv_len and not
-        // sinks <= j < low.
+        // sinks <= j < kv_len - window.
         WindowUnits units{0, 0};
-        int low = 0;
-        if constexpr (VAR != kVarPlain) {
-            if (p.window > 0) {
-                low = kv_len - p.window;
-                units = window_units(low, p.sinks);
-            }
-        }
-        // Block scales: lane i holds those of this head's sub-page i of the
-        // current 32 and of the next 32, and the page id of the 32 after, so
-        // that neither lookup is waited for but at a segment's start; there the
-        // page ids' load goes before the query's, the scales' after it.
-        float bk = 1.f, bv = 1.f, bk_next = 1.f, bv_next = 1.f;
-        SubPageAt at_first{0, 0}, at_next{0, 0};
+        if constexpr (VAR != kVarPlain)
+            if (p.window > 0) units = window_units(kv_len - p.window, p.sinks);
+        // Block scales: lane i holds the K scale of this head's sub-page i of the
+        // current 32 and the step of the V scale to it, both scales of the next
+        // 32, and the page id of the 32 after, so that neither lookup is waited
+        // for but at a segment's start; there the page ids' load goes before the
+        // query's, the scales' after it.  O is kept in units of the current
+        // page's V scale: the rescaling by the maximum's change, which every page
+        // has anyway, carries the step (the last page's scale over this one's),
+        // and the products need none.  v_end: the scale of the last page of the
+        // current 32.  (O in units of 1 with every page's product scaled before
+        // it is added takes four registers more, and at 154 and above no block of
+        // the merge fits beside this one until it exits: 8 requests of 5021 keys
+        // 28.1 us in place of 25.)
+        float bk = 1.f, v_step = 1.f, v_end = 1.f, bk_next = 1.f, bv_next = 1.f;
+        int at_first = 0, at_next = 0;  // (sub-pages of the pool: below 2^31)
         auto look_up = [&](int vp) {
-            if (vp >= p1) return SubPageAt{0, 0};
+            if (vp >= p1) return 0;
             bool bad;
-            return sub_page(p.kv_indices + req_page[b], units.at(vp), p.page_mult, p.num_pages, bad);
+            const SubPageAt at = sub_page(p.kv_indices + req_page[b], units.at(vp), p.page_mult, p.num_pages, bad);
+            return at.page * p.page_mult + at.slot / P;
         };
-        auto load_scales = [&](SubPageAt at, float& k, float& v) {
-            const size_t i = ((size_t)at.page * p.page_mult + at.slot / P) * p.num_kv_heads + kvh;
+        auto load_scales = [&](int at, float& k, float& v) {
+            const size_t i = (size_t)at * p.num_kv_heads + kvh;
             k = __ldg(p.k_blocks + i);
             v = __ldg(p.v_blocks + i);
         };
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(32 * 9, 1)
                 sc1 = fold_scale_log2(p.sm_scale, q1, ks) * qfactor;
             }
         }
-        if constexpr (k2) sc1 = sc0;
+        if constexpr (k2 || VAR == kVarBlocks) sc1 = sc0;
 
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         float acc[NA][4];
@@ -466,19 +470,17 @@ __global__ void __launch_bounds__(32 * 9, 1)
         for (int i = 0; i < NA; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
         for (int pg = p0; pg < p1; ++pg) {
-            float page_k = 1.f, page_v = 1.f;
             if constexpr (VAR == kVarBlocks) {
-                const int i = (pg - p0) & 31;
-                if (i == 0) {
+                if (((pg - p0) & 31) == 0) {
                     bk = bk_next;
-                    bv = bv_next;
+                    const float before = __shfl_up_sync(0xFFFFFFFFu, bv_next, 1);
+                    v_step = lane == 0 ? (pg == p0 ? 1.f : __fdiv_rn(v_end, bv_next)) : __fdiv_rn(before, bv_next);
+                    v_end = __shfl_sync(0xFFFFFFFFu, bv_next, min(31, p1 - 1 - pg));
                     if (pg + 32 < p1) {
                         load_scales(at_next, bk_next, bv_next);
                         at_next = look_up(pg + 64 + lane);
                     }
                 }
-                page_k = __shfl_sync(0xFFFFFFFFu, bk, i);
-                page_v = __shfl_sync(0xFFFFFFFFu, bv, i);
             }
             // mma.sync and movmatrix below are warp-collective: the warp
             // leaves together if any lane's wait gave up.
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(32 * 9, 1)
             int hide = P, show = 0;
             if constexpr (VAR != kVarPlain) {
                 hide = max(p.sinks - tok0, 0);
-                show = low - tok0;
+                show = p.window > 0 ? valid - p.window : 0;
             }
             auto hidden = [&](int i) { return i >= valid || (VAR != kVarPlain && i >= hide && i < show); };
             if (valid < P || (VAR != kVarPlain && hide < P && show > 0)) {
@@ -630,7 +632,8 @@ __global__ void __launch_bounds__(32 * 9, 1)
                 }
             }
             // (tok g | tok g+8) x (head 2t | head 2t+1), log2 units.
-            const float ps0 = VAR == kVarBlocks ? sc0 * page_k : sc0, ps1 = VAR == kVarBlocks ? sc1 * page_k : sc1;
+            float ps0 = sc0, ps1 = sc1;
+            if constexpr (VAR == kVarBlocks) ps0 = ps1 = sc0 * __shfl_sync(0xFFFFFFFFu, bk, (pg - p0) & 31);
             float x0 = (sa[0] + sb[0]) * ps0, x1 = (sa[1] + sb[1]) * ps1;
             float x2 = (sa[2] + sb[2]) * ps0, x3 = (sa[3] + sb[3]) * ps1;
             if (hidden(g)) x0 = x1 = -INFINITY;
@@ -649,12 +652,18 @@ __global__ void __launch_bounds__(32 * 9, 1)
             l1 = l1 * al1 + e1 + e3;
             m0 = mn0;
             m1 = mn1;
+            float ao0 = al0, ao1 = al1;
+            if constexpr (VAR == kVarBlocks) {
+                const float step = __shfl_sync(0xFFFFFFFFu, v_step, (pg - p0) & 31);
+                ao0 *= step;
+                ao1 *= step;
+            }
 #pragma unroll
             for (int i = 0; i < NA; ++i) {
-                acc[i][0] *= al0;
-                acc[i][1] *= al1;
-                acc[i][2] *= al0;
-                acc[i][3] *= al1;
+                acc[i][0] *= ao0;
+                acc[i][1] *= ao1;
+                acc[i][2] *= ao0;
+                acc[i][3] *= ao1;
             }
             // P^T as the B operand: transpose the two 8x8 (token x head) blocks.
             const uint32_t pb0 = movmatrix_t(kBF ? pack_bf162(e0, e1) : pack_half2(e0, e1));
@@ -671,25 +680,14 @@ __global__ void __launch_bounds__(32 * 9, 1)
             } else {
                 const uint32_t va[4] = {v0.x, v0.y, v0.z, v0.w}, vb[4] = {v1.x, v1.y, v1.z, v1.w};
                 const uint32_t vc[4] = {v2.x, v2.y, v2.z, v2.w}, vd[4] = {v3.x, v3.y, v3.z, v3.w};
-                // Under block scales the page's product is formed apart and added
-                // with its V scale in fp32, so P keeps its own range in f16.
-                auto add_pv = [&](float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-                    if constexpr (VAR == kVarBlocks) {
-                        float r[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_16816(r, a0, a1, a2, a3, pb0, pb1);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) c[k] = fmaf(r[k], page_v, c[k]);
-                    } else {
-                        mma_16816(c, a0, a1, a2, a3, pb0, pb1);
-                    }
-                };
 #pragma unroll
                 for (int j = 0; j < NA / 2; ++j) {
                     const uint32_t ab_lo = prmt(va[j], vb[j], 0x5140u), ab_hi = prmt(va[j], vb[j], 0x7362u);
                     const uint32_t cd_lo = prmt(vc[j], vd[j], 0x5140u), cd_hi = prmt(vc[j], vd[j], 0x7362u);
-                    add_pv(acc[2 * j], fp8x2_lo<KT>(ab_lo), fp8x2_hi<KT>(ab_lo), fp8x2_lo<KT>(cd_lo), fp8x2_hi<KT>(cd_lo));
-                    add_pv(acc[2 * j + 1], fp8x2_lo<KT>(ab_hi), fp8x2_hi<KT>(ab_hi), fp8x2_lo<KT>(cd_hi),
-                           fp8x2_hi<KT>(cd_hi));
+                    mma_16816(acc[2 * j], fp8x2_lo<KT>(ab_lo), fp8x2_hi<KT>(ab_lo), fp8x2_lo<KT>(cd_lo),
+                              fp8x2_hi<KT>(cd_lo), pb0, pb1);
+                    mma_16816(acc[2 * j + 1], fp8x2_lo<KT>(ab_hi), fp8x2_hi<KT>(ab_hi), fp8x2_lo<KT>(cd_hi),
+                              fp8x2_hi<KT>(cd_hi), pb0, pb1);
                 }
             }
         }
@@ -713,6 +711,10 @@ __global__ void __launch_bounds__(32 * 9, 1)
             for (int i = 0; i < NA; ++i) {
                 vals[2 * i] = acc[i][hh] * inv;
                 vals[2 * i + 1] = acc[i][2 + hh] * inv;
+                if constexpr (VAR == kVarBlocks) {
+                    vals[2 * i] *= v_end;
+                    vals[2 * i + 1] *= v_end;
+                }
             }
             const int head = kvh * group + n;
             if (slot < 0) {

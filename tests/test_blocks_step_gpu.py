@@ -140,10 +140,11 @@ def test_two_batches_on_two_streams(cuda_device):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(lens=[900, 40], scales="block"), dict(lens=[900, 40], window=300, sinks=4), dict(lens=[300, 60], new=[129, 40], scales="block"),
+    dict(lens=[9000, 40], scales="block"), dict(lens=[9000, 40], window=8000, sinks=4), dict(lens=[300, 60], new=[129, 40], scales="block"),
     dict(lens=[300, 60], new=[129, 40], scales="block", q="e4m3fn", window=100, sinks=4),
     dict(lens=[300, 60], new=[129, 40], window=100, sinks=4), dict(lens=[1900], new=[300], window=800, sinks=4, q="bf16", kv="bf16")])
 def test_expired_wait_is_reported_and_the_next_run_is_clean(cuda_device, monkeypatch, kw):
+    """(Decode: 60 pages and more a block, through a ring of 8, so that its producer has to wait for a page's use.)"""
     b = Batch(num_ctas=8, **kw).upload()
     monkeypatch.delenv("PAFP8_DEBUG", raising=False)
     monkeypatch.setenv("PAFP8_WAIT_CYCLES", "1")
