@@ -455,14 +455,13 @@ def pafp8_run_block_scales(handle: int, q, k_cache, v_cache, kv_indices, o, lse,
     k_scales and v_scales, float32 [pages, page_size / 16, Hkv].  Arrays are
     contiguous and on the current CUDA device; kv_indices is int32, lse float32
     or None; dtypes come from the tensors."""
-    T = _torch()
+    T = _T or _torch()
     dev = _device_of(q, "q")
     qt, kt, ot, i32, f32 = q.dtype, k_cache.dtype, o.dtype, T.int32, T.float32
     for t, name, dtype in ((q, "q", qt), (k_cache, "k_cache", kt), (v_cache, "v_cache", kt), (kv_indices, "kv_indices", i32),
-                           (o, "o", ot), (lse, "lse", f32), (workspace, "workspace", workspace.dtype), (k_scales, "k_scales", f32),
-                           (v_scales, "v_scales", f32)):
-        if t is not None and (t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous()):
-            _refuse(t, name, dtype, dev)
+                           (o, "o", ot), (lse, "lse", f32), (workspace, "workspace", None)):
+        if t is not None and (t.get_device() != dev or (t.dtype is not dtype and dtype is not None) or not t.is_contiguous()):
+            _refuse(t, name, dtype or t.dtype, dev)
     rows_of, pool, lse_of, blocks, n_index = _sizes(handle)
     if q.shape != rows_of or o.shape != rows_of or k_cache.shape != pool or v_cache.shape != pool or \
             (lse is not None and lse.shape != lse_of) or (kv_indices is not None and kv_indices.numel() < n_index):
@@ -470,13 +469,13 @@ def pafp8_run_block_scales(handle: int, q, k_cache, v_cache, kv_indices, o, lse,
                          f"{tuple(v_cache.shape)}, lse {lse is not None and tuple(lse.shape)} and kv_indices "
                          f"{kv_indices is not None and kv_indices.numel()} do not fit the plan's {rows_of}, {pool}, {lse_of} "
                          f"and {n_index} page ids")
-    if k_scales.shape != blocks or v_scales.shape != blocks:
-        raise ValueError(f"k_scales {tuple(k_scales.shape)} and v_scales {tuple(v_scales.shape)} are not {blocks} (pages, "
-                         "blocks of 16 tokens, KV heads)")
+    code = _OBJ_CODES.get
+    kc = code(kt) or dtype_code(kt)
     _check(lib().pafp8_run_block_scales(
-        handle, dtype_code(qt), q.data_ptr(), dtype_code(kt), k_cache.data_ptr(), dtype_code(kt), v_cache.data_ptr(),
-        _ptr(kv_indices), q_scale, k_scales.data_ptr(), v_scales.data_ptr(), dtype_code(ot), o.data_ptr(), _ptr(lse),
-        workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream)))
+        handle, code(qt) or dtype_code(qt), q.data_ptr(), kc, k_cache.data_ptr(), kc, v_cache.data_ptr(),
+        None if kv_indices is None else kv_indices.data_ptr(), q_scale, _block_scales(k_scales, "k_scales", blocks, dev),
+        _block_scales(v_scales, "v_scales", blocks, dev), code(ot) or dtype_code(ot), o.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream)))
 
 
 def pafp8_device_status(handle: int, workspace, stream=None) -> None:
@@ -672,22 +671,28 @@ def pafp8_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, slot
 def _cache_shape(k_cache, v_cache, hkv, d, layout, kv_layout, dev):
     """(pages, page size) of two caches that hold `hkv` heads of `d` in this layout."""
     shape, kt = k_cache.shape, k_cache.dtype
-    if len(shape) != 4 or v_cache.shape != shape or shape[3] != d or shape[1 if layout == LAYOUT_HND else 2] != hkv:
-        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} do not hold {hkv} heads of {d} in "
+    if len(shape) != 4 or v_cache.shape != shape:
+        shape = (0, 0, 0, -1)
+    pages, ps, heads, cd = shape
+    if layout == LAYOUT_HND:
+        ps, heads = heads, ps
+    if cd != d or heads != hkv:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} do not hold {hkv} heads of {d} in "
                          f"layout {kv_layout}")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.get_device() != dev or t.dtype is not kt or not t.is_contiguous():
-            _refuse(t, name, kt, dev)
-    return shape[0], shape[2 if layout == LAYOUT_HND else 1]
+    if k_cache.get_device() != dev or not k_cache.is_contiguous():
+        _refuse(k_cache, "k_cache", kt, dev)
+    if v_cache.get_device() != dev or v_cache.dtype is not kt or not v_cache.is_contiguous():
+        _refuse(v_cache, "v_cache", kt, dev)
+    return pages, ps
 
 
-def _block_scales(t, name, pages, page_size, hkv, dev) -> int:
-    """The address of a contiguous float32 [pages, page_size / 16, hkv] tensor."""
-    f32 = _torch().float32
-    if t.shape != (pages, page_size // 16, hkv):
-        raise ValueError(f"{name} {tuple(t.shape)} is not [{pages}, {page_size // 16}, {hkv}] (pages, blocks of 16 tokens, "
-                         "KV heads)")
-    return _addr(t, name, 0, f32, dev)
+def _block_scales(t, name, shape, dev) -> int:
+    """The address of a contiguous float32 tensor of `shape`: pages, blocks of 16 tokens, KV heads."""
+    if t.shape != shape:
+        raise ValueError(f"{name} {tuple(t.shape)} is not {shape} (pages, blocks of 16 tokens, KV heads)")
+    if t.get_device() != dev or t.dtype is not _T.float32 or not t.is_contiguous():
+        _refuse(t, name, _T.float32, dev)
+    return t.data_ptr()
 
 
 def pafp8_append_kv_blocks(k_new, v_new, qo_indptr, cached_lens, kv_indptr, kv_indices, k_cache, v_cache, k_scales, v_scales,
@@ -699,11 +704,11 @@ def pafp8_append_kv_blocks(k_new, v_new, qo_indptr, cached_lens, kv_indptr, kv_i
     Hkv].  k_new and v_new may be slices of one packed projection (any token
     stride); rows from qo_indptr[batch] on are not read.  Index arrays are
     device int32."""
-    T = _torch()
-    i32, dt = T.int32, k_new.dtype
-    if k_new.dim() != 3 or v_new.shape != k_new.shape:
+    T = _T or _torch()
+    i32, shape, dt = T.int32, k_new.shape, k_new.dtype
+    if len(shape) != 3 or v_new.shape != shape:
         raise ValueError(f"k_new {tuple(k_new.shape)} and v_new {tuple(v_new.shape)} are not [n, Hkv, D] both")
-    n, hkv, d = k_new.shape
+    n, hkv, d = shape
     layout = _LAYOUTS[kv_layout] if kv_layout in _LAYOUTS else int(kv_layout)
     dev = _device_of(k_new, "k_new")
     (ks, kh, k1), (vs, vh, v1) = k_new.stride(), v_new.stride()
@@ -712,16 +717,18 @@ def pafp8_append_kv_blocks(k_new, v_new, qo_indptr, cached_lens, kv_indptr, kv_i
                          f"{k_new.stride()}, {v_new.stride()}) must have one dtype and lie on the current CUDA device with "
                          "the heads of a token contiguous")
     pages, ps = _cache_shape(k_cache, v_cache, hkv, d, layout, kv_layout, dev)
+    blocks = (pages, ps // 16, hkv)
     batch = qo_indptr.numel() - 1
     if batch < 0:
         raise ValueError("qo_indptr is empty (it has a request more than cached_lens)")
+    code = _OBJ_CODES.get
     _check(lib().pafp8_append_kv_blocks(_BLOCK_APPEND.pack(
         k_new.data_ptr(), v_new.data_ptr(), _addr(qo_indptr, "qo_indptr", 1, i32, dev),
         _addr(cached_lens, "cached_lens", batch, i32, dev), _addr(kv_indptr, "kv_indptr", batch + 1, i32, dev),
         _addr(kv_indices, "kv_indices", 0, i32, dev), k_cache.data_ptr(), v_cache.data_ptr(),
-        _block_scales(k_scales, "k_scales", pages, ps, hkv, dev), _block_scales(v_scales, "v_scales", pages, ps, hkv, dev),
-        _addr(status, "status", 1, i32, dev), n, ks, vs, batch, dtype_code(dt), dtype_code(k_cache.dtype), layout, hkv, d,
-        pages, ps), _stream_on(dev, stream)))
+        _block_scales(k_scales, "k_scales", blocks, dev), _block_scales(v_scales, "v_scales", blocks, dev),
+        0 if status is None else _addr(status, "status", 1, i32, dev), n, ks, vs, batch, code(dt) or dtype_code(dt),
+        code(k_cache.dtype) or dtype_code(k_cache.dtype), layout, hkv, d, pages, ps), _stream_on(dev, stream)))
 
 
 def pafp8_read_kv(k_cache, v_cache, out_indptr, starts, kv_indptr, kv_indices, k_out, v_out, *, k_scale=1.0, v_scale=1.0,
@@ -732,25 +739,27 @@ def pafp8_read_kv(k_cache, v_cache, out_indptr, starts, kv_indptr, kv_indices, k
     [pages, page_size / 16, Hkv]) or, without them, k_scale and v_scale.  Rows
     from out_indptr[batch] on are left as they were.  Index arrays are device
     int32."""
-    T = _torch()
-    i32, dt = T.int32, k_out.dtype
-    if k_out.dim() != 3 or v_out.shape != k_out.shape:
+    T = _T or _torch()
+    i32, shape, dt = T.int32, k_out.shape, k_out.dtype
+    if len(shape) != 3 or v_out.shape != shape:
         raise ValueError(f"k_out {tuple(k_out.shape)} and v_out {tuple(v_out.shape)} are not [n, Hkv, D] both")
-    n, hkv, d = k_out.shape
+    n, hkv, d = shape
     layout = _LAYOUTS[kv_layout] if kv_layout in _LAYOUTS else int(kv_layout)
     dev = _device_of(k_out, "k_out")
     pages, ps = _cache_shape(k_cache, v_cache, hkv, d, layout, kv_layout, dev)
     batch = out_indptr.numel() - 1
     if batch < 0:
         raise ValueError("out_indptr is empty (it has a request more than starts)")
+    blocks, code = (pages, ps // 16, hkv), _OBJ_CODES.get
     _check(lib().pafp8_read_kv(_READ.pack(
         k_cache.data_ptr(), v_cache.data_ptr(), _addr(out_indptr, "out_indptr", 1, i32, dev),
         _addr(starts, "starts", batch, i32, dev), _addr(kv_indptr, "kv_indptr", batch + 1, i32, dev),
         _addr(kv_indices, "kv_indices", 0, i32, dev), _addr(k_out, "k_out", 0, dt, dev), _addr(v_out, "v_out", 0, dt, dev),
-        0 if k_scales is None else _block_scales(k_scales, "k_scales", pages, ps, hkv, dev),
-        0 if v_scales is None else _block_scales(v_scales, "v_scales", pages, ps, hkv, dev),
-        _addr(status, "status", 1, i32, dev), n, batch, dtype_code(k_cache.dtype), dtype_code(dt), layout, hkv, d, pages, ps,
-        k_scale, v_scale), _stream_on(dev, stream)))
+        0 if k_scales is None else _block_scales(k_scales, "k_scales", blocks, dev),
+        0 if v_scales is None else _block_scales(v_scales, "v_scales", blocks, dev),
+        0 if status is None else _addr(status, "status", 1, i32, dev), n, batch,
+        code(k_cache.dtype) or dtype_code(k_cache.dtype), code(dt) or dtype_code(dt), layout, hkv, d, pages, ps, k_scale,
+        v_scale), _stream_on(dev, stream)))
 
 
 class StepTables:

@@ -150,7 +150,7 @@ def test_binding_refuses(call):
             (dict(lse=g["lse"].double()), "lse has dtype"), (dict(lse=g["lse"][:-1]), "do not fit"),
             (dict(k_cache=g["k_cache"][:-1]), "do not fit"), (dict(v_cache=g["v_cache"].view(torch.float8_e5m2)), "v_cache has dtype"),
             (dict(kv_indices=g["kv_indices"].long()), "kv_indices has dtype"), (dict(kv_indices=g["kv_indices"][:9]), "do not fit"),
-            (dict(k_scales=torch.ones(POOL, HKV)), "are not"), (dict(v_scales=torch.ones(POOL, 2, HKV)), "are not"),
+            (dict(k_scales=torch.ones(POOL, HKV)), "k_scales .* is not"), (dict(v_scales=torch.ones(POOL, 2, HKV)), "v_scales .* is not"),
             (dict(k_scales=g["k_scales"].double()), "k_scales has dtype"), (dict(q=g["q"].transpose(0, 1)), "contiguous"),
             (dict(k_scales=torch.ones(POOL, 1, 2 * HKV)[..., ::2]), "contiguous")]:
         with pytest.raises(ValueError, match=match):
