@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(32 * 9, 1)
     decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, int hpc, int group, int stages,
                   int heads_per_box) {
+    // Nothing is read or written before the stream's earlier work is complete.
+    if constexpr (VAR != kVarPlain) asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;      // 128B swizzle wants 1024-B alignment
@@ -760,8 +762,25 @@ cudaError_t launch_decode_t(const DecodeParams& p, const CUtensorMap& tmap_k, co
                      : (p.page_mult != 1 ? decode_kernel<KT, DH, false, true, VAR> : decode_kernel<KT, DH, false, false, VAR>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, block, smem, stream>>>(p, tmap_k, tmap_v, hpc, group, stages, heads_per_box);
-    return cudaGetLastError();
+    if constexpr (VAR == kVarPlain) {
+        kern<<<grid, block, smem, stream>>>(p, tmap_k, tmap_v, hpc, group, stages, heads_per_box);
+        return cudaGetLastError();
+    } else {
+        // The variants wait for the stream's work before them in the kernel
+        // rather than before the launch: eager calls one after the other save the
+        // launch's latency (8 requests, window 5001: 28.3 -> 26.0 us a call).
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, p, tmap_k, tmap_v, hpc, group, stages, heads_per_box);
+    }
 }
 
 template <int KT, int VAR>

@@ -139,6 +139,58 @@ def test_two_batches_on_two_streams(cuda_device):
         b.check()
 
 
+@pytest.mark.parametrize("scales", ["tensor", "block"])
+def test_each_call_sees_the_work_before_it(cuda_device, scales):
+    """Decode launches early and waits in the kernel: every input is rewritten right before a call -- by copies, kernels and
+    the append -- and right after it, eager and captured with the plan's upload, forty times over one workspace."""
+    bs = [Batch([700, 33, 260], window=300, sinks=5, scales=scales, num_ctas=40, seed=i).upload() for i in range(2)]
+    a = bs[0]
+    want = []
+    for b in bs:
+        b.run()
+        b.check()
+        want.append((raw(b.o).clone(), b.lse.clone()))
+    held = [[raw(t).clone() for t in (b.q_d, b.k_d, b.v_d)] + [b.ids_d.clone()] +
+            ([b.ks_d.clone(), b.vs_d.clone()] if scales == "block" else []) for b in bs]
+    into = [raw(a.q_d), raw(a.k_d), raw(a.v_d), a.ids_d] + ([a.ks_d, a.vs_d] if scales == "block" else [])
+    scal = [(b.k_scale, b.v_scale) if scales == "tensor" else (1.0, 1.0) for b in bs]
+    got = []
+
+    def step(i):
+        for x, y in zip(into, held[i]):
+            x.copy_(y)
+        if scales == "tensor":
+            a.k_scale, a.v_scale = scal[i]
+        a.run()
+        out = raw(a.o).clone(), a.lse.clone()
+        for x in into[:1] + into[3:4]:
+            x.zero_()
+        a.o.fill_(7)
+        return out
+
+    for k in range(40):
+        got.append((k % 2, *step(k % 2)))
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(0)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    outs = []
+    with torch.cuda.graph(g):
+        for k in range(6):
+            a.plan.upload(a.ws)
+            outs.append((k % 2, *step(k % 2)))
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        got += [(i, o.clone(), l.clone()) for i, o, l in outs]
+    torch.cuda.synchronize()
+    for i, o, l in got:
+        assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+
+
 @pytest.mark.parametrize("kw", [
     dict(lens=[9000, 40], scales="block"), dict(lens=[9000, 40], window=8000, sinks=4), dict(lens=[300, 60], new=[129, 40], scales="block"),
     dict(lens=[300, 60], new=[129, 40], scales="block", q="e4m3fn", window=100, sinks=4),
