@@ -13,16 +13,24 @@
 //            that holds tokens of earlier steps
 //   code   = fp8(RNE, saturating)(x * fp32(1 / s))
 //   code'  = fp8(RNE)(code * fp32(s_old / s)) for those tokens, if s > s_old.
-// A request's new tokens are contiguous, so one warp owns a (block, head, K or
-// V): no atomics, and the result is a function of the inputs.  The warp keeps
-// the block's 16 rows in registers between the maximum and the conversion, so
-// the source is read once.
+// A request's new tokens are contiguous, so one warp owns a block of K or V of
+// one head (of two heads of 64): no atomics, and the result is a function of the
+// inputs.  The warp keeps the block's 16 rows in registers between the maximum
+// and the conversion, so the source is read once.
 //
 // Reading.  Rows out_indptr[b] .. out_indptr[b + 1] - 1 are tokens starts[b]
 // on of request b, as fp32(code) * scale rounded once to the output's type.
 //
 // Both are streams, bounded by HBM, and by launch and table lookups for a few
-// tokens.
+// tokens.  Measured in a graph, inputs of three steps in turn: the append of 16
+// ragged prompts (8 heads of 128, bf16 to e4m3fn, 45.7 MB) 11.9 us, 57 % of the
+// measured copy rate: two waves of warps, each of which waits for its request
+// (32 probes of qo_indptr a step), lengths and page before its rows.  One
+// warp for K and V both (half the warps, twice the registers) takes 14.8 us; 80
+// registers (6 thread blocks of 4 warps an SM) 11.9, 64 registers with spills
+// 12.6, 96 12.8; conditions on every row of every block 13.4.  64 single tokens
+// take 4.0 us.  The read-back of 64 requests of 512-4096 tokens (891 MB) takes
+// 138 us, 95 % of the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -35,7 +43,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAppendThreads = 128;
-constexpr int kAppendBlocks = 6;
+constexpr int kAppendBlocks = 6;  // thread blocks an SM, for 80 registers a thread (fp32 rows: 3, for 168)
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 // The request that owns row t, by one warp together: the last r with
@@ -347,6 +355,9 @@ __global__ void __launch_bounds__(kAppendThreads, SRC == PAFP8_F32 ? 3 : kAppend
 
 template <int SRC, int KV, int DH>
 cudaError_t launch_append_t(BlockAppendParams p, cudaStream_t stream) {
+    // A warp looks through 16 tokens for its blocks, which in a prompt are one
+    // or two; up to four tokens a request it takes one token, so that a decode
+    // step's requests go to a warp each rather than 16 to one in turn.
     p.span = p.nnz <= 4LL * p.batch ? 1 : kPageSize;
     constexpr int HPW = 128 / DH, W = kAppendThreads / 32;
     const long long units = (p.nnz + p.span - 1) / p.span * (2LL * ((p.num_kv_heads + HPW - 1) / HPW));
