@@ -662,7 +662,7 @@ pafp8_status pafp8_norm_rope_append(const pafp8_rope_desc *desc, void *stream);
  *   s     = s_new, or max(s_old, s_new) when the block holds tokens before
  *           position cached_lens[b]
  *   code  = fp8(RNE, saturating)(fp32(x) * fp32(1 / s))
- * and where s > s_old the codes of those tokens become fp8(RNE, saturating)(
+ * (products rounded in fp32) and where s > s_old the codes of those tokens become fp8(RNE, saturating)(
  * code * fp32(s_old / s)): exact for the powers of two this call writes, but
  * for codes that fall below the type's normal range.  s is stored as the
  * block's scale.  An infinite element stores the largest value with its sign,

@@ -22,6 +22,12 @@ def grid(x, fmt):
     return np.where(np.isnan(x), np.nan, out)
 
 
+def times(x, by, fmt):
+    """Codes of x * by, the product rounded to fp32 first (x holds fp32 numbers)."""
+    with np.errstate(invalid="ignore", over="ignore", under="ignore"):
+        return grid((np.asarray(x, np.float32) * np.float32(by)).astype(np.float64), fmt)
+
+
 def own_scale(x, fmt):
     """The block's scale from its new values: the smallest 2^k >= 2^-64 with amax <= TOP 2^k, by trying."""
     x = np.abs(np.asarray(x, np.float64))
@@ -55,9 +61,9 @@ class Cache:
                         old = self.scales[page, blk, h]
                         s = max(s, old)
                         if s > old:
-                            self.values[page, first:slot, h] = grid(self.values[page, first:slot, h] * np.float64(
-                                np.float32(old) / np.float32(s)), self.fmt)
-                    self.values[page, slot:slot + m, h] = grid(rows * np.float64(np.float32(1) / np.float32(s)), self.fmt)
+                            self.values[page, first:slot, h] = times(self.values[page, first:slot, h], np.float32(old) / np.float32(s),
+                                                                     self.fmt)
+                    self.values[page, slot:slot + m, h] = times(rows, np.float32(1) / np.float32(s), self.fmt)
                     self.scales[page, blk, h] = s
                 r0, pos = r0 + m, pos + m
 

@@ -90,6 +90,22 @@ def test_a_token_written_again(cuda_device):
         s.check()
 
 
+@pytest.mark.parametrize("fmt,src", [("e4m3fn", "f32"), ("e5m2", "bf16")])
+def test_scales_that_are_not_powers_of_two(cuda_device, fmt, src):
+    """A cache whose blocks have other scales (another writer's): a larger one is kept, a smaller one grows to a power of two."""
+    s = Setup([16 * i + 9 for i in range(60)], fmt=fmt)
+    for t, ref in ((s.ks, s.rk), (s.vs, s.rv)):
+        t.mul_(1 + torch.rand(t.shape, generator=s.gen).cuda())
+        ref.scales = t.double().cpu().numpy()
+    cached = [16 * i + 5 for i in range(60)]
+    k, v = s.rows(240, src, big=8.0)
+    s.append(k, v, ints(np.arange(0, 241, 4)), ints(cached))
+    s.expect(k, v, np.arange(0, 241, 4), cached)
+    s.check()
+    frac = np.frexp(np.stack([s.rk.scales[s.ids[s.ptr[b] + b], 0] for b in range(60)]))[0]
+    assert (frac != 0.5).any() and (frac == 0.5).any()  # both happened
+
+
 @pytest.mark.parametrize("fmt", ["e4m3fn", "e5m2"])
 @pytest.mark.parametrize("src", ["bf16", "f16", "f32"])
 def test_special_values(cuda_device, fmt, src):
