@@ -124,19 +124,20 @@ struct Layout {
     // The 2-byte-query path spends its shared memory on two f16 K tiles (the
     // dequant of K_{j+1} may start while QK_B(j) still reads K_j) and keeps a
     // single raw fp8 stage per tensor; the fp8 path multiplies raw K directly.
-    // A 2-byte cache (k2) brings K straight into the 16-bit K tiles and only
-    // copies V (zeroing the keys past the request's end), so it has no raw K
-    // stage and a 2-byte raw V stage.
+    // A 2-byte cache (k2) brings K and V straight into the 16-bit tiles and has
+    // no raw stages, but a third V tile: the dequant warps only zero, in place,
+    // the V rows that no query row sees.  (Copying V from a raw stage took 130.7
+    // us where this takes 126.3: 9 prompts, 16 / 4 heads of 64.)
     static constexpr int NKR = kF8 ? 4 : (k2 ? 0 : 1);  // raw K stages
-    static constexpr int NVR = kF8 ? 2 : 1;             // raw V stages
-    static constexpr uint32_t kRawV = k2 ? Dm::kF16Tile : Dm::kRawTile;
+    static constexpr int NVR = kF8 ? 2 : (k2 ? 0 : 1);  // raw V stages
     static constexpr int NK16 = kF8 ? 0 : 2;   // f16 K stages
-    static constexpr int NV16 = 2;             // f16 V stages
+    static constexpr int NV16 = k2 ? 3 : 2;    // f16 V stages
+    static constexpr int nVr = k2 ? NV16 : NVR;  // V tiles that copies land in
     static constexpr uint32_t kQTile = kF8 ? kTileRows * DH : Dm::kF16Tile;
     static constexpr uint32_t q = 0;                     // Q_A, then Q_B
     static constexpr uint32_t kr = 2 * kQTile;
     static constexpr uint32_t vr = kr + NKR * Dm::kRawTile;
-    static constexpr uint32_t k16 = vr + NVR * kRawV;
+    static constexpr uint32_t k16 = vr + NVR * Dm::kRawTile;
     static constexpr uint32_t v16 = k16 + NK16 * Dm::kF16Tile;
     // fp8 query: a 16 KB staging half per query tile for the output's bulk
     // tensor stores (64 dims of 128 rows, 128-byte rows swizzled).
@@ -147,7 +148,7 @@ struct Layout {
     // barrier indices (8 bytes each)
     static constexpr int bQFull = 0, bQReady = 1, bQEmpty = 2;
     static constexpr int bKrFull = 3, bKrEmpty = bKrFull + NKR;
-    static constexpr int bVrFull = bKrEmpty + NKR, bVrEmpty = bVrFull + NVR;
+    static constexpr int bVrFull = bKrEmpty + NKR, bVrEmpty = bVrFull + nVr;
     static constexpr int bK16Full = bVrEmpty + NVR, bK16Empty = bK16Full + NK16;
     static constexpr int bV16Full = bK16Empty + NK16, bV16Empty = bV16Full + NV16;
     static constexpr int bSFull = bV16Empty + NV16;  // [2]
@@ -293,10 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(L::bKrFull + i), 1);
             mbar_init(bar(L::bKrEmpty + i), kF8 ? 1 : 128);
         }
-        for (int i = 0; i < L::NVR; ++i) {
-            mbar_init(bar(L::bVrFull + i), 1);
-            mbar_init(bar(L::bVrEmpty + i), 128);
-        }
+        for (int i = 0; i < L::nVr; ++i) mbar_init(bar(L::bVrFull + i), 1);
+        for (int i = 0; i < L::NVR; ++i) mbar_init(bar(L::bVrEmpty + i), 128);
         for (int i = 0; i < L::NK16; ++i) {
             mbar_init(bar(L::bK16Full + i), k2 ? 1 : 128);  // TMA, or the dequant warps
             mbar_init(bar(L::bK16Empty + i), 1);
@@ -451,14 +450,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++issued_k;
                 kr.next(nkr);
                 if (lane == 0) {
-                    ok = wait_or_abort<kDiag>(bar(L::bVrEmpty + vr.idx), vr.phase ^ 1u, flag_addr, p.status, p.wait_cycles);
+                    ok = wait_or_abort<kDiag>(bar((k2 ? L::bV16Empty : L::bVrEmpty) + vr.idx), vr.phase ^ 1u, flag_addr,
+                                              p.status, p.wait_cycles);
                     if (ok) mbar_arrive_expect_tx(bar(L::bVrFull + vr.idx), (uint32_t)np * kPageSize * DH * (k2 ? 2 : 1));
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
                 if (!ok) break;
                 if (k2) {
                     if (half_lane) {
-                        const uint32_t dst = base + L::vr + vr.idx * L::kRawV;
+                        const uint32_t dst = base + L::v16 + vr.idx * Dm::kF16Tile;
                         const int h = lane >> 3, i = lane & 7;
                         for_half_page([&](int slot, int pg) {
                             tma_load_5d(dst + h * kHalfTile + i * 2048u, &tmv, bar(L::bVrFull + vr.idx), 0, h, slot, it.hk,
@@ -466,13 +466,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         });
                     }
                 } else if (lane < np) {
-                    const uint32_t dst = base + L::vr + vr.idx * L::kRawV;
+                    const uint32_t dst = base + L::vr + vr.idx * Dm::kRawTile;
                     for_page([&](int slot, int pg) {
                         tma_load_4d(dst + lane * Dm::kRawPage, &tmv, bar(L::bVrFull + vr.idx), 0, it.hk, slot, pg);
                     });
                 }
                 ++issued_v;
-                vr.next(L::NVR);
+                vr.next(L::nVr);
             }
         }
         if (lane == 0) {
@@ -480,8 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (issued_q > 0) mbar_wait(bar(L::bQFull), (uint32_t)((issued_q - 1) & 1));
             for (int s = 0; s < nkr && s < issued_k; ++s)
                 mbar_wait(bar(bkf + s), (uint32_t)(((issued_k - 1 - s) / nkr) & 1));
-            for (int s = 0; s < L::NVR && s < issued_v; ++s)
-                mbar_wait(bar(L::bVrFull + s), (uint32_t)(((issued_v - 1 - s) / L::NVR) & 1));
+            for (int s = 0; s < L::nVr && s < issued_v; ++s)
+                mbar_wait(bar(L::bVrFull + s), (uint32_t)(((issued_v - 1 - s) / L::nVr) & 1));
         }
       } else if (warp == 13) {
         // ------------------------------------------------------------- MMA
@@ -705,30 +705,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     k16.next(L::NK16);
                 }
                 ok = wait_or_abort<kDiag>(bar(L::bVrFull + vr.idx), vr.phase, flag_addr, p.status, p.wait_cycles) &&
-                     wait_or_abort<kDiag>(bar(L::bV16Empty + v16.idx), v16.phase ^ 1u, flag_addr, p.status, p.wait_cycles);
+                     (k2 || wait_or_abort<kDiag>(bar(L::bV16Empty + v16.idx), v16.phase ^ 1u, flag_addr, p.status,
+                                                 p.wait_cycles));
                 if (!ok) break;
-                const uint32_t src = base + L::vr + vr.idx * L::kRawV;
                 const uint32_t dst = base + L::v16 + v16.idx * Dm::kF16Tile;
                 if constexpr (k2) {
-                    // A 2-byte V tile is already in the layout the MMA reads: copied
-                    // 16 bytes per thread and step (consecutive threads, consecutive
-                    // chunks), keys past the request's end zeroed.
-#pragma unroll 2
-                    for (int i = 0; i < 8 * NH; ++i) {
-                        const int q = i * 128 + (int)threadIdx.x;
-                        const uint32_t off = (uint32_t)q * 16u;  // [half][key][128 B]
-                        const int row = (q >> 3) & (kTileKeys - 1);
-                        uint4 w = lds128(src + off);
-                        if (row >= valid || (VAR != kVarPlain && row >= hide && row < show)) w = make_uint4(0u, 0u, 0u, 0u);
-                        sts128(dst + off, w.x, w.y, w.z, w.w);
+                    // A 2-byte V tile is where the MMA reads it: thread t zeroes key
+                    // row t if no query row sees it.
+                    const int row = (int)threadIdx.x;
+                    if (row >= valid || (VAR != kVarPlain && row >= hide && row < show)) {
+#pragma unroll
+                        for (int c = 0; c < 8 * NH; ++c)
+                            sts128(dst + (c >> 3) * kHalfTile + row * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
                     }
                 } else {
-                    widen(src, dst, valid, hide, show);
+                    widen(base + L::vr + vr.idx * Dm::kRawTile, dst, valid, hide, show);
                 }
                 fence_async_smem();
                 mbar_arrive(bar(L::bV16Full + v16.idx));
-                mbar_arrive(bar(L::bVrEmpty + vr.idx));
-                vr.next(L::NVR);
+                if constexpr (!k2) mbar_arrive(bar(L::bVrEmpty + vr.idx));
+                vr.next(L::nVr);
                 v16.next(L::NV16);
             }
         }
