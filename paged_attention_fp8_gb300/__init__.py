@@ -316,6 +316,10 @@ def pafp8_plan_create(desc: plan_desc, kv_indptr, last_page_len, qo_indptr=None)
 
 def pafp8_plan_create_window(desc: plan_desc, window: int, sinks: int, kv_indptr, last_page_len, qo_indptr=None) -> int:
     """pafp8_plan_create with a sliding window and attention sinks (see include/pafp8.h)."""
+    for n, x in (("window", window), ("sinks", sinks)):
+        if x != int(x) or not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{n} {x} is not a 32-bit integer")
+    window, sinks = int(window), int(sinks)
     kv_indptr, last_page_len, qo_indptr = _i32_host(kv_indptr), _i32_host(last_page_len), _i32_host(qo_indptr)
     out = ctypes.c_void_p()
     _check(lib().pafp8_plan_create_window(ctypes.byref(desc), window, sinks, _ptr(kv_indptr), _ptr(last_page_len),
@@ -688,8 +692,8 @@ def _cache_shape(k_cache, v_cache, hkv, d, layout, kv_layout, dev):
 
 def _block_scales(t, name, shape, dev) -> int:
     """The address of a contiguous float32 tensor of `shape`: pages, blocks of 16 tokens, KV heads."""
-    if t.shape != shape:
-        raise ValueError(f"{name} {tuple(t.shape)} is not {shape} (pages, blocks of 16 tokens, KV heads)")
+    if t is None or t.shape != shape:
+        raise ValueError(f"{name} {t if t is None else tuple(t.shape)} is not {shape} (pages, blocks of 16 tokens, KV heads)")
     if t.get_device() != dev or t.dtype is not _T.float32 or not t.is_contiguous():
         _refuse(t, name, _T.float32, dev)
     return t.data_ptr()
@@ -826,7 +830,7 @@ class Plan:
             kv_layout=_LAYOUTS[kv_layout] if isinstance(kv_layout, str) else int(kv_layout))
         self.handle = None
         self.handle = pafp8_plan_create(self.desc, kv_indptr_h, last_page_len, qo_indptr) if not window and not sinks else \
-            pafp8_plan_create_window(self.desc, int(window), int(sinks), kv_indptr_h, last_page_len, qo_indptr)
+            pafp8_plan_create_window(self.desc, window, sinks, kv_indptr_h, last_page_len, qo_indptr)
 
     def __del__(self):
         if getattr(self, "handle", None):

@@ -27,6 +27,14 @@ def test_window_refusals(kw, match):
         plan(**kw)
 
 
+@pytest.mark.parametrize("kw", [dict(window=2 ** 31), dict(window=2 ** 32 + 5), dict(window=4, sinks=2 ** 32), dict(window=-2 ** 33),
+                                dict(window=0.5), dict(window=float("inf"))])
+def test_the_binding_does_not_wrap_or_cut_numbers(kw):
+    with pytest.raises((ValueError, OverflowError)):
+        plan(**kw)
+    plan(window=2 ** 31 - 1, sinks=2 ** 31 - 1)
+
+
 def test_window_length_limit():
     pages = (2 ** 31 - 1) // 16
     a = dict(mode="decode", num_qo_heads=1, num_kv_heads=1, num_pages=1, kv_indptr=[0, pages], last_page_len=[16], q_dtype="bf16",
@@ -150,7 +158,7 @@ def test_binding_refuses(call):
             (dict(lse=g["lse"].double()), "lse has dtype"), (dict(lse=g["lse"][:-1]), "do not fit"),
             (dict(k_cache=g["k_cache"][:-1]), "do not fit"), (dict(v_cache=g["v_cache"].view(torch.float8_e5m2)), "v_cache has dtype"),
             (dict(kv_indices=g["kv_indices"].long()), "kv_indices has dtype"), (dict(kv_indices=g["kv_indices"][:9]), "do not fit"),
-            (dict(k_scales=torch.ones(POOL, HKV)), "k_scales .* is not"), (dict(v_scales=torch.ones(POOL, 2, HKV)), "v_scales .* is not"),
+            (dict(k_scales=None), "k_scales None is not"), (dict(k_scales=torch.ones(POOL, HKV)), "k_scales .* is not"), (dict(v_scales=torch.ones(POOL, 2, HKV)), "v_scales .* is not"),
             (dict(k_scales=g["k_scales"].double()), "k_scales has dtype"), (dict(q=g["q"].transpose(0, 1)), "contiguous"),
             (dict(k_scales=torch.ones(POOL, 1, 2 * HKV)[..., ::2]), "contiguous")]:
         with pytest.raises(ValueError, match=match):
