@@ -315,12 +315,12 @@ cudaError_t launch_merge(const DecodeParams& p, int num_merge, int heads_per_cta
 // writes full output tiles with bulk tensor stores through it).  One
 // translation unit per head size (prefill_d128.cu, prefill_d64.cu).
 // Whether a prefill plan's items are those of CTA pairs: a 2-byte cache at
-// head_dim 128, with a window of 768 keys or more if it has one.  (A prompt of
-// 16384 tokens, 32 / 8 heads: window 1000 290 us on pairs and 308 on single
-// CTAs, 700 248 and 245, 500 219 and 194, 300 167 and 142: short windows mean
+// head_dim 128, with a window of 896 keys or more if it has one.  (A prompt of
+// 16384 tokens, 32 / 8 heads: window 1000 288 us on pairs and 301 on single
+// CTAs, 700 248 and 232, 500 219 and 189, 300 167 and 142: short windows mean
 // many items of a few tiles, and a pair's item covers twice the tokens, so more
 // of its tiles lie outside each row's window.)
-constexpr int kPairWindow = 768;
+constexpr int kPairWindow = 896;
 inline bool prefill_pairs(int head_dim, int kv_dtype, int window) {
     return head_dim == kHeadDim && (kv_dtype == PAFP8_F16 || kv_dtype == PAFP8_BF16) &&
            (window == 0 || window >= kPairWindow);

@@ -38,7 +38,7 @@ def test_prefill_window(cuda_device, window, sinks, kw):
         run(lens, new, window=window, sinks=sinks, num_ctas=13, seed=window % 97 + sinks % 89, **kw)
 
 
-@pytest.mark.parametrize("window", [600, 767, 768, 900])
+@pytest.mark.parametrize("window", [600, 767, 895, 896, 900])
 @pytest.mark.parametrize("kv", ["bf16", "f16"])
 def test_prefill_window_on_pairs(cuda_device, window, kv):
     """A 2-byte cache at head_dim 128: windows on both sides of the rule that picks CTA pairs."""

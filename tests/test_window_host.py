@@ -70,7 +70,7 @@ def test_prefill_items_cover_what_their_rows_see(window, sinks, kv):
     lens, new = [700, 40, 300], [500, 40, 3]
     m = plan("prefill", lens, new, window=window, sinks=sinks, kv=kv).metadata()
     tiles = m[m[META["off_tile"]]:][:8 * m[META["num_tiles"]]].reshape(-1, 8)
-    span = 64 * (2 if kv == "bf16" and window >= 768 else 1)
+    span = 64 * (2 if kv == "bf16" and window >= 896 else 1)
     rows = {}
     for gap, hk, t0, nkv, qo0, qo_len, kv_len, page0 in tiles.tolist():
         b = [0, 500, 540].index(qo0)
