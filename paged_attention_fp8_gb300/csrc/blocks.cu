@@ -15,24 +15,26 @@
 //   code'  = fp8(RNE)(code * fp32(s_old / s)) for those tokens, if s > s_old.
 // A request's new tokens are contiguous, so one warp owns a block of K or V of
 // one head (of two heads of 64): no atomics, and the result is a function of the
-// inputs.  The warp keeps the block's 16 rows in registers between the maximum
-// and the conversion, so the source is read once.
+// inputs.  The warp keeps the block's 16 rows in shared memory (fp32 rows in
+// registers) between the maximum and the conversion, so the source is read once.
 //
 // Reading.  Rows out_indptr[b] .. out_indptr[b + 1] - 1 are tokens starts[b]
 // on of request b, as fp32(code) * scale rounded once to the output's type.
 //
 // Both are streams, bounded by HBM, and by launch and table lookups for a few
 // tokens.  Measured in a graph, inputs of three steps in turn: the append of 16
-// ragged prompts (8 heads of 128, bf16 to e4m3fn, 45.7 MB) 11.9 us, 57 % of the
-// measured copy rate: two waves of warps, each of which waits for its request
-// (32 probes of qo_indptr a step), lengths and page before its rows.  One
-// warp for K and V both (half the warps, twice the registers) takes 14.8 us; 80
-// registers (6 thread blocks of 4 warps an SM) 11.9, 64 registers with spills
-// 12.6, 96 12.8; conditions on every row of every block 13.4.  64 single tokens
-// take 4.0 us.  The read-back of 64 requests of 512-4096 tokens (891 MB) takes
-// 138 us, 95 % of the copy rate.
+// ragged prompts (8 heads of 128, bf16 to e4m3fn, 45.7 MB) 12.4 us, 54 % of the
+// measured copy rate, of 64 such prompts (206 MB) 36.3 us, 84 %: a warp waits for
+// its request (32 probes of qo_indptr a step), lengths and page before its rows,
+// which few calls are long enough to hide.  One warp for K and V both takes a
+// fourth longer; positions in 64 bits, whose divisions were a third of the
+// instructions, 43.2 us with 64 prompts where 32 bits took 41.9.  64 single
+// tokens take 4.0 us.  The read-back of 64 requests of 512-4096 tokens (891 MB)
+// takes 138 us, 95 % of the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "../../include/pafp8.h"
 #include "internal.h"
@@ -43,28 +45,27 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAppendThreads = 128;
-constexpr int kAppendBlocks = 6;  // thread blocks an SM, for 80 registers a thread (fp32 rows: 3, for 168)
+constexpr int kAppendBlocks = 8;  // thread blocks an SM, for 64 registers a thread (fp32 rows: 3, for 168)
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 // The request that owns row t, by one warp together: the last r with
 // indptr[r] <= t (32 probes a step; any r for a t outside the rows), and the
 // rows it starts and ends at.  Every index probed lies in (0, n), n >= 1.
 struct Owner {
-    int r;
-    long long begin, end;
+    int r, begin, end;
 };
-__device__ __forceinline__ Owner owner(const int32_t* indptr, int n, long long t) {
+__device__ __forceinline__ Owner owner(const int32_t* indptr, int n, int t) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = n, at_lo = __ldg(indptr), at_hi = __ldg(indptr + n);
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
-        const long long at = (long long)lo + (long long)(lane + 1) * step;
-        const int v = at < hi ? __ldg(indptr + at) : 0;
-        const uint32_t b = __ballot_sync(kAll, at < hi && v <= t);
+        const uint32_t at = (uint32_t)lo + (uint32_t)(lane + 1) * (uint32_t)step;
+        const int v = at < (uint32_t)hi ? __ldg(indptr + at) : 0;
+        const uint32_t b = __ballot_sync(kAll, at < (uint32_t)hi && v <= t);
         const int steps = b == kAll ? 32 : __ffs(~b) - 1;
         const int below = __shfl_sync(kAll, v, max(steps - 1, 0)), above = __shfl_sync(kAll, v, min(steps, 31));
         if (steps > 0) at_lo = below;
-        if (steps < 32 && (long long)lo + (long long)(steps + 1) * step < hi) at_hi = above;
+        if (steps < 32 && (uint32_t)lo + (uint32_t)(steps + 1) * (uint32_t)step < (uint32_t)hi) at_hi = above;
         lo += steps * step;
         hi = min(hi, lo + step);
     }
@@ -74,12 +75,12 @@ __device__ __forceinline__ Owner owner(const int32_t* indptr, int n, long long t
 // Where token `pos` of the request with page entries e0 .. e1 - 1 lies: its
 // page and the slot in it, or page -1 when the position or the page id is out
 // of range.
-__device__ __forceinline__ int page_of(const int32_t* kv_indices, int e0, int e1, long long pos, int page_size, int num_pages,
+__device__ __forceinline__ int page_of(const int32_t* kv_indices, int e0, int e1, uint32_t pos, int page_size, int num_pages,
                                        int& slot) {
-    if (pos < 0) return -1;
-    const long long e = e0 + pos / page_size;
-    slot = (int)(pos % page_size);
-    if (e0 < 0 || e >= e1) return -1;
+    const uint32_t at = pos / (uint32_t)page_size;  // (at most 2^28, so that e0 + at does not wrap)
+    slot = (int)(pos - at * (uint32_t)page_size);
+    const uint32_t e = (uint32_t)e0 + at;
+    if (e0 < 0 || e1 < 0 || e >= (uint32_t)e1) return -1;
     const int pg = __ldg(kv_indices + e);
     return pg >= 0 && pg < num_pages ? pg : -1;
 }
@@ -155,70 +156,114 @@ __device__ __forceinline__ float power_scale(uint32_t amax) {
 
 // A block's rows of K or V in one warp: lane l holds dims 8 (l % 16) .. + 7 (of
 // 128: one head of 128, or two of 64) of rows 2 i + l / 16.  Rows of earlier
-// tokens hold their 8 codes in the first two words, new rows their elements.
-// FULL: all 16 rows are new (nearly every block of a prompt), so that no row
-// needs a condition of its own.
+// tokens hold their 8 codes, new rows their elements.
+//
+// Rows of a 2-byte type go through shared memory by asynchronous copies, 16
+// bytes of which each lane writes and reads alone: 64 registers a thread, so 32
+// warps an SM with their rows in flight.  64 ragged prompts (8 heads of 128)
+// take 36.3 us where rows in registers (80 a thread, 24 warps) take 41.9, 512
+// single tokens 8.9 and 9.9, 16 prompts 12.4 and 11.8.  fp32 rows, twice the
+// bytes a lane, stay in registers: 15.9 us for 16 prompts against 23.5.
 constexpr int kRowsPerPass = 2, kPasses = kPageSize / kRowsPerPass;
 
+template <int SRC>
+struct InShared {
+    static constexpr int kBytes = kPasses * 512;  // of a warp
+    uint32_t buf;                                 // this lane's first 16 bytes
+    __device__ __forceinline__ void fetch(int i, const uint4* g) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(buf + i * 512), "l"(g) : "memory");
+    }
+    __device__ __forceinline__ void fetch_codes(int i, const uint2* g) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(buf + i * 512), "l"(g) : "memory");
+    }
+    __device__ __forceinline__ void clear(int i) { ptx::sts128(buf + i * 512, 0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+    __device__ __forceinline__ Raw8<SRC> row(int i) const { return Raw8<SRC>{{ptx::lds128(buf + i * 512)}}; }
+    __device__ __forceinline__ uint2 codes(int i) const { return ptx::lds64(buf + i * 512); }
+};
+
+template <int SRC>
+struct InRegisters {
+    static constexpr int kBytes = 0;
+    Raw8<SRC> raw[kPasses];
+    __device__ __forceinline__ void fetch(int i, const uint4* g) {
+#pragma unroll
+        for (int k = 0; k < Raw8<SRC>::kVecs; ++k) raw[i].v[k] = __ldcs(g + k);
+    }
+    __device__ __forceinline__ void fetch_codes(int i, const uint2* g) {
+        const uint2 c = *g;
+        raw[i].v[0].x = c.x;
+        raw[i].v[0].y = c.y;
+    }
+    __device__ __forceinline__ void clear(int i) { raw[i] = Raw8<SRC>{}; }
+    __device__ __forceinline__ void wait() {}
+    __device__ __forceinline__ Raw8<SRC> row(int i) const { return raw[i]; }
+    __device__ __forceinline__ uint2 codes(int i) const { return make_uint2(raw[i].v[0].x, raw[i].v[0].y); }
+};
+
+template <int SRC>
+using Rows = std::conditional_t<SRC == PAFP8_F32, InRegisters<SRC>, InShared<SRC>>;
+
+// FULL: all 16 rows are new (nearly every block of a prompt), so that no row
+// needs a condition of its own.
 template <int SRC, bool FULL>
-__device__ __forceinline__ void load_rows(Raw8<SRC> (&raw)[kPasses], const uint8_t* src, size_t stride, int s0, int m) {
+__device__ __forceinline__ void load_rows(Rows<SRC>& rows, const uint8_t* src, size_t stride, int s0, int m) {
     const int sub = (threadIdx.x & 31) / 16;
     const uint8_t* row = src + (ptrdiff_t)(sub - s0) * (ptrdiff_t)stride;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i, row += kRowsPerPass * stride) {
         const int s = i * kRowsPerPass + sub - s0;
-        if (!FULL) {
-#pragma unroll
-            for (int k = 0; k < Raw8<SRC>::kVecs; ++k) raw[i].v[k] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (FULL || (s >= 0 && s < m)) {
-            const uint4* g = reinterpret_cast<const uint4*>(row);
-#pragma unroll
-            for (int k = 0; k < Raw8<SRC>::kVecs; ++k) raw[i].v[k] = __ldcs(g + k);
-        }
+        if (FULL || (s >= 0 && s < m)) rows.fetch(i, reinterpret_cast<const uint4*>(row));
+        else rows.clear(i);
     }
 }
 
 template <int SRC>
-__device__ __forceinline__ void load_codes(Raw8<SRC> (&raw)[kPasses], const uint8_t* dst, size_t row_bytes, int s0) {
+__device__ __forceinline__ void load_codes(Rows<SRC>& rows, const uint8_t* dst, size_t row_bytes, int s0) {
     const int sub = (threadIdx.x & 31) / 16;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int at = i * kRowsPerPass + sub;
-        if (at < s0) {
-            const uint2 c = *reinterpret_cast<const uint2*>(dst + at * row_bytes);
-            raw[i].v[0].x = c.x;
-            raw[i].v[0].y = c.y;
-        }
+        if (at < s0) rows.fetch_codes(i, reinterpret_cast<const uint2*>(dst + at * row_bytes));
     }
 }
 
 // The bits (as fp32) of this lane's largest finite magnitude among the new rows.
 template <int SRC, bool FULL>
-__device__ __forceinline__ uint32_t largest(const Raw8<SRC> (&raw)[kPasses], int s0) {
+__device__ __forceinline__ uint32_t largest(const Rows<SRC>& rows, int s0) {
     const int sub = (threadIdx.x & 31) / 16;
-    // Magnitudes order like their bits; a 2-byte type's two to a word.
-    constexpr uint32_t kMag = SRC == PAFP8_F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
     constexpr uint32_t kInf = SRC == PAFP8_F32 ? 0x7F800000u : SRC == PAFP8_BF16 ? 0x7F80u : 0x7C00u;
-    auto fold = [](uint32_t m) { return SRC == PAFP8_F32 ? m : max(m & 0xFFFFu, m >> 16); };
-    uint32_t top = 0;
+    uint32_t top = 0;  // (the maximum of a number and a NaN is the number)
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        const uint32_t keep = FULL || i * kRowsPerPass + sub >= s0 ? kMag : 0u;
+        const Raw8<SRC> raw = rows.row(i);
 #pragma unroll
         for (int k = 0; k < Raw8<SRC>::kVecs; ++k) {
-            const uint32_t w[4] = {raw[i].v[k].x, raw[i].v[k].y, raw[i].v[k].z, raw[i].v[k].w};
+            const uint32_t w[4] = {raw.v[k].x, raw.v[k].y, raw.v[k].z, raw.v[k].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = SRC == PAFP8_F32 ? max(top, w[j] & keep) : __vmaxu2(top, w[j] & keep);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = FULL || i * kRowsPerPass + sub >= s0 ? w[j] : 0u;
+                if constexpr (SRC == PAFP8_F32) {
+                    top = __float_as_uint(fmaxf(__uint_as_float(top), fabsf(__uint_as_float(x))));
+                } else if constexpr (SRC == PAFP8_BF16) {
+                    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top),
+                                                     __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x)));
+                    top = *reinterpret_cast<const uint32_t*>(&r);
+                } else {
+                    const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&top), __habs2(*reinterpret_cast<const __half2*>(&x)));
+                    top = *reinterpret_cast<const uint32_t*>(&r);
+                }
+            }
         }
     }
-    uint32_t best = fold(top);
-    if (best >= kInf) {  // infinities and NaN do not count: once more without them
+    uint32_t best = SRC == PAFP8_F32 ? top : max(top & 0xFFFFu, top >> 16);
+    if (best >= kInf) {  // infinities do not count: once more without them
         best = 0;
-#pragma unroll
+        constexpr int kUnroll = SRC == PAFP8_F32 ? kPasses : 1;  // (rows in registers need constant indices)
+#pragma unroll kUnroll
         for (int i = 0; i < kPasses; ++i) {
             float x[8];
-            to_float8<SRC>(raw[i], x);
+            to_float8<SRC>(rows.row(i), x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const uint32_t a = __float_as_uint(x[k]) & 0x7FFFFFFFu;
@@ -232,13 +277,14 @@ __device__ __forceinline__ uint32_t largest(const Raw8<SRC> (&raw)[kPasses], int
     else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)best)));
 }
 
-// Scale, earlier codes and new codes of the block whose rows are in `raw` (new
+// Scale, earlier codes and new codes of the block whose rows are loaded (new
 // ones: slots s0 .. s0 + m - 1).  dst: this lane's dims of the block's first row.
 template <int SRC, int KV, int DH, bool FULL>
-__device__ __forceinline__ void write_rows(const Raw8<SRC> (&raw)[kPasses], uint8_t* dst, size_t row_bytes, float* scale,
+__device__ __forceinline__ void write_rows(Rows<SRC>& rows, uint8_t* dst, size_t row_bytes, float* scale,
                                            float old, int s0, int m, bool active) {
     const int lane = threadIdx.x & 31, sub = lane / 16;
-    uint32_t amax = largest<SRC, FULL>(raw, s0);
+    rows.wait();
+    uint32_t amax = largest<SRC, FULL>(rows, s0);
     if constexpr (DH == 128) {
         amax = __reduce_max_sync(kAll, amax);
     } else {  // lanes l and l ^ 8 hold different heads
@@ -256,7 +302,7 @@ __device__ __forceinline__ void write_rows(const Raw8<SRC> (&raw)[kPasses], uint
             const int at = i * kRowsPerPass + sub;
             if (at < s0) {
                 float x[8];
-                values8<KV>(make_uint2(raw[i].v[0].x, raw[i].v[0].y), x);
+                values8<KV>(rows.codes(i), x);
                 *reinterpret_cast<uint2*>(dst + at * row_bytes) = codes8<KV>(x, ratio);
             }
         }
@@ -268,7 +314,7 @@ __device__ __forceinline__ void write_rows(const Raw8<SRC> (&raw)[kPasses], uint
         const int at = i * kRowsPerPass + sub;
         if (FULL || (at >= s0 && at < s0 + m)) {
             float x[8];
-            to_float8<SRC>(raw[i], x);
+            to_float8<SRC>(rows.row(i), x);
             *reinterpret_cast<uint2*>(row) = codes8<KV>(x, inv);
         }
     }
@@ -285,23 +331,30 @@ __global__ void __launch_bounds__(kAppendThreads, SRC == PAFP8_F32 ? 3 : kAppend
     constexpr int ESZ = SRC == PAFP8_F32 ? 4 : 2;
     const int lane = threadIdx.x & 31;
     const int col = 8 * (lane & 15);
+    Rows<SRC> rows_of;
+    if constexpr (SRC != PAFP8_F32) {
+        __shared__ __align__(16) uint8_t held[kAppendThreads / 32][Rows<SRC>::kBytes];
+        rows_of.buf = ptx::smem_addr(held[threadIdx.x >> 5]) + lane * 16;
+    }
     const int head_groups = (p.num_kv_heads + HPW - 1) / HPW;
-    const long long u = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
-    const long long group = u / (2 * head_groups);
-    const int part = (int)(u - group * (2 * head_groups));
+    const uint32_t u = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t group = u / (uint32_t)(2 * head_groups);
+    const int part = (int)(u - group * (uint32_t)(2 * head_groups));
     const bool is_v = part >= head_groups;
     const int h = (is_v ? part - head_groups : part) * HPW + col / DH;  // this lane's head
     const bool active = h < p.num_kv_heads;
-    long long t = group * p.span;
-    if (t >= p.nnz || p.batch == 0) return;
-    const long long all = __ldg(p.qo_indptr + p.batch), first_row = __ldg(p.qo_indptr);
-    const Owner who = owner(p.qo_indptr, p.batch, max(t, first_row));
-    const long long rows = min(p.nnz, all);
-    if (all > p.nnz && u == 0 && lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
-    const long long t_end = min(t + p.span, rows);
+    // Rows are below 2^31, so that sums of two of them fit 32 unsigned bits.
+    const uint32_t nnz = (uint32_t)p.nnz;
+    uint32_t t = group * (uint32_t)p.span;
+    if (t >= nnz || p.batch == 0) return;
+    const uint32_t all = (uint32_t)max(0, __ldg(p.qo_indptr + p.batch)), first_row = (uint32_t)max(0, __ldg(p.qo_indptr));
+    const Owner who = owner(p.qo_indptr, p.batch, (int)max(t, first_row));
+    const uint32_t rows = min(nnz, all);
+    if (all > nnz && u == 0 && lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
+    const uint32_t t_end = min(t + (uint32_t)p.span, rows);
     t = max(t, first_row);
     int r = who.r;
-    long long r0 = who.begin, r1 = min(who.end, rows);
+    uint32_t r0 = (uint32_t)max(0, who.begin), r1 = min((uint32_t)max(0, who.end), rows);
     const uint8_t* const src = static_cast<const uint8_t*>(is_v ? p.v : p.k) + ((size_t)h * DH + col % DH) * ESZ;
     const size_t stride = (size_t)(is_v ? p.v_stride : p.k_stride) * ESZ;
     uint8_t* const cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache);
@@ -309,30 +362,30 @@ __global__ void __launch_bounds__(kAppendThreads, SRC == PAFP8_F32 ? 3 : kAppend
     while (t < t_end) {
         if (t >= r1) {  // (requests without new tokens lie in between)
             if (++r >= p.batch) break;
-            r0 = __ldg(p.qo_indptr + r);
-            r1 = min((long long)__ldg(p.qo_indptr + r + 1), rows);
+            r0 = (uint32_t)max(0, __ldg(p.qo_indptr + r));
+            r1 = min((uint32_t)max(0, __ldg(p.qo_indptr + r + 1)), rows);
             continue;
         }
         const int cached = __ldg(p.cached_lens + r), e0 = __ldg(p.kv_indptr + r), e1 = __ldg(p.kv_indptr + r + 1);
-        const long long pos = (long long)cached + (t - r0);
+        const uint32_t pos = (uint32_t)cached + (t - r0);
         const int s0 = (int)(pos & (kPageSize - 1));
-        const int m = (int)min((long long)(kPageSize - s0), r1 - t);
+        const int m = (int)min((uint32_t)(kPageSize - s0), r1 - t);
         if (s0 != 0 && t != r0) {  // the block belongs to an earlier token's warp
             t += m;
             continue;
         }
-        Raw8<SRC> raw[kPasses];
         const uint8_t* const from = src + (size_t)t * stride;
         // (two heads of 64 a warp: the last warp of an odd count has one)
         const bool full = m == kPageSize && (DH == 128 || __all_sync(kAll, active));
         if (full)
-            load_rows<SRC, true>(raw, from, stride, 0, kPageSize);
+            load_rows<SRC, true>(rows_of, from, stride, 0, kPageSize);
         else
-            load_rows<SRC, false>(raw, from, stride, s0, active ? m : 0);
+            load_rows<SRC, false>(rows_of, from, stride, s0, active ? m : 0);
         int slot = 0;
         const int page = cached < 0 ? -1 : page_of(p.kv_indices, e0, e1, pos, p.page_size, p.num_pages, slot);
         t += m;
         if (page < 0) {
+            rows_of.wait();
             if (lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
             continue;
         }
@@ -344,25 +397,32 @@ __global__ void __launch_bounds__(kAppendThreads, SRC == PAFP8_F32 ? 3 : kAppend
         float old = 0.f;
         if (s0 != 0) {
             old = *scale;
-            if (active) load_codes<SRC>(raw, dst, row_bytes, s0);
+            if (active) load_codes<SRC>(rows_of, dst, row_bytes, s0);
         }
         if (full)
-            write_rows<SRC, KV, DH, true>(raw, dst, row_bytes, scale, 0.f, 0, kPageSize, true);
+            write_rows<SRC, KV, DH, true>(rows_of, dst, row_bytes, scale, 0.f, 0, kPageSize, true);
         else
-            write_rows<SRC, KV, DH, false>(raw, dst, row_bytes, scale, old, s0, m, active);
+            write_rows<SRC, KV, DH, false>(rows_of, dst, row_bytes, scale, old, s0, m, active);
     }
 }
 
+// A warp looks through `span` new tokens for its blocks: 16, which in a prompt
+// hold one or two, or fewer where requests have fewer tokens each or where the
+// call is so short that twice the warps are still resident at once (24 of them
+// an SM), so that a decode step's requests go to a warp each rather than 16 to
+// one in turn.  (64 requests of 1-8 tokens 5.6 us, 16 tokens a warp 11.5; 256 of
+// 4 tokens 7.1 and 11.4; one of 100 3.8 and 4.4.)
+constexpr long long kSpanWarps = 152 * 24;
+
 template <int SRC, int KV, int DH>
 cudaError_t launch_append_t(BlockAppendParams p, cudaStream_t stream) {
-    // A warp looks through 16 tokens for its blocks, which in a prompt are one
-    // or two; up to four tokens a request it takes one token, so that a decode
-    // step's requests go to a warp each rather than 16 to one in turn.
-    p.span = p.nnz <= 4LL * p.batch ? 1 : kPageSize;
     constexpr int HPW = 128 / DH, W = kAppendThreads / 32;
-    const long long units = (p.nnz + p.span - 1) / p.span * (2LL * ((p.num_kv_heads + HPW - 1) / HPW));
+    const long long parts = 2LL * ((p.num_kv_heads + HPW - 1) / HPW);
+    p.span = kPageSize;
+    while (p.span > 1 && (p.nnz < (long long)p.span * p.batch || p.nnz * parts * 2 <= kSpanWarps * p.span)) p.span /= 2;
+    const long long units = (p.nnz + p.span - 1) / p.span * parts;
     const long long blocks = (units + W - 1) / W;
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (blocks > INT32_MAX / W) return cudaErrorInvalidConfiguration;
     append_blocks_kernel<SRC, KV, DH><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
@@ -400,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
         const int lane = threadIdx.x;
         const long long low = __ldg(p.out_indptr);
         const long long base = max(t0, low);
-        const int r0 = base < rows ? owner(p.out_indptr, p.batch, base).r : 0;
+        const int r0 = base < rows ? owner(p.out_indptr, p.batch, (int)base).r : 0;
         const long long t = t0 + lane;
         if (lane < p.tile) {
             long long row = -1, scale = 0;
@@ -410,9 +470,10 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
                 int slot = 0;
                 const int start = __ldg(p.starts + r);
                 const long long pos = (long long)start + (t - __ldg(p.out_indptr + r));
-                const int page = start < 0 ? -1
-                                           : page_of(p.kv_indices, __ldg(p.kv_indptr + r), __ldg(p.kv_indptr + r + 1), pos,
-                                                     p.page_size, p.num_pages, slot);
+                const int page = start < 0 || pos > 0xFFFFFFFFLL
+                                     ? -1
+                                     : page_of(p.kv_indices, __ldg(p.kv_indptr + r), __ldg(p.kv_indptr + r + 1), (uint32_t)pos,
+                                               p.page_size, p.num_pages, slot);
                 if (page >= 0) {
                     row = p.hnd ? ((long long)page * p.num_kv_heads * p.page_size + slot) * DH
                                 : ((long long)page * p.page_size + slot) * p.num_kv_heads * DH;

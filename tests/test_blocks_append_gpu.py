@@ -69,6 +69,20 @@ def test_one_step(cuda_device, cached, new, heads, d, fmt, layout, page_size, sr
     s.check()
 
 
+@pytest.mark.parametrize("batch,low,high", [(40, 1, 8), (300, 1, 3), (300, 4, 7), (300, 8, 15), (120, 16, 40)])
+@pytest.mark.parametrize("src", ["bf16", "f32"])
+def test_many_requests(cuda_device, batch, low, high, src):
+    """Requests of like lengths: a warp looks through 1, 2, 4, 8 or 16 tokens, with borders of requests and blocks anywhere in them."""
+    gen = np.random.default_rng(batch + high)
+    cached, new = gen.integers(0, 50, batch), gen.integers(low, high + 1, batch)
+    s = Setup(cached + new, heads=4, seed=high)
+    qo = np.concatenate([[0], np.cumsum(new)])
+    k, v = s.rows(int(qo[-1]), src)
+    s.append(k, v, ints(qo), ints(cached))
+    s.expect(k, v, qo, cached)
+    s.check()
+
+
 @pytest.mark.parametrize("fmt,layout", [("e4m3fn", "NHD"), ("e5m2", "HND")])
 def test_token_by_token_while_values_grow_and_shrink(cuda_device, fmt, layout):
     """Forty steps of one token: a block's scale follows its largest value, its earlier codes are written anew."""
