@@ -62,12 +62,12 @@ L2_FLUSH_BYTES = 256 << 20
 # workload, from one ncu capture of the kernel source with this SHA-256; a
 # changed kernel reports null until it is captured again.
 NCU_TRAFFIC = {
-    "8c94b805d7f854b2a685a89adaf643807277c06c16f5fca2b27cb39f45c3fc53": 309745408,
+    "f0621be6840a37ca4f69ce546c54658ff2f27b2666869c9fbf93c44b3ad230b1": 309449984,
 }
 # The same for the prefill kernels, per workload index, keyed by the SHA-256
 # of their sources (prefill.cuh, then prefill_pair.cuh).
 NCU_TRAFFIC_PREFILL = {
-    "8a8b8f6abc782551a2f5f796339847147b0b8e84b8d94dfafe4ad22d16bf1a66": {4: 168300544, 5: 190012928, 7: 259149824},
+    "13e796694e6f1c2d5d497947a4371033f883bb701b6790feb69dc203f76c97a3": {4: 168334848, 5: 186891520, 7: 256020992},
 }
 
 
@@ -849,7 +849,7 @@ def run_ours(args):
 
     peak, peak_kind = measured_peaks()
     achieved = nbytes / (ms_dec * 1e-3) / 1e9
-    traffic = NCU_TRAFFIC.get(kernel_sha("decode.cu"))
+    traffic = NCU_TRAFFIC.get(kernel_sha("decode.cuh"))
     value = world * nbytes / (ms_step * 1e-3) / 1e9
     step_roof = {"bound": "hbm", "achieved": round(nbytes / (ms_step * 1e-3) / 1e9, 1), "peak": peak,
                  "unit": "GB/s", "frac": round(nbytes / (ms_step * 1e-3) / 1e9 / peak, 4)}
