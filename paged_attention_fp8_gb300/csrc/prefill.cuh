@@ -68,11 +68,12 @@
 // their own first one, and a row whose tiles so far showed it nothing keeps its
 // maximum at -inf, so that its first visible key sets it.  A prompt of 16384
 // tokens under a window of 1024 with 4 sinks (276 GFLOP in visible pairs) takes
-// 312 us: 885 TFLOP/s, 45 % of the measured rate, where the plain kernel reaches
-// 52 %; an item's 9 tiles hold 1152 keys for each row's 1028, at the plain
-// kernel's time a tile (2.35 us) and 1.8 us an item.  Leaving out the softmax of
-// the columns that no row of a warp sees gained nothing there (314) and cost
-// block scales a fifth.
+// 304 us: 908 TFLOP/s, 46 % of the measured rate, where the plain kernel reaches
+// 53 %.  A CTA has 13 or 14 items of 9 tiles (1152 keys for each row's 1028), about
+// 3700 cycles a tile and, between an item's last P and the next item's first S,
+// 10,000 with Q's arrival and fit, the output and the first QK.  Leaving out the
+// softmax of the columns that no row of a warp sees gained nothing (314 against
+// the 312 of that time) and cost block scales a fifth.
 // Block scales: with s = ks_c q.k (ks_c the K scale of 16-key block c, folded
 // with the softmax scale) and vs_c the block's V scale, P' = 2^(s + log2 vs_c -
 // m) and m the running maximum of s + log2 vs_c: the V scale rides in the
@@ -177,6 +178,13 @@ static_assert(1024 + Layout<false, false, 128, kVarBlocks>::bytes <= 232448 &&
 static_assert(Layout<true, false, 64>::kr % 1024 == 0 && Layout<true, false, 64>::v16 % 1024 == 0 &&
                   Layout<false, false, 64>::v16 % 1024 == 0 && Layout<false, true, 64>::v16 % 1024 == 0,
               "1024-byte alignment of the D 64 tiles");
+
+// The larger magnitude of two bf16 pairs, each half by itself.
+__device__ __forceinline__ uint32_t max_abs_bf162(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 struct Ring {
     int idx = 0;
@@ -752,33 +760,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             qphase ^= 1u;
             if (!ok) return up;
             if (r < TQ * g) {
+                // The row stays in registers between its maximum and its conversion;
+                // block scales, short of registers, read it twice (with the row held
+                // they take 265 us in place of 242, with packed maxima 247).
+                constexpr bool kHold = VAR != kVarBlocks;
+                constexpr int kTurns = kHold ? 8 * NH : 4;
                 const uint32_t qrow = base + L::q + x * L::kQTile + r * 128;
+                auto at = [&](int c) { return qrow + (c >> 3) * kHalfTile + (((c & 7) ^ (r & 7)) << 4); };
+                uint4 held[kHold ? 8 * NH : 1];
+                [[maybe_unused]] uint32_t top[4] = {};  // pairs of bf16 magnitudes (a NaN beside a number does not count)
                 uint32_t mx = 0;
 #pragma unroll
                 for (int c = 0; c < 8 * NH; ++c) {
-                    const uint4 w = lds128(qrow + (c >> 3) * kHalfTile + (((c & 7) ^ (r & 7)) << 4));
+                    const uint4 w = lds128(at(c));
+                    if constexpr (kHold) held[c] = w;
                     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        mx = max(mx, (ws[k] & 0x7FFFu) << 16);
-                        mx = max(mx, ws[k] & 0x7FFF0000u);
+                        if constexpr (kHold) {
+                            top[k] = max_abs_bf162(top[k], ws[k]);
+                        } else {
+                            mx = max(mx, (ws[k] & 0x7FFFu) << 16);
+                            mx = max(mx, ws[k] & 0x7FFF0000u);
+                        }
                     }
+                }
+                if constexpr (kHold) {
+                    top[0] = max_abs_bf162(max_abs_bf162(top[0], top[1]), max_abs_bf162(top[2], top[3]));
+                    mx = max(top[0] << 16, top[0] & 0xFFFF0000u);
                 }
                 const int ex = (int)((mx >> 23) & 0xFF) - 127;
                 const int shift = ex > 14 ? ex - 14 : 0;
                 const float down = __int_as_float((127 - shift) << 23);
                 up = __int_as_float((127 + shift) << 23);
-#pragma unroll 4
+#pragma unroll kTurns
                 for (int c = 0; c < 8 * NH; ++c) {
-                    const uint32_t a = qrow + (c >> 3) * kHalfTile + (((c & 7) ^ (r & 7)) << 4);
-                    const uint4 w = lds128(a);
+                    uint4 w;
+                    if constexpr (kHold) w = held[c];
+                    else w = lds128(at(c));
                     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
                     uint32_t o4[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         o4[k] = pack_half2(__uint_as_float(ws[k] << 16) * down,
                                            __uint_as_float(ws[k] & 0xFFFF0000u) * down);
-                    sts128(a, o4[0], o4[1], o4[2], o4[3]);
+                    sts128(at(c), o4[0], o4[1], o4[2], o4[3]);
                 }
                 fence_async_smem();
             }
