@@ -68,12 +68,13 @@
 // their own first one, and a row whose tiles so far showed it nothing keeps its
 // maximum at -inf, so that its first visible key sets it.  A prompt of 16384
 // tokens under a window of 1024 with 4 sinks (276 GFLOP in visible pairs) takes
-// 304 us: 908 TFLOP/s, 46 % of the measured rate, where the plain kernel reaches
-// 53 %.  A CTA has 13 or 14 items of 9 tiles (1152 keys for each row's 1028), about
-// 3700 cycles a tile and, between an item's last P and the next item's first S,
-// 10,000 with Q's arrival and fit, the output and the first QK.  Leaving out the
-// softmax of the columns that no row of a warp sees gained nothing (314 against
-// the 312 of that time) and cost block scales a fifth.
+// 299 us: 923 TFLOP/s, 47 % of the measured rate, where the plain kernel reaches
+// 53 % (and this one 64 % under a window of 4000).  A CTA has 13 or 14 items of 9
+// tiles (1152 keys for each row's 1028), about 3700 cycles a tile; between an item's
+// last P and the next item's first S passed 10,000 with Q's arrival and fit, the
+// output and the first QK.  Leaving out the softmax of the columns that no row of a
+// warp sees gained nothing (314 us against the 312 of that time) and cost block
+// scales a fifth.
 // Block scales: with s = ks_c q.k (ks_c the K scale of 16-key block c, folded
 // with the softmax scale) and vs_c the block's V scale, P' = 2^(s + log2 vs_c -
 // m) and m the running maximum of s + log2 vs_c: the V scale rides in the
@@ -87,6 +88,8 @@
 // scale arithmetic the kernel's structure takes 222.  What it costs most are
 // registers: at 192 a softmax thread 285 us, at 200 262, at 208 242.
 #pragma once
+#include <type_traits>
+
 #include "../../include/pafp8.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -186,6 +189,13 @@ __device__ __forceinline__ uint32_t max_abs_bf162(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// f16x2 of fp8 values as bf16x2: exact, since an fp8 value has 4 significant bits
+// and an exponent that both types hold.
+__device__ __forceinline__ uint32_t half2_to_bf162(uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_bf162(f.x, f.y);
+}
+
 struct Ring {
     int idx = 0;
     uint32_t phase = 0;
@@ -279,7 +289,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kBF = KT == PAFP8_BF16;                    // bf16 MMA operands
     // A bf16 query on an fp8 cache is brought into f16 range (per row, by the
     // softmax warps) before the QK MMAs; every other path multiplies Q as loaded.
-    const bool fit_q = !kF8 && !k2 && p.q_dtype == PAFP8_BF16;
+    // Under a window K is widened to bf16 for it instead, exactly too: a hundred
+    // cycles a tile in the dequant warps, but no fit between two items, of which a
+    // window makes many short ones.  (A prompt of 16384 tokens: window 300 150 us
+    // against 160, 1024 299 and 305, 1536 399 and 400, 2048 498 and 494, 4000 835
+    // and 816; a rule between the two costs both ways 1 %.  Block scales, whose
+    // dequant warps have fewer registers, take 254 us so and 242 with the fit.)
+    const bool wide_k = VAR == kVarWindow && !kF8 && !k2 && p.q_dtype == PAFP8_BF16;
+    const bool fit_q = VAR != kVarWindow && !kF8 && !k2 && p.q_dtype == PAFP8_BF16;
+    const bool bf_qk = kBF || wide_k;  // QK of bf16 operands
     using L = Layout<kF8, k2, DH, VAR>;
     using Dm = Dims<DH>;
     constexpr int NH = Dm::NH;
@@ -496,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const uint32_t idesc_qk =
                 kF8 ? make_idesc(p.q_dtype == PAFP8_E5M2 ? 1 : 0, KT == PAFP8_E5M2 ? 1 : 0, 128, 128)
-                    : make_idesc(kBF ? 1 : 0, kBF ? 1 : 0, 128, 128);
+                    : make_idesc(bf_qk ? 1 : 0, bf_qk ? 1 : 0, 128, 128);
             const uint32_t idesc_pv = make_idesc_bmn(kBF ? 1 : 0, kBF ? 1 : 0, 128, DH);
             const int nk = kF8 ? L::NKR : L::NK16;
             const int kfull = kF8 ? L::bKrFull : L::bK16Full;
@@ -658,7 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // `valid` and beyond zeroed.  K serves as the K-major B operand of Q K^T,
         // V as the MN-major B operand of P V.
         // (Under a window so are keys hide .. show - 1 of a V tile.)
-        auto widen = [&](uint32_t src, uint32_t dst, int valid, int hide, int show) {
+        auto widen_as = [&](auto bf, uint32_t src, uint32_t dst, int valid, int hide, int show) {
+            constexpr bool kToBf = decltype(bf)::value;
+            auto lo = [](uint32_t w) { return kToBf ? half2_to_bf162(fp8x2_lo<KT>(w)) : fp8x2_lo<KT>(w); };
+            auto hi = [](uint32_t w) { return kToBf ? half2_to_bf162(fp8x2_hi<KT>(w)) : fp8x2_hi<KT>(w); };
             auto gone = [&](int row) { return row >= valid || (VAR != kVarPlain && row >= hide && row < show); };
             if constexpr (k2) {
                 return;  // a 2-byte cache has no fp8 tile
@@ -671,10 +692,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 w = lds128(src + row * 128 + ((c ^ e) << 4));
                     if (gone(row)) w = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t hb = dst + (c >> 2) * kHalfTile + row * 128;
-                    sts128(hb + (((2 * q8) ^ e) << 4), fp8x2_lo<KT>(w.x), fp8x2_hi<KT>(w.x), fp8x2_lo<KT>(w.y),
-                           fp8x2_hi<KT>(w.y));
-                    sts128(hb + (((2 * q8 + 1) ^ e) << 4), fp8x2_lo<KT>(w.z), fp8x2_hi<KT>(w.z), fp8x2_lo<KT>(w.w),
-                           fp8x2_hi<KT>(w.w));
+                    sts128(hb + (((2 * q8) ^ e) << 4), lo(w.x), hi(w.x), lo(w.y),
+                           hi(w.y));
+                    sts128(hb + (((2 * q8 + 1) ^ e) << 4), lo(w.z), hi(w.z), lo(w.w),
+                           hi(w.w));
                 }
             } else {
                 // 64-B fp8 rows under the 64-byte swizzle (16-byte chunk c of
@@ -685,12 +706,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 w = lds128(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
                     if (gone(row)) w = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t hb = dst + row * 128;
-                    sts128(hb + (((2 * c) ^ e) << 4), fp8x2_lo<KT>(w.x), fp8x2_hi<KT>(w.x), fp8x2_lo<KT>(w.y),
-                           fp8x2_hi<KT>(w.y));
-                    sts128(hb + (((2 * c + 1) ^ e) << 4), fp8x2_lo<KT>(w.z), fp8x2_hi<KT>(w.z), fp8x2_lo<KT>(w.w),
-                           fp8x2_hi<KT>(w.w));
+                    sts128(hb + (((2 * c) ^ e) << 4), lo(w.x), hi(w.x), lo(w.y),
+                           hi(w.y));
+                    sts128(hb + (((2 * c + 1) ^ e) << 4), lo(w.z), hi(w.z), lo(w.w),
+                           hi(w.w));
                 }
             }
+        };
+        auto widen = [&](uint32_t src, uint32_t dst, int valid, int hide, int show) {
+            widen_as(std::false_type{}, src, dst, valid, hide, show);
         };
         for (int rnd = 0, t = blockIdx.x; t < n_items && ok; t = item_at(++rnd, blockIdx.x, gridDim.x)) {
             const Item it = load_item(items, t);
@@ -705,7 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = wait_or_abort<kDiag>(bar(L::bKrFull + kr.idx), kr.phase, flag_addr, p.status, p.wait_cycles) &&
                          wait_or_abort<kDiag>(bar(L::bK16Empty + k16.idx), k16.phase ^ 1u, flag_addr, p.status, p.wait_cycles);
                     if (!ok) break;
-                    widen(base + L::kr + kr.idx * Dm::kRawTile, base + L::k16 + k16.idx * Dm::kF16Tile, kTileKeys, 0, 0);
+                    const uint32_t from = base + L::kr + kr.idx * Dm::kRawTile, to = base + L::k16 + k16.idx * Dm::kF16Tile;
+                    if (wide_k) widen_as(std::true_type{}, from, to, kTileKeys, 0, 0);
+                    else widen(from, to, kTileKeys, 0, 0);
                     fence_async_smem();
                     mbar_arrive(bar(L::bK16Full + k16.idx));
                     mbar_arrive(bar(L::bKrEmpty + kr.idx));
@@ -760,8 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             qphase ^= 1u;
             if (!ok) return up;
             if (r < TQ * g) {
-                // The row stays in registers between its maximum and its conversion;
-                // block scales, short of registers, read it twice (with the row held
+                // The row stays in registers between its maximum and its conversion
+                // (209 us for the ragged prefill in place of 213); block scales, short of registers, read it twice (with the row held
                 // they take 265 us in place of 242, with packed maxima 247).
                 constexpr bool kHold = VAR != kVarBlocks;
                 constexpr int kTurns = kHold ? 8 * NH : 4;

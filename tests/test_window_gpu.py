@@ -38,6 +38,19 @@ def test_prefill_window(cuda_device, window, sinks, kw):
         run(lens, new, window=window, sinks=sinks, num_ctas=13, seed=window % 97 + sinks % 89, **kw)
 
 
+@pytest.mark.parametrize("window", [100, 1600, 0])
+@pytest.mark.parametrize("kv,d,scales", [("e4m3fn", 128, "tensor"), ("e5m2", 64, "head"), ("e5m2", 128, "block")])
+def test_bf16_queries_beyond_f16(cuda_device, window, kv, d, scales):
+    """Rows of 2^18 and of 2^-20 times the others, under windows and without one."""
+    b = Batch([2000, 129], [300, 129], window=window, sinks=4 if window else 0, q="bf16", kv=kv, d=d, scales=scales, num_ctas=13)
+    b.q[::3] *= 2.0 ** 18
+    b.q[1::3] *= 2.0 ** -20
+    b.upload()
+    b.run()
+    b.plan.device_status(b.ws)
+    b.check()
+
+
 @pytest.mark.parametrize("window", [600, 767, 895, 896, 900])
 @pytest.mark.parametrize("kv", ["bf16", "f16"])
 def test_prefill_window_on_pairs(cuda_device, window, kv):
