@@ -67,7 +67,7 @@ NCU_TRAFFIC = {
 # The same for the prefill kernels, per workload index, keyed by the SHA-256
 # of their sources (prefill.cuh, then prefill_pair.cuh).
 NCU_TRAFFIC_PREFILL = {
-    "13e796694e6f1c2d5d497947a4371033f883bb701b6790feb69dc203f76c97a3": {4: 168334848, 5: 186891520, 7: 256020992},
+    "4b29834ed63f74be032a391979b987fa86b726940b9dad160293a91a9390856c": {4: 168413696, 5: 186634496, 7: 250971136},
 }
 
 
