@@ -213,8 +213,9 @@ __device__ __forceinline__ void load_rows(Rows<SRC>& rows, const uint8_t* src, s
 #pragma unroll
     for (int i = 0; i < kPasses; ++i, row += kRowsPerPass * stride) {
         const int s = i * kRowsPerPass + sub - s0;
+        // (Rows of earlier tokens are read as codes alone, which load_codes brings.)
         if (FULL || (s >= 0 && s < m)) rows.fetch(i, reinterpret_cast<const uint4*>(row));
-        else rows.clear(i);
+        else if (s >= m || Rows<SRC>::kBytes == 0) rows.clear(i);
     }
 }
 
