@@ -83,10 +83,10 @@
 // vs_c is the softmax's sum.  Warp 14, idle otherwise, looks the scales up four
 // tiles at a time and hands them over through a ring of kScaleSlots tiles; the
 // softmax warps read them before they wait for S.  The ragged prefill of 16
-// prompts (32 / 8 heads of 128, bf16 query, 218 GFLOP) takes 242 us where one
-// scale for the tensor takes 213; with an fp8 query 205 and 177.  Without any
-// scale arithmetic the kernel's structure takes 222.  What it costs most are
-// registers: at 192 a softmax thread 285 us, at 200 262, at 208 242.
+// prompts (32 / 8 heads of 128, bf16 query, 218 GFLOP) takes 237 us where one
+// scale for the tensor takes 209; with an fp8 query 204 and 177.  What it costs
+// most are registers: with 48 for the dequant and producer warps each, 192 a
+// softmax thread took 285 us, 200 262 and 208 242; 208, 32 and 64 take 237.
 #pragma once
 #include <type_traits>
 
@@ -355,11 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Registers per thread: launched at 128; each warpgroup's branch below
     // starts by resizing: softmax 192, dequant 64, producer/MMA 64
     // (4 x 32 x (64 + 2 x 192 + 64) = 65,536, what the block launched with);
-    // with block scales 208, 48 and 48, the same sum.
+    // with block scales softmax 208, dequant 32, producer/MMA 64, the same sum.
 
     if (warp >= 12) {
-      if constexpr (VAR == kVarBlocks) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
-      else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
       if (warp == 12) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
@@ -665,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp < 4) {
-        if constexpr (VAR == kVarBlocks) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        if constexpr (VAR == kVarBlocks) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
         // ---------------------------------------------------------- dequant
         const int wd = warp, q8 = lane >> 3, e = lane & 7;
@@ -678,13 +677,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (Under a window so are keys hide .. show - 1 of a V tile.)
         auto widen_as = [&](auto bf, uint32_t src, uint32_t dst, int valid, int hide, int show) {
             constexpr bool kToBf = decltype(bf)::value;
+            // (Block scales leave 32 registers: K and V two rows at a time take 250
+            // us in place of 237.)
+            constexpr int kTurns = VAR == kVarBlocks && !kF8 ? 1 : 2;
             auto lo = [](uint32_t w) { return kToBf ? half2_to_bf162(fp8x2_lo<KT>(w)) : fp8x2_lo<KT>(w); };
             auto hi = [](uint32_t w) { return kToBf ? half2_to_bf162(fp8x2_hi<KT>(w)) : fp8x2_hi<KT>(w); };
             auto gone = [&](int row) { return row >= valid || (VAR != kVarPlain && row >= hide && row < show); };
             if constexpr (k2) {
                 return;  // a 2-byte cache has no fp8 tile
             } else if constexpr (DH == 128) {
-#pragma unroll 2
+#pragma unroll kTurns
                 for (int i = 0; i < 8; ++i) {
                     const int combo = wd * 8 + i;
                     const int row = (combo >> 1) * 8 + e;
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 // 64-B fp8 rows under the 64-byte swizzle (16-byte chunk c of
                 // row r at c ^ ((r >> 1) & 3)) -> one 128-B f16 half.
-#pragma unroll 2
+#pragma unroll kTurns
                 for (int i = 0; i < 4; ++i) {
                     const int row = (wd * 4 + i) * 8 + e, c = q8;
                     uint4 w = lds128(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
@@ -787,8 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) return up;
             if (r < TQ * g) {
                 // The row stays in registers between its maximum and its conversion
-                // (209 us for the ragged prefill in place of 213); block scales, short of registers, read it twice (with the row held
-                // they take 265 us in place of 242, with packed maxima 247).
+                // (209 us for the ragged prefill in place of 213); block scales read it
+                // twice and compare word by word (held 252 us in place of 237, with
+                // packed maxima 241: a faster fit is in the other query tile's way).
                 constexpr bool kHold = VAR != kVarBlocks;
                 constexpr int kTurns = kHold ? 8 * NH : 4;
                 const uint32_t qrow = base + L::q + x * L::kQTile + r * 128;
