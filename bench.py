@@ -67,7 +67,7 @@ NCU_TRAFFIC = {
 # The same for the prefill kernels, per workload index, keyed by the SHA-256
 # of their sources (prefill.cuh, then prefill_pair.cuh).
 NCU_TRAFFIC_PREFILL = {
-    "4b29834ed63f74be032a391979b987fa86b726940b9dad160293a91a9390856c": {4: 168413696, 5: 186634496, 7: 250971136},
+    "a8074eba7c5462d66e34b8efd4dfe424f516197e981e7eb5ea371acaa04aa74f": {4: 168376832, 5: 187184640, 7: 250864384},
 }
 
 
