@@ -67,7 +67,7 @@ NCU_TRAFFIC = {
 # The same for the prefill kernels, per workload index, keyed by the SHA-256
 # of their sources (prefill.cuh, then prefill_pair.cuh).
 NCU_TRAFFIC_PREFILL = {
-    "a8074eba7c5462d66e34b8efd4dfe424f516197e981e7eb5ea371acaa04aa74f": {4: 168376832, 5: 187184640, 7: 250864384},
+    "d137c0377f7eba09d8a6099901863c344503d8ee15283a4080c2284e6552558c": {4: 168592128, 5: 186473728, 7: 250888960},
 }
 
 
