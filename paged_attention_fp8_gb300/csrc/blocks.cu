@@ -85,6 +85,22 @@ __device__ __forceinline__ int page_of(const int32_t* kv_indices, int e0, int e1
     return pg >= 0 && pg < num_pages ? pg : -1;
 }
 
+// Both kernels wait for the stream's work before them themselves, so that the
+// launch passes under that work.
+template <typename P>
+cudaError_t launch_dependent(void (*kern)(P), unsigned blocks, int threads, const P& p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 // ------------------------------------------------------------------ writing
 
 // Eight elements of a row.
@@ -330,6 +346,8 @@ __global__ void __launch_bounds__(kAppendThreads, SRC == PAFP8_F32 ? 3 : kAppend
     append_blocks_kernel(const BlockAppendParams p) {
     constexpr int HPW = 128 / DH;
     constexpr int ESZ = SRC == PAFP8_F32 ? 4 : 2;
+    // Nothing is read or written before the stream's earlier work is complete.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const int col = 8 * (lane & 15);
     Rows<SRC> rows_of;
@@ -424,8 +442,7 @@ cudaError_t launch_append_t(BlockAppendParams p, cudaStream_t stream) {
     const long long units = (p.nnz + p.span - 1) / p.span * parts;
     const long long blocks = (units + W - 1) / W;
     if (blocks > INT32_MAX / W) return cudaErrorInvalidConfiguration;
-    append_blocks_kernel<SRC, KV, DH><<<(unsigned)blocks, kAppendThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(append_blocks_kernel<SRC, KV, DH>, (unsigned)blocks, kAppendThreads, p, stream);
 }
 
 template <int SRC, int KV>
@@ -451,6 +468,8 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
     constexpr int ESZ = OUT == PAFP8_F32 ? 4 : 2;
     __shared__ long long s_row[kReadRows];    // byte offset of head 0's row in the cache, or -1
     __shared__ long long s_scale[kReadRows];  // index of head 0's scale
+    // Nothing is read or written before the stream's earlier work is complete.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long all = __ldg(p.out_indptr + p.batch);
     const long long rows = min(p.nnz, all);
     const long long t0 = (long long)blockIdx.x * p.tile;
@@ -528,8 +547,7 @@ cudaError_t launch_read_t(ReadParams p, cudaStream_t stream) {
     // in tiles of 16.
     p.tile = 2;
     while (p.tile < kReadRows && p.nnz > 1216LL * p.tile) p.tile *= 2;
-    read_kv_kernel<OUT, KV, DH><<<(unsigned)((p.nnz + p.tile - 1) / p.tile), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(read_kv_kernel<OUT, KV, DH>, (unsigned)((p.nnz + p.tile - 1) / p.tile), kThreads, p, stream);
 }
 
 template <int OUT>

@@ -285,6 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmq,
                    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                    const __grid_constant__ CUtensorMap tmo) {
+    // Nothing is read or written before the stream's earlier work is complete.
+    if constexpr (VAR != kVarPlain) asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr bool k2 = KT == PAFP8_F16 || KT == PAFP8_BF16;  // 2-byte cache, same dtype as q
     constexpr bool kBF = KT == PAFP8_BF16;                    // bf16 MMA operands
     // A bf16 query on an fp8 cache is brought into f16 range (per row, by the
@@ -1181,8 +1183,24 @@ cudaError_t launch_t(const PrefillParams& p, const CUtensorMap& tq, const CUtens
     auto kern = prefill_kernel<kF8, KT, kDiag, DH, kSlots, VAR>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<num_ctas, kThreads, smem, stream>>>(p, tq, tk, tv, to);
-    return cudaGetLastError();
+    if constexpr (VAR == kVarPlain) {
+        kern<<<num_ctas, kThreads, smem, stream>>>(p, tq, tk, tv, to);
+        return cudaGetLastError();
+    } else {
+        // The variants wait for the stream's work before them in the kernel
+        // rather than before the launch, which then passes under that work.
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(num_ctas);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, p, tq, tk, tv, to);
+    }
 }
 
 // The diagnostic instantiation runs only under a shortened wait bound (and
