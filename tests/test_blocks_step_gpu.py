@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import paged_attention_fp8_gb300 as pa
-from blocks_ref import TORCH, Cache, as_tokens, raw
+from blocks_ref import TORCH, Cache, as_tokens, raw, table
 from window_ref import OUT, Batch
 
 pytestmark = pytest.mark.gpu
@@ -139,11 +139,12 @@ def test_two_batches_on_two_streams(cuda_device):
         b.check()
 
 
+@pytest.mark.parametrize("new", [None, [90, 33, 200]])
 @pytest.mark.parametrize("scales", ["tensor", "block"])
-def test_each_call_sees_the_work_before_it(cuda_device, scales):
-    """Decode launches early and waits in the kernel: every input is rewritten right before a call -- by copies, kernels and
+def test_each_call_sees_the_work_before_it(cuda_device, scales, new):
+    """The attention kernels launch early and waits in the kernel: every input is rewritten right before a call -- by copies, kernels and
     the append -- and right after it, eager and captured with the plan's upload, forty times over one workspace."""
-    bs = [Batch([700, 33, 260], window=300, sinks=5, scales=scales, num_ctas=40, seed=i).upload() for i in range(2)]
+    bs = [Batch([700, 33, 260], new, window=300, sinks=5, scales=scales, num_ctas=40, seed=i).upload() for i in range(2)]
     a = bs[0]
     want = []
     for b in bs:
@@ -210,3 +211,35 @@ def test_expired_wait_is_reported_and_the_next_run_is_clean(cuda_device, monkeyp
     b.run()
     b.plan.device_status(b.ws)
     b.check()
+
+
+def test_appends_and_reads_one_after_the_other(cuda_device):
+    """Both launch early and wait in the kernel: forty rounds of new rows (written right before the call and over right after
+    it), the append and the read-back of the whole cache, against rows kept aside."""
+    g = torch.Generator().manual_seed(3)
+    lens, hkv, d = [130, 47, 64], 2, 128
+    ptr, ids, pool = table(lens, 16, g)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ptr_d, ids_d = torch.as_tensor(ptr, **i32), torch.as_tensor(ids, **i32)
+    rows = torch.as_tensor(np.concatenate([[0], np.cumsum(lens)]), **i32)
+    zero = torch.zeros(3, **i32)
+    n = sum(lens)
+    kc, vc = (torch.zeros(pool, 16, hkv, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.ones(pool, 1, hkv, device="cuda") for _ in range(2))
+    # Numbers of few bits, so that a code holds them exactly under their block's power of two.
+    kept = [(torch.randint(-7, 8, (n, hkv, d), generator=g).float() * 2.0 ** (i % 5)).to(torch.bfloat16).cuda() for i in range(8)]
+    x, y = torch.zeros_like(kept[0]), torch.zeros_like(kept[0])
+    a, b = torch.zeros_like(x), torch.zeros_like(x)
+    got = []
+    for i in range(40):
+        x.copy_(kept[i % 8])
+        y.copy_(kept[(i + 3) % 8])
+        pa.pafp8_append_kv_blocks(x, y, rows, zero, ptr_d, ids_d, kc, vc, ks, vs)
+        x.fill_(float("nan"))
+        y.fill_(float("nan"))
+        pa.pafp8_read_kv(kc, vc, rows, zero, ptr_d, ids_d, a, b, k_scales=ks, v_scales=vs)
+        got.append((a.clone(), b.clone()))
+        a.fill_(7)
+        b.fill_(7)
+    for i, (p, q) in enumerate(got):
+        assert torch.equal(p, kept[i % 8]) and torch.equal(q, kept[(i + 3) % 8])
