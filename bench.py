@@ -67,7 +67,7 @@ NCU_TRAFFIC = {
 # The same for the prefill kernels, per workload index, keyed by the SHA-256
 # of their sources (prefill.cuh, then prefill_pair.cuh).
 NCU_TRAFFIC_PREFILL = {
-    "d137c0377f7eba09d8a6099901863c344503d8ee15283a4080c2284e6552558c": {4: 168592128, 5: 186473728, 7: 250888960},
+    "8a13c3d40a1851bf48fd09fd4fc3daf8cf33f5b13a39a02edc79f236a82824a6": {4: 168310784, 5: 186613504, 7: 257421568},
 }
 
 
