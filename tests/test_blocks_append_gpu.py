@@ -71,7 +71,7 @@ def test_one_step(cuda_device, cached, new, heads, d, fmt, layout, page_size, sr
 
 @pytest.mark.parametrize("batch,low,high", [(40, 1, 8), (300, 1, 3), (300, 4, 7), (300, 8, 15), (120, 16, 40)])
 @pytest.mark.parametrize("src", ["bf16", "f32"])
-def test_many_requests(cuda_device, batch, low, high, src):
+def test_requests_of_like_lengths(cuda_device, batch, low, high, src):
     """Requests of like lengths: a warp looks through 1, 2, 4, 8 or 16 tokens, with borders of requests and blocks anywhere in them."""
     gen = np.random.default_rng(batch + high)
     cached, new = gen.integers(0, 50, batch), gen.integers(low, high + 1, batch)
