@@ -263,3 +263,12 @@ def test_scales_past_two_gib_of_codes(cuda_device):
     o, lse = torch.zeros(1, 16, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 16, device="cuda")
     plan.run_block_scales(small.q.cuda(), k, v, at.to(torch.int32).cuda(), o, lse, ws, k_scales=ks, v_scales=vs)
     small.check(o, lse)
+
+
+@pytest.mark.parametrize("window,sinks", [(900, 0), (900, 4), (1000, 40), (300, 40), (17, 130)])
+@pytest.mark.parametrize("kv,layout,page_size", [("bf16", "NHD", 32), ("f16", "HND", 48), ("bf16", "HND", 16), ("f16", "NHD", 64)])
+def test_2_byte_prefill_with_a_gap_in_larger_pages(cuda_device, window, sinks, kv, layout, page_size):
+    """Pages of several 16-token blocks and sinks over several of them, with lengths well past the window, so that items leave
+    pages out; windows on both sides of the rule that picks CTA pairs."""
+    run([2500, 40, 1700], [900, 40, 33], window=window, sinks=sinks, q=kv, kv=kv, hq=8, hkv=2, num_ctas=12, layout=layout,
+        page_size=page_size)
