@@ -724,8 +724,10 @@ pafp8_status pafp8_append_kv_blocks(const pafp8_block_append_desc *desc, void *s
  * times k_scales | v_scales[page][slot / 16][h].  For decode and prefill plans,
  * with a window or without, over an E4M3FN or E5M2 cache; any scales that are
  * finite and > 0 (device memory, not checked): those of K such that the logits
- * are finite in fp32, those of V of one request and head within 2^90 of one
- * another and between 2^-96 and 2^96.
+ * are finite in fp32 (where sm_scale * q_scale, or its product with one of them,
+ * is below 2^-126 it has fewer bits, and below fp32's smallest number it counts
+ * as that), those of V of one request and head within 2^90 of one another and
+ * between 2^-96 and 2^96.
  *   q_scale    as in pafp8_run (an fp8 query)
  *   k_scales,
  *   v_scales   device float [num_pages, page_size / 16, num_kv_heads]

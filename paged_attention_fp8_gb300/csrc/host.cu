@@ -1230,8 +1230,7 @@ pafp8_status run_body(const pafp8_plan* plan, int32_t stage, int32_t q_dtype, co
 
     cudaStream_t s = (cudaStream_t)stream;
     char* ws = (char*)workspace;
-    const float sm_log2 = (float)((double)d.sm_scale * (is_fp8(q_dtype) ? (double)q_scale : 1.0) *
-                                  (double)k_scale * 1.4426950408889634);
+    const float sm_log2 = fold_scale_log2(d.sm_scale, is_fp8(q_dtype) ? q_scale : 1.0f, k_scale);
     if (d.mode == PAFP8_MODE_PREFILL) {
         if (stage == 2 || plan->num_ctas == 0) return PAFP8_OK;  // prefill has no merge stage
         PrefillParams pp{};
@@ -1624,8 +1623,7 @@ pafp8_status pafp8_run_decode_noalloc(const pafp8_plan* plan, int32_t q_dtype, c
     p.num_pages = d.num_pages;
     p.page_mult = plan->page_mult;
     p.head_dim = d.head_dim;
-    p.sm_scale_log2 = (float)((double)d.sm_scale * (is_fp8(q_dtype) ? (double)q_scale : 1.0) *
-                              (double)k_scale * 1.4426950408889634);
+    p.sm_scale_log2 = fold_scale_log2(d.sm_scale, is_fp8(q_dtype) ? q_scale : 1.0f, k_scale);
     p.v_scale = v_scale;
     p.window = plan->window;
     p.sinks = plan->sinks;

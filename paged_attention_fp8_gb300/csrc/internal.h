@@ -74,11 +74,25 @@ constexpr int kDynMinRowsDiv = 4;
 constexpr int kStatusWord = 0, kChunkCounterWord = 32, kChunkDoneWord = 48;
 constexpr int32_t kMetaMagicValue = 0x38464150;
 
-// log2-domain softmax scale of one head from per-head scales, folded in
-// double in the same order as the host folds the per-tensor ones, so equal
-// scales give the same float.
-__device__ __forceinline__ float fold_scale_log2(float sm_scale, float q_scale, float k_scale) {
-    return (float)((double)sm_scale * (double)q_scale * (double)k_scale * 1.4426950408889634);
+// What masked logits (-inf) are multiplied by stays above zero, or they would
+// turn into NaN: a product of small scales that underflows becomes fp32's
+// smallest number, under which every logit is zero all the same.  (One maximum
+// that passes NaN on; a comparison and a selection took the bf16-query prefill
+// over block scales 1 us longer.)
+__host__ __device__ __forceinline__ float above_zero(float factor) {
+#ifdef __CUDA_ARCH__
+    asm("max.NaN.f32 %0, %1, 0f00000001;" : "=f"(factor) : "f"(factor));
+    return factor;
+#else
+    return factor == 0.0f ? 1.4012984643e-45f : factor;
+#endif
+}
+
+// log2-domain softmax scale, folded in double by the host (per-tensor scales)
+// and the kernels (per-head ones) in the same order, so equal scales give the
+// same float.
+__host__ __device__ __forceinline__ float fold_scale_log2(float sm_scale, float q_scale, float k_scale) {
+    return above_zero((float)((double)sm_scale * (double)q_scale * (double)k_scale * 1.4426950408889634));
 }
 
 // A request's 16-token sub-page vp (a page of 16 m tokens is m of them) as

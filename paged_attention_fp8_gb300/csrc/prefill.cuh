@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const SubPageAt at = sub_page(idx, page_at<VAR>(p, it, vp), m, p.num_pages, bad);
                     const size_t e = ((size_t)at.page * m + at.slot / kPageSize) * p.num_kv_heads + it.hk;
                     const float v = __ldg(p.v_blocks + e);
-                    ks = p.sm_scale_log2 * __ldg(p.k_blocks + e);
+                    ks = above_zero(p.sm_scale_log2 * __ldg(p.k_blocks + e));
                     lv = __log2f(v);
                     rv = __frcp_rn(v);
                 }
