@@ -271,6 +271,9 @@ def _tree_sizes(desc, kv_indptr, qo_indptr):
 
 
 def _note_sizes(handle, desc, kv_indptr, qo_indptr) -> None:
+    if desc.mode == MODE_TREE:
+        _TREE_SIZES[handle] = _tree_sizes(desc, kv_indptr, qo_indptr)
+        return
     batch = desc.batch
     last = ctypes.c_int32.from_address
     _SIZES[handle] = (batch if qo_indptr is None or batch <= 0 else last(_ptr(qo_indptr) + 4 * batch).value,
@@ -307,10 +310,7 @@ def pafp8_plan_create(desc: plan_desc, kv_indptr, last_page_len, qo_indptr=None)
     out = ctypes.c_void_p()
     _check(lib().pafp8_plan_create(ctypes.byref(desc), _ptr(kv_indptr), _ptr(last_page_len),
                                    _ptr(qo_indptr), ctypes.byref(out)))
-    if desc.mode == MODE_TREE:
-        _TREE_SIZES[out.value] = _tree_sizes(desc, kv_indptr, qo_indptr)
-    else:
-        _note_sizes(out.value, desc, kv_indptr, qo_indptr)
+    _note_sizes(out.value, desc, kv_indptr, qo_indptr)
     return out.value
 
 

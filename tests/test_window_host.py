@@ -188,3 +188,44 @@ def test_the_plain_plan_call_is_unchanged():
                                              ctypes.byref(out)) == 0
     assert np.array_equal(pa.pafp8_plan_metadata(out.value), a.metadata())
     pa.lib().pafp8_plan_destroy(out)
+
+
+def test_a_tree_plan_without_a_window_keeps_its_checks(monkeypatch):
+    """pafp8_plan_create_window with a window of 0 makes every plan that pafp8_plan_create makes, tree plans too: their run
+    call knows their sizes and refuses arrays that are too small."""
+    desc = pa.plan_desc(mode=pa.MODE_TREE, batch=1, num_qo_heads=8, num_kv_heads=2, head_dim=128, page_size=16, num_pages=6,
+                        q_dtype=pa.BF16, kv_dtype=pa.E4M3FN, o_dtype=pa.BF16, num_ctas=8)
+    calls = []
+
+    class Recorder:
+        @staticmethod
+        def pafp8_run_tree(*a):
+            calls.append(a)
+            return 0
+
+        def __getattr__(self, name):
+            return getattr(real, name)
+
+    real, recorder = pa.lib(), Recorder()
+    monkeypatch.setattr(pa, "lib", lambda: recorder)
+    monkeypatch.setattr(pa, "_device_of", lambda t, name: -1)
+    for make in (lambda: pa.pafp8_plan_create(desc, [0, 3], [5], [0, 4]), lambda: pa.pafp8_plan_create_window(desc, 0, 0, [0, 3], [5], [0, 4])):
+        plan = make()
+        try:
+            args = [torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(6, 16, 2, 128, dtype=torch.float8_e4m3fn),
+                    torch.zeros(6, 16, 2, 128, dtype=torch.float8_e4m3fn), torch.zeros(3, dtype=torch.int32),
+                    torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(4, 8),
+                    torch.zeros(pa.pafp8_workspace_bytes(plan), dtype=torch.uint8)]
+            pa.pafp8_run_tree(plan, *args, stream=1)
+            n = len(calls)
+            for at in (1, 3, 4, 5, 6):  # a cache, page ids, mask rows, o, lse: one element or row less
+                short = list(args)
+                short[at] = args[at][:-1].contiguous()
+                with pytest.raises(ValueError):
+                    pa.pafp8_run_tree(plan, *short, stream=1)
+            assert len(calls) == n
+            with pytest.raises(ValueError, match="decode or prefill plan"):
+                pa.pafp8_run_block_scales(plan, *args[:4], *args[5:], k_scales=None, v_scales=None, stream=1)
+        finally:
+            pa.pafp8_plan_destroy(plan)
+        assert plan not in pa._TREE_SIZES and plan not in pa._SIZES
