@@ -48,6 +48,12 @@ constexpr int kAppendThreads = 128;
 constexpr int kAppendBlocks = 8;  // thread blocks an SM, for 64 registers a thread (fp32 rows: 3, for 168)
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
+// Both kernels are launched early (launch_dependent below).
+template <typename T>
+__device__ __forceinline__ T now(const T* p) {
+    return load_input<true>(p);
+}
+
 // The request that owns row t, by one warp together: the last r with
 // indptr[r] <= t (32 probes a step; any r for a t outside the rows), and the
 // rows it starts and ends at.  Every index probed lies in (0, n), n >= 1.
@@ -56,11 +62,11 @@ struct Owner {
 };
 __device__ __forceinline__ Owner owner(const int32_t* indptr, int n, int t) {
     const int lane = threadIdx.x & 31;
-    int lo = 0, hi = n, at_lo = __ldg(indptr), at_hi = __ldg(indptr + n);
+    int lo = 0, hi = n, at_lo = now(indptr), at_hi = now(indptr + n);
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const uint32_t at = (uint32_t)lo + (uint32_t)(lane + 1) * (uint32_t)step;
-        const int v = at < (uint32_t)hi ? __ldg(indptr + at) : 0;
+        const int v = at < (uint32_t)hi ? now(indptr + at) : 0;
         const uint32_t b = __ballot_sync(kAll, at < (uint32_t)hi && v <= t);
         const int steps = b == kAll ? 32 : __ffs(~b) - 1;
         const int below = __shfl_sync(kAll, v, max(steps - 1, 0)), above = __shfl_sync(kAll, v, min(steps, 31));
@@ -81,7 +87,7 @@ __device__ __forceinline__ int page_of(const int32_t* kv_indices, int e0, int e1
     slot = (int)(pos - at * (uint32_t)page_size);
     const uint32_t e = (uint32_t)e0 + at;
     if (e0 < 0 || e1 < 0 || e >= (uint32_t)e1) return -1;
-    const int pg = __ldg(kv_indices + e);
+    const int pg = now(kv_indices + e);
     return pg >= 0 && pg < num_pages ? pg : -1;
 }
 
@@ -368,7 +374,7 @@ __global__ void __launch_bounds__(kAppendThreads, SRC == PAFP8_F32 ? 3 : kAppend
     const uint32_t nnz = (uint32_t)p.nnz;
     uint32_t t = group * (uint32_t)p.span;
     if (t >= nnz || p.batch == 0) return;
-    const uint32_t all = (uint32_t)max(0, __ldg(p.qo_indptr + p.batch)), first_row = (uint32_t)max(0, __ldg(p.qo_indptr));
+    const uint32_t all = (uint32_t)max(0, now(p.qo_indptr + p.batch)), first_row = (uint32_t)max(0, now(p.qo_indptr));
     const Owner who = owner(p.qo_indptr, p.batch, (int)max(t, first_row));
     const uint32_t rows = min(nnz, all);
     if (all > nnz && u == 0 && lane == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
@@ -383,11 +389,11 @@ __global__ void __launch_bounds__(kAppendThreads, SRC == PAFP8_F32 ? 3 : kAppend
     while (t < t_end) {
         if (t >= r1) {  // (requests without new tokens lie in between)
             if (++r >= p.batch) break;
-            r0 = (uint32_t)max(0, __ldg(p.qo_indptr + r));
-            r1 = min((uint32_t)max(0, __ldg(p.qo_indptr + r + 1)), rows);
+            r0 = (uint32_t)max(0, now(p.qo_indptr + r));
+            r1 = min((uint32_t)max(0, now(p.qo_indptr + r + 1)), rows);
             continue;
         }
-        const int cached = __ldg(p.cached_lens + r), e0 = __ldg(p.kv_indptr + r), e1 = __ldg(p.kv_indptr + r + 1);
+        const int cached = now(p.cached_lens + r), e0 = now(p.kv_indptr + r), e1 = now(p.kv_indptr + r + 1);
         const uint32_t pos = (uint32_t)cached + (t - r0);
         const int s0 = (int)(pos & (kPageSize - 1));
         const int m = (int)min((uint32_t)(kPageSize - s0), r1 - t);
@@ -472,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
     __shared__ long long s_scale[kReadRows];  // index of head 0's scale
     // Nothing is read or written before the stream's earlier work is complete.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long all = __ldg(p.out_indptr + p.batch);
+    const long long all = now(p.out_indptr + p.batch);
     const long long rows = min(p.nnz, all);
     const long long t0 = (long long)blockIdx.x * p.tile;
     if (all > p.nnz && blockIdx.x == 0 && threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, kStatusBounds);
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
     const long long head_step = p.hnd ? (long long)p.page_size * DH : DH;
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        const long long low = __ldg(p.out_indptr);
+        const long long low = now(p.out_indptr);
         const long long base = max(t0, low);
         const int r0 = base < rows ? owner(p.out_indptr, p.batch, (int)base).r : 0;
         const long long t = t0 + lane;
@@ -488,13 +494,13 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
             long long row = -1, scale = 0;
             if (t >= low && t < rows) {
                 int r = r0;
-                while (r + 1 < p.batch && t >= __ldg(p.out_indptr + r + 1)) ++r;
+                while (r + 1 < p.batch && t >= now(p.out_indptr + r + 1)) ++r;
                 int slot = 0;
-                const int start = __ldg(p.starts + r);
-                const long long pos = (long long)start + (t - __ldg(p.out_indptr + r));
+                const int start = now(p.starts + r);
+                const long long pos = (long long)start + (t - now(p.out_indptr + r));
                 const int page = start < 0 || pos > 0xFFFFFFFFLL
                                      ? -1
-                                     : page_of(p.kv_indices, __ldg(p.kv_indptr + r), __ldg(p.kv_indptr + r + 1), (uint32_t)pos,
+                                     : page_of(p.kv_indices, now(p.kv_indptr + r), now(p.kv_indptr + r + 1), (uint32_t)pos,
                                                p.page_size, p.num_pages, slot);
                 if (page >= 0) {
                     row = p.hnd ? ((long long)page * p.num_kv_heads * p.page_size + slot) * DH
@@ -518,7 +524,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
         if (s_row[row] < 0) continue;
         const uint8_t* src = static_cast<const uint8_t*>(kv ? p.v_cache : p.k_cache) + s_row[row] + h * head_step + d;
         const float* scales = kv ? p.v_scales : p.k_scales;
-        const float s = scales != nullptr ? __ldg(scales + s_scale[row] + h) : (kv ? p.v_scale : p.k_scale);
+        const float s = scales != nullptr ? now(scales + s_scale[row] + h) : (kv ? p.v_scale : p.k_scale);
         const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src));
         float x[16];
         values8<KV>(make_uint2(w.x, w.y), reinterpret_cast<float(&)[8]>(x[0]));

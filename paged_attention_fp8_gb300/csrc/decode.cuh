@@ -90,7 +90,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // power-of-two factor the logits must be multiplied by (a bf16 query is
 // brought into f16 range by an exact power-of-two scaling when its magnitude
 // needs it).
-template <bool kBF16, int DH>
+template <bool kBF16, int DH, bool EARLY>
 __device__ __forceinline__ float load_q(uint32_t (&qf)[16], uint32_t (&qlo)[16], const void* q, int q_dtype,
                                         size_t head_off, bool active, int t) {
     constexpr int QW = DH / 8;   // words per lane
@@ -106,7 +106,7 @@ __device__ __forceinline__ float load_q(uint32_t (&qf)[16], uint32_t (&qlo)[16],
             const uint4* src = reinterpret_cast<const uint4*>(
                 static_cast<const uint16_t*>(q) + head_off + (DH / 4) * t);
 #pragma unroll
-            for (int i = 0; i < Q4; ++i) w[i] = __ldg(src + i);
+            for (int i = 0; i < Q4; ++i) w[i] = load_input<EARLY>(src + i);
         }
         const uint32_t* ws = reinterpret_cast<const uint32_t*>(w);
 #pragma unroll
@@ -128,7 +128,7 @@ __device__ __forceinline__ float load_q(uint32_t (&qf)[16], uint32_t (&qlo)[16],
             const uint4* src = reinterpret_cast<const uint4*>(
                 static_cast<const uint16_t*>(q) + head_off + (DH / 4) * t);
 #pragma unroll
-            for (int i = 0; i < Q4; ++i) w[i] = __ldg(src + i);
+            for (int i = 0; i < Q4; ++i) w[i] = load_input<EARLY>(src + i);
         }
         const uint32_t* ws = reinterpret_cast<const uint32_t*>(w);
         if (q_dtype == PAFP8_F16) {
@@ -161,7 +161,7 @@ __device__ __forceinline__ float load_q(uint32_t (&qf)[16], uint32_t (&qlo)[16],
             const uint4* src = reinterpret_cast<const uint4*>(
                 static_cast<const uint8_t*>(q) + head_off + (DH / 4) * t);
 #pragma unroll
-            for (int i = 0; i < DH / 64; ++i) w[i] = __ldg(src + i);
+            for (int i = 0; i < DH / 64; ++i) w[i] = load_input<EARLY>(src + i);
         }
         const uint32_t* ws = reinterpret_cast<const uint32_t*>(w);
 #pragma unroll
@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(32 * 9, 1)
                   const __grid_constant__ CUtensorMap tmv, int hpc, int group, int stages,
                   int heads_per_box) {
     // Nothing is read or written before the stream's earlier work is complete.
-    if constexpr (VAR != kVarPlain) asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr bool kEarly = VAR != kVarPlain;  // launched programmatically
+    if constexpr (kEarly) asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;      // 128B swizzle wants 1024-B alignment
@@ -289,9 +290,9 @@ __global__ void __launch_bounds__(32 * 9, 1)
                 SubPageAt sp{0, 0};
                 if constexpr (kSlots) {
                     if (lane < n)
-                        sp = sub_page(idx, VAR != kVarPlain ? units.at(pb + lane) : pb + lane, p.page_mult, p.num_pages, bad);
+                        sp = sub_page<kEarly>(idx, VAR != kVarPlain ? units.at(pb + lane) : pb + lane, p.page_mult, p.num_pages, bad);
                 } else if (lane < n) {
-                    const int pg = __ldg(idx + (VAR != kVarPlain ? units.at(pb + lane) : pb + lane));
+                    const int pg = load_input<kEarly>(idx + (VAR != kVarPlain ? units.at(pb + lane) : pb + lane));
                     bad = pg < 0 || pg >= p.num_pages;
                     sp.page = bad ? 0 : pg;
                 }
@@ -439,13 +440,13 @@ __global__ void __launch_bounds__(32 * 9, 1)
         auto look_up = [&](int vp) {
             if (vp >= p1) return 0;
             bool bad;
-            const SubPageAt at = sub_page(p.kv_indices + req_page[b], units.at(vp), p.page_mult, p.num_pages, bad);
+            const SubPageAt at = sub_page<kEarly>(p.kv_indices + req_page[b], units.at(vp), p.page_mult, p.num_pages, bad);
             return at.page * p.page_mult + at.slot / P;
         };
         auto load_scales = [&](int at, float& k, float& v) {
             const size_t i = (size_t)at * p.num_kv_heads + kvh;
-            k = __ldg(p.k_blocks + i);
-            v = __ldg(p.v_blocks + i);
+            k = load_input<kEarly>(p.k_blocks + i);
+            v = load_input<kEarly>(p.v_blocks + i);
         };
         if constexpr (VAR == kVarBlocks) {
             at_first = look_up(p0 + lane);
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(32 * 9, 1)
 
         uint32_t qf[16], qlo[16];
         const size_t q_head_off = ((size_t)b * Hq + (size_t)kvh * group + g) * DH;
-        const float qfactor = load_q<kBF, DH>(qf, qlo, p.q, p.q_dtype, q_head_off, g < group, t);
+        const float qfactor = load_q<kBF, DH, kEarly>(qf, qlo, p.q, p.q_dtype, q_head_off, g < group, t);
         if constexpr (VAR == kVarBlocks) load_scales(at_first, bk_next, bv_next);
         const bool split_q = kBF && p.q_dtype == PAFP8_F16;
         // log2 softmax scale of heads 2t and 2t+1 (this lane's S columns).
@@ -462,13 +463,13 @@ __global__ void __launch_bounds__(32 * 9, 1)
         // cache never has: there one scale serves both columns.
         float sc0 = p.sm_scale_log2 * qfactor, sc1 = sc0;
         if (p.k_scales != nullptr) {
-            const float ks = __ldg(p.k_scales + kvh);
+            const float ks = load_input<kEarly>(p.k_scales + kvh);
             if constexpr (k2) {
                 sc0 = fold_scale_log2(p.sm_scale, 1.0f, ks) * qfactor;
             } else {
                 const int h0 = kvh * group + min(2 * t, group - 1), h1 = kvh * group + min(2 * t + 1, group - 1);
-                const float q0 = p.q_scales != nullptr ? __ldg(p.q_scales + h0) : 1.0f;
-                const float q1 = p.q_scales != nullptr ? __ldg(p.q_scales + h1) : 1.0f;
+                const float q0 = p.q_scales != nullptr ? load_input<kEarly>(p.q_scales + h0) : 1.0f;
+                const float q1 = p.q_scales != nullptr ? load_input<kEarly>(p.q_scales + h1) : 1.0f;
                 sc0 = fold_scale_log2(p.sm_scale, q0, ks) * qfactor;
                 sc1 = fold_scale_log2(p.sm_scale, q1, ks) * qfactor;
             }
@@ -729,7 +730,7 @@ __global__ void __launch_bounds__(32 * 9, 1)
             }
             const int head = kvh * group + n;
             if (slot < 0) {
-                const float vs = p.v_scales != nullptr ? __ldg(p.v_scales + kvh) : p.v_scale;
+                const float vs = p.v_scales != nullptr ? load_input<kEarly>(p.v_scales + kvh) : p.v_scale;
                 uint32_t w[NA];
 #pragma unroll
                 for (int i = 0; i < NA; ++i) w[i] = pack_out2(vals[2 * i] * vs, vals[2 * i + 1] * vs, p.o_dtype);

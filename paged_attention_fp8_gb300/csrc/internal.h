@@ -95,6 +95,18 @@ __host__ __device__ __forceinline__ float fold_scale_log2(float sm_scale, float 
     return above_zero((float)((double)sm_scale * (double)q_scale * (double)k_scale * 1.4426950408889634));
 }
 
+// A load from an array that earlier work of the stream may have written (page
+// ids, lengths, queries, scales).  A grid launched programmatically (EARLY) is
+// resident while that work still runs, and __ldg wants memory that nothing
+// writes as long as the grid lives: such a grid loads plainly, after its
+// griddepcontrol.wait.  The plans' metadata comes by copies, which no launch
+// overlaps, and keeps __ldg.
+template <bool EARLY, typename T>
+__device__ __forceinline__ T load_input(const T* p) {
+    if constexpr (EARLY) return *p;
+    else return __ldg(p);
+}
+
 // A request's 16-token sub-page vp (a page of 16 m tokens is m of them) as
 // TMA coordinates: the pool page holding it and its first token slot there
 // (the cache maps span whole pages, page_size slots; sub-page j of a page
@@ -103,9 +115,10 @@ __host__ __device__ __forceinline__ float fold_scale_log2(float sm_scale, float 
 struct SubPageAt {
     int slot, page;
 };
+template <bool EARLY>
 __device__ __forceinline__ SubPageAt sub_page(const int32_t* idx, int vp, int m, int num_pages, bool& bad) {
     const int e = m == 1 ? vp : vp / m;
-    const int pg = __ldg(idx + e);
+    const int pg = load_input<EARLY>(idx + e);
     bad = pg < 0 || pg >= num_pages;
     return SubPageAt{(vp - e * m) * kPageSize, bad ? 0 : pg};
 }

@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                    const __grid_constant__ CUtensorMap tmo) {
     // Nothing is read or written before the stream's earlier work is complete.
-    if constexpr (VAR != kVarPlain) asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr bool kEarly = VAR != kVarPlain;  // launched programmatically
+    if constexpr (kEarly) asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr bool k2 = KT == PAFP8_F16 || KT == PAFP8_BF16;  // 2-byte cache, same dtype as q
     constexpr bool kBF = KT == PAFP8_BF16;                    // bf16 MMA operands
     // A bf16 query on an fp8 cache is brought into f16 range (per row, by the
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int page_next = 0;
             {
                 const int np0 = min(kTileKeys / kPageSize, npages), e = page_at<VAR>(p, it, lane);
-                if (lane < np0) page_next = __ldg(idx + (m == 1 ? e : e / m));
+                if (lane < np0) page_next = load_input<kEarly>(idx + (m == 1 ? e : e / m));
             }
             if (lane == 0) {
                 ok = wait_or_abort<kDiag>(bar(L::bQEmpty), qphase ^ 1u, flag_addr, p.status, p.wait_cycles);
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int pg1 = pg0 + kTileKeys / kPageSize;
                     const int np1 = min(kTileKeys / kPageSize, npages - pg1);
                     const int e = page_at<VAR>(p, it, pg1 + lane);
-                    page_next = lane < np1 ? __ldg(idx + (m == 1 ? e : e / m)) : 0;
+                    page_next = lane < np1 ? load_input<kEarly>(idx + (m == 1 ? e : e / m)) : 0;
                 }
                 const bool bad = lane < np && (page < 0 || page >= p.num_pages);
                 if (bad) page = 0;
@@ -642,10 +643,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int vp = j * (kTileKeys / kPageSize) + i;
                 if (j < it.nkv && vp < npages) {
                     bool bad;  // (the producer reports it)
-                    const SubPageAt at = sub_page(idx, page_at<VAR>(p, it, vp), m, p.num_pages, bad);
+                    const SubPageAt at = sub_page<kEarly>(idx, page_at<VAR>(p, it, vp), m, p.num_pages, bad);
                     const size_t e = ((size_t)at.page * m + at.slot / kPageSize) * p.num_kv_heads + it.hk;
-                    const float v = __ldg(p.v_blocks + e);
-                    ks = above_zero(p.sm_scale_log2 * __ldg(p.k_blocks + e));
+                    const float v = load_input<kEarly>(p.v_blocks + e);
+                    ks = above_zero(p.sm_scale_log2 * load_input<kEarly>(p.k_blocks + e));
                     lv = __log2f(v);
                     rv = __frcp_rn(v);
                 }
@@ -865,10 +866,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float vsc = p.v_scale;
             if (VAR != kVarBlocks && p.k_scales != nullptr) {  // per-head scale tensors
                 const int qh = it.hk * g + min(hh, g - 1);
-                scale = fold_scale_log2(p.sm_scale, p.q_scales != nullptr ? __ldg(p.q_scales + qh) : 1.0f,
-                                        __ldg(p.k_scales + it.hk)) *
+                scale = fold_scale_log2(p.sm_scale, p.q_scales != nullptr ? load_input<kEarly>(p.q_scales + qh) : 1.0f,
+                                        load_input<kEarly>(p.k_scales + it.hk)) *
                         up_next;
-                vsc = __ldg(p.v_scales + it.hk);
+                vsc = load_input<kEarly>(p.v_scales + it.hk);
             }
             float m = -INFINITY, l = 0.f;  // m in scaled (log2) units
             for (int j = 0; j < nX && ok; ++j) {
