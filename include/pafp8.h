@@ -669,7 +669,10 @@ pafp8_status pafp8_norm_rope_append(const pafp8_rope_desc *desc, void *stream);
  * a NaN a NaN code; neither counts in amax.  Token slots behind a request's
  * last new token keep their codes and take on the block's new scale: a token
  * taken back (a rejected draft) is written anew by the step that reaches its
- * position again.
+ * position again.  A block of zeros (or of values up to M * 2^-64) has a scale of
+ * 2^-64: beside such a block, pafp8_run_block_scales serves V values up to
+ * M * 2^26 (3.0e10 for E4M3FN, 3.8e12 for E5M2) in the same request and head, by
+ * the range of scales it states.
  *
  *   src_dtype      F16, BF16 or F32: k and v
  *   k, v           device [nnz, num_kv_heads, head_dim], heads of a token
@@ -727,7 +730,8 @@ pafp8_status pafp8_append_kv_blocks(const pafp8_block_append_desc *desc, void *s
  * are finite in fp32 (where sm_scale * q_scale, or its product with one of them,
  * is below 2^-126 it has fewer bits, and below fp32's smallest number it counts
  * as that), those of V of one request and head within 2^90 of one another and
- * between 2^-96 and 2^96.
+ * between 2^-96 and 2^96 -- blocks of zeros among them, whose scale is 2^-64 if
+ * pafp8_append_kv_blocks wrote it.
  *   q_scale    as in pafp8_run (an fp8 query)
  *   k_scales,
  *   v_scales   device float [num_pages, page_size / 16, num_kv_heads]

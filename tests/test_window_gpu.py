@@ -272,3 +272,23 @@ def test_2_byte_prefill_with_a_gap_in_larger_pages(cuda_device, window, sinks, k
     pages out; windows on both sides of the rule that picks CTA pairs."""
     run([2500, 40, 1700], [900, 40, 33], window=window, sinks=sinks, q=kv, kv=kv, hq=8, hkv=2, num_ctas=12, layout=layout,
         page_size=page_size)
+
+
+@pytest.mark.parametrize("new", [None, [150]])
+@pytest.mark.parametrize("kv,q", [("e4m3fn", "bf16"), ("e5m2", "e4m3fn")])
+def test_zero_blocks_beside_the_largest_values_they_go_with(cuda_device, new, kv, q):
+    """V scales 2^90 apart, as the append writes them for blocks of zeros (2^-64) and for values of 2^26 times the type's
+    largest: the border that the header states, with the zeros first, between and last, keys of zeros and others."""
+    b = Batch([333], new, scales="block", q=q, kv=kv, num_ctas=3)
+    b.vs = b.vs / b.vs.max() * 2.0 ** 26  # within a factor of 8 of one another
+    for i, at in enumerate((0, 1, 7, 12, 20)):
+        page = int(b.ids[at])
+        raw(b.v)[page] = 0
+        b.vs[page] = 2.0 ** -64
+        if i % 2:
+            raw(b.k)[page] = 0
+            b.ks[page] = 2.0 ** -64
+    b.upload()
+    b.run()
+    b.plan.device_status(b.ws)
+    b.check()
