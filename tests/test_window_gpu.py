@@ -292,3 +292,39 @@ def test_zero_blocks_beside_the_largest_values_they_go_with(cuda_device, new, kv
     b.run()
     b.plan.device_status(b.ws)
     b.check()
+
+
+@pytest.mark.parametrize("new", [None, [120]])
+@pytest.mark.parametrize("kv,q", [("e4m3fn", "bf16"), ("e5m2", "e4m3fn")])
+def test_small_blocks_carry_the_output_where_the_large_ones_weigh_little(cuda_device, new, kv, q):
+    """V scales 2^12 apart and logits that leave the large blocks next to nothing.  Below f16's normal range a probability loses
+    at most 2^-25 of the largest one, and itself (decode), or the product with its V scale 2^-25 of the largest such product
+    (prefill): the bound counts that in place of 2^-25 of the largest V scale."""
+    b = Batch([300], new, scales="block", q=q, kv=kv, num_ctas=4)
+    big = torch.as_tensor(b.ids[::3])
+    b.q = b.q.double().abs().to(b.q.dtype)
+    for pages, sign in ((torch.arange(b.pool), 1), (big, -1)):  # keys of large blocks point away from every query
+        x = b.k.view(torch.uint8)[pages] & 0x7F
+        b.k.view(torch.uint8)[pages] = x | (0x80 if sign < 0 else 0)
+    b.vs = b.vs / 2.0 ** 12
+    b.vs[big] *= 2.0 ** 12
+    b.upload()
+    b.run()
+    b.check()
+    o, _, tol, _ = b.expect()
+    key, qs = b.dense("k", 0), b.q_scale
+    page = torch.as_tensor(b.ids[np.arange(300) // 16])
+    group, rows = b.hq // b.hkv, len(b.q)
+    z = torch.einsum("uhgd,jhd->uhgj", (b.q.double() * qs).view(rows, b.hkv, group, b.d), key) * b.sm_scale
+    w = torch.softmax(z.masked_fill(~b.visible(0)[:, None, None], -np.inf), -1)
+    top = 448.0 if kv == "e4m3fn" else 57344.0
+    scale = b.vs.double()[page, 0].T[None, :, None]
+    if new is None:
+        lost = (torch.minimum(w, 2.0 ** -25 * w.amax(-1, keepdim=True)) * scale).sum(-1)
+    else:
+        lost = b.visible(0).sum(-1)[:, None, None] * 2.0 ** -25 * (w * scale).amax(-1)
+    counted = b.visible(0).sum(-1)[:, None] * 2.0 ** -25 * float(b.vs.max())
+    tight = tol - (counted - lost.view(rows, b.hq))[..., None] * top * (1 + torch.finfo(b.o.dtype).eps / 2)
+    over = (b.o.double().cpu() - o).abs() - tight
+    assert over.max() <= 0, float(over.max())
+    assert (tight < o.abs() / 8).double().mean() > 0.5  # an output of zero would not pass
