@@ -181,10 +181,13 @@ pafp8_status pafp8_plan_create(const pafp8_plan_desc *desc, const int32_t *kv_in
  * the request's first `sinks` tokens.  Every run call takes such a plan
  * (pafp8_run_pod also with one windowed phase); only the visible keys' pages
  * are read, in granules of 16 tokens, and the split-KV options count those
- * pages.  Values of tokens that no row of a
- * decode request, or of a prefill item (two tiles of 128 / group new tokens
- * and one KV head), sees are not used, whatever they hold; a NaN in the value
- * row of any other token reaches every row of the item.
+ * pages.  Values of tokens that no row of a decode request, or of a prefill item
+ * (two tiles of 128 / group new tokens and one KV head), sees are not used,
+ * whatever they hold; a NaN in the value row of any other token reaches every
+ * row of the item.
+ * Prefill multiplies a bf16 query over an fp8 cache as it is: its products with
+ * the codes must be finite in fp32 (magnitudes up to 5e33 for E4M3FN, 4e31 for
+ * E5M2).
  *   window  0: no window (sinks must then be 0); > 0: keys seen
  *   sinks   >= 0
  * Lengths up to 2^31 - 129 keys a request with a window; tree plans take

@@ -435,10 +435,14 @@ __global__ void __launch_bounds__(kAppendThreads, SRC == PAFP8_F32 ? 3 : kAppend
 
 // A warp looks through `span` new tokens for its blocks: 16, which in a prompt
 // hold one or two, or fewer where requests have fewer tokens each or where the
-// call is so short that twice the warps are still resident at once (24 of them
-// an SM), so that a decode step's requests go to a warp each rather than 16 to
-// one in turn.  (64 requests of 1-8 tokens 5.6 us, 16 tokens a warp 11.5; 256 of
-// 4 tokens 7.1 and 11.4; one of 100 3.8 and 4.4.)
+// call is so short that twice the warps are still at most 24 an SM, so that a
+// decode step's requests go to a warp each rather than 16 to one in turn.  (64
+// requests of 1-8 tokens 5.4 us, 16 tokens a warp 11.5; 256 of 4 tokens 6.7 and
+// 11.4; one of 100 3.4 and 4.4.)  24 is a measure for either row size, not what
+// is resident, 32 warps for 2-byte rows and 12 for fp32 ones: with these in its
+// place 2-byte rows take the same (one request of 1000 tokens 3.8 us and 3.95
+// with 32), fp32 rows mostly longer (64 requests of 1-8 5.0 and 5.65 with 12,
+// one of 1000 4.1 and 4.35, two prompts 3.97 and 3.71, 16 the same 15.8).
 constexpr long long kSpanWarps = 152 * 24;
 
 template <int SRC, int KV, int DH>

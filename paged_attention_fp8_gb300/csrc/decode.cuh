@@ -48,9 +48,9 @@
 //    V rows zeroed.  64 requests of 1000-32768 tokens, window 4096, 4 sinks: 88
 //    us, 88 % of the measured copy rate.  Block scales: a page's K scale
 //    multiplies its logits, its V scale is the unit O is kept in.  64 requests of
-//    512-4096 tokens 52.9 us where one scale for the tensor takes 50.2: the 2.7
-//    are the scales' lookups at each segment's start (with constants in their
-//    place 50.9).
+//    512-4096 tokens 52.9 us where one scale for the tensor takes 50.2: 2.0 of the
+//    2.7 are the scales' lookups (50.9 with constants in their place), the rest
+//    the products with them.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -338,21 +338,23 @@ cudaError_t noalloc_scratch(void** ptr);
 
 cudaError_t launch_merge(const DecodeParams& p, int num_merge, int heads_per_cta, int group,
                          cudaStream_t stream);
-// tmap_o: map over o with the 2-byte query tile's box (the fp8-query kernel
-// writes full output tiles with bulk tensor stores through it).  One
-// translation unit per head size (prefill_d128.cu, prefill_d64.cu).
 // Whether a prefill plan's items are those of CTA pairs: a 2-byte cache at
-// head_dim 128, with a window of 896 keys or more if it has one.  (A prompt of
-// 16384 tokens, 32 / 8 heads: window 1000 288 us on pairs and 301 on single
-// CTAs, 700 248 and 232, 500 219 and 189, 300 167 and 142: short windows mean
-// many items of a few tiles, and a pair's item covers twice the tokens, so more
-// of its tiles lie outside each row's window.)
+// head_dim 128, with a window of 896 keys or more if it has one.  Short windows
+// mean many items of a few tiles, and a pair's item covers twice the tokens, so
+// more of its tiles lie outside each row's window.  (us on pairs / on single
+// CTAs, one prompt of 16384 tokens, 32 / 8 heads: window 500 219 / 184, 700 248 /
+// 233, 896 286 / 266, 1000 289 / 295, 1500 386 / 411; 9 prompts of 1000-4000, 16 /
+// 4 heads: 500 178 / 148, 700 195 / 184, 896 226 / 210, 1000 238 / 231, 1500 284 /
+// 303.  The two meet at 1000: just above the bound pairs still cost up to 8 %.)
 constexpr int kPairWindow = 896;
 inline bool prefill_pairs(int head_dim, int kv_dtype, int window) {
     return head_dim == kHeadDim && (kv_dtype == PAFP8_F16 || kv_dtype == PAFP8_BF16) &&
            (window == 0 || window >= kPairWindow);
 }
 
+// tmap_o: map over o with the 2-byte query tile's box (the fp8-query kernel
+// writes full output tiles with bulk tensor stores through it).  One
+// translation unit per head size (prefill_d128.cu, prefill_d64.cu).
 using PrefillLaunch = cudaError_t(const PrefillParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
                                   const CUtensorMap& tmap_v, const CUtensorMap& tmap_o, int num_ctas, cudaStream_t stream);
 PrefillLaunch launch_prefill_d128, launch_prefill_d64, launch_prefill_window_d128, launch_prefill_window_d64,

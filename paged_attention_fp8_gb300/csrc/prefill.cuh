@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // cycles a tile in the dequant warps, but no fit between two items, of which a
     // window makes many short ones.  (A prompt of 16384 tokens: window 300 150 us
     // against 160, 1024 299 and 305, 1536 399 and 400, 2048 498 and 494, 4000 835
-    // and 816; a rule between the two costs both ways 1 %.  Block scales, whose
+    // and 816: the longest lose 2 % by it.  Block scales, whose
     // dequant warps have fewer registers, take 254 us so and 242 with the fit.)
     const bool wide_k = VAR == kVarWindow && !kF8 && !k2 && p.q_dtype == PAFP8_BF16;
     const bool fit_q = VAR != kVarWindow && !kF8 && !k2 && p.q_dtype == PAFP8_BF16;
@@ -698,10 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 w = lds128(src + row * 128 + ((c ^ e) << 4));
                     if (gone(row)) w = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t hb = dst + (c >> 2) * kHalfTile + row * 128;
-                    sts128(hb + (((2 * q8) ^ e) << 4), lo(w.x), hi(w.x), lo(w.y),
-                           hi(w.y));
-                    sts128(hb + (((2 * q8 + 1) ^ e) << 4), lo(w.z), hi(w.z), lo(w.w),
-                           hi(w.w));
+                    sts128(hb + (((2 * q8) ^ e) << 4), lo(w.x), hi(w.x), lo(w.y), hi(w.y));
+                    sts128(hb + (((2 * q8 + 1) ^ e) << 4), lo(w.z), hi(w.z), lo(w.w), hi(w.w));
                 }
             } else {
                 // 64-B fp8 rows under the 64-byte swizzle (16-byte chunk c of
@@ -712,10 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint4 w = lds128(src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
                     if (gone(row)) w = make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t hb = dst + row * 128;
-                    sts128(hb + (((2 * c) ^ e) << 4), lo(w.x), hi(w.x), lo(w.y),
-                           hi(w.y));
-                    sts128(hb + (((2 * c + 1) ^ e) << 4), lo(w.z), hi(w.z), lo(w.w),
-                           hi(w.w));
+                    sts128(hb + (((2 * c) ^ e) << 4), lo(w.x), hi(w.x), lo(w.y), hi(w.y));
+                    sts128(hb + (((2 * c + 1) ^ e) << 4), lo(w.z), hi(w.z), lo(w.w), hi(w.w));
                 }
             }
         };

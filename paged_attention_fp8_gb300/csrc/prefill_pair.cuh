@@ -731,8 +731,7 @@ cudaError_t launch_pair_one(const PrefillParams& p, const CUtensorMap& tq, const
 
 template <int VAR = kVarPlain>
 cudaError_t launch_prefill_pair(const PrefillParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
-                                       const CUtensorMap& tmap_v, const CUtensorMap& tmap_o, int num_ctas,
-                                       cudaStream_t stream) {
+                                const CUtensorMap& tmap_v, const CUtensorMap& tmap_o, int num_ctas, cudaStream_t stream) {
     switch (p.kv_dtype) {
         case PAFP8_F16: return launch_pair_one<PAFP8_F16, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
         case PAFP8_BF16: return launch_pair_one<PAFP8_BF16, VAR>(p, tmap_q, tmap_k, tmap_v, tmap_o, num_ctas, stream);
