@@ -677,7 +677,8 @@ __global__ void __launch_bounds__(32 * 9, 1)
                 acc[i][2] *= ao0;
                 acc[i][3] *= ao1;
             }
-            // P^T as the B operand: transpose the two 8x8 (token x head) blocks.
+            // P^T as the B operand, in V's type (half a step of bf16 is 2^-8, of f16
+            // 2^-11): transpose the two 8x8 (token x head) blocks.
             const uint32_t pb0 = movmatrix_t(kBF ? pack_bf162(e0, e1) : pack_half2(e0, e1));
             const uint32_t pb1 = movmatrix_t(kBF ? pack_bf162(e2, e3) : pack_half2(e2, e3));
 

@@ -531,7 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_wait_st();
                 }
-                // P = exp2(s * scale - m) over the first half of S in TMEM.
+                // P = exp2(s * scale - m) over the first half of S in TMEM, in V's type
+                // (a product's operands have one): half a step of bf16 is 2^-8, of f16
+                // 2^-11; the sum is of the fp32 values.
                 const f32x2 scale2 = make_f32x2(scale, scale), negm2 = make_f32x2(-m_use, -m_use);
                 f32x2 ps[2] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
 #pragma unroll
