@@ -62,12 +62,12 @@ L2_FLUSH_BYTES = 256 << 20
 # workload, from one ncu capture of the kernel source with this SHA-256; a
 # changed kernel reports null until it is captured again.
 NCU_TRAFFIC = {
-    "f0621be6840a37ca4f69ce546c54658ff2f27b2666869c9fbf93c44b3ad230b1": 309449984,
+    "623c810159a0dcff14cdb76c8d7259b22ccac8be276550fb867846f2747dc7c5": 309247744,
 }
 # The same for the prefill kernels, per workload index, keyed by the SHA-256
 # of their sources (prefill.cuh, then prefill_pair.cuh).
 NCU_TRAFFIC_PREFILL = {
-    "8a13c3d40a1851bf48fd09fd4fc3daf8cf33f5b13a39a02edc79f236a82824a6": {4: 168310784, 5: 186613504, 7: 257421568},
+    "264c6c34ee86a850bb8a08b942386f60d85cb6cbbf41ea99f812832e48f99f93": {4: 168386304, 5: 186654464, 7: 250890496},
 }
 
 
