@@ -256,9 +256,10 @@ def pafp8_last_error() -> str:
 # What pafp8_run_tree needs of its arrays, by the handles of the tree plans that
 # exist: the shapes of q and o, of the caches and of lse, page ids, mask rows, KV heads.
 _TREE_SIZES = {}
-# The same of the other plans, for pafp8_run_block_scales: plain numbers until
-# its first call makes the shapes of them (a plan is made anew in every step of
-# some callers).
+# The same of the other plans, for pafp8_run_block_scales: the description's
+# bytes and two numbers until its first call makes the shapes of them (a plan is
+# made anew in every step of some callers, and reading seven fields of a
+# description takes as long as a tenth of the plan).
 _SIZES = {}
 _ITEM = {F16: 2, BF16: 2, E4M3FN: 1, E5M2: 1}  # bytes of an element; the library refuses other types
 
@@ -270,15 +271,19 @@ def _tree_sizes(desc, kv_indptr, qo_indptr):
     return (rows, hq, d), (desc.num_pages, *page), (rows, hq), int(kv_indptr[-1]) if desc.batch > 0 else 0, rows, hkv
 
 
-def _note_sizes(handle, desc, kv_indptr, qo_indptr) -> None:
+_last_i32 = ctypes.c_int32.from_address
+
+
+def _note_sizes(handle, desc, kv_indptr, qo_indptr, kv_at, qo_at) -> None:
+    """kv_at, qo_at: the addresses of the host arrays."""
+    batch = desc.batch
     if desc.mode == MODE_TREE:
         _TREE_SIZES[handle] = _tree_sizes(desc, kv_indptr, qo_indptr)
-        return
-    batch = desc.batch
-    last = ctypes.c_int32.from_address
-    _SIZES[handle] = (batch if qo_indptr is None or batch <= 0 else last(_ptr(qo_indptr) + 4 * batch).value,
-                      desc.num_qo_heads, desc.num_kv_heads, desc.page_size, desc.head_dim, desc.num_pages, desc.kv_layout,
-                      last(_ptr(kv_indptr) + 4 * batch).value if batch > 0 else 0)
+    elif batch <= 0:
+        _SIZES[handle] = bytes(desc), 0, 0
+    else:
+        _SIZES[handle] = bytes(desc), batch if qo_at is None else _last_i32(qo_at + 4 * batch).value, \
+            _last_i32(kv_at + 4 * batch).value
 
 
 def _sizes(handle):
@@ -286,10 +291,11 @@ def _sizes(handle):
     s = _SIZES.get(handle)
     if s is None:
         raise ValueError("block scales need a decode or prefill plan that exists")
-    if len(s) == 8:
-        rows, hq, hkv, ps, d, pages, layout, ids = s
-        s = _SIZES[handle] = ((rows, hq, d), (pages, hkv, ps, d) if layout == LAYOUT_HND else (pages, ps, hkv, d), (rows, hq),
-                              (pages, ps // 16, hkv), ids)
+    if len(s) == 3:
+        p, rows, ids = plan_desc.from_buffer_copy(s[0]), s[1], s[2]
+        pages, ps, hq, hkv, d = p.num_pages, p.page_size, p.num_qo_heads, p.num_kv_heads, p.head_dim
+        s = _SIZES[handle] = ((rows, hq, d), (pages, hkv, ps, d) if p.kv_layout == LAYOUT_HND else (pages, ps, hkv, d),
+                              (rows, hq), (pages, ps // 16, hkv), ids)
     return s
 
 
@@ -307,10 +313,9 @@ def _tree_fits(sizes, arrays, kv_indices, lse) -> None:
 
 def pafp8_plan_create(desc: plan_desc, kv_indptr, last_page_len, qo_indptr=None) -> int:
     kv_indptr, last_page_len, qo_indptr = _i32_host(kv_indptr), _i32_host(last_page_len), _i32_host(qo_indptr)
-    out = ctypes.c_void_p()
-    _check(lib().pafp8_plan_create(ctypes.byref(desc), _ptr(kv_indptr), _ptr(last_page_len),
-                                   _ptr(qo_indptr), ctypes.byref(out)))
-    _note_sizes(out.value, desc, kv_indptr, qo_indptr)
+    kv_at, qo_at, out = _ptr(kv_indptr), _ptr(qo_indptr), ctypes.c_void_p()
+    _check(lib().pafp8_plan_create(ctypes.byref(desc), kv_at, _ptr(last_page_len), qo_at, ctypes.byref(out)))
+    _note_sizes(out.value, desc, kv_indptr, qo_indptr, kv_at, qo_at)
     return out.value
 
 
@@ -321,10 +326,10 @@ def pafp8_plan_create_window(desc: plan_desc, window: int, sinks: int, kv_indptr
             raise ValueError(f"{n} {x} is not a 32-bit integer")
     window, sinks = int(window), int(sinks)
     kv_indptr, last_page_len, qo_indptr = _i32_host(kv_indptr), _i32_host(last_page_len), _i32_host(qo_indptr)
-    out = ctypes.c_void_p()
-    _check(lib().pafp8_plan_create_window(ctypes.byref(desc), window, sinks, _ptr(kv_indptr), _ptr(last_page_len),
-                                          _ptr(qo_indptr), ctypes.byref(out)))
-    _note_sizes(out.value, desc, kv_indptr, qo_indptr)
+    kv_at, qo_at, out = _ptr(kv_indptr), _ptr(qo_indptr), ctypes.c_void_p()
+    _check(lib().pafp8_plan_create_window(ctypes.byref(desc), window, sinks, kv_at, _ptr(last_page_len), qo_at,
+                                          ctypes.byref(out)))
+    _note_sizes(out.value, desc, kv_indptr, qo_indptr, kv_at, qo_at)
     return out.value
 
 

@@ -416,11 +416,16 @@ void build_prefill_meta(pafp8_plan* pl) {
     // (tiles of TQ).
     const bool pair = prefill_pairs(pl->desc.head_dim, pl->desc.kv_dtype, pl->window);
     const int span = (pair ? 4 : 2) * TQ;
-    // Under a window an item is one of a request without the `gap` 16-token
-    // pages between the sinks' and the first that its first row sees.
-    struct T { int32_t b, hk, t0, nkv, gap; };
+    // (16 bytes: with the gap in it, sorting and all took a plan of 1100 items
+    // 26.5 us of an Arm core in place of 22.2.)
+    struct T { int32_t b, hk, t0, nkv; };
     std::vector<T> tiles;
     std::vector<int32_t> req_page(B), req_kv(B);
+    // Under a window an item is one of a request without the `gap` 16-token
+    // pages between the sinks' and the first that its first row sees.
+    auto gap_of = [&](int b, int t0, int qo) {
+        return pl->window > 0 ? window_units(t0 + req_kv[b] - qo - pl->window + 1, pl->sinks).gap : 0;
+    };
     for (int b = 0; b < B; ++b) {
         req_page[b] = pl->kv_indptr[b];
         const int32_t n = pl->kv_indptr[b + 1] - pl->kv_indptr[b];
@@ -431,13 +436,10 @@ void build_prefill_meta(pafp8_plan* pl) {
                 // An item is two query tiles, A starting at t0 and B right
                 // after; its KV tiles are those of its last token.
                 const int last = std::min(t0 + span, qo) - 1;
-                const int gap = pl->window > 0
-                                    ? window_units(t0 + req_kv[b] - qo - pl->window + 1, pl->sinks).gap
-                                    : 0;
-                const int kv = req_kv[b] - gap * kPageSize;
+                const int kv = req_kv[b] - gap_of(b, t0, qo) * kPageSize;
                 const int lim = last + kv - qo;
                 const int nkv = std::min((kv + kTileKeys - 1) / kTileKeys, lim / kTileKeys + 1);
-                tiles.push_back({b, hk, t0, nkv, gap});
+                tiles.push_back({b, hk, t0, nkv});
             }
     }
     std::stable_sort(tiles.begin(), tiles.end(), [](const T& a, const T& c) { return a.nkv > c.nkv; });
@@ -466,13 +468,14 @@ void build_prefill_meta(pafp8_plan* pl) {
     // reads one record per item and no dependent loads.
     std::vector<int32_t> tw;
     for (auto& t : tiles) {
-        tw.push_back(pl->window > 0 ? t.gap : t.b);
+        const int qo = pl->qo_indptr[t.b + 1] - pl->qo_indptr[t.b], gap = gap_of(t.b, t.t0, qo);
+        tw.push_back(pl->window > 0 ? gap : t.b);
         tw.push_back(t.hk);
         tw.push_back(t.t0);
         tw.push_back(t.nkv);
         tw.push_back(pl->qo_indptr[t.b]);
-        tw.push_back(pl->qo_indptr[t.b + 1] - pl->qo_indptr[t.b]);
-        tw.push_back(req_kv[t.b] - t.gap * kPageSize);
+        tw.push_back(qo);
+        tw.push_back(req_kv[t.b] - gap * kPageSize);
         tw.push_back(req_page[t.b]);
     }
     put(kMetaOffTile, tw);
